@@ -65,6 +65,7 @@ typedef enum {
 #define BSG_MAX_K 133144
 #define BSG_DSTATUS_NONFINITE 0x1 /* an input row or column held Inf or NaN */
 #define BSG_DSTATUS_TIMEOUT 0x2   /* a bounded wait inside a kernel expired */
+#define BSG_DSTATUS_RANGE 0x4     /* an index read from device memory (a page, a length, a token) was out of range */
 
 /* Human-readable name of a status code (static storage). */
 const char *bsg_status_str(bsg_status s);
@@ -317,6 +318,140 @@ bsg_status bsg_wquant_cols(const float *W, int64_t K, int64_t N, int64_t ldw, in
  * f32 K x N, ldo >= N.  Asynchronous. */
 bsg_status bsg_wdequant_cols(const void *Q, int64_t K, int64_t N, int64_t ldq, int bits,
                              const float *scale, float *W_hat, int64_t ldo, void *stream);
+
+/* ---- serving a model stored in codes ------------------------------------------ */
+
+/* The calls of a token-by-token decode step: products with weights stored as
+ * int4 codes, an int8 key/value cache with the attention over it, and what is
+ * reported of the logits.  Activations are f32, f16 or bf16 (`dtype` names the
+ * type of every activation argument of a call); codes and scales are as
+ * stored; sums, softmax statistics and scales are f32.  The results are the
+ * same in every run and on every stream; the order of the sums depends on the
+ * sizes alone.  The pages describe the codes (as cited below), not these
+ * calls. */
+typedef enum { BSG_F32 = 0, BSG_F16 = 1, BSG_BF16 = 2 } bsg_dtype;
+
+/* Weight storage as int4 codes with one scale per group of rows and column:
+ * bsg_wquant_cols' scheme ("Integer weights": absmax / 7 rounded to f32,
+ * all-zero groups 0, codes to nearest, ties to even) applied to each block of
+ * `group` consecutive rows of W (K x N f32, ldw >= N) by itself; the last
+ * block may be shorter.  group: a multiple of 32, or 0 for one block of all K
+ * rows (the same codes and scales as bsg_wquant_cols with bits = 4).
+ * Q: K rows of ceil(N/2) bytes (ldq >= ceil(N/2)) in bsg_wquant_cols' packing;
+ * scale: ceil(K/group) x N f32 (lds >= N).  Inf or NaN in W sets
+ * BSG_DSTATUS_NONFINITE; those groups are then unspecified. */
+bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, int group,
+                             uint8_t *Q, int64_t ldq, float *scale, int64_t lds,
+                             int32_t *dstatus, void *stream);
+
+/* Y = X . W_hat for a few rows X (M x K, 1 <= M <= BSG_MATVEC_MAX_M, ldx >= K)
+ * and weights stored as int4 codes with group scales:
+ *   Y[m][n] = sum over groups g of scale[g][n] * sum over k in g of X[m][k] q[k][n],
+ * then max(., 0) with relu != 0.  Q, scale, group: as written by
+ * bsg_wquant_groups, or by bsg_wquant_cols with bits = 4 and group = 0.
+ * Y: M x N (ldy >= N), of X's type.  Inf or NaN in X sets
+ * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  Fastest with Q
+ * 8-byte aligned and ldq a multiple of 8. */
+#define BSG_MATVEC_MAX_M 16
+bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const uint8_t *Q,
+                              int64_t ldq, const float *scale, int64_t lds, int group, int64_t M,
+                              int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
+                              int32_t *dstatus, void *stream);
+
+/* A key/value cache in int8 codes: a pool of pages of `page_tokens` tokens,
+ * with one scale for each page and head.  Layout: k, v int8
+ * [pages][heads][page_tokens][dim], 16-byte aligned; k_scale, v_scale f32
+ * [pages][heads].  page_tokens: a multiple of 16, at most 1024; dim: 32, 64,
+ * 96, 128 or 256.  A sequence b owns the pages table[b][0..table_ld-1] (int32,
+ * DEVICE; table_ld pages hold table_ld * page_tokens tokens at most), its
+ * token at position p being token p % page_tokens of page
+ * table[b][p / page_tokens].  Nothing has to be cleared: what a page holds
+ * beyond the tokens appended to it does not matter. */
+typedef struct {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages;
+    int heads, page_tokens, dim;
+} bsg_kv8_cache;
+
+/* Keys, values, queries or outputs of a step: element d of head h of token t
+ * of sequence b is data[b * stride_batch + t * stride_token + h * stride_head + d]
+ * (strides in elements; a slice of a fused projection needs no copy). */
+typedef struct {
+    void *data;
+    int64_t stride_batch, stride_token, stride_head;
+} bsg_tokens;
+
+/* Append k and v (B sequences of up to T tokens; cache->heads heads of
+ * cache->dim) to the cache: token t of sequence b goes to position
+ * starts[b] + t, for t < counts[b] (counts NULL: T for all; both int32, DEVICE).
+ * The codes follow the unit's step 1, the scale with one f32 product in place
+ * of the quotient: with m the largest |x| of a block's new tokens of one head,
+ *   s = max(RN(m * f32(1/127)), f32(1e-8)),   and, where the page already holds
+ *       tokens before starts[b], s = max(s, the page's scale before the call);
+ *   q = floor(RN(RN(x * f32(1/s)) + 0.5)) for the new tokens;
+ * the page's older codes q0 become floor(RN(RN(q0 * RN(s0 / s)) + 0.5)) where
+ * the scale grew from s0 to s.  A sequence whose start is negative or whose
+ * count is not in 0..T is left out, and so are positions past the table and
+ * pages outside the pool; each sets BSG_DSTATUS_RANGE.  Inf or NaN sets
+ * BSG_DSTATUS_NONFINITE (that page and head are then unspecified).  Two
+ * sequences of one call must not append to the same page. */
+bsg_status bsg_kv8_append(const bsg_kv8_cache *cache, const int32_t *table, int64_t table_ld,
+                          const int32_t *starts, const int32_t *counts, const bsg_tokens *k,
+                          const bsg_tokens *v, bsg_dtype dtype, int64_t B, int64_t T,
+                          int32_t *dstatus, void *stream);
+
+/* Attention of the newest T tokens (1 <= T <= BSG_KV8_MAX_T) of each of B
+ * sequences over the cache: with lens[b] tokens cached (int32, DEVICE; the
+ * new ones among them), query t stands at position lens[b] - T + t and sees
+ * the positions up to its own:
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),  k_j, v_j = code * page scale.
+ * A query at a negative position sees nothing: its output is 0, its lse -inf.
+ * q, out: B x T x heads x cache->dim; `heads` a multiple of cache->heads, query
+ * head h reading key/value head h / (heads / cache->heads).  lse (may be NULL):
+ * f32 [B][T][heads], the natural log of the softmax's denominator.  `workspace`:
+ * bsg_kv8_attend_workspace_size bytes (which depends on the table's width, not
+ * on lens).  A length or page out of range sets BSG_DSTATUS_RANGE (the length
+ * is cut to the table's; the page is skipped); Inf or NaN in q sets
+ * BSG_DSTATUS_NONFINITE (that row is then unspecified). */
+#define BSG_KV8_MAX_T 16
+size_t bsg_kv8_attend_workspace_size(const bsg_kv8_cache *cache, int64_t table_ld, int64_t B,
+                                     int64_t T, int heads);
+bsg_status bsg_kv8_attend(const bsg_kv8_cache *cache, const int32_t *table, int64_t table_ld,
+                          const int32_t *lens, const bsg_tokens *q, const bsg_tokens *out,
+                          bsg_dtype dtype, int64_t B, int64_t T, int heads, float scale,
+                          float *lse, void *workspace, size_t ws_bytes, int32_t *dstatus,
+                          void *stream);
+
+/* What is reported of logits x (M x V, ldl >= V), per row:
+ *   lse = log sum_j exp x_j;  logprob = x_target - lse;  entropy = -sum_j p_j log p_j;
+ *   and the `top` largest (0 <= top <= BSG_MAX_TOP, top <= V), value descending and the
+ *   lowest index first among equals: top_logprob (M x top), top_id (M x top).
+ * target (int64[M], DEVICE; NULL: none): a negative entry marks a row without
+ * a given token, logprob 0; an entry >= V sets BSG_DSTATUS_RANGE, logprob NaN.
+ * -inf is a logit like any other (probability 0); a row of nothing else has
+ * lse -inf, entropy 0 and log probabilities -inf.  +inf or NaN sets
+ * BSG_DSTATUS_NONFINITE (that row is then unspecified).  logprob, entropy, lse:
+ * f32[M], each may be NULL; top_logprob, top_id: not NULL where top > 0. */
+#define BSG_MAX_TOP 32
+bsg_status bsg_logprobs(const void *logits, bsg_dtype dtype, int64_t M, int64_t V, int64_t ldl,
+                        const int64_t *target, int top, float *logprob, float *entropy,
+                        float *lse, float *top_logprob, int32_t *top_id, int32_t *dstatus,
+                        void *stream);
+
+/* The gradient of logprob and entropy with respect to the logits:
+ *   dx_j = g_logprob ([j = target] - p_j) - g_entropy p_j (x_j - lse + entropy),
+ * with lse and entropy as bsg_logprobs gave them (f32[M]).  g_logprob or
+ * g_entropy (f32[M]) may be NULL (zeros); rows without a given token take none
+ * of g_logprob; entropy may be NULL where g_entropy is.  dlogits: M x V of the
+ * logits' type (ldd >= V); it may be the logits themselves.  Where p_j = 0, so
+ * is dx_j (but for the target's own term).  A row whose lse is -inf gets
+ * zeros.  Status bits as bsg_logprobs (a target >= V: that row gets NaN). */
+bsg_status bsg_logprobs_backward(const void *logits, bsg_dtype dtype, int64_t M, int64_t V,
+                                 int64_t ldl, const int64_t *target, const float *lse,
+                                 const float *entropy, const float *g_logprob,
+                                 const float *g_entropy, void *dlogits, int64_t ldd,
+                                 int32_t *dstatus, void *stream);
 
 /* ---- verification of live results ----------------------------------------- */
 

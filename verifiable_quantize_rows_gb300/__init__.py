@@ -26,7 +26,9 @@ import threading
 __all__ = ["BsgError", "load", "exported_symbols", "quantize_rows", "quantize_cols",
            "gemm_s32", "epilogue", "bsgemm_i8", "bsgemm_i8_ex", "bsgemm_i8_host",
            "bsgemm_i8_quantize", "bsgemm_i8_contract", "launch_count", "selftest_scales", "gemm_tile_width", "hash_f32", "probe_hash", "probe_hash_async", "workspace_size", "Workspace",
-           "DSTATUS_NONFINITE", "DSTATUS_TIMEOUT", "MAX_K"]
+           "DSTATUS_NONFINITE", "DSTATUS_TIMEOUT", "DSTATUS_RANGE", "MAX_K",
+           "Kv8Cache", "wquant_groups", "wgroups_matvec", "kv8_append", "kv8_attend", "logprobs",
+           "logprobs_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libbsgemm.so")
@@ -35,6 +37,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "bsgemm.h")
 MAX_K = 133144
 DSTATUS_NONFINITE = 0x1
 DSTATUS_TIMEOUT = 0x2
+DSTATUS_RANGE = 0x4
 
 STATUS = {0: "BSG_OK", 1: "BSG_ERR_ARG", 2: "BSG_ERR_K_TOO_LARGE", 3: "BSG_ERR_WORKSPACE",
           4: "BSG_ERR_CUDA", 5: "BSG_ERR_NONFINITE", 6: "BSG_ERR_TIMEOUT",
@@ -116,6 +119,17 @@ def _declare(lib):
         "bsgemm_i8_chain_workspace_size": ([_i64, _i64, _i64, _i64], _sz),
         "bsgemm_i8_chain": ([_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp,
                              _sz, _vp, _vp], _i32),
+        "bsg_wquant_groups": ([_vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
+        "bsg_wgroups_matvec": ([_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64,
+                                _i32, _vp, _i64, _vp, _vp], _i32),
+        "bsg_kv8_append": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp], _i32),
+        "bsg_kv8_attend_workspace_size": ([_vp, _i64, _i64, _i64, _i32], _sz),
+        "bsg_kv8_attend": ([_vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, ctypes.c_float,
+                            _vp, _vp, _sz, _vp, _vp], _i32),
+        "bsg_logprobs": ([_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                          _vp], _i32),
+        "bsg_logprobs_backward": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                   _vp, _vp], _i32),
         "bsg_mma_ceiling": ([_i32, _vp, ctypes.POINTER(ctypes.c_double), _vp], _i32),
     }
     for name, (args, res) in sigs.items():
@@ -600,3 +614,19 @@ def probe_hash(seed: int, M: int = 1024, N: int = 1024, K: int = 1024, stream=No
     _check(lib.bsg_probe_hash(ctypes.c_uint64(seed), M, N, K, buf, wp, wn, _stream_ptr(stream)),
            "bsg_probe_hash")
     return bytes(buf)
+
+
+# ---------------------------------------------------------------------------
+# The serving calls live in serving.py, which imports torch at its top; they
+# load on first use, so that importing this package still does not.
+_SERVING = ("Kv8Cache", "Logprobs", "wquant_groups", "wgroups_matvec", "kv8_append", "kv8_attend",
+            "logprobs", "logprobs_backward", "MATVEC_MAX_M", "KV8_MAX_T", "MAX_TOP")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -38,6 +38,9 @@ size_t colmax_partial_bytes(int64_t rows, int64_t cols);
 
 int device_sm_count();
 
+// BSG_OK on a device that the kernels are built for (sm_103).
+bsg_status check_device();
+
 // Host-side count of kernel launches made by this library.
 void count_launches(int n);
 
@@ -95,6 +98,34 @@ cudaError_t launch_wquant_cols(const float *W, int64_t K, int64_t N, int64_t ldw
                                int32_t *dstatus, cudaStream_t st);
 cudaError_t launch_wdequant_cols(const void *Q, int64_t K, int64_t N, int64_t ldq, int bits,
                                  const float *scale, float *out, int64_t ldo, cudaStream_t st);
+
+// The serving calls (arguments as the C ABI's, checked there).
+cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, int64_t group,
+                                 uint8_t *Q, int64_t ldq, float *scale, int64_t lds,
+                                 int32_t *dstatus, cudaStream_t st);
+cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const uint8_t *Q,
+                                  int64_t ldq, const float *scale, int64_t lds, int64_t group,
+                                  int64_t M, int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
+                                  int32_t *dstatus, cudaStream_t st);
+cudaError_t launch_kv8_append(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
+                              const int32_t *starts, const int32_t *counts, const bsg_tokens &k,
+                              const bsg_tokens &v, int dtype, int64_t B, int64_t T,
+                              int32_t *dstatus, cudaStream_t st);
+size_t kv8_attend_workspace_bytes(const bsg_kv8_cache &c, int64_t table_ld, int64_t B, int64_t T,
+                                  int heads);
+cudaError_t launch_kv8_attend(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
+                              const int32_t *lens, const bsg_tokens &q, const bsg_tokens &out,
+                              int dtype, int64_t B, int64_t T, int heads, float scale, float *lse,
+                              void *ws, int32_t *dstatus, cudaStream_t st);
+cudaError_t launch_logprobs(const void *logits, int dtype, int64_t M, int64_t V, int64_t ldl,
+                            const int64_t *target, int top, float *logprob, float *entropy,
+                            float *lse, float *top_logprob, int32_t *top_id, int32_t *dstatus,
+                            cudaStream_t st);
+cudaError_t launch_logprobs_backward(const void *logits, int dtype, int64_t M, int64_t V,
+                                     int64_t ldl, const int64_t *target, const float *lse,
+                                     const float *entropy, const float *g_logprob,
+                                     const float *g_entropy, void *dlogits, int64_t ldd,
+                                     int32_t *dstatus, cudaStream_t st);
 
 // Device check of the scale derivation over absmax bit patterns [first, last].
 cudaError_t launch_selftest_scales(uint32_t first, uint32_t last, unsigned long long *bad,

@@ -29,8 +29,6 @@ int device_sm_count() {
     return count[dev];
 }
 
-namespace {
-
 // The kernels are built for sm_103a only.
 bsg_status check_device() {
     static int ok[64] = {0};  // 0 unknown, 1 yes, 2 no
@@ -45,6 +43,8 @@ bsg_status check_device() {
     }
     return ok[dev] == 1 ? BSG_OK : BSG_ERR_UNSUPPORTED;
 }
+
+namespace {
 
 bsg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? BSG_OK : BSG_ERR_CUDA; }
 

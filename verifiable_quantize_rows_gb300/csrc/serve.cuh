@@ -1,0 +1,57 @@
+// serve.cuh -- what the serving kernels share: activation types, the scale
+// and code of a value, and status bits.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bsgemm.h"
+
+namespace bsg {
+namespace {
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+    return __float2bfloat16_rn(x);
+}
+
+// The cache's scale of an absmax, one product where the unit of rows has a
+// quotient (the codes stay within +-127: m / s <= 127 (1 + 2^-22)), and the
+// unit's code floor(RN(RN(x inv) + 0.5)), clamped so that a non-finite x,
+// whose code is unspecified, stays in int8.
+__device__ __forceinline__ float kv8_scale(float absmax) {
+    return fmaxf(__fmul_rn(absmax, 1.0f / 127.0f), 1e-8f);
+}
+__device__ __forceinline__ int unit_code(float x, float inv) {
+    const float f = floorf(__fadd_rn(__fmul_rn(x, inv), 0.5f));
+    return (int)fminf(fmaxf(f, -127.0f), 127.0f);
+}
+
+__device__ __forceinline__ void set_status(int32_t *dstatus, int32_t bits) {
+    if (dstatus && bits) atomicOr(dstatus, bits);
+}
+
+// f(T{}) with the C++ type T of a bsg_dtype.
+template <typename F>
+cudaError_t with_dtype(int dtype, F &&f) {
+    switch (dtype) {
+        case BSG_F32: return f(float{});
+        case BSG_F16: return f(__half{});
+        default: return f(__nv_bfloat16{});
+    }
+}
+
+}  // namespace
+}  // namespace bsg
