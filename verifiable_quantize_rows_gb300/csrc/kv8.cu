@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "bsg_internal.h"
+#include "bsg_ptx.cuh"
 #include "serve.cuh"
 
 namespace bsg {
@@ -109,10 +110,11 @@ __global__ void __launch_bounds__(128)
 //   p = 2^(S' - ref),  S' = S * page scale * softmax scale * log2 e
 //   O^T (dim x 8 slots) += page scale * (V^T (dim x 16) . P^T (16 x 8 slots))
 //
-// Codes go from global memory to registers to the tensor cores, with no
-// shared memory between: a lane's 16 bytes of a row serve as the A operand's
-// rows and columns in whatever order they come, because the order of the
-// summed index and of dim are free as long as Q and the output follow it.
+// Each warp copies its own tiles ahead into a ring of shared memory (cp.async,
+// kStages tiles of 32 dim bytes) and takes them from there to the tensor cores
+// as they lie: a lane's 16 bytes of a row serve as the A operand's rows and
+// columns in whatever order they come, because the order of the summed index
+// and of dim are free as long as Q and the output follow it.
 // An int8 code q becomes the f16 q exactly: the byte q + 128 placed under the
 // exponent of 1024, less 1152.  m16n8k16 and not tcgen05: up to 16 rows are
 // 64 operations to a byte at most, and what bounds the kernel is HBM.
@@ -128,27 +130,20 @@ __global__ void __launch_bounds__(128)
 // outputs are rescaled a few times per row instead of at every tile.
 
 constexpr int kWarps = 4;
+constexpr int kStages = 3;
 constexpr float kRefNone = -3.0e38f;  // the reference of a row that has seen nothing
 constexpr float kSlack = 8.0f;
 
-__device__ __forceinline__ uint4 ld_stream16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// 16 bytes from global to shared memory, asynchronously, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ld_stream8(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "l"(p));
-    return v;
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t ld_stream4(const void *p) {
-    uint32_t v;
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups are done
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // D = A B + C, A 16 x 16 f16 (row), B 16 x 8 f16 (column), C and D f32.
@@ -202,33 +197,48 @@ __host__ __device__ constexpr int value_dim(int w, int g) {
                      : (D / 8) * g + 4 * w;
 }
 
+// Where byte `col` (the start of a lane's piece) of row `r` of a tile lies in
+// shared memory.  Rows of 128 bytes or more would put the rows that one
+// instruction reads on the same banks; their 16-byte pieces are permuted by
+// the row so that both products read without conflicts.
 template <int D>
-__device__ __forceinline__ void load_key_row(uint32_t (&r)[D / 16], const int8_t *row, int t) {
+__device__ __forceinline__ int tile_at(int r, int col) {
+    if (D < 128) return r * D + col;
+    return r * D + (col ^ ((((r >> 1 & 3) << 1) ^ ((r & 1) << 2)) << 4));
+}
+
+template <int D>
+__device__ __forceinline__ void load_key_row(uint32_t (&w)[D / 16], const uint8_t *tile, int r,
+                                             int t) {
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-        const uint4 v = ld_stream16(row + 64 * c + 16 * t);
-        r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+        const uint4 v = *reinterpret_cast<const uint4 *>(tile + tile_at<D>(r, 64 * c + 16 * t));
+        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
     }
     if (D % 64) {
-        const uint2 v = ld_stream8(row + D / 64 * 64 + 8 * t);
-        r[D / 16 - 2] = v.x, r[D / 16 - 1] = v.y;
+        const uint2 v =
+            *reinterpret_cast<const uint2 *>(tile + tile_at<D>(r, D / 64 * 64 + 8 * t));
+        w[D / 16 - 2] = v.x, w[D / 16 - 1] = v.y;
     }
 }
 
 template <int D>
-__device__ __forceinline__ void load_value_row(uint32_t (&r)[D / 32], const int8_t *row, int g) {
+__device__ __forceinline__ void load_value_row(uint32_t (&w)[D / 32], const uint8_t *tile, int r,
+                                               int g) {
     if constexpr (D >= 128) {
 #pragma unroll
         for (int c = 0; c < D / 128; ++c) {
-            const uint4 v = ld_stream16(row + 128 * c + 16 * g);
-            r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+            const uint4 v =
+                *reinterpret_cast<const uint4 *>(tile + tile_at<D>(r, 128 * c + 16 * g));
+            w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
         }
     } else if constexpr (D >= 64) {
-        const uint2 v = ld_stream8(row + 8 * g);
-        r[0] = v.x, r[1] = v.y;
-        if constexpr (D == 96) r[2] = ld_stream4(row + 64 + 4 * g);
+        const uint2 v = *reinterpret_cast<const uint2 *>(tile + tile_at<D>(r, 8 * g));
+        w[0] = v.x, w[1] = v.y;
+        if constexpr (D == 96)
+            w[2] = *reinterpret_cast<const uint32_t *>(tile + tile_at<D>(r, 64 + 4 * g));
     } else {
-        r[0] = ld_stream4(row + 4 * g);
+        w[0] = *reinterpret_cast<const uint32_t *>(tile + tile_at<D>(r, 4 * g));
     }
 }
 
@@ -289,10 +299,13 @@ __device__ __forceinline__ void store_row(const AttendArgs &a, int b, int hk, in
             l > 0.0f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// Shared memory: the queries, then the warps' rings, whose place the partial
+// outputs take at the end.
 template <int D, int NT, int kParts>
 constexpr int attend_smem() {
-    constexpr int rows = 8 * NT / kParts;
-    return NT * (D / 16) * 32 * 8 + kWarps * rows * (D + 2) * 4;
+    constexpr int rings = kWarps * kStages * 32 * D;
+    constexpr int join = kWarps * (8 * NT / kParts) * (D + 2) * 4;
+    return NT * (D / 16) * 32 * 8 + (rings > join ? rings : join);
 }
 
 // grid (splits, heads x row tiles, B)
@@ -302,7 +315,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
     constexpr int kStep = D / 16;           // k16 steps of q.k, m16 tiles of the output
     extern __shared__ __align__(16) uint8_t smem[];
     uint2 *q_s = reinterpret_cast<uint2 *>(smem);                   // [NT][kStep][32 lanes]
-    float *o_s = reinterpret_cast<float *>(q_s + NT * kStep * 32);  // [warp][row][D + 2]: m, l last
+    uint8_t *ring_s = smem + NT * kStep * 32 * 8;                   // [warp][stage][K, V tile]
+    float *o_s = reinterpret_cast<float *>(ring_s);                 // [warp][row][D + 2]: l last
+    __shared__ float4 scales_s[kWarps][kStages];                    // of a stage's tile; z: 1 if there
     __shared__ float mul_s[kRows];                                  // score multiplier of each row
     __shared__ float max_s[kRows][kWarps];
     const int b = blockIdx.z, hk = blockIdx.y / a.row_tiles;
@@ -336,25 +351,34 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
         }
     };
     look_up();
-    // Byte offset of a tile's first code in the pool; -1 where its page is none.
-    auto tile_offset = [&](int tile, int page) -> int64_t {
-        return page < 0 ? -1 : (((int64_t)page * a.c.heads + hk) * P + tile * 16 % P) * D;
+    // Copy the warp's next tile into a stage (nothing past the last, or where
+    // the page is none); a group of copies each time, so that they count.
+    uint8_t *ring = ring_s + warp * kStages * 32 * D;
+    int next = first, in_batch = 0;
+    auto fetch = [&](int stage) {
+        if (in_batch == 32) {
+            in_batch = 0;
+            first = next;
+            look_up();
+        }
+        const int page = __shfl_sync(0xffffffffu, my_page, in_batch);
+        if (lane == in_batch) scales_s[warp][stage] = make_float4(my_ks, my_vs, page < 0 ? 0.0f : 1.0f, 0.0f);
+        if (page >= 0) {
+            const int64_t at = (((int64_t)page * a.c.heads + hk) * P + next * 16 % P) * D;
+            const uint32_t dst = smem_u32(ring + stage * 32 * D);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int e = (i * 32 + lane) * 16, r = e / D, col = e % D;
+                copy16(dst + tile_at<D>(r, col), a.c.k + at + e);
+                copy16(dst + 16 * D + tile_at<D>(r, col), a.c.v + at + e);
+            }
+        }
+        copies_commit();
+        ++in_batch;
+        next += kWarps;
     };
-    uint32_t kr[2][D / 16], vr[4][D / 32];
-    auto load_keys = [&](int64_t at) {
-        const int8_t *k = a.c.k + at;
-        load_key_row<D>(kr[0], k + g * D, t);
-        load_key_row<D>(kr[1], k + (g + 8) * D, t);
-    };
-    auto load_values = [&](int64_t at) {
-        const int8_t *v = a.c.v + at;
-        load_value_row<D>(vr[0], v + (2 * t) * D, g);
-        load_value_row<D>(vr[1], v + (2 * t + 1) * D, g);
-        load_value_row<D>(vr[2], v + (2 * t + 8) * D, g);
-        load_value_row<D>(vr[3], v + (2 * t + 9) * D, g);
-    };
-    int64_t at = tile_offset(first, __shfl_sync(0xffffffffu, my_page, 0));
-    if (at >= 0) load_keys(at), load_values(at);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(i);
 
     // Queries: each row relative to a power of two near its largest |q|, in
     // f16 parts, laid out as the B operand.
@@ -418,24 +442,22 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             for (int u = 0; u < 4; ++u) acc[n][i][u] = 0.0f;
     }
 
-    int in_batch = 0;
-    for (int tile = first; tile < tiles; tile += kWarps) {
-        const float ks = __shfl_sync(0xffffffffu, my_ks, in_batch);
-        const float vs = __shfl_sync(0xffffffffu, my_vs, in_batch);
-        const bool live = at >= 0;
-        // where the next tile is
-        if (++in_batch == 32) {
-            in_batch = 0;
-            first = tile + kWarps;
-            look_up();
-        }
-        const int64_t next =
-            tile_offset(tile + kWarps, __shfl_sync(0xffffffffu, my_page, in_batch));
-        if (!live) {
-            at = next;
-            if (at >= 0) load_keys(at), load_values(at);
+    int stage = 0;
+    for (int tile = j0 / 16 + warp; tile < tiles; tile += kWarps) {
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        const uint8_t *kt = ring + stage * 32 * D, *vt = kt + 16 * D;
+        const float4 of_tile = scales_s[warp][stage];
+        const float ks = of_tile.x, vs = of_tile.y;
+        if (of_tile.z == 0.0f) {
+            __syncwarp();
+            fetch(stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
             continue;
         }
+        uint32_t kr[2][D / 16];
+        load_key_row<D>(kr[0], kt, g, t);
+        load_key_row<D>(kr[1], kt, g + 8, t);
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -452,7 +474,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
                 mma_16816(s[n], a0, a1, a2, a3, q.x, q.y);
             }
         }
-        if (next >= 0) load_keys(next);
 
         // Scores in powers of two; kParts = 2: one row's in s[n][0] and s[n][2].
         bool above = false;
@@ -521,6 +542,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
                 p89[n] = transpose8(pack_half2(p[2], p[3]));
             }
         }
+        uint32_t vr[4][D / 32];
+        load_value_row<D>(vr[0], vt, 2 * t, g);
+        load_value_row<D>(vr[1], vt, 2 * t + 1, g);
+        load_value_row<D>(vr[2], vt, 2 * t + 8, g);
+        load_value_row<D>(vr[3], vt, 2 * t + 9, g);
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
             const uint32_t x0 = vr[0][w] ^ 0x80808080u, x1 = vr[1][w] ^ 0x80808080u;
@@ -542,9 +568,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
                 }
             }
         }
-        at = next;
-        if (at >= 0) load_values(at);
+        __syncwarp();  // every lane has read the stage
+        fetch(stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    copies_wait<0>();
+    __syncthreads();  // the rings are free
 
     // Join the warps: sums over the lanes of a column, then over the warps,
     // each relative to the largest reference.
