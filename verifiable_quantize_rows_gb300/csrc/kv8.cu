@@ -107,8 +107,13 @@ __global__ void __launch_bounds__(128)
 // tile of 16 positions each, and all is joined at the end.  Per tile and warp:
 //
 //   S^T (16 positions x 8 slots) = K (16 x dim) . Q^T      mma m16n8k16, f32 sums
-//   p = 2^(S' - ref),  S' = S * page scale * softmax scale * log2 e
-//   O^T (dim x 8 slots) += page scale * (V^T (dim x 16) . P^T (16 x 8 slots))
+//   p' = 2^(S' - ref),  S' = S * key scale * softmax scale * log2 e + log2(value scale)
+//   O^T (dim x 8 slots) += V^T (dim x 16) . P'^T (16 x 8 slots),  l += p' / value scale
+//
+// The value scale rides in the exponent, so the second product adds up in the
+// tensor cores' own accumulators; `ref` is then a maximum of p v's size, and
+// what f16 drops of a p' is small beside the row's output.  Value scales below
+// 1e-30 count as 1e-30.
 //
 // Each warp copies its own tiles ahead into a ring of shared memory (cp.async,
 // kStages tiles of 32 dim bytes) and takes them from there to the tensor cores
@@ -129,8 +134,17 @@ __global__ void __launch_bounds__(128)
 // than 2^8 above it: probabilities stay below 2^8 (f16 holds 2^15) and the
 // outputs are rescaled a few times per row instead of at every tile.
 
+// The positions are cut into chunks, a CTA each, several for each place on the
+// card, so that the hardware's own scheduling evens out what SMs and lengths
+// differ by.  (Equal shares of all tiles for just the resident CTAs were slower,
+// 143 against 135 us at two sequences of 131071 and 262143 and 113 against 93 at
+// 64 ragged ones: SMs do not read at the same rate.  Chunks of one size were too,
+// by up to 10 % where their waves came out badly.)  A chunk that is its whole
+// sequence is finished in place; otherwise a second launch joins the chunks.
+
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
+constexpr int kMaxSplits = 1024;
 constexpr float kRefNone = -3.0e38f;  // the reference of a row that has seen nothing
 constexpr float kSlack = 8.0f;
 
@@ -146,7 +160,7 @@ __device__ __forceinline__ void copies_wait() {  // all but the newest N groups 
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// D = A B + C, A 16 x 16 f16 (row), B 16 x 8 f16 (column), C and D f32.
+// D += A B, A 16 x 16 f16 (row), B 16 x 8 f16 (column), D f32.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -248,17 +262,15 @@ struct AttendArgs {
     int64_t table_ld;
     const int32_t *lens;
     bsg_tokens q, out;
-    int dtype, tokens, heads, rows, row_tiles, chunk, splits;
+    int dtype, tokens, heads, rows, row_tiles;
+    int width, splits;  // tiles of a table's width, and the chunks it is cut into
     float scale;
-    float *lse, *part_o, *part_ml;
+    float *lse;
+    float *part_o;    // [sequence][head][row][split][D]: the chunks' outputs
+    float2 *part_ml;  // their reference and sum
     int32_t *dstatus;
 };
 
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
-    return dtype == BSG_F32   ? static_cast<const float *>(p)[i]
-           : dtype == BSG_F16 ? __half2float(static_cast<const __half *>(p)[i])
-                              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
 __device__ __forceinline__ void store_any(void *p, int64_t i, int dtype, float x) {
     if (dtype == BSG_F32)
         static_cast<float *>(p)[i] = x;
@@ -279,7 +291,7 @@ __device__ __forceinline__ RowAt row_at(const AttendArgs &a, int hk, int r) {
 
 // The cached length of sequence b, cut to the table's.
 __device__ __forceinline__ int length_of(const AttendArgs &a, int b, bool report) {
-    const int len = a.lens[b];
+    const int len = __ldg(a.lens + b);
     const int64_t most = a.table_ld * a.c.page_tokens;
     if (len >= 0 && len <= most) return len;
     if (report) set_status(a.dstatus, BSG_DSTATUS_RANGE);
@@ -293,84 +305,137 @@ __device__ __forceinline__ void store_row(const AttendArgs &a, int b, int hk, in
     store_any(a.out.data,
               b * a.out.stride_batch + at.token * a.out.stride_token +
                   at.head * a.out.stride_head + d,
-              a.dtype, l > 0.0f || l != l ? __fdividef(o, l) : 0.0f);
+              a.dtype, l > 0.0f || l != l ? o / l : 0.0f);
     if (d == 0 && a.lse)
         a.lse[((int64_t)b * a.tokens + at.token) * a.heads + at.head] =
             l > 0.0f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Shared memory: the queries, then the warps' rings, whose place the partial
+// Floats of a row of partial outputs: its dims, then its sum.
+template <int D>
+__host__ __device__ constexpr int pitch() { return D + 4; }
+
+// Shared memory: the queries, then the warps' rings, whose place the warps'
 // outputs take at the end.
 template <int D, int NT, int kParts>
 constexpr int attend_smem() {
     constexpr int rings = kWarps * kStages * 32 * D;
-    constexpr int join = kWarps * (8 * NT / kParts) * (D + 2) * 4;
+    constexpr int join = kWarps * (8 * NT / kParts) * pitch<D>() * 4;
     return NT * (D / 16) * 32 * 8 + (rings > join ? rings : join);
 }
 
-// grid (splits, heads x row tiles, B)
+// CTAs on an SM: what registers and shared memory allow.
+template <int D, int NT>
+constexpr int attend_per_sm() {
+    return D == 32    ? (NT == 1 ? 7 : NT == 2 ? 5 : 3)
+           : D == 64  ? (NT == 1 ? 5 : NT == 2 ? 4 : 3)
+           : D == 96  ? (NT == 1 ? 5 : NT == 2 ? 4 : 2)
+           : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2)
+                      : 2;
+}
+
+// Where chunk i begins: chunks shrink from 1.6 to 0.4 of their mean, so that
+// those that start together do not end together, and the last are small.
+__device__ __forceinline__ int chunk_begin(const AttendArgs &a, int i) {
+    const int64_t n = a.splits, part = (16 * n - 6 * i) * i;  // of 10 n^2
+    return i >= n ? a.width : (int)(part * (a.width / kWarps) / (10 * n * n)) * kWarps;
+}
+
+// grid (heads x row tiles, B, splits): the first chunks of all first
 template <int D, int NT, int kParts>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArgs a) {
-    constexpr int kRows = 8 * NT / kParts;  // rows of a CTA
+__global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
+    kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int kRows = 8 * NT / kParts;  // rows of a group
+    constexpr int kPitch = pitch<D>();
     constexpr int kStep = D / 16;           // k16 steps of q.k, m16 tiles of the output
     extern __shared__ __align__(16) uint8_t smem[];
     uint2 *q_s = reinterpret_cast<uint2 *>(smem);                   // [NT][kStep][32 lanes]
     uint8_t *ring_s = smem + NT * kStep * 32 * 8;                   // [warp][stage][K, V tile]
-    float *o_s = reinterpret_cast<float *>(ring_s);                 // [warp][row][D + 2]: l last
-    __shared__ float4 scales_s[kWarps][kStages];                    // of a stage's tile; z: 1 if there
+    float *o_s = reinterpret_cast<float *>(ring_s);                 // [warp][row][kPitch]: l at D
+    __shared__ float4 scales_s[kWarps][kStages];                    // of a stage's tile; w: 1 if there
     __shared__ float mul_s[kRows];                                  // score multiplier of each row
     __shared__ float max_s[kRows][kWarps];
-    const int b = blockIdx.z, hk = blockIdx.y / a.row_tiles;
-    const int r0 = blockIdx.y % a.row_tiles * kRows;
-    const int rows = min(kRows, a.rows - r0);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
-    const int len = length_of(a, b, blockIdx.x == 0 && tid == 0);
-    const int j0 = blockIdx.x * a.chunk;
-    if (j0 >= len && (blockIdx.x > 0 || a.splits > 1)) return;  // the join knows that it has no part
-    const int j1 = min(len, j0 + a.chunk);
-
-    // The pages and scales of the warp's next 32 tiles, one to a lane.
     const int P = a.c.page_tokens;
+    const int b = blockIdx.y, hk = blockIdx.x / a.row_tiles, r0 = blockIdx.x % a.row_tiles * kRows;
+    const int split = blockIdx.z;
+    const int rows = min(kRows, a.rows - r0);
+    griddep_launch_dependents();
+
+    // Tiles [tile0, tiles) of the sequence; the pages of the warp's first 32 of
+    // them are looked up, one to a lane, before the length is known.
     const int32_t *table = a.table + b * a.table_ld;
-    const int tiles = (j1 + 15) / 16;
-    int first = j0 / 16 + warp;             // the tile of lane 0
-    int my_page = -1;
-    float my_ks = 0.0f, my_vs = 0.0f;
-    auto look_up = [&]() {
-        const int tile = first + lane * kWarps;
-        my_page = -1;
-        if (tile < tiles) {
-            const int p = table[tile * 16 / P];
-            if (p >= 0 && p < a.c.pages) {
-                my_page = p;
-                my_ks = a.c.k_scale[(int64_t)p * a.c.heads + hk];
-                my_vs = a.c.v_scale[(int64_t)p * a.c.heads + hk];
-            } else {
-                set_status(a.dstatus, BSG_DSTATUS_RANGE);
-            }
+    const int tile0 = chunk_begin(a, split), tile1 = chunk_begin(a, split + 1);
+    int next = tile0 + warp, in_batch = 0;
+    int64_t slot = (int64_t)(next + lane * kWarps) * 16 / P;
+    int my_page = slot < a.table_ld ? __ldg(table + slot) : -1;
+    const int len = length_of(a, b, blockIdx.x == 0 && split == 0 && tid == 0);
+    const int all = (len + 15) / 16;
+    const int tiles = min(all, tile1);
+    if (tile0 >= all && split > 0) return;  // the join knows that it has no part
+
+    // The queries' loads go first, all of them together.
+    constexpr int kMine = (kRows + kWarps - 1) / kWarps;  // rows of a warp
+    float q[kMine][D / 32];
+    auto load_queries = [&](auto type) {
+        using T = decltype(type);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int r = warp + i * kWarps;
+            const RowAt at = row_at(a, hk, r0 + r);
+            const T *row = static_cast<const T *>(a.q.data) + b * a.q.stride_batch +
+                           at.token * a.q.stride_token + at.head * a.q.stride_head + lane;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) q[i][j] = r < rows ? to_f32(row[32 * j]) : 0.0f;
         }
     };
-    look_up();
-    // Copy the warp's next tile into a stage (nothing past the last, or where
-    // the page is none); a group of copies each time, so that they count.
+    if (kParts == 2)
+        load_queries(float{});
+    else if (a.dtype == BSG_F16)
+        load_queries(__half{});
+    else
+        load_queries(__nv_bfloat16{});
+
+    // The warp's tiles are fetched kStages ahead: where its next 32 lie in the
+    // pool (in tiles; -1: nowhere) and their scales, one to a lane.
     uint8_t *ring = ring_s + warp * kStages * 32 * D;
-    int next = first, in_batch = 0;
+    const int8_t *k_lane = a.c.k + lane * 16, *v_lane = a.c.v + lane * 16;
+    int my_at;
+    float4 my_scales;
+    auto look_up = [&]() {
+        const int tile = next + lane * kWarps;
+        my_at = -1;
+        my_scales = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tile >= tiles) return;
+        if (my_page < 0 || my_page >= a.c.pages) {
+            set_status(a.dstatus, BSG_DSTATUS_RANGE);
+            return;
+        }
+        const int64_t ph = (int64_t)my_page * a.c.heads + hk;
+        my_at = (int)(ph * (P / 16) + tile % (P / 16));
+        const float vs = fmaxf(a.c.v_scale[ph], 1e-30f);
+        my_scales = make_float4(a.c.k_scale[ph], log2f(vs), __frcp_rn(vs), 1.0f);
+    };
+    look_up();
+    // A group of copies each time, so that they count; no copies past the last
+    // tile, or where its page is none.
     auto fetch = [&](int stage) {
         if (in_batch == 32) {
             in_batch = 0;
-            first = next;
+            const int tile = next + lane * kWarps;
+            if (tile < tiles) my_page = __ldg(table + (int64_t)tile * 16 / P);
             look_up();
         }
-        const int page = __shfl_sync(0xffffffffu, my_page, in_batch);
-        if (lane == in_batch) scales_s[warp][stage] = make_float4(my_ks, my_vs, page < 0 ? 0.0f : 1.0f, 0.0f);
-        if (page >= 0) {
-            const int64_t at = (((int64_t)page * a.c.heads + hk) * P + next * 16 % P) * D;
+        const int at = __shfl_sync(0xffffffffu, my_at, in_batch);
+        if (lane == in_batch) scales_s[warp][stage] = my_scales;
+        if (at >= 0) {
+            const int8_t *k = k_lane + (int64_t)at * (16 * D), *v = v_lane + (int64_t)at * (16 * D);
             const uint32_t dst = smem_u32(ring + stage * 32 * D);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const int e = (i * 32 + lane) * 16, r = e / D, col = e % D;
-                copy16(dst + tile_at<D>(r, col), a.c.k + at + e);
-                copy16(dst + 16 * D + tile_at<D>(r, col), a.c.v + at + e);
+                const int e = (i * 32 + lane) * 16;
+                copy16(dst + tile_at<D>(e / D, e % D), k + i * 512);
+                copy16(dst + 16 * D + tile_at<D>(e / D, e % D), v + i * 512);
             }
         }
         copies_commit();
@@ -379,20 +444,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(i);
+    int stage = 0;
 
     // Queries: each row relative to a power of two near its largest |q|, in
     // f16 parts, laid out as the B operand.
-    for (int r = warp; r < kRows; r += kWarps) {
-        float m = 0.0f, x[(D + 31) / 32];
-        bool bad = false;
-        const RowAt ra = row_at(a, hk, min(r0 + r, a.rows - 1));
-        const int64_t base = b * a.q.stride_batch + ra.token * a.q.stride_token +
-                             ra.head * a.q.stride_head;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            x[i] = r < rows ? load_any(a.q.data, base + lane + 32 * i, a.dtype) : 0.0f;
-            bad |= !isfinite(x[i]);
-            m = fmaxf(m, fabsf(x[i]));
+    for (int i = 0; i < kMine; ++i) {
+        const int r = warp + i * kWarps;
+        if (r >= kRows) break;
+        float m = 0.0f;
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            bad |= !isfinite(q[i][j]);
+            m = fmaxf(m, fabsf(q[i][j]));
         }
         if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
 #pragma unroll
@@ -404,15 +469,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             mul_s[r] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - max(e, -126)) << 23);
         __half *qh = reinterpret_cast<__half *>(q_s);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int d = lane + 32 * i;
+        for (int j = 0; j < D / 32; ++j) {
+            const int d = lane + 32 * j;
             // the step and lane whose word covers dim d
             int w, tt;
             if (d < D / 64 * 64)
                 w = d / 64 * 4 + d % 16 / 4, tt = d % 64 / 16;
             else
                 w = D / 64 * 4 + d % 8 / 4, tt = d % 32 / 8;
-            const float y = x[i] * up;
+            const float y = q[i][j] * up;
             const __half hi = __float2half_rn(y);
             const int slot = r * kParts;
             const int word = ((slot / 8 * kStep + w) * 32 + slot % 8 * 4 + tt) * 4 + d % 4;
@@ -432,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
         for (int u = 0; u < 2; ++u) {
             const int r = (8 * n + 2 * t + u) / kParts;
             mul[n][u] = mul_s[r];
-            ref[n][u] = kRefNone;
+            ref[n][u] = 0.0f;
             sum[n][u] = 0.0f;
             see[n][u] = r < rows ? len - a.tokens + row_at(a, hk, r0 + r).token + 1 : 0;
         }
@@ -442,14 +507,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             for (int u = 0; u < 4; ++u) acc[n][i][u] = 0.0f;
     }
 
-    int stage = 0;
-    for (int tile = j0 / 16 + warp; tile < tiles; tile += kWarps) {
+    // Rows that have seen nothing yet (bit 2n + u; their ref is 0): only before
+    // the warp's first tile, or where that is one some row may not see.
+    uint32_t none = 0xffffffffu;
+    bool fresh = true;
+    for (int tile = tile0 + warp; tile < tiles; tile += kWarps) {
         copies_wait<kStages - 1>();
         __syncwarp();
         const uint8_t *kt = ring + stage * 32 * D, *vt = kt + 16 * D;
         const float4 of_tile = scales_s[warp][stage];
-        const float ks = of_tile.x, vs = of_tile.y;
-        if (of_tile.z == 0.0f) {
+        if (of_tile.w == 0.0f) {
             __syncwarp();
             fetch(stage);
             stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -475,42 +542,41 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             }
         }
 
-        // Scores in powers of two; kParts = 2: one row's in s[n][0] and s[n][2].
-        bool above = false;
+        // Exponents relative to the reference; kParts = 2: one row's in x[n][0]
+        // and x[n][2].
+        float x[NT][4], most = -INFINITY;
         const bool edge = tile * 16 + 16 > len - a.tokens;  // some row may not see all of it
+        auto exponents = [&]() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (kParts == 2) {
-                s[n][0] = fmaf(s[n][1], 0x1p-11f, s[n][0]) * (ks * mul[n][0]);
-                s[n][2] = fmaf(s[n][3], 0x1p-11f, s[n][2]) * (ks * mul[n][0]);
-            } else {
-                s[n][0] *= ks * mul[n][0], s[n][1] *= ks * mul[n][1];
-                s[n][2] *= ks * mul[n][0], s[n][3] *= ks * mul[n][1];
-            }
-            if (edge) {
-                const int p0 = tile * 16 + g;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (p0 + u / 2 * 8 >= see[n][u % 2]) s[n][u] = -INFINITY;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; u += kParts) above |= s[n][u] > ref[n][u % 2] + kSlack;
-        }
-        if (__any_sync(0xffffffffu, above)) {
+                for (int u = 0; u < 4; u += kParts) {
+                    const float score = kParts == 2 ? fmaf(s[n][u + 1], 0x1p-11f, s[n][u]) : s[n][u];
+                    x[n][u] = fmaf(score, of_tile.x * mul[n][u % 2], of_tile.y - ref[n][u % 2]);
+                    if (edge && tile * 16 + g + u / 2 * 8 >= see[n][u % 2]) x[n][u] = -INFINITY;
+                    most = fmaxf(most, x[n][u]);
+                }
+        };
+        exponents();
+        if (__any_sync(0xffffffffu, most > kSlack || fresh || edge)) {
+            fresh = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float keep[2];
 #pragma unroll
                 for (int u = 0; u < 2; u += kParts) {
-                    float m = fmaxf(s[n][u], s[n][u + 2]);
+                    float m = fmaxf(x[n][u], x[n][u + 2]);
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     keep[u] = 1.0f;
-                    if (m > ref[n][u] + kSlack) {  // of this row alone
-                        keep[u] = exp2_fast(ref[n][u] - m);
-                        ref[n][u] = m;
+                    // each row by itself: no other row's values move its reference
+                    const uint32_t bit = 1u << (2 * n + u);
+                    if (none & bit ? m > -INFINITY : m > kSlack) {
+                        ref[n][u] += m;
+                        keep[u] = none & bit ? 0.0f : exp2_fast(-m);
                         sum[n][u] *= keep[u];
+                        none &= ~bit;
                     }
                 }
                 if (kParts == 2) keep[1] = keep[0];
@@ -519,15 +585,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
 #pragma unroll
                     for (int u = 0; u < 4; ++u) acc[n][i][u] *= keep[u % 2];
             }
+            exponents();
         }
         // Probabilities, as the B operand of the second product.
         uint32_t p01[NT], p89[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (kParts == 2) {
-                const float pa = exp2_fast(s[n][0] - ref[n][0]);
-                const float pb = exp2_fast(s[n][2] - ref[n][0]);
-                sum[n][0] += pa + pb;
+                const float pa = exp2_fast(x[n][0]), pb = exp2_fast(x[n][2]);
+                sum[n][0] = fmaf(pa + pb, of_tile.z, sum[n][0]);
                 const float ha = __half2float(__float2half_rn(pa));
                 const float hb = __half2float(__float2half_rn(pb));
                 p01[n] = transpose8(pack_half2(ha, (pa - ha) * 2048.0f));
@@ -535,9 +601,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             } else {
                 float p[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) p[u] = exp2_fast(s[n][u] - ref[n][u % 2]);
-                sum[n][0] += p[0] + p[2];
-                sum[n][1] += p[1] + p[3];
+                for (int u = 0; u < 4; ++u) p[u] = exp2_fast(x[n][u]);
+                sum[n][0] = fmaf(p[0] + p[2], of_tile.z, sum[n][0]);
+                sum[n][1] = fmaf(p[1] + p[3], of_tile.z, sum[n][1]);
                 p01[n] = transpose8(pack_half2(p[0], p[1]));
                 p89[n] = transpose8(pack_half2(p[2], p[3]));
             }
@@ -559,25 +625,21 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
                 const uint32_t a0 = codes_half2<0x4140>(lo), a1 = codes_half2<0x4342>(lo);
                 const uint32_t a2 = codes_half2<0x4140>(hi), a3 = codes_half2<0x4342>(hi);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_16816(d, a0, a1, a2, a3, p01[n], p89[n]);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        acc[n][2 * w + h][u] = fmaf(d[u], vs, acc[n][2 * w + h][u]);
-                }
+                for (int n = 0; n < NT; ++n)
+                    mma_16816(acc[n][2 * w + h], a0, a1, a2, a3, p01[n], p89[n]);
             }
         }
         __syncwarp();  // every lane has read the stage
         fetch(stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+
     copies_wait<0>();
     __syncthreads();  // the rings are free
 
     // Join the warps: sums over the lanes of a column, then over the warps,
     // each relative to the largest reference.
-    float *mine = o_s + warp * kRows * (D + 2);
+    float *mine = o_s + warp * kRows * kPitch;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -588,8 +650,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             const int r = (8 * n + 2 * t + u) / kParts;
             if (g == 0) {
-                mine[r * (D + 2) + D] = l;
-                max_s[r][warp] = ref[n][u];
+                mine[r * kPitch + D] = l;
+                max_s[r][warp] = none & (1u << (2 * n + u)) ? kRefNone : ref[n][u];
             }
 #pragma unroll
             for (int i = 0; i < kStep; ++i) {
@@ -600,51 +662,95 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attend_kernel(const AttendArg
                                     fmaf(acc[n][i][3], 0x1p-11f, acc[n][i][2]));
                 else
                     o = make_float2(acc[n][i][u], acc[n][i][u + 2]);
-                *reinterpret_cast<float2 *>(mine + r * (D + 2) + d) = o;
+                *reinterpret_cast<float2 *>(mine + r * kPitch + d) = o;
             }
         }
     }
     __syncthreads();
-    for (int e = tid; e < rows * D; e += kWarps * 32) {
-        const int r = e / D, d = e % D;
+    for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = max_s[r][0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) m = fmaxf(m, max_s[r][w]);
-        float o = 0.0f, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = exp2_fast(max_s[r][w] - m);
-            o = fmaf(o_s[(w * kRows + r) * (D + 2) + d], f, o);
-            l = fmaf(o_s[(w * kRows + r) * (D + 2) + D], f, l);
+            const float *p = o_s + (w * kRows + r) * kPitch;
+            const float4 v = *reinterpret_cast<const float4 *>(p + d);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+            l = fmaf(p[D], f, l);
         }
-        if (a.splits == 1) {
-            store_row(a, b, hk, r0 + r, d, o, m, l);
+        if (split == 0 && all <= tile1) {
+            store_row(a, b, hk, r0 + r, d, o.x, m, l);
+            store_row(a, b, hk, r0 + r, d + 1, o.y, m, l);
+            store_row(a, b, hk, r0 + r, d + 2, o.z, m, l);
+            store_row(a, b, hk, r0 + r, d + 3, o.w, m, l);
         } else {
-            const int64_t part =
-                (((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + blockIdx.x;
-            a.part_o[part * D + d] = o;
-            if (d == 0) a.part_ml[2 * part] = m, a.part_ml[2 * part + 1] = l;
+            const int64_t part = (((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + split;
+            *reinterpret_cast<float4 *>(a.part_o + part * D + d) = o;
+            if (d == 0) a.part_ml[part] = make_float2(m, l);
         }
     }
 }
 
-// Joins the splits of one row: grid (rows, heads, B), dim threads.
-__global__ void kv8_join_kernel(const AttendArgs a) {
-    const int r = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, d = threadIdx.x, D = blockDim.x;
-    const int len = length_of(a, b, false);
-    const int n = (len + a.chunk - 1) / a.chunk;
+// Joins the chunks of one row: grid (rows, heads, B), a column of four and
+// every kSides-th chunk to a thread.
+constexpr int kJoin = 128;
+template <int D>
+__global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int kCols = D / 4, kSides = kJoin / kCols;
+    __shared__ float f_s[kMaxSplits], red[kJoin / 32];
+    __shared__ float4 o_s[kSides][kCols];
+    const int r = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int all = (length_of(a, b, false) + 15) / 16;
+    if (all <= chunk_begin(a, 1)) return;  // finished where it was computed
+    int n = 0;                             // chunks that begin within the length
+    for (int i0 = 0; i0 < a.splits; i0 += kJoin)
+        n += __syncthreads_count(i0 + tid < a.splits && chunk_begin(a, i0 + tid) < all);
+    griddep_wait();
     const int64_t part = (((int64_t)b * a.c.heads + hk) * a.rows + r) * a.splits;
-    const float *ml = a.part_ml + 2 * part, *po = a.part_o + part * D + d;
+    const float2 *ml = a.part_ml + part;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + part * D);
+    const int col = tid % kCols, side = tid / kCols;
+    // the first outputs are on their way while the weights are found
+    constexpr int kAhead = 4;
+    float4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (side < kSides && side + i * kSides < n) v[i] = po[(int64_t)(side + i * kSides) * kCols + col];
     float m = kRefNone;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[2 * i]);
-    float o = 0.0f, l = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float f = exp2_fast(ml[2 * i] - m);
-        o = fmaf(po[(int64_t)i * D], f, o);
-        l = fmaf(ml[2 * i + 1], f, l);
+    for (int i = tid; i < n; i += kJoin) m = fmaxf(m, ml[i].x);
+    m = block_max<kJoin>(m, red);
+    float l = 0.0f;
+    for (int i = tid; i < n; i += kJoin) {
+        const float2 x = ml[i];
+        f_s[i] = exp2_fast(x.x - m);
+        l = fmaf(x.y, f_s[i], l);
     }
-    store_row(a, b, hk, r, d, o, m, l);
+    l = block_sum<kJoin>(l, red);  // and f_s is complete
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = side; i0 < n && side < kSides; i0 += kAhead * kSides) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int at = i0 + i * kSides, then = at + kAhead * kSides;
+            if (at >= n) break;
+            const float f = f_s[at];
+            o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y);
+            o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+            if (then < n) v[i] = po[(int64_t)then * kCols + col];
+        }
+    }
+    if (side < kSides) o_s[side][col] = o;
+    __syncthreads();
+    for (int d = tid; d < D; d += kJoin) {
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSides; ++i) y += reinterpret_cast<const float *>(&o_s[i][d / 4])[d % 4];
+        store_row(a, b, hk, r, d, y, m, l);
+    }
 }
 
 }  // namespace
@@ -666,12 +772,17 @@ cudaError_t launch_kv8_append(const bsg_kv8_cache &c, const int32_t *table, int6
     });
 }
 
-// How a call is laid out: slots of 8 that a CTA holds, and how the positions
-// are split.  Splits follow the table's width alone (lengths are in device
-// memory).
+// How a call is laid out: the slots of 8 that a CTA holds, and the chunks.
+// Chunks follow the table's width alone (lengths are in device memory).
 struct AttendPlan {
-    int parts, nt, rows, row_tiles, chunk, splits;
+    int parts, nt, rows, row_tiles, width, splits;
 };
+
+template <int D>
+static int per_sm(int nt) {
+    return nt == 1 ? attend_per_sm<D, 1>() : nt == 2 ? attend_per_sm<D, 2>() : attend_per_sm<D, 4>();
+}
+
 static AttendPlan attend_plan(const bsg_kv8_cache &c, int64_t table_ld, int64_t B, int64_t T,
                               int heads, int parts) {
     AttendPlan p;
@@ -680,15 +791,20 @@ static AttendPlan attend_plan(const bsg_kv8_cache &c, int64_t table_ld, int64_t 
     const int slots = p.rows * parts;
     p.nt = slots <= 8 ? 1 : slots <= 16 || c.dim == 256 ? 2 : 4;
     p.row_tiles = (slots + 8 * p.nt - 1) / (8 * p.nt);
-    const int64_t groups = B * c.heads * p.row_tiles, most = table_ld * c.page_tokens;
-    const int64_t ctas = (int64_t)device_sm_count() * 16;
-    int64_t splits = (ctas + groups - 1) / groups;
-    const int64_t least = 64;  // positions of a split: one tile for each warp
-    if (splits > (most + least - 1) / least) splits = (most + least - 1) / least;
-    if (splits > 1024) splits = 1024;
-    const int64_t chunk = ((most + splits - 1) / splits + least - 1) / least * least;
-    p.chunk = (int)chunk;
-    p.splits = (int)((most + chunk - 1) / chunk);
+    const int n = c.dim == 32    ? per_sm<32>(p.nt)
+                  : c.dim == 64  ? per_sm<64>(p.nt)
+                  : c.dim == 96  ? per_sm<96>(p.nt)
+                  : c.dim == 128 ? per_sm<128>(p.nt)
+                                 : per_sm<256>(p.nt);
+    const int64_t places = (int64_t)device_sm_count() * n, groups = B * c.heads * p.row_tiles;
+    const int64_t most = table_ld * (c.page_tokens / 16);  // tiles of a sequence
+    // 3 and 6 chunks a place: 99 and 96 us against 94 (64 ragged sequences), 145 and 154 against 146 (two long ones)
+    constexpr int kPerPlace = 4;
+    int64_t splits = (kPerPlace * places + groups - 1) / groups;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits > (most + kWarps - 1) / kWarps) splits = (most + kWarps - 1) / kWarps;
+    p.splits = (int)splits;
+    p.width = (int)((most + kWarps - 1) / kWarps * kWarps);
     return p;
 }
 
@@ -697,37 +813,62 @@ size_t kv8_attend_workspace_bytes(const bsg_kv8_cache &c, int64_t table_ld, int6
     size_t most = 256;
     for (int parts = 1; parts <= 2; ++parts) {
         const AttendPlan p = attend_plan(c, table_ld, B, T, heads, parts);
-        const size_t n = (size_t)B * c.heads * p.rows * p.splits * (c.dim + 2) * 4;
+        const size_t n = (size_t)B * c.heads * p.rows * p.splits * (c.dim * 4 + 8);
         if (p.splits > 1 && n > most) most = n;
     }
     return (most + 255) / 256 * 256;
 }
 
 template <int D, int NT, int kParts>
-static cudaError_t launch_attend(const AttendArgs &a, const dim3 &grid, cudaStream_t st) {
+static cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
     constexpr int smem = attend_smem<D, NT, kParts>();
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D, NT, kParts>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static bool set[64] = {false};  // this kernel's shared memory, on each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024 && (dev >= 64 || !set[dev])) {
+        e = cudaFuncSetAttribute(kv8_attend_kernel<D, NT, kParts>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
     }
+    const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)B, (unsigned)p.splits);
     kv8_attend_kernel<D, NT, kParts><<<grid, kWarps * 32, smem, st>>>(a);
+    count_launches(1);
     return cudaGetLastError();
 }
 
+// The join, launched while the attention still runs: its blocks wait for it.
 template <int D>
-static cudaError_t launch_attend_dim(const AttendArgs &a, const AttendPlan &p, const dim3 &grid,
-                                     cudaStream_t st) {
+static cudaError_t launch_join(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)B);
+    cfg.blockDim = dim3(kJoin);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, a);
+}
+
+template <int D>
+static cudaError_t launch_attend_dim(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
+    cudaError_t e = cudaErrorInvalidValue;
     if (p.parts == 1) {
-        if (p.nt == 1) return launch_attend<D, 1, 1>(a, grid, st);
-        if (p.nt == 2) return launch_attend<D, 2, 1>(a, grid, st);
-        if constexpr (D < 256) return launch_attend<D, 4, 1>(a, grid, st);
+        if (p.nt == 1) e = launch_attend<D, 1, 1>(a, p, B, st);
+        if (p.nt == 2) e = launch_attend<D, 2, 1>(a, p, B, st);
+        if constexpr (D < 256)
+            if (p.nt == 4) e = launch_attend<D, 4, 1>(a, p, B, st);
     } else {
-        if (p.nt == 1) return launch_attend<D, 1, 2>(a, grid, st);
-        if (p.nt == 2) return launch_attend<D, 2, 2>(a, grid, st);
-        if constexpr (D < 256) return launch_attend<D, 4, 2>(a, grid, st);
+        if (p.nt == 1) e = launch_attend<D, 1, 2>(a, p, B, st);
+        if (p.nt == 2) e = launch_attend<D, 2, 2>(a, p, B, st);
+        if constexpr (D < 256)
+            if (p.nt == 4) e = launch_attend<D, 4, 2>(a, p, B, st);
     }
-    return cudaErrorInvalidValue;
+    return e == cudaSuccess && p.splits > 1 ? launch_join<D>(a, p, B, st) : e;
 }
 
 cudaError_t launch_kv8_attend(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
@@ -735,28 +876,18 @@ cudaError_t launch_kv8_attend(const bsg_kv8_cache &c, const int32_t *table, int6
                               int dtype, int64_t B, int64_t T, int heads, float scale, float *lse,
                               void *ws, int32_t *dstatus, cudaStream_t st) {
     const AttendPlan p = attend_plan(c, table_ld, B, T, heads, dtype == BSG_F32 ? 2 : 1);
-    AttendArgs a{c, table, table_ld, lens, q, out, dtype, (int)T, heads, p.rows, p.row_tiles,
-                 p.chunk, p.splits, scale, lse, nullptr, nullptr, dstatus};
-    a.part_o = static_cast<float *>(ws);
-    a.part_ml = a.part_o + (size_t)B * c.heads * p.rows * p.splits * c.dim;
     if ((int64_t)c.heads * p.row_tiles > 65535) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)p.splits, (unsigned)(c.heads * p.row_tiles), (unsigned)B);
-    cudaError_t e;
+    AttendArgs a{c, table, table_ld, lens, q, out, dtype, (int)T, heads, p.rows, p.row_tiles,
+                 p.width, p.splits, scale, lse, nullptr, nullptr, dstatus};
+    a.part_o = static_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)B * c.heads * p.rows * p.splits * c.dim);
     switch (c.dim) {
-        case 32: e = launch_attend_dim<32>(a, p, grid, st); break;
-        case 64: e = launch_attend_dim<64>(a, p, grid, st); break;
-        case 96: e = launch_attend_dim<96>(a, p, grid, st); break;
-        case 128: e = launch_attend_dim<128>(a, p, grid, st); break;
-        default: e = launch_attend_dim<256>(a, p, grid, st); break;
+        case 32: return launch_attend_dim<32>(a, p, B, st);
+        case 64: return launch_attend_dim<64>(a, p, B, st);
+        case 96: return launch_attend_dim<96>(a, p, B, st);
+        case 128: return launch_attend_dim<128>(a, p, B, st);
+        default: return launch_attend_dim<256>(a, p, B, st);
     }
-    if (e != cudaSuccess) return e;
-    count_launches(1);
-    if (p.splits > 1) {
-        kv8_join_kernel<<<dim3((unsigned)p.rows, (unsigned)c.heads, (unsigned)B), c.dim, 0, st>>>(a);
-        count_launches(1);
-        e = cudaGetLastError();
-    }
-    return e;
 }
 
 }  // namespace bsg
