@@ -350,8 +350,8 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
  * then max(., 0) with relu != 0.  Q, scale, group: as written by
  * bsg_wquant_groups, or by bsg_wquant_cols with bits = 4 and group = 0.
  * Y: M x N (ldy >= N), of X's type.  Inf or NaN in X sets
- * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  Fastest with Q
- * 8-byte aligned and ldq a multiple of 8. */
+ * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  N <= 2^25, K <=
+ * 2^30.  Fastest with Q 16-byte aligned and ldq a multiple of 16. */
 #define BSG_MATVEC_MAX_M 16
 bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const uint8_t *Q,
                               int64_t ldq, const float *scale, int64_t lds, int group, int64_t M,

@@ -67,7 +67,7 @@ bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const
                               int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
                               int32_t *dstatus, void *stream) {
     if (!typed(X, dtype) || !typed(Y, dtype) || !Q || !typed(scale, BSG_F32) || M < 1 ||
-        M > BSG_MATVEC_MAX_M || !size_ok(N) || !size_ok(K) || ldx < K || ldy < N ||
+        M > BSG_MATVEC_MAX_M || N < 1 || N > (1 << 25) || K < 1 || K > (1 << 30) || ldx < K || ldy < N ||
         ldq < (N + 1) / 2 || lds < N || !group_ok(group) || (relu != 0 && relu != 1))
         return BSG_ERR_ARG;
     const bsg_status s = check_device();

@@ -4,12 +4,16 @@
 // The storage is wquant.cu's scheme ("Precision" manual, section "Integer
 // weights") on blocks of `group` rows: s = absmax / 7 rounded to f32, codes
 // the integer nearest w / s, ties to even, all-zero blocks s = 0.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "bsg_internal.h"
+#include "bsg_ptx.cuh"
 #include "serve.cuh"
 #include "wq_round.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace bsg {
 namespace {
@@ -48,36 +52,389 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// One thread per byte column and row of X: the plain sum over k.
-template <typename T>
-__global__ void __launch_bounds__(128)
-    wgroups_matvec_kernel(const T *__restrict__ X, int64_t ldx, const uint8_t *__restrict__ Q,
-                          int64_t ldq, const float *__restrict__ scale, int64_t lds,
-                          int64_t group, int64_t N, int64_t K, int relu, T *__restrict__ Y,
-                          int64_t ldy, int32_t *__restrict__ dstatus) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (2 * c >= N) return;
-    const T *x = X + blockIdx.y * ldx;
-    const bool two = 2 * c + 1 < N;
-    float y0 = 0.0f, y1 = 0.0f;
-    bool bad = false;
-    for (int64_t k0 = 0, g = 0; k0 < K; k0 += group, ++g) {
-        const int64_t k1 = k0 + group < K ? k0 + group : K;
-        float a0 = 0.0f, a1 = 0.0f;
-        for (int64_t k = k0; k < k1; ++k) {
-            const int b = Q[k * ldq + c];
-            const float v = to_f32(x[k]);
-            bad |= !isfinite(v);
-            a0 = fmaf(v, (float)((b << 28) >> 28), a0);
-            a1 = fmaf(v, (float)((b << 24) >> 28), a1);
+// ---- products ---------------------------------------------------------------
+//
+// Y[m][n] = sum_g s[g][n] sum_{k in g} X[m][k] q[k][n] for up to 16 rows.  What
+// has to be read is half a byte per weight, and at most 16 rows are 64
+// operations to a byte: HBM bounds it, provided a weight costs the SM less than
+// 2.7 instructions per lane.  So the products run on the tensor cores
+// (m16n8k16, the weights as the 16-row operand, X's rows as the 8 columns), and
+// a weight is unpacked with one and a quarter:
+//
+//   Two rows' 16-bit pieces of 4 codes side by side (a byte permute), masked to
+//   one nibble each, are two f16 subnormals, u 2^-24 (low nibble of a byte) or
+//   u 2^-20 (high), with u = q + 8 after the nibble's top bit is flipped in the
+//   same three-input logic operation; one f16 multiply-add makes them q 2^-10.
+//   (Left subnormal, with 8 sum_k x taken off the sums, they cost a third less
+//   and lost ten bits: the tensor cores align products by the exponent field.)
+//
+// f32 rows are two f16 parts, hi + 2^-11 lo (two columns), 16-bit rows one, all
+// relative to a power of two near the largest |x| of kChunk consecutive k of
+// the row, so that f16's range holds them.
+//
+// A warp takes 128 columns (64 bytes of each row of Q), in units of 32 rows that
+// it copies ahead itself (cp.async, kStages units); the 8 warps of a CTA are
+// side by side and share X's parts in shared memory.  The CTAs of a cluster
+// split K and join their sums through distributed shared memory, in rank order.
+
+constexpr int kWarps = 8, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
+constexpr int kUnit = 32;
+constexpr int kStageBytes = kUnit * kWarpCols / 2 + kWarpCols * 4;  // codes, then scales
+
+template <int NT>
+__host__ __device__ constexpr int chunk_k() { return NT == 1 ? 512 : 256; }
+template <int NT>
+__host__ __device__ constexpr int stages() { return NT == 1 ? 4 : 8; }
+template <int NT>
+constexpr int matvec_smem() {
+    return kWarps * stages<NT>() * kStageBytes + 2 * chunk_k<NT>() / 16 * NT * 256;
+}
+
+struct MatvecArgs {
+    const void *X;
+    int64_t ldx;
+    const uint8_t *Q;
+    int64_t ldq;
+    const float *scale;
+    int64_t lds;
+    void *Y;
+    int64_t ldy;
+    int32_t *dstatus;
+    int64_t group;
+    int M, N, K, relu;
+    int aligned;  // bit 0: Q's rows start on 16 bytes, bit 1: the scales' rows do
+};
+
+// cp.async of `bytes` of 16 (or 4) bytes, the rest zeros.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+// D = A B + C with A 16 x 16 and B 16 x 8 f16, C and D f32.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint2 b, float c0, float c1, float c2,
+                                        float c3) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(c0), "f"(c1), "f"(c2),
+          "f"(c3));
+}
+
+// The codes in the low (high) nibbles of bytes 0 and 2 as f16 q 2^-10.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
+    const uint32_t minus8 = 0xa000a000u;  // -8 2^-10
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&up),
+                              *reinterpret_cast<const __half2 *>(&minus8));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t low_codes(uint32_t v) {
+    return codes_f16((v & 0x000f000fu) ^ 0x00080008u, 0x74007400u);  // u 2^-24 times 2^14
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t v) {
+    return codes_f16((v & 0x00f000f0u) ^ 0x00800080u, 0x64006400u);  // u 2^-20 times 2^10
+}
+
+// 16 bytes at any address, of which the first `bytes` are wanted; whole words
+// where they lie inside [lo, hi), bytes at its ends.
+__device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, const uint8_t *lo,
+                                                  const uint8_t *hi) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint8_t *q = p - off;
+    uint32_t w[4];
+    if (q >= lo && q + 20 <= hi) {
+        uint32_t x[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) x[i] = __ldg(reinterpret_cast<const uint32_t *>(q) + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], 8 * off);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 0;
+            for (int j = 0; j < 4; ++j)
+                if (4 * i + j < bytes) w[i] |= (uint32_t)p[4 * i + j] << (8 * j);
         }
-        y0 = fmaf(a0, scale[g * lds + 2 * c], y0);
-        if (two) y1 = fmaf(a1, scale[g * lds + 2 * c + 1], y1);
     }
-    if (bad) set_status(dstatus, BSG_DSTATUS_NONFINITE);
-    T *y = Y + blockIdx.y * ldy + 2 * c;
-    y[0] = from_f32<T>(relu && !(y0 > 0.0f) ? 0.0f : y0);
-    if (two) y[1] = from_f32<T>(relu && !(y1 > 0.0f) ? 0.0f : y1);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// grid (cluster, column tiles)
+template <typename T, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
+    wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kChunk = chunk_k<NT>(), kStages = stages<NT>();
+    constexpr int kBuf = kChunk / 16 * NT * 32;  // uint2 of one buffer of X's parts
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint2 *x_s = reinterpret_cast<uint2 *>(smem + kWarps * kStages * kStageBytes);  // [2][step][NT][lane]
+    __shared__ int up_s[2][16];  // exponent that a row's chunk is raised by
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+    const int units = (a.K + kUnit - 1) / kUnit;
+    const int u0 = (int)((int64_t)units * rank / ranks), u1 = (int)((int64_t)units * (rank + 1) / ranks);
+    const int64_t col0 = (int64_t)blockIdx.y * kCtaCols + warp * kWarpCols;  // the warp's first column
+    const int half = (a.N + 1) / 2;
+    const int row_bytes = (int)min((int64_t)64, max((int64_t)0, half - col0 / 2));  // of its 64 in a row
+    const bool busy = row_bytes > 0;
+
+    // The ring: unit u's codes, 16-byte pieces of a row permuted so that the
+    // products' reads touch every bank once, and its group's scales.
+    uint8_t *ring = smem + warp * kStages * kStageBytes;
+    const uint32_t ring_u32 = smem_u32(ring);
+    const uint8_t *q_end = a.Q + (int64_t)(a.K - 1) * a.ldq + half;
+    const float *f_scale = a.scale + (int64_t)u0 * kUnit / a.group * a.lds + col0;
+    int64_t f_end = ((int64_t)u0 * kUnit / a.group + 1) * a.group;  // of the fetched unit's group
+    auto fetch = [&](int u, int stage) {
+        if (busy && u < u1) {
+            const int k0 = u * kUnit;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + lane / 4, c = lane % 4;
+                const int bytes = min(16, row_bytes - 16 * c);
+                const int at = stage * kStageBytes + r * 64 + ((c ^ (r & 2)) << 4);
+                if (k0 + r < a.K && bytes > 0) {
+                    const uint8_t *p = a.Q + (int64_t)(k0 + r) * a.ldq + col0 / 2 + 16 * c;
+                    if (a.aligned & 1)
+                        copy_async16(ring_u32 + at, p, bytes);
+                    else
+                        *reinterpret_cast<uint4 *>(ring + at) = load_unaligned16(p, bytes, a.Q, q_end);
+                }
+            }
+            if (k0 >= f_end) {
+                f_end += a.group;
+                f_scale += a.lds;
+            }
+            const uint32_t at = ring_u32 + stage * kStageBytes + kUnit * 64;
+            const int left = (int)min((int64_t)kWarpCols, a.N - col0);
+            if (a.aligned & 2) {
+                const int bytes = max(0, min(16, 4 * (left - 4 * lane)));
+                copy_async16(at + lane * 16, bytes ? f_scale + 4 * lane : f_scale, bytes);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = i * 32 + lane < left;
+                    copy_async4(at + (i * 32 + lane) * 4, in ? f_scale + i * 32 + lane : f_scale, in ? 4 : 0);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(u0 + i, i);
+
+    // X's parts of one chunk, a row to a warp, as the B operand: the lane that
+    // holds k mod 4, four k of a 16-row step 4 apart.
+    const int chunk_units = kChunk / kUnit;
+    auto stage_x = [&](int first_unit, int buf) {
+        const int k0 = first_unit * kUnit, k1 = min(min(u1 * kUnit, a.K), k0 + kChunk);
+        for (int r = warp; r < 8 * NT / kParts; r += kWarps) {
+            float x[kChunk / 32], m = 0.0f;
+            bool bad = false;
+            const T *row = static_cast<const T *>(a.X) + (int64_t)min(r, a.M - 1) * a.ldx;
+#pragma unroll
+            for (int j = 0; j < kChunk / 32; ++j) {
+                const int k = k0 + 32 * j + lane;
+                x[j] = r < a.M && k < k1 ? to_f32(row[k]) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kChunk / 32; ++j) {
+                bad |= !isfinite(x[j]);
+                m = fmaxf(m, fabsf(x[j]));
+            }
+            if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            // 2^e with the largest |x| 2^e in [2^13, 2^14)
+            const int e = max(-126, min(126, 13 + 127 - (int)(top >> 23)));
+            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+            if (lane == 0) up_s[buf][r] = e;
+            __half *xh = reinterpret_cast<__half *>(x_s + buf * kBuf);
+            const int slot = r * kParts;
+#pragma unroll
+            for (int j = 0; j < kChunk / 32; ++j) {
+                const float y = x[j] * up;
+                const __half hi = __float2half_rn(y);
+                const int step = 2 * j + lane / 16, kk = lane % 16;
+                const int at = ((step * NT + slot / 8) * 32 + slot % 8 * 4 + kk % 4) * 4 + kk / 4;
+                xh[at] = hi;
+                if (kParts == 2) xh[at + 16] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
+            }
+        }
+    };
+
+    // The lane's 16 columns 16g .. 16g + 15, its slots 2t and 2t + 1 of each 8.
+    float acc[8][NT][4];
+    int up[NT][2];
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+
+    int stage = 0, buf = 0;
+    if (u0 < u1) stage_x(u0, 0);
+    for (int c0 = u0; c0 < u1; c0 += chunk_units, buf ^= 1) {
+        __syncthreads();  // this chunk's parts are there, and the other buffer is free
+        if (c0 + chunk_units < u1) stage_x(c0 + chunk_units, buf ^ 1);
+        // sums so far to this chunk's power of two
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = up_s[buf][(8 * n + 2 * t + i) / kParts];
+                // at most 2^60 up: what a chunk below that adds is nothing beside the sums
+                const int to = c0 == u0 ? e : min(e, up[n][i] + 60);
+                if (c0 != u0 && to != up[n][i]) {
+                    const float f = exp2f((float)(to - up[n][i]));
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
+                }
+                up[n][i] = to;
+            }
+        if (!busy) continue;
+        const int c1 = min(u1, c0 + chunk_units);
+        for (int u = c0; u < c1; ++u) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+            const uint8_t *codes = ring + stage * kStageBytes;
+            const float4 *scales = reinterpret_cast<const float4 *>(codes + kUnit * 64) + 4 * g;
+            const uint2 *xb = x_s + buf * kBuf + (u - c0) * 2 * NT * 32 + lane;
+            uint2 x[2][NT];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) x[s][n] = xb[(s * NT + n) * 32];
+            // codes of rows t, t + 4, t + 8, t + 12 of both steps
+            uint2 w[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * s + t + 4 * i;
+                    w[s][i] = *reinterpret_cast<const uint2 *>(
+                        codes + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
+                }
+#pragma unroll
+            for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
+                float d[2][NT][4];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t sel = quad % 2 ? 0x7632 : 0x5410;
+                    const uint32_t p0 = quad < 2 ? __byte_perm(w[s][0].x, w[s][1].x, sel)
+                                                 : __byte_perm(w[s][0].y, w[s][1].y, sel);
+                    const uint32_t p1 = quad < 2 ? __byte_perm(w[s][2].x, w[s][3].x, sel)
+                                                 : __byte_perm(w[s][2].y, w[s][3].y, sel);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t v0 = p0 >> (8 * h), v1 = p1 >> (8 * h);
+                        const uint32_t a0 = low_codes(v0), a1 = high_codes(v0);
+                        const uint32_t a2 = low_codes(v1), a3 = high_codes(v1);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if (s == 0)
+                                mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], 0.0f, 0.0f, 0.0f, 0.0f);
+                            else
+                                mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], d[h][n][0], d[h][n][1],
+                                        d[h][n][2], d[h][n][3]);
+                        }
+                    }
+                }
+                const float4 sc = scales[quad];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[2 * quad][n][i] = fmaf(d[0][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
+                        acc[2 * quad + 1][n][i] = fmaf(d[1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
+                    }
+            }
+            __syncwarp();  // every lane has read the stage
+            fetch(u + kStages, stage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rings are free
+
+    // This CTA's sums, [row][column], at their true size; then each CTA of the
+    // cluster adds up its share of the columns over all ranks.
+    float *y_s = reinterpret_cast<float *>(smem);
+    if (u0 < u1) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; i += kParts) {
+                const int r = (8 * n + 2 * t + i) / kParts;
+                if (r >= a.M) continue;
+                const float down = __uint_as_float((uint32_t)(max(1, min(254, 137 - up[n][i]))) << 23);  // 2^10 / 2^e
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    float2 v = make_float2(acc[m][n][i], acc[m][n][i + 2]);
+                    if (kParts == 2)
+                        v = make_float2(fmaf(acc[m][n][1], 0x1p-11f, acc[m][n][0]),
+                                        fmaf(acc[m][n][3], 0x1p-11f, acc[m][n][2]));
+                    *reinterpret_cast<float2 *>(y_s + r * kCtaCols + warp * kWarpCols + 16 * g + 2 * m) =
+                        make_float2(v.x * down, v.y * down);
+                }
+            }
+    } else {
+        for (int e = tid; e < a.M * kCtaCols; e += kWarps * 32) y_s[e] = 0.0f;
+    }
+    cluster.sync();
+    const int c0 = kCtaCols * rank / ranks, c1 = kCtaCols * (rank + 1) / ranks;
+    for (int r = 0; r < a.M; ++r)
+        for (int c = c0 + tid; c < c1; c += kWarps * 32) {
+            const int64_t n = (int64_t)blockIdx.y * kCtaCols + c;
+            if (n >= a.N) break;
+            float y = 0.0f;
+            for (int k = 0; k < ranks; ++k) y += cluster.map_shared_rank(y_s, k)[r * kCtaCols + c];
+            if (a.relu && !(y > 0.0f)) y = 0.0f;
+            static_cast<T *>(a.Y)[r * a.ldy + n] = from_f32<T>(y);
+        }
+    cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+template <typename T, int NT>
+cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
+    constexpr int smem = matvec_smem<NT>();
+    static bool set[64] = {false};  // this kernel's attributes, on each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(wgroups_matvec_kernel<T, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(wgroups_matvec_kernel<T, NT>,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
+    }
+    // K is split until the CTAs fill the card, but not below two units
+    const int tiles = (a.N + kCtaCols - 1) / kCtaCols, units = (a.K + kUnit - 1) / kUnit;
+    int ranks = 1;
+    while (ranks < 16 && tiles * ranks < 2 * device_sm_count() && units >= 4 * ranks) ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, wgroups_matvec_kernel<T, NT>, a);
 }
 
 }  // namespace
@@ -97,13 +454,16 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
                                   int64_t ldq, const float *scale, int64_t lds, int64_t group,
                                   int64_t M, int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
                                   int32_t *dstatus, cudaStream_t st) {
+    MatvecArgs a{X, ldx, Q, ldq, scale, lds, Y, ldy, dstatus, group, (int)M, (int)N, (int)K, relu, 0};
+    if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0) a.aligned |= 1;
+    if (reinterpret_cast<uintptr_t>(scale) % 16 == 0 && lds % 4 == 0) a.aligned |= 2;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        const dim3 grid((unsigned)(((N + 1) / 2 + 127) / 128), (unsigned)M);
-        wgroups_matvec_kernel<T><<<grid, 128, 0, st>>>((const T *)X, ldx, Q, ldq, scale, lds,
-                                                       group, N, K, relu, (T *)Y, ldy, dstatus);
-        count_launches(1);
-        return cudaGetLastError();
+        const int slots = (int)M * (sizeof(T) == 4 ? 2 : 1);
+        if (slots <= 8) return launch_matvec<T, 1>(a, st);
+        if (slots <= 16) return launch_matvec<T, 2>(a, st);
+        if constexpr (sizeof(T) == 4) return launch_matvec<T, 4>(a, st);
+        return cudaErrorInvalidValue;
     });
 }
 
