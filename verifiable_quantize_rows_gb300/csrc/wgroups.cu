@@ -61,10 +61,10 @@ __global__ void __launch_bounds__(128)
 // (m16n8k16, the weights as the 16-row operand, X's rows as the 8 columns), and
 // a weight is unpacked with one and a quarter:
 //
-//   Two rows' 16-bit pieces of 4 codes side by side (a byte permute), masked to
-//   one nibble each, are two f16 subnormals, u 2^-24 (low nibble of a byte) or
-//   u 2^-20 (high), with u = q + 8 after the nibble's top bit is flipped in the
-//   same three-input logic operation; one f16 multiply-add makes them q 2^-10.
+//   Every nibble's top bit flipped (8 codes at once) is u = q + 8.  Two rows'
+//   16-bit pieces of 4 codes side by side (a byte permute), masked to one nibble
+//   each, are two f16 subnormals, u 2^-24 (low nibble of a byte) or u 2^-20
+//   (high); one f16 multiply-add makes them q 2^-10.
 //   (Left subnormal, with 8 sum_k x taken off the sums, they cost a third less
 //   and lost ten bits: the tensor cores align products by the exponent field.)
 //
@@ -73,21 +73,23 @@ __global__ void __launch_bounds__(128)
 // the row, so that f16's range holds them.
 //
 // A warp takes 128 columns (64 bytes of each row of Q), in units of 32 rows that
-// it copies ahead itself (cp.async, kStages units); the 8 warps of a CTA are
+// it copies ahead itself (cp.async, kStages units); the warps of a CTA are
 // side by side and share X's parts in shared memory.  The CTAs of a cluster
 // split K and join their sums through distributed shared memory, in rank order.
 
-constexpr int kWarps = 8, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
+constexpr int kWarps = 4, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 32;
 constexpr int kStageBytes = kUnit * kWarpCols / 2 + kWarpCols * 4;  // codes, then scales
 
+constexpr int kChunk = 256;  // k that X's parts are staged for at a time
+
 template <int NT>
-__host__ __device__ constexpr int chunk_k() { return NT == 1 ? 512 : 256; }
+__host__ __device__ constexpr int stages() { return NT == 4 ? 6 : 4; }
 template <int NT>
-__host__ __device__ constexpr int stages() { return NT == 1 ? 4 : 8; }
+__host__ __device__ constexpr int matvec_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 template <int NT>
 constexpr int matvec_smem() {
-    return kWarps * stages<NT>() * kStageBytes + 2 * chunk_k<NT>() / 16 * NT * 256;
+    return kWarps * stages<NT>() * kStageBytes + 2 * kChunk / 16 * NT * 256;
 }
 
 struct MatvecArgs {
@@ -127,7 +129,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
           "f"(c3));
 }
 
-// The codes in the low (high) nibbles of bytes 0 and 2 as f16 q 2^-10.
+// The codes in the low (high) nibbles of bytes 0 and 2, as u = q + 8, as f16 q 2^-10.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
     const uint32_t minus8 = 0xa000a000u;  // -8 2^-10
     const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&up),
@@ -135,10 +137,10 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t low_codes(uint32_t v) {
-    return codes_f16((v & 0x000f000fu) ^ 0x00080008u, 0x74007400u);  // u 2^-24 times 2^14
+    return codes_f16(v & 0x000f000fu, 0x74007400u);  // u 2^-24 times 2^14
 }
 __device__ __forceinline__ uint32_t high_codes(uint32_t v) {
-    return codes_f16((v & 0x00f000f0u) ^ 0x00800080u, 0x64006400u);  // u 2^-20 times 2^10
+    return codes_f16(v & 0x00f000f0u, 0x64006400u);  // u 2^-20 times 2^10
 }
 
 // 16 bytes at any address, of which the first `bytes` are wanted; whole words
@@ -167,9 +169,9 @@ __device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, c
 
 // grid (cluster, column tiles)
 template <typename T, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kChunk = chunk_k<NT>(), kStages = stages<NT>();
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kStages = stages<NT>();
     constexpr int kBuf = kChunk / 16 * NT * 32;  // uint2 of one buffer of X's parts
     extern __shared__ __align__(16) uint8_t smem[];
     uint2 *x_s = reinterpret_cast<uint2 *>(smem + kWarps * kStages * kStageBytes);  // [2][step][NT][lane]
@@ -184,50 +186,64 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
     const int row_bytes = (int)min((int64_t)64, max((int64_t)0, half - col0 / 2));  // of its 64 in a row
     const bool busy = row_bytes > 0;
 
-    // The ring: unit u's codes, 16-byte pieces of a row permuted so that the
-    // products' reads touch every bank once, and its group's scales.
+    // The ring: a unit's codes, 16-byte pieces of a row permuted so that the
+    // products' reads touch every bank once, and its group's scales.  The lane
+    // copies piece lane % 4 of rows lane / 4, + 8, + 16, + 24, and the scales
+    // of 4 columns (or, unaligned, of columns lane, + 32, + 64, + 96).
     uint8_t *ring = smem + warp * kStages * kStageBytes;
     const uint32_t ring_u32 = smem_u32(ring);
-    const uint8_t *q_end = a.Q + (int64_t)(a.K - 1) * a.ldq + half;
-    const float *f_scale = a.scale + (int64_t)u0 * kUnit / a.group * a.lds + col0;
-    int64_t f_end = ((int64_t)u0 * kUnit / a.group + 1) * a.group;  // of the fetched unit's group
-    auto fetch = [&](int u, int stage) {
-        if (busy && u < u1) {
-            const int k0 = u * kUnit;
+    const int my_bytes = max(0, min(16, row_bytes - 16 * (lane % 4)));
+    const int my_at = lane / 4 * 64 + (((lane % 4) ^ (lane / 4 & 2)) << 4);
+    const uint8_t *f_q = a.Q + ((int64_t)u0 * kUnit + lane / 4) * a.ldq + col0 / 2 + 16 * (lane % 4);
+    const int64_t ldq8 = 8 * a.ldq;
+    const int my_cols = (int)min((int64_t)kWarpCols, a.N - col0);
+    const int my_scale_bytes = max(0, min(16, 4 * (my_cols - 4 * lane)));
+    const float *f_scale = a.scale + (int64_t)u0 * kUnit / a.group * a.lds + col0 +
+                           (a.aligned & 2 ? (my_scale_bytes ? 4 * lane : 0) : 0);
+    int f_left = (int)min((int64_t)INT32_MAX, ((int64_t)u0 * kUnit / a.group + 1) * a.group - (int64_t)u0 * kUnit);
+    int f_unit = u0;
+    auto fetch = [&](int stage) {
+        if (busy && f_unit < u1) {
+            const uint32_t at = ring_u32 + stage * kStageBytes;
+            if (a.aligned & 1) {
+                const uint8_t *p = f_q;
+                if ((f_unit + 1) * kUnit <= a.K) {
+                    if (my_bytes)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i * 8 + lane / 4, c = lane % 4;
-                const int bytes = min(16, row_bytes - 16 * c);
-                const int at = stage * kStageBytes + r * 64 + ((c ^ (r & 2)) << 4);
-                if (k0 + r < a.K && bytes > 0) {
-                    const uint8_t *p = a.Q + (int64_t)(k0 + r) * a.ldq + col0 / 2 + 16 * c;
-                    if (a.aligned & 1)
-                        copy_async16(ring_u32 + at, p, bytes);
-                    else
-                        *reinterpret_cast<uint4 *>(ring + at) = load_unaligned16(p, bytes, a.Q, q_end);
+                        for (int i = 0; i < 4; ++i, p += ldq8) copy_async16(at + my_at + i * 512, p, my_bytes);
+                } else {
+                    for (int i = 0; i < 4; ++i, p += ldq8)
+                        if (my_bytes && f_unit * kUnit + i * 8 + lane / 4 < a.K)
+                            copy_async16(at + my_at + i * 512, p, my_bytes);
                 }
+            } else {
+                const uint8_t *q_end = a.Q + (int64_t)(a.K - 1) * a.ldq + half;
+                for (int i = 0; i < 4; ++i)
+                    if (my_bytes && f_unit * kUnit + i * 8 + lane / 4 < a.K)
+                        *reinterpret_cast<uint4 *>(ring + stage * kStageBytes + my_at + i * 512) =
+                            load_unaligned16(f_q + i * ldq8, my_bytes, a.Q, q_end);
             }
-            if (k0 >= f_end) {
-                f_end += a.group;
+            f_q += 4 * ldq8;
+            if (f_left <= 0) {
+                f_left = (int)min((int64_t)INT32_MAX, a.group);
                 f_scale += a.lds;
             }
-            const uint32_t at = ring_u32 + stage * kStageBytes + kUnit * 64;
-            const int left = (int)min((int64_t)kWarpCols, a.N - col0);
+            f_left -= kUnit;
             if (a.aligned & 2) {
-                const int bytes = max(0, min(16, 4 * (left - 4 * lane)));
-                copy_async16(at + lane * 16, bytes ? f_scale + 4 * lane : f_scale, bytes);
+                copy_async16(at + kUnit * 64 + lane * 16, f_scale, my_scale_bytes);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool in = i * 32 + lane < left;
-                    copy_async4(at + (i * 32 + lane) * 4, in ? f_scale + i * 32 + lane : f_scale, in ? 4 : 0);
+                    const bool in = i * 32 + lane < my_cols;
+                    copy_async4(at + kUnit * 64 + (i * 32 + lane) * 4, in ? f_scale + i * 32 + lane : f_scale, in ? 4 : 0);
                 }
             }
         }
+        ++f_unit;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(u0 + i, i);
+    for (int i = 0; i < kStages; ++i) fetch(i);
 
     // X's parts of one chunk, a row to a warp, as the B operand: the lane that
     // holds k mod 4, four k of a 16-row step 4 apart.
@@ -235,33 +251,29 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
     auto stage_x = [&](int first_unit, int buf) {
         const int k0 = first_unit * kUnit, k1 = min(min(u1 * kUnit, a.K), k0 + kChunk);
         for (int r = warp; r < 8 * NT / kParts; r += kWarps) {
-            float x[kChunk / 32], m = 0.0f;
-            bool bad = false;
-            const T *row = static_cast<const T *>(a.X) + (int64_t)min(r, a.M - 1) * a.ldx;
+            float x[kChunk / 32];
+            uint32_t top = 0;
+            const T *row = static_cast<const T *>(a.X) + (int64_t)min(r, a.M - 1) * a.ldx + k0 + lane;
+            const int left = r < a.M ? k1 - k0 - lane : 0;
 #pragma unroll
-            for (int j = 0; j < kChunk / 32; ++j) {
-                const int k = k0 + 32 * j + lane;
-                x[j] = r < a.M && k < k1 ? to_f32(row[k]) : 0.0f;
-            }
+            for (int j = 0; j < kChunk / 32; ++j) x[j] = 32 * j < left ? to_f32(row[32 * j]) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < kChunk / 32; ++j) {
-                bad |= !isfinite(x[j]);
-                m = fmaxf(m, fabsf(x[j]));
-            }
-            if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            for (int j = 0; j < kChunk / 32; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (top >= 0x7f800000u && lane == 0) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
             // 2^e with the largest |x| 2^e in [2^13, 2^14)
             const int e = max(-126, min(126, 13 + 127 - (int)(top >> 23)));
             const float up = __uint_as_float((uint32_t)(e + 127) << 23);
             if (lane == 0) up_s[buf][r] = e;
             __half *xh = reinterpret_cast<__half *>(x_s + buf * kBuf);
-            const int slot = r * kParts;
+            const int slot = r * kParts, kk = lane % 16;  // of step 2j + lane / 16
+            const int my_half =
+                ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + kk % 4) * 4 + kk / 4;
 #pragma unroll
             for (int j = 0; j < kChunk / 32; ++j) {
                 const float y = x[j] * up;
                 const __half hi = __float2half_rn(y);
-                const int step = 2 * j + lane / 16, kk = lane % 16;
-                const int at = ((step * NT + slot / 8) * 32 + slot % 8 * 4 + kk % 4) * 4 + kk / 4;
+                const int at = my_half + j * 2 * NT * 128;
                 xh[at] = hi;
                 if (kParts == 2) xh[at + 16] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
             }
@@ -278,6 +290,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
+    // where the lane finds its codes of row t in a unit, and its scales
+    const int codes_at = t * 64 + (((g >> 1) ^ (t & 2)) << 4) + (g & 1) * 8;
     int stage = 0, buf = 0;
     if (u0 < u1) stage_x(u0, 0);
     for (int c0 = u0; c0 < u1; c0 += chunk_units, buf ^= 1) {
@@ -317,9 +331,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * s + t + 4 * i;
-                    w[s][i] = *reinterpret_cast<const uint2 *>(
-                        codes + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
+                    w[s][i] = *reinterpret_cast<const uint2 *>(codes + codes_at + (16 * s + 4 * i) * 64);
+                    w[s][i].x ^= 0x88888888u, w[s][i].y ^= 0x88888888u;
                 }
 #pragma unroll
             for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
@@ -356,7 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1)
                     }
             }
             __syncwarp();  // every lane has read the stage
-            fetch(u + kStages, stage);
+            fetch(stage);
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
     }
@@ -417,10 +430,16 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
-    // K is split until the CTAs fill the card, but not below two units
+    // The split of K that ends first: waves of CTAs times units of each, a CTA's
+    // start and join counting as four units.
     const int tiles = (a.N + kCtaCols - 1) / kCtaCols, units = (a.K + kUnit - 1) / kUnit;
+    const int64_t places = (int64_t)device_sm_count() * matvec_per_sm<NT>();
     int ranks = 1;
-    while (ranks < 16 && tiles * ranks < 2 * device_sm_count() && units >= 4 * ranks) ranks *= 2;
+    int64_t best = INT64_MAX;
+    for (int r = 1; r <= 16 && r <= units; ++r) {
+        const int64_t cost = ((int64_t)tiles * r + places - 1) / places * ((units + r - 1) / r + 4);
+        if (cost < best) best = cost, ranks = r;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
     cfg.blockDim = dim3(kWarps * 32);
