@@ -1,6 +1,7 @@
 // bsg_internal.h -- launchers shared by the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -98,6 +99,12 @@ cudaError_t launch_wquant_cols(const float *W, int64_t K, int64_t N, int64_t ldw
                                int32_t *dstatus, cudaStream_t st);
 cudaError_t launch_wdequant_cols(const void *Q, int64_t K, int64_t N, int64_t ldq, int bits,
                                  const float *scale, float *out, int64_t ldo, cudaStream_t st);
+
+// A 2-D tensor map of row-major elements (base 16-byte aligned, rows a
+// multiple of 16 bytes apart), zeros past its ends; false if it cannot be.
+bool make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, size_t esz, const void *base,
+                  uint64_t inner, uint64_t outer, uint64_t row_stride_elems, uint32_t box_inner,
+                  uint32_t box_outer, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // The serving calls (arguments as the C ABI's, checked there).
 cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, int64_t group,

@@ -72,27 +72,27 @@ __global__ void __launch_bounds__(128)
 // relative to a power of two near the largest |x| of kChunk consecutive k of
 // the row, so that f16's range holds them.
 //
-// A warp takes 128 columns (64 bytes of each row of Q), in units of 32 rows that
-// it copies ahead itself (cp.async, kStages units); the warps of a CTA are
-// side by side and share X's parts in shared memory.  The CTAs of a cluster
-// split K and join their sums through distributed shared memory, in rank order.
+// A warp takes 128 columns (64 bytes of each row of Q) in units of 64 rows, each
+// one TMA copy (and one of its scales) that the warp itself issues kStages units
+// ahead; groups' sums are scaled once a unit, or once each 32 rows where a group
+// may end there (kFolds).  The warps of a CTA are side by side and share X's parts
+// in shared memory.  The CTAs of a cluster split K and join their sums through
+// distributed shared memory, in rank order.
 
 constexpr int kWarps = 4, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
-constexpr int kUnit = 32;
-constexpr int kStageBytes = kUnit * kWarpCols / 2 + kWarpCols * 4;  // codes, then scales
+constexpr int kUnit = 64, kStages = 3;
+constexpr int kChunk = 256;                    // k that X's parts are staged for at a time
+constexpr int kCodes = kUnit * kWarpCols / 2;  // bytes of a unit's codes
 
-constexpr int kChunk = 256;  // k that X's parts are staged for at a time
-
 template <int NT>
-__host__ __device__ constexpr int stages() { return NT == 4 ? 6 : 4; }
-template <int NT>
-__host__ __device__ constexpr int matvec_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
-template <int NT>
+__host__ __device__ constexpr int matvec_per_sm() { return NT == 4 ? 2 : 3; }
+template <int NT, int kFolds>
 constexpr int matvec_smem() {
-    return kWarps * stages<NT>() * kStageBytes + 2 * kChunk / 16 * NT * 256;
+    return kWarps * kStages * (kCodes + kFolds * kWarpCols * 4) + 2 * kChunk / 16 * NT * 256 + 512;
 }
 
 struct MatvecArgs {
+    CUtensorMap q_map, s_map;  // where tma_q, tma_s
     const void *X;
     int64_t ldx;
     const uint8_t *Q;
@@ -102,16 +102,10 @@ struct MatvecArgs {
     void *Y;
     int64_t ldy;
     int32_t *dstatus;
-    int64_t group;
-    int M, N, K, relu;
-    int aligned;  // bit 0: Q's rows start on 16 bytes, bit 1: the scales' rows do
+    int group, M, N, K, relu;
+    int tma_q, tma_s;  // Q's (the scales') rows start on 16 bytes
 };
 
-// cp.async of `bytes` of 16 (or 4) bytes, the rest zeros.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
@@ -121,8 +115,7 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void *src, int b
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint2 b, float c0, float c1, float c2,
                                         float c3) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
         " {%8, %9}, {%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(c0), "f"(c1), "f"(c2),
@@ -168,85 +161,84 @@ __device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, c
 }
 
 // grid (cluster, column tiles)
-template <typename T, int NT>
+template <typename T, int NT, int kFolds>
 __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kStages = stages<NT>();
-    constexpr int kBuf = kChunk / 16 * NT * 32;  // uint2 of one buffer of X's parts
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint2 *x_s = reinterpret_cast<uint2 *>(smem + kWarps * kStages * kStageBytes);  // [2][step][NT][lane]
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    constexpr int kBuf = kChunk / 16 * NT * 32;         // uint2 of one buffer of X's parts
+    constexpr int kScales = kFolds * kWarpCols;         // floats of a unit's scales
+    constexpr int kSteps = kUnit / 16, kFoldSteps = kSteps / kFolds;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 511);  // the swizzle's period
+    float *scale_s = reinterpret_cast<float *>(smem + kWarps * kStages * kCodes);  // [warp][stage][fold][128]
+    uint2 *x_s = reinterpret_cast<uint2 *>(scale_s + kWarps * kStages * kScales);  // [2][step][NT][lane]
+    __shared__ uint64_t full_s[kWarps][kStages];
     __shared__ int up_s[2][16];  // exponent that a row's chunk is raised by
+    __shared__ volatile int gave_up, never;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int units = (a.K + kUnit - 1) / kUnit;
     const int u0 = (int)((int64_t)units * rank / ranks), u1 = (int)((int64_t)units * (rank + 1) / ranks);
-    const int64_t col0 = (int64_t)blockIdx.y * kCtaCols + warp * kWarpCols;  // the warp's first column
-    const int half = (a.N + 1) / 2;
-    const int row_bytes = (int)min((int64_t)64, max((int64_t)0, half - col0 / 2));  // of its 64 in a row
-    const bool busy = row_bytes > 0;
+    const int col0 = blockIdx.y * kCtaCols + warp * kWarpCols;  // the warp's first column
+    const bool busy = col0 < a.N;
 
-    // The ring: a unit's codes, 16-byte pieces of a row permuted so that the
-    // products' reads touch every bank once, and its group's scales.  The lane
-    // copies piece lane % 4 of rows lane / 4, + 8, + 16, + 24, and the scales
-    // of 4 columns (or, unaligned, of columns lane, + 32, + 64, + 96).
-    uint8_t *ring = smem + warp * kStages * kStageBytes;
-    const uint32_t ring_u32 = smem_u32(ring);
-    const int my_bytes = max(0, min(16, row_bytes - 16 * (lane % 4)));
-    const int my_at = lane / 4 * 64 + (((lane % 4) ^ (lane / 4 & 2)) << 4);
-    const uint8_t *f_q = a.Q + ((int64_t)u0 * kUnit + lane / 4) * a.ldq + col0 / 2 + 16 * (lane % 4);
-    const int64_t ldq8 = 8 * a.ldq;
-    const int my_cols = (int)min((int64_t)kWarpCols, a.N - col0);
-    const int my_scale_bytes = max(0, min(16, 4 * (my_cols - 4 * lane)));
-    const float *f_scale = a.scale + (int64_t)u0 * kUnit / a.group * a.lds + col0 +
-                           (a.aligned & 2 ? (my_scale_bytes ? 4 * lane : 0) : 0);
-    int f_left = (int)min((int64_t)INT32_MAX, ((int64_t)u0 * kUnit / a.group + 1) * a.group - (int64_t)u0 * kUnit);
+    // The ring.  A unit's rows are 64 bytes each, their 16-byte pieces permuted
+    // by the 64-byte swizzle.
+    uint8_t *codes_s = smem + warp * kStages * kCodes;
+    float *scales_s = scale_s + warp * kStages * kScales;
+    uint64_t *full = full_s[warp];
+    if (lane < kStages) mbar_init(&full[lane], 1);
+    if (tid == 0) gave_up = never = 0;
+    fence_mbar_init();
+    __syncthreads();
+    const int copied = (a.tma_q ? kCodes : 0) + (a.tma_s ? kScales * 4 : 0);
+    const int my_cols = min(kWarpCols, a.N - col0);
     int f_unit = u0;
     auto fetch = [&](int stage) {
         if (busy && f_unit < u1) {
-            const uint32_t at = ring_u32 + stage * kStageBytes;
-            if (a.aligned & 1) {
-                const uint8_t *p = f_q;
-                if ((f_unit + 1) * kUnit <= a.K) {
-                    if (my_bytes)
+            const int k0 = f_unit * kUnit;
+            if (copied && lane == 0) {
+                mbar_arrive_expect_tx(&full[stage], copied);
+                if (a.tma_q) tma_load_2d(&a.q_map, &full[stage], codes_s + stage * kCodes, col0 / 2, k0);
+                if (a.tma_s)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i, p += ldq8) copy_async16(at + my_at + i * 512, p, my_bytes);
-                } else {
-                    for (int i = 0; i < 4; ++i, p += ldq8)
-                        if (my_bytes && f_unit * kUnit + i * 8 + lane / 4 < a.K)
-                            copy_async16(at + my_at + i * 512, p, my_bytes);
-                }
-            } else {
+                    for (int f = 0; f < kFolds; ++f)
+                        tma_load_2d(&a.s_map, &full[stage], scales_s + stage * kScales + f * kWarpCols,
+                                    col0, (k0 + 32 * f) / a.group);
+            }
+            if (!a.tma_q) {
+                const int half = (a.N + 1) / 2, c = lane % 4;
+                const int bytes = min(16, half - col0 / 2 - 16 * c);
                 const uint8_t *q_end = a.Q + (int64_t)(a.K - 1) * a.ldq + half;
-                for (int i = 0; i < 4; ++i)
-                    if (my_bytes && f_unit * kUnit + i * 8 + lane / 4 < a.K)
-                        *reinterpret_cast<uint4 *>(ring + stage * kStageBytes + my_at + i * 512) =
-                            load_unaligned16(f_q + i * ldq8, my_bytes, a.Q, q_end);
+                const uint8_t *p = a.Q + (int64_t)(k0 + lane / 4) * a.ldq + col0 / 2 + 16 * c;
+#pragma unroll 4
+                for (int r = lane / 4; r < kUnit; r += 8, p += 8 * a.ldq)
+                    if (bytes > 0 && k0 + r < a.K)
+                        *reinterpret_cast<uint4 *>(codes_s + stage * kCodes + r * 64 + ((c ^ (r >> 1 & 3)) << 4)) =
+                            load_unaligned16(p, bytes, a.Q, q_end);
             }
-            f_q += 4 * ldq8;
-            if (f_left <= 0) {
-                f_left = (int)min((int64_t)INT32_MAX, a.group);
-                f_scale += a.lds;
-            }
-            f_left -= kUnit;
-            if (a.aligned & 2) {
-                copy_async16(at + kUnit * 64 + lane * 16, f_scale, my_scale_bytes);
-            } else {
+            if (!a.tma_s) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = i * 32 + lane < my_cols;
-                    copy_async4(at + kUnit * 64 + (i * 32 + lane) * 4, in ? f_scale + i * 32 + lane : f_scale, in ? 4 : 0);
+                for (int f = 0; f < kFolds; ++f) {
+                    const float *s = a.scale + (int64_t)(min(k0 + 32 * f, a.K - 1) / a.group) * a.lds + col0;
+                    const uint32_t at = smem_u32(scales_s + stage * kScales + f * kWarpCols);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = i * 32 + lane < my_cols;
+                        copy_async4(at + (i * 32 + lane) * 4, in ? s + i * 32 + lane : s, in ? 4 : 0);
+                    }
                 }
             }
         }
         ++f_unit;
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (!a.tma_s) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(i);
 
     // X's parts of one chunk, a row to a warp, as the B operand: the lane that
-    // holds k mod 4, four k of a 16-row step 4 apart.
+    // holds rows {0, 1, 4, 5}[t] + {0, 2, 8, 10} of each 16 (see codes_at below).
     const int chunk_units = kChunk / kUnit;
     auto stage_x = [&](int first_unit, int buf) {
         const int k0 = first_unit * kUnit, k1 = min(min(u1 * kUnit, a.K), k0 + kChunk);
@@ -267,8 +259,8 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
             if (lane == 0) up_s[buf][r] = e;
             __half *xh = reinterpret_cast<__half *>(x_s + buf * kBuf);
             const int slot = r * kParts, kk = lane % 16;  // of step 2j + lane / 16
-            const int my_half =
-                ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + kk % 4) * 4 + kk / 4;
+            const int tt = (kk & 1) | (kk >> 1 & 2), i = (kk >> 1 & 1) | (kk >> 2 & 2);
+            const int my_half = ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + tt) * 4 + i;
 #pragma unroll
             for (int j = 0; j < kChunk / 32; ++j) {
                 const float y = x[j] * up;
@@ -290,8 +282,11 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
-    // where the lane finds its codes of row t in a unit, and its scales
-    const int codes_at = t * 64 + (((g >> 1) ^ (t & 2)) << 4) + (g & 1) * 8;
+    // Where the lane finds its 16 columns' codes of rows {0, 1, 4, 5}[t] and, other
+    // swizzle, of 2 rows on: every four lanes' rows are on banks of their own.
+    const int row_t = (t & 1) | (t & 2) << 1;
+    const int codes_at = row_t * 64 + (((g >> 1) ^ (t & 2)) << 4) + (g & 1) * 8;
+    uint32_t parity = 0;
     int stage = 0, buf = 0;
     if (u0 < u1) stage_x(u0, 0);
     for (int c0 = u0; c0 < u1; c0 += chunk_units, buf ^= 1) {
@@ -315,65 +310,76 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
         if (!busy) continue;
         const int c1 = min(u1, c0 + chunk_units);
         for (int u = c0; u < c1; ++u) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            if (copied && !mbar_wait(&full[stage], parity, &gave_up)) {
+                gave_up = 1;
+                set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
+                break;
+            }
+            if (!a.tma_s) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
-            const uint8_t *codes = ring + stage * kStageBytes;
-            const float4 *scales = reinterpret_cast<const float4 *>(codes + kUnit * 64) + 4 * g;
-            const uint2 *xb = x_s + buf * kBuf + (u - c0) * 2 * NT * 32 + lane;
-            uint2 x[2][NT];
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int f = 0; f < kFolds; ++f) {
+                const float4 *scales = reinterpret_cast<const float4 *>(scales_s + stage * kScales + f * kWarpCols) + 4 * g;
+                const uint8_t *codes = codes_s + stage * kCodes + f * kFoldSteps * 1024;
+                const uint2 *xb = x_s + buf * kBuf + ((u - c0) * kSteps + f * kFoldSteps) * NT * 32 + lane;
+                uint2 x[kFoldSteps][NT], w[kFoldSteps][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) x[s][n] = xb[(s * NT + n) * 32];
-            // codes of rows t, t + 4, t + 8, t + 12 of both steps
-            uint2 w[2][4];
+                for (int s = 0; s < kFoldSteps; ++s) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[s][i] = *reinterpret_cast<const uint2 *>(codes + codes_at + (16 * s + 4 * i) * 64);
-                    w[s][i].x ^= 0x88888888u, w[s][i].y ^= 0x88888888u;
-                }
-#pragma unroll
-            for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
-                float d[2][NT][4];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t sel = quad % 2 ? 0x7632 : 0x5410;
-                    const uint32_t p0 = quad < 2 ? __byte_perm(w[s][0].x, w[s][1].x, sel)
-                                                 : __byte_perm(w[s][0].y, w[s][1].y, sel);
-                    const uint32_t p1 = quad < 2 ? __byte_perm(w[s][2].x, w[s][3].x, sel)
-                                                 : __byte_perm(w[s][2].y, w[s][3].y, sel);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t v0 = p0 >> (8 * h), v1 = p1 >> (8 * h);
-                        const uint32_t a0 = low_codes(v0), a1 = high_codes(v0);
-                        const uint32_t a2 = low_codes(v1), a3 = high_codes(v1);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (s == 0)
-                                mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], 0.0f, 0.0f, 0.0f, 0.0f);
-                            else
-                                mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], d[h][n][0], d[h][n][1],
-                                        d[h][n][2], d[h][n][3]);
-                        }
-                    }
-                }
-                const float4 sc = scales[quad];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n) x[s][n] = xb[(s * NT + n) * 32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        acc[2 * quad][n][i] = fmaf(d[0][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
-                        acc[2 * quad + 1][n][i] = fmaf(d[1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(
+                            codes + ((codes_at + s * 1024 + (i & 2) * 256 + (i & 1) * 128) ^ (i & 1) << 4));
+                        w[s][i] = make_uint2(v.x ^ 0x88888888u, v.y ^ 0x88888888u);
                     }
+                }
+#pragma unroll
+                for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
+                    float d[2][NT][4];
+#pragma unroll
+                    for (int s = 0; s < kFoldSteps; ++s) {
+                        const uint32_t sel = quad % 2 ? 0x7632 : 0x5410;
+                        const uint32_t p0 = quad < 2 ? __byte_perm(w[s][0].x, w[s][1].x, sel)
+                                                     : __byte_perm(w[s][0].y, w[s][1].y, sel);
+                        const uint32_t p1 = quad < 2 ? __byte_perm(w[s][2].x, w[s][3].x, sel)
+                                                     : __byte_perm(w[s][2].y, w[s][3].y, sel);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t v0 = p0 >> (8 * h), v1 = p1 >> (8 * h);
+                            const uint32_t a0 = low_codes(v0), a1 = high_codes(v0);
+                            const uint32_t a2 = low_codes(v1), a3 = high_codes(v1);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                if (s == 0)
+                                    mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], 0.0f, 0.0f, 0.0f, 0.0f);
+                                else
+                                    mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], d[h][n][0], d[h][n][1],
+                                            d[h][n][2], d[h][n][3]);
+                            }
+                        }
+                    }
+                    const float4 sc = scales[quad];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            acc[2 * quad][n][i] = fmaf(d[0][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
+                            acc[2 * quad + 1][n][i] = fmaf(d[1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
+                        }
+                }
             }
             __syncwarp();  // every lane has read the stage
             fetch(stage);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (++stage == kStages) stage = 0, parity ^= 1;
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (gave_up && copied && busy) {  // its own copies in flight, with the same limit
+        const int done = f_unit - kStages;  // units waited for
+        for (int u = max(u0, done); u < min(u1, f_unit); ++u)
+            mbar_wait(&full[(u - u0) % kStages], (u - u0) / kStages & 1, &never);
+    }
+    if (!a.tma_s) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the rings are free
 
     // This CTA's sums, [row][column], at their true size; then each CTA of the
@@ -414,46 +420,56 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     cluster.sync();  // no CTA leaves while another reads its sums
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int kFolds>
 cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
-    constexpr int smem = matvec_smem<NT>();
-    static bool set[64] = {false};  // this kernel's attributes, on each device
+    constexpr int smem = matvec_smem<NT, kFolds>();
+    static_assert(BSG_MATVEC_MAX_M * kCtaCols * 4 <= kWarps * kStages * kCodes, "the sums fit where the codes were");
+    auto *kernel = wgroups_matvec_kernel<T, NT, kFolds>;
+    static bool set[64] = {false};       // this kernel's attributes, on each device
+    static int clusters[64][17] = {{0}};  // how many clusters of each size fit the card
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(wgroups_matvec_kernel<T, NT>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(wgroups_matvec_kernel<T, NT>,
-                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) set[dev] = true;
-    }
-    // The split of K that ends first: waves of CTAs times units of each, a CTA's
-    // start and join counting as four units.
-    const int tiles = (a.N + kCtaCols - 1) / kCtaCols, units = (a.K + kUnit - 1) / kUnit;
-    const int64_t places = (int64_t)device_sm_count() * matvec_per_sm<NT>();
-    int ranks = 1;
-    int64_t best = INT64_MAX;
-    for (int r = 1; r <= 16 && r <= units; ++r) {
-        const int64_t cost = ((int64_t)tiles * r + places - 1) / places * ((units + r - 1) / r + 4);
-        if (cost < best) best = cost, ranks = r;
-    }
+    if (e != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    const int tiles = (a.N + kCtaCols - 1) / kCtaCols, units = (a.K + kUnit - 1) / kUnit;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (int r = 1; r <= 16 && e == cudaSuccess; ++r) {
+            attr[0].val.clusterDim.x = (unsigned)r;
+            cfg.gridDim = dim3((unsigned)r, 1);
+            e = cudaOccupancyMaxActiveClusters(&clusters[dev][r], kernel, &cfg);
+        }
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    // The split of K that ends first: waves of clusters times units of a CTA, its
+    // start and join counting as two units.
+    int ranks = 1;
+    int64_t best = INT64_MAX;
+    for (int r = 1; r <= 16 && r <= units; ++r) {
+        if (!clusters[dev][r]) continue;
+        const int64_t cost = (int64_t)((tiles + clusters[dev][r] - 1) / clusters[dev][r]) * ((units + r - 1) / r + 2);
+        if (cost < best) best = cost, ranks = r;
+    }
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, wgroups_matvec_kernel<T, NT>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T, int NT>
+cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
+    return a.group % kUnit ? launch_matvec<T, NT, 2>(a, st) : launch_matvec<T, NT, 1>(a, st);
 }
 
 }  // namespace
@@ -473,9 +489,16 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
                                   int64_t ldq, const float *scale, int64_t lds, int64_t group,
                                   int64_t M, int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
                                   int32_t *dstatus, cudaStream_t st) {
-    MatvecArgs a{X, ldx, Q, ldq, scale, lds, Y, ldy, dstatus, group, (int)M, (int)N, (int)K, relu, 0};
-    if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0) a.aligned |= 1;
-    if (reinterpret_cast<uintptr_t>(scale) % 16 == 0 && lds % 4 == 0) a.aligned |= 2;
+    // one group to a column ends wherever it likes
+    if (group >= K) group = round_up(K, kUnit);
+    const int64_t groups = (K + group - 1) / group;
+    MatvecArgs a{{}, {}, X, ldx, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
+    if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)
+        a.tma_q = make_tmap_2d(&a.q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Q, (uint64_t)(N + 1) / 2, (uint64_t)K,
+                               (uint64_t)ldq, kWarpCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (reinterpret_cast<uintptr_t>(scale) % 16 == 0 && lds % 4 == 0)
+        a.tma_s = make_tmap_2d(&a.s_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scale, (uint64_t)N, (uint64_t)groups,
+                               (uint64_t)lds, kWarpCols, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const int slots = (int)M * (sizeof(T) == 4 ? 2 : 1);
