@@ -80,6 +80,16 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap *m, uint64_t *bar,
         : "memory");
 }
 
+// `bytes` contiguous bytes global -> shared (16-byte aligned, a multiple of 16),
+// counted on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // 2-D tiled store shared -> global (bulk-group completion), with the L2
 // evict-first policy: the stored lines are the first L2 gives up, so a large
 // output streaming through L2 does not push out the operands that other CTAs

@@ -15,6 +15,10 @@ cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+bool ws_ok(const void *ws, size_t have, size_t need) {
+    return ws != nullptr && aligned(ws, 256) && have >= need;
+}
+
 // A known type, and a pointer on one of its elements.
 bool typed(const void *p, bsg_dtype t) {
     return p != nullptr && (t == BSG_F32 || t == BSG_F16 || t == BSG_BF16) &&
@@ -62,18 +66,24 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
                                      stream_of(stream)));
 }
 
+size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t K) {
+    if (M < 1 || M > BSG_MATVEC_MAX_M || K < 1 || K > (1 << 30)) return 0;
+    return matvec_workspace_bytes(M, K);
+}
+
 bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const uint8_t *Q,
                               int64_t ldq, const float *scale, int64_t lds, int group, int64_t M,
                               int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
-                              int32_t *dstatus, void *stream) {
+                              void *workspace, size_t ws_bytes, int32_t *dstatus, void *stream) {
     if (!typed(X, dtype) || !typed(Y, dtype) || !Q || !typed(scale, BSG_F32) || M < 1 ||
         M > BSG_MATVEC_MAX_M || N < 1 || N > (1 << 25) || K < 1 || K > (1 << 30) || ldx < K || ldy < N ||
         ldq < (N + 1) / 2 || lds < N || !group_ok(group) || (relu != 0 && relu != 1))
         return BSG_ERR_ARG;
+    if (!ws_ok(workspace, ws_bytes, matvec_workspace_bytes(M, K))) return BSG_ERR_WORKSPACE;
     const bsg_status s = check_device();
     if (s != BSG_OK) return s;
     return done(launch_wgroups_matvec(X, dtype, ldx, Q, ldq, scale, lds, group ? group : K, M, N,
-                                      K, relu, Y, ldy, dstatus, stream_of(stream)));
+                                      K, relu, Y, ldy, workspace, dstatus, stream_of(stream)));
 }
 
 bsg_status bsg_kv8_append(const bsg_kv8_cache *cache, const int32_t *table, int64_t table_ld,
@@ -107,8 +117,7 @@ bsg_status bsg_kv8_attend(const bsg_kv8_cache *cache, const int32_t *table, int6
         !typed(q->data, dtype) || !typed(out->data, dtype) || T < 1 || T > BSG_KV8_MAX_T ||
         heads < 1 || heads > 65535 || heads % cache->heads || !(scale - scale == 0.0f))
         return BSG_ERR_ARG;
-    if (!workspace || !aligned(workspace, 256) ||
-        ws_bytes < kv8_attend_workspace_bytes(*cache, table_ld, B, T, heads))
+    if (!ws_ok(workspace, ws_bytes, kv8_attend_workspace_bytes(*cache, table_ld, B, T, heads)))
         return BSG_ERR_WORKSPACE;
     const bsg_status s = check_device();
     if (s != BSG_OK) return s;

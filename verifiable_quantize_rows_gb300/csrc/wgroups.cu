@@ -70,31 +70,44 @@ __global__ void __launch_bounds__(128)
 //
 // f32 rows are two f16 parts, hi + 2^-11 lo (two columns), 16-bit rows one, all
 // relative to a power of two near the largest |x| of kChunk consecutive k of
-// the row, so that f16's range holds them.
+// the row, so that f16's range holds them.  A first, small launch lays them out
+// as the B operand; it runs beside the start of the second, whose weights are
+// on their way meanwhile.  (With each CTA making its own parts in shared memory
+// its warps met at a barrier every kChunk: 62 against XX us at 16384^2, 8 rows.)
 //
 // A warp takes 128 columns (64 bytes of each row of Q) in units of 64 rows, each
 // one TMA copy (and one of its scales) that the warp itself issues kStages units
 // ahead; groups' sums are scaled once a unit, or once each 32 rows where a group
-// may end there (kFolds).  The warps of a CTA are side by side and share X's parts
-// in shared memory.  The CTAs of a cluster split K and join their sums through
-// distributed shared memory, in rank order.
+// may end there (kFolds).  The CTAs of a cluster split K and join their sums
+// through distributed shared memory, in rank order.
 
 constexpr int kWarps = 4, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
-constexpr int kUnit = 64, kStages = 3;
-constexpr int kChunk = 256;                    // k that X's parts are staged for at a time
+constexpr int kUnit = 64;
+constexpr int kChunk = 256;                    // k that share a power of two
 constexpr int kCodes = kUnit * kWarpCols / 2;  // bytes of a unit's codes
+constexpr int kSteps = kUnit / 16;
 
 template <int NT>
-__host__ __device__ constexpr int matvec_per_sm() { return NT == 4 ? 2 : 3; }
+__host__ __device__ constexpr int matvec_per_sm() { return NT == 1 ? 4 : NT == 2 ? 2 : 2; }
+template <int NT>
+__host__ __device__ constexpr int stages() { return NT == 1 ? 2 : 3; }
+
+// Bytes of a unit's parts of X, and of a CTA's rings.
+template <int NT>
+__host__ __device__ constexpr int part_bytes() { return kSteps * NT * 256; }
 template <int NT, int kFolds>
 constexpr int matvec_smem() {
-    return kWarps * kStages * (kCodes + kFolds * kWarpCols * 4) + 2 * kChunk / 16 * NT * 256 + 512;
+    return kWarps * stages<NT>() * (kCodes + part_bytes<NT>() + kFolds * kWarpCols * 4) + 512;
 }
+
+// The parts of X: [step of 16 k][NT][lane] pairs of registers, then the
+// exponents that chunks are raised by, [chunk][16].
+inline int64_t part_chunks(int64_t K) { return (K + kChunk - 1) / kChunk; }
 
 struct MatvecArgs {
     CUtensorMap q_map, s_map;  // where tma_q, tma_s
-    const void *X;
-    int64_t ldx;
+    const uint2 *parts;
+    const int *up;
     const uint8_t *Q;
     int64_t ldq;
     const float *scale;
@@ -160,20 +173,62 @@ __device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, c
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// X's parts: one CTA to a chunk, a row to a warp.  Lane 4s + t of a step holds, of
+// slot s, rows {0, 1, 4, 5}[t] + {0, 2, 8, 10} (see codes_at below).
+template <typename T, int NT>
+__global__ void __launch_bounds__(256)
+    wgroups_parts_kernel(const T *__restrict__ X, int64_t ldx, int M, int K, uint2 *__restrict__ parts,
+                         int *__restrict__ up, int32_t *__restrict__ dstatus) {
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    __shared__ uint2 x_s[kChunk / 16 * NT * 32];
+    __half *xh = reinterpret_cast<__half *>(x_s);
+    const int k0 = blockIdx.x * kChunk, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    griddep_launch_dependents();
+    for (int r = warp; r < 8 * NT / kParts; r += 8) {
+        float x[kChunk / 32];
+        uint32_t top = 0;
+        const T *row = X + (int64_t)min(r, M - 1) * ldx + k0 + lane;
+        const int left = r < M ? K - k0 - lane : 0;
+#pragma unroll
+        for (int j = 0; j < kChunk / 32; ++j) x[j] = 32 * j < left ? to_f32(row[32 * j]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kChunk / 32; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        // 2^e with the largest |x| 2^e in [2^13, 2^14)
+        const int e = max(-126, min(126, 13 + 127 - (int)(top >> 23)));
+        const float by = __uint_as_float((uint32_t)(e + 127) << 23);
+        if (lane == 0) {
+            if (top >= 0x7f800000u) set_status(dstatus, BSG_DSTATUS_NONFINITE);
+            up[blockIdx.x * 16 + r] = e;
+        }
+        const int slot = r * kParts, kk = lane % 16;  // of step 2j + lane / 16
+        const int t = (kk & 1) | (kk >> 1 & 2), i = (kk >> 1 & 1) | (kk >> 2 & 2);
+        const int at = ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + t) * 4 + i;
+#pragma unroll
+        for (int j = 0; j < kChunk / 32; ++j) {
+            const float y = x[j] * by;
+            const __half hi = __float2half_rn(y);
+            xh[at + j * 2 * NT * 128] = hi;
+            if (kParts == 2) xh[at + j * 2 * NT * 128 + 16] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
+        }
+    }
+    __syncthreads();
+    const uint4 *from = reinterpret_cast<const uint4 *>(x_s);
+    uint4 *to = reinterpret_cast<uint4 *>(parts) + (int64_t)blockIdx.x * (kChunk / 16 * NT * 16);
+    for (int i = threadIdx.x; i < kChunk / 16 * NT * 16; i += 256) to[i] = from[i];
+}
+
 // grid (cluster, column tiles)
 template <typename T, int NT, int kFolds>
 __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kBuf = kChunk / 16 * NT * 32;         // uint2 of one buffer of X's parts
     constexpr int kScales = kFolds * kWarpCols;         // floats of a unit's scales
-    constexpr int kSteps = kUnit / 16, kFoldSteps = kSteps / kFolds;
+    constexpr int kFoldSteps = kSteps / kFolds, kStages = stages<NT>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 511);  // the swizzle's period
     float *scale_s = reinterpret_cast<float *>(smem + kWarps * kStages * kCodes);  // [warp][stage][fold][128]
-    uint2 *x_s = reinterpret_cast<uint2 *>(scale_s + kWarps * kStages * kScales);  // [2][step][NT][lane]
     __shared__ uint64_t full_s[kWarps][kStages];
-    __shared__ int up_s[2][16];  // exponent that a row's chunk is raised by
     __shared__ volatile int gave_up, never;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -187,19 +242,25 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     // by the 64-byte swizzle.
     uint8_t *codes_s = smem + warp * kStages * kCodes;
     float *scales_s = scale_s + warp * kStages * kScales;
+    uint2 *parts_s = reinterpret_cast<uint2 *>(scale_s + kWarps * kStages * kScales) + warp * kStages * (part_bytes<NT>() / 8);
     uint64_t *full = full_s[warp];
     if (lane < kStages) mbar_init(&full[lane], 1);
     if (tid == 0) gave_up = never = 0;
     fence_mbar_init();
     __syncthreads();
-    const int copied = (a.tma_q ? kCodes : 0) + (a.tma_s ? kScales * 4 : 0);
+    const int copied = part_bytes<NT>() + (a.tma_q ? kCodes : 0) + (a.tma_s ? kScales * 4 : 0);
     const int my_cols = min(kWarpCols, a.N - col0);
     int f_unit = u0;
-    auto fetch = [&](int stage) {
+    auto copy_parts = [&](int stage, int unit) {
+        bulk_load(parts_s + stage * (part_bytes<NT>() / 8), a.parts + (int64_t)unit * (part_bytes<NT>() / 8),
+                  part_bytes<NT>(), &full[stage]);
+    };
+    auto fetch = [&](int stage, bool with_parts) {
         if (busy && f_unit < u1) {
             const int k0 = f_unit * kUnit;
-            if (copied && lane == 0) {
+            if (lane == 0) {
                 mbar_arrive_expect_tx(&full[stage], copied);
+                if (with_parts) copy_parts(stage, f_unit);
                 if (a.tma_q) tma_load_2d(&a.q_map, &full[stage], codes_s + stage * kCodes, col0 / 2, k0);
                 if (a.tma_s)
 #pragma unroll
@@ -235,46 +296,14 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
         if (!a.tma_s) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(i);
-
-    // X's parts of one chunk, a row to a warp, as the B operand: the lane that
-    // holds rows {0, 1, 4, 5}[t] + {0, 2, 8, 10} of each 16 (see codes_at below).
-    const int chunk_units = kChunk / kUnit;
-    auto stage_x = [&](int first_unit, int buf) {
-        const int k0 = first_unit * kUnit, k1 = min(min(u1 * kUnit, a.K), k0 + kChunk);
-        for (int r = warp; r < 8 * NT / kParts; r += kWarps) {
-            float x[kChunk / 32];
-            uint32_t top = 0;
-            const T *row = static_cast<const T *>(a.X) + (int64_t)min(r, a.M - 1) * a.ldx + k0 + lane;
-            const int left = r < a.M ? k1 - k0 - lane : 0;
-#pragma unroll
-            for (int j = 0; j < kChunk / 32; ++j) x[j] = 32 * j < left ? to_f32(row[32 * j]) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < kChunk / 32; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (top >= 0x7f800000u && lane == 0) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
-            // 2^e with the largest |x| 2^e in [2^13, 2^14)
-            const int e = max(-126, min(126, 13 + 127 - (int)(top >> 23)));
-            const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-            if (lane == 0) up_s[buf][r] = e;
-            __half *xh = reinterpret_cast<__half *>(x_s + buf * kBuf);
-            const int slot = r * kParts, kk = lane % 16;  // of step 2j + lane / 16
-            const int tt = (kk & 1) | (kk >> 1 & 2), i = (kk >> 1 & 1) | (kk >> 2 & 2);
-            const int my_half = ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + tt) * 4 + i;
-#pragma unroll
-            for (int j = 0; j < kChunk / 32; ++j) {
-                const float y = x[j] * up;
-                const __half hi = __float2half_rn(y);
-                const int at = my_half + j * 2 * NT * 128;
-                xh[at] = hi;
-                if (kParts == 2) xh[at + 16] = __float2half_rn((y - __half2float(hi)) * 2048.0f);
-            }
-        }
-    };
+    for (int i = 0; i < kStages; ++i) fetch(i, false);
+    griddep_wait();  // X's parts are there
+    if (busy && lane == 0)
+        for (int i = 0; i < kStages && u0 + i < u1; ++i) copy_parts(i, u0 + i);
 
     // The lane's 16 columns 16g .. 16g + 15, its slots 2t and 2t + 1 of each 8.
     float acc[8][NT][4];
-    int up[NT][2];
+    int up[NT][2], up_next[NT][2];  // of its columns' rows: of the sums, of the coming chunk
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -287,30 +316,51 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     const int row_t = (t & 1) | (t & 2) << 1;
     const int codes_at = row_t * 64 + (((g >> 1) ^ (t & 2)) << 4) + (g & 1) * 8;
     uint32_t parity = 0;
-    int stage = 0, buf = 0;
-    if (u0 < u1) stage_x(u0, 0);
-    for (int c0 = u0; c0 < u1; c0 += chunk_units, buf ^= 1) {
-        __syncthreads();  // this chunk's parts are there, and the other buffer is free
-        if (c0 + chunk_units < u1) stage_x(c0 + chunk_units, buf ^ 1);
-        // sums so far to this chunk's power of two
+    int stage = 0;
+    constexpr int kChunkUnits = kChunk / kUnit;
+    auto load_up = [&](int chunk) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = up_s[buf][(8 * n + 2 * t + i) / kParts];
-                // at most 2^60 up: what a chunk below that adds is nothing beside the sums
-                const int to = c0 == u0 ? e : min(e, up[n][i] + 60);
-                if (c0 != u0 && to != up[n][i]) {
-                    const float f = exp2f((float)(to - up[n][i]));
+            for (int i = 0; i < 2; ++i) up_next[n][i] = __ldg(a.up + chunk * 16 + (8 * n + 2 * t + i) / kParts);
+    };
+    bool first = true, held = false;
+    __half2 lower[NT];  // what the parts of slot g are multiplied by while held
+    if (u0 < u1) load_up(u0 / kChunkUnits);
+    if (busy)
+        for (int u = u0; u < u1; ++u) {
+            if (first || u % kChunkUnits == 0) {
+                // Sums so far to this chunk's power of two.  Where that is over 2^60 more
+                // than theirs, no further: the chunk is small beside what they were made
+                // of, and its parts are lowered instead.
+                held = false;
 #pragma unroll
-                    for (int m = 0; m < 8; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
+                for (int n = 0; n < NT; ++n) {
+                    int low[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int e = up_next[n][i], to = first ? e : min(e, up[n][i] + 60);
+                        low[i] = to - e;
+                        if (!first && to != up[n][i]) {
+                            const float f = exp2f((float)(to - up[n][i]));
+#pragma unroll
+                            for (int m = 0; m < 8; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
+                        }
+                        up[n][i] = to;
+                    }
+                    if (__any_sync(0xffffffffu, (low[0] | low[1]) != 0)) {
+                        held = true;
+                        const int l0 = __shfl_sync(0xffffffffu, low[0], g >> 1);
+                        const int l1 = __shfl_sync(0xffffffffu, low[1], g >> 1);
+                        lower[n] = __float2half2_rn(exp2f((float)(g & 1 ? l1 : l0)));
+                    } else {
+                        lower[n] = __float2half2_rn(1.0f);
+                    }
                 }
-                up[n][i] = to;
+                first = false;
+                if ((u / kChunkUnits + 1) * kChunkUnits < u1) load_up(u / kChunkUnits + 1);
             }
-        if (!busy) continue;
-        const int c1 = min(u1, c0 + chunk_units);
-        for (int u = c0; u < c1; ++u) {
-            if (copied && !mbar_wait(&full[stage], parity, &gave_up)) {
+            if (!mbar_wait(&full[stage], parity, &gave_up)) {
                 gave_up = 1;
                 set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
                 break;
@@ -321,29 +371,30 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
             for (int f = 0; f < kFolds; ++f) {
                 const float4 *scales = reinterpret_cast<const float4 *>(scales_s + stage * kScales + f * kWarpCols) + 4 * g;
                 const uint8_t *codes = codes_s + stage * kCodes + f * kFoldSteps * 1024;
-                const uint2 *xb = x_s + buf * kBuf + ((u - c0) * kSteps + f * kFoldSteps) * NT * 32 + lane;
-                uint2 x[kFoldSteps][NT], w[kFoldSteps][4];
+                const uint2 *xb = parts_s + stage * (part_bytes<NT>() / 8) + f * kFoldSteps * NT * 32 + lane;
+                float d[8][NT][4];  // this fold's sums: of the lane's column pairs
 #pragma unroll
                 for (int s = 0; s < kFoldSteps; ++s) {
+                    uint2 x[NT], w[4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) x[s][n] = xb[(s * NT + n) * 32];
+                    for (int n = 0; n < NT; ++n) {
+                        x[n] = xb[(s * NT + n) * 32];
+                        if (held) {
+                            __half2 *h = reinterpret_cast<__half2 *>(&x[n]);
+                            h[0] = __hmul2(h[0], lower[n]), h[1] = __hmul2(h[1], lower[n]);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint2 v = *reinterpret_cast<const uint2 *>(
                             codes + ((codes_at + s * 1024 + (i & 2) * 256 + (i & 1) * 128) ^ (i & 1) << 4));
-                        w[s][i] = make_uint2(v.x ^ 0x88888888u, v.y ^ 0x88888888u);
+                        w[i] = make_uint2(v.x ^ 0x88888888u, v.y ^ 0x88888888u);
                     }
-                }
 #pragma unroll
-                for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
-                    float d[2][NT][4];
-#pragma unroll
-                    for (int s = 0; s < kFoldSteps; ++s) {
+                    for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
                         const uint32_t sel = quad % 2 ? 0x7632 : 0x5410;
-                        const uint32_t p0 = quad < 2 ? __byte_perm(w[s][0].x, w[s][1].x, sel)
-                                                     : __byte_perm(w[s][0].y, w[s][1].y, sel);
-                        const uint32_t p1 = quad < 2 ? __byte_perm(w[s][2].x, w[s][3].x, sel)
-                                                     : __byte_perm(w[s][2].y, w[s][3].y, sel);
+                        const uint32_t p0 = quad < 2 ? __byte_perm(w[0].x, w[1].x, sel) : __byte_perm(w[0].y, w[1].y, sel);
+                        const uint32_t p1 = quad < 2 ? __byte_perm(w[2].x, w[3].x, sel) : __byte_perm(w[2].y, w[3].y, sel);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t v0 = p0 >> (8 * h), v1 = p1 >> (8 * h);
@@ -351,30 +402,33 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                             const uint32_t a2 = low_codes(v1), a3 = high_codes(v1);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
+                                float(&y)[4] = d[2 * quad + h][n];
                                 if (s == 0)
-                                    mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], 0.0f, 0.0f, 0.0f, 0.0f);
+                                    mma_f16(y, a0, a1, a2, a3, x[n], 0.0f, 0.0f, 0.0f, 0.0f);
                                 else
-                                    mma_f16(d[h][n], a0, a1, a2, a3, x[s][n], d[h][n][0], d[h][n][1],
-                                            d[h][n][2], d[h][n][3]);
+                                    mma_f16(y, a0, a1, a2, a3, x[n], y[0], y[1], y[2], y[3]);
                             }
                         }
                     }
+                }
+#pragma unroll
+                for (int quad = 0; quad < 4; ++quad) {
                     const float4 sc = scales[quad];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            acc[2 * quad][n][i] = fmaf(d[0][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
-                            acc[2 * quad + 1][n][i] = fmaf(d[1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
+                            acc[2 * quad][n][i] = fmaf(d[2 * quad][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
+                            acc[2 * quad + 1][n][i] =
+                                fmaf(d[2 * quad + 1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
                         }
                 }
             }
             __syncwarp();  // every lane has read the stage
-            fetch(stage);
+            fetch(stage, true);
             if (++stage == kStages) stage = 0, parity ^= 1;
         }
-    }
-    if (gave_up && copied && busy) {  // its own copies in flight, with the same limit
+    if (gave_up && busy) {  // its own copies in flight, with the same limit
         const int done = f_unit - kStages;  // units waited for
         for (int u = max(u0, done); u < min(u1, f_unit); ++u)
             mbar_wait(&full[(u - u0) % kStages], (u - u0) / kStages & 1, &never);
@@ -407,23 +461,28 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
         for (int e = tid; e < a.M * kCtaCols; e += kWarps * 32) y_s[e] = 0.0f;
     }
     cluster.sync();
-    const int c0 = kCtaCols * rank / ranks, c1 = kCtaCols * (rank + 1) / ranks;
-    for (int r = 0; r < a.M; ++r)
-        for (int c = c0 + tid; c < c1; c += kWarps * 32) {
-            const int64_t n = (int64_t)blockIdx.y * kCtaCols + c;
-            if (n >= a.N) break;
-            float y = 0.0f;
-            for (int k = 0; k < ranks; ++k) y += cluster.map_shared_rank(y_s, k)[r * kCtaCols + c];
-            if (a.relu && !(y > 0.0f)) y = 0.0f;
-            static_cast<T *>(a.Y)[r * a.ldy + n] = from_f32<T>(y);
-        }
+    const int c0 = kCtaCols * rank / ranks, cols = kCtaCols * (rank + 1) / ranks - c0;
+    for (int e = tid; e < a.M * cols; e += kWarps * 32) {
+        const int r = e / cols, c = c0 + e - r * cols;
+        const int64_t n = (int64_t)blockIdx.y * kCtaCols + c;
+        if (n >= a.N) continue;
+        float part[16];  // all of them on their way at once
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            part[k] = k < ranks ? *cluster.map_shared_rank(y_s + r * kCtaCols + c, k) : 0.0f;
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y += part[k];
+        if (a.relu && !(y > 0.0f)) y = 0.0f;
+        static_cast<T *>(a.Y)[r * a.ldy + n] = from_f32<T>(y);
+    }
     cluster.sync();  // no CTA leaves while another reads its sums
 }
 
 template <typename T, int NT, int kFolds>
 cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
     constexpr int smem = matvec_smem<NT, kFolds>();
-    static_assert(BSG_MATVEC_MAX_M * kCtaCols * 4 <= kWarps * kStages * kCodes, "the sums fit where the codes were");
+    static_assert(BSG_MATVEC_MAX_M * kCtaCols * 4 <= kWarps * stages<NT>() * kCodes, "the sums fit where the codes were");
     auto *kernel = wgroups_matvec_kernel<T, NT, kFolds>;
     static bool set[64] = {false};       // this kernel's attributes, on each device
     static int clusters[64][17] = {{0}};  // how many clusters of each size fit the card
@@ -434,7 +493,7 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -462,13 +521,25 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         if (cost < best) best = cost, ranks = r;
     }
     attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside X's parts
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename T, int NT>
-cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
+cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cudaStream_t st) {
+    const int64_t chunks = part_chunks(a.K);
+    uint2 *parts = static_cast<uint2 *>(ws);
+    int *up = reinterpret_cast<int *>(parts + chunks * (kChunk / 16 * NT * 32));
+    wgroups_parts_kernel<T, NT><<<(unsigned)chunks, 256, 0, st>>>(X, ldx, a.M, a.K, parts, up, a.dstatus);
+    count_launches(1);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    a.parts = parts;
+    a.up = up;
     return a.group % kUnit ? launch_matvec<T, NT, 2>(a, st) : launch_matvec<T, NT, 1>(a, st);
 }
 
@@ -485,14 +556,20 @@ cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t l
     return cudaGetLastError();
 }
 
+// Enough for f32 parts of M rows.
+size_t matvec_workspace_bytes(int64_t M, int64_t K) {
+    const int64_t nt = 2 * M <= 8 ? 1 : 2 * M <= 16 ? 2 : 4;
+    return (size_t)round_up(part_chunks(K) * (kChunk / 16 * nt * 256 + 64), 256);
+}
+
 cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const uint8_t *Q,
                                   int64_t ldq, const float *scale, int64_t lds, int64_t group,
                                   int64_t M, int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
-                                  int32_t *dstatus, cudaStream_t st) {
+                                  void *ws, int32_t *dstatus, cudaStream_t st) {
     // one group to a column ends wherever it likes
     if (group >= K) group = round_up(K, kUnit);
     const int64_t groups = (K + group - 1) / group;
-    MatvecArgs a{{}, {}, X, ldx, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
+    MatvecArgs a{{}, {}, nullptr, nullptr, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
     if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)
         a.tma_q = make_tmap_2d(&a.q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Q, (uint64_t)(N + 1) / 2, (uint64_t)K,
                                (uint64_t)ldq, kWarpCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -502,9 +579,10 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const int slots = (int)M * (sizeof(T) == 4 ? 2 : 1);
-        if (slots <= 8) return launch_matvec<T, 1>(a, st);
-        if (slots <= 16) return launch_matvec<T, 2>(a, st);
-        if constexpr (sizeof(T) == 4) return launch_matvec<T, 4>(a, st);
+        const T *x = static_cast<const T *>(X);
+        if (slots <= 8) return launch_matvec<T, 1>(a, x, ldx, ws, st);
+        if (slots <= 16) return launch_matvec<T, 2>(a, x, ldx, ws, st);
+        if constexpr (sizeof(T) == 4) return launch_matvec<T, 4>(a, x, ldx, ws, st);
         return cudaErrorInvalidValue;
     });
 }

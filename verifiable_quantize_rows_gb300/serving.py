@@ -141,7 +141,7 @@ def wquant_groups(W, group: int = 64, dstatus=None, stream=None):
 
 
 def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, dstatus=None,
-                   stream=None):
+                   stream=None, workspace=None):
     """Y = X . W_hat (+ReLU) for up to MATVEC_MAX_M rows of X (M x K) and a
     weight stored by wquant_groups -- or by wquant_cols with bits=4, with
     group=0 and scale viewed as (1, N).  Y: M x N of X's dtype."""
@@ -163,9 +163,11 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     if Q.shape != (K, (N + 1) // 2) or Q.stride(1) != 1 and Q.shape[1] != 1:
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
     Y = _output(out, (M, N), X.dtype, dev, stream)
-    _bsg._check(_bsg.load().bsg_wgroups_matvec(
+    lib = _bsg.load()
+    wp, wn = _bsg._ws(workspace, lib.bsg_wgroups_matvec_workspace_size(M, K))
+    _bsg._check(lib.bsg_wgroups_matvec(
         X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
-        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), _status(dstatus, dev),
+        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev),
         _stream(stream, dev)), "bsg_wgroups_matvec")
     return Y
 
