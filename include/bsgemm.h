@@ -351,11 +351,11 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
  * bsg_wquant_groups, or by bsg_wquant_cols with bits = 4 and group = 0.
  * Y: M x N (ldy >= N), of X's type.  Inf or NaN in X sets
  * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  N <= 2^25, K <=
- * 2^30.  `workspace`: bsg_wgroups_matvec_workspace_size(M, K) bytes, 256-byte
- * aligned.  Fastest with Q 16-byte aligned and ldq a multiple of
+ * 2^30.  `workspace`: bsg_wgroups_matvec_workspace_size(M, N, K) bytes,
+ * 256-byte aligned.  Fastest with Q 16-byte aligned and ldq a multiple of
  * 16, and scale likewise (lds a multiple of 4). */
 #define BSG_MATVEC_MAX_M 16
-size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t K);
+size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t N, int64_t K);
 bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const uint8_t *Q,
                               int64_t ldq, const float *scale, int64_t lds, int group, int64_t M,
                               int64_t N, int64_t K, int relu, void *Y, int64_t ldy,

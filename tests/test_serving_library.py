@@ -43,13 +43,13 @@ def test_wquant_groups(lib):
 
 def test_wgroups_matvec(lib):
     good = dict(X=D, dtype=0, ldx=100, Q=D, ldq=4, scale=D, lds=7, group=32, M=3, N=7, K=100, relu=0, Y=D, ldy=7,
-                ws=D, n=lib.bsg_wgroups_matvec_workspace_size(3, 100), st=None, stream=None)
+                ws=D, n=lib.bsg_wgroups_matvec_workspace_size(3, 7, 100), st=None, stream=None)
     refused(lib.bsg_wgroups_matvec, good,
             [("X", None), ("X", D + 2), ("dtype", 3), ("dtype", -1), ("ldx", 99), ("Q", None), ("ldq", 3), ("scale", None),
              ("lds", 6), ("group", 48), ("M", 0), ("M", 17), ("N", 0), ("K", 0), ("relu", 2), ("Y", None), ("ldy", 6),
              ("N", (1 << 25) + 1), ("K", (1 << 30) + 1)])
     refused(lib.bsg_wgroups_matvec, good, [("ws", None), ("ws", D + 16), ("n", good["n"] - 1)], WORKSPACE)
-    assert lib.bsg_wgroups_matvec_workspace_size(0, 5) == lib.bsg_wgroups_matvec_workspace_size(17, 5) == 0
+    assert lib.bsg_wgroups_matvec_workspace_size(0, 5, 5) == lib.bsg_wgroups_matvec_workspace_size(17, 5, 5) == 0
 
 
 def cache(**kw):

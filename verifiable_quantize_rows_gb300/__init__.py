@@ -122,7 +122,7 @@ def _declare(lib):
         "bsg_wquant_groups": ([_vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
         "bsg_wgroups_matvec": ([_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64,
                                 _i32, _vp, _i64, _vp, _sz, _vp, _vp], _i32),
-        "bsg_wgroups_matvec_workspace_size": ([_i64, _i64], _sz),
+        "bsg_wgroups_matvec_workspace_size": ([_i64, _i64, _i64], _sz),
         "bsg_kv8_append": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp], _i32),
         "bsg_kv8_attend_workspace_size": ([_vp, _i64, _i64, _i64, _i32], _sz),
         "bsg_kv8_attend": ([_vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, ctypes.c_float,

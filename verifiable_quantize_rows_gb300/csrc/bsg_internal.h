@@ -114,7 +114,7 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
                                   int64_t ldq, const float *scale, int64_t lds, int64_t group,
                                   int64_t M, int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
                                   void *ws, int32_t *dstatus, cudaStream_t st);
-size_t matvec_workspace_bytes(int64_t M, int64_t K);
+size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_kv8_append(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
                               const int32_t *starts, const int32_t *counts, const bsg_tokens &k,
                               const bsg_tokens &v, int dtype, int64_t B, int64_t T,

@@ -66,9 +66,9 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
                                      stream_of(stream)));
 }
 
-size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t K) {
-    if (M < 1 || M > BSG_MATVEC_MAX_M || K < 1 || K > (1 << 30)) return 0;
-    return matvec_workspace_bytes(M, K);
+size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || M > BSG_MATVEC_MAX_M || N < 1 || N > (1 << 25) || K < 1 || K > (1 << 30)) return 0;
+    return matvec_workspace_bytes(M, N, K);
 }
 
 bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const uint8_t *Q,
@@ -79,7 +79,7 @@ bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const
         M > BSG_MATVEC_MAX_M || N < 1 || N > (1 << 25) || K < 1 || K > (1 << 30) || ldx < K || ldy < N ||
         ldq < (N + 1) / 2 || lds < N || !group_ok(group) || (relu != 0 && relu != 1))
         return BSG_ERR_ARG;
-    if (!ws_ok(workspace, ws_bytes, matvec_workspace_bytes(M, K))) return BSG_ERR_WORKSPACE;
+    if (!ws_ok(workspace, ws_bytes, matvec_workspace_bytes(M, N, K))) return BSG_ERR_WORKSPACE;
     const bsg_status s = check_device();
     if (s != BSG_OK) return s;
     return done(launch_wgroups_matvec(X, dtype, ldx, Q, ldq, scale, lds, group ? group : K, M, N,

@@ -4,16 +4,15 @@
 // The storage is wquant.cu's scheme ("Precision" manual, section "Integer
 // weights") on blocks of `group` rows: s = absmax / 7 rounded to f32, codes
 // the integer nearest w / s, ties to even, all-zero blocks s = 0.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "bsg_internal.h"
 #include "bsg_ptx.cuh"
 #include "serve.cuh"
 #include "wq_round.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace bsg {
 namespace {
@@ -75,39 +74,49 @@ __global__ void __launch_bounds__(128)
 // on their way meanwhile.  (With each CTA making its own parts in shared memory
 // its warps met at a barrier every kChunk: 62 against XX us at 16384^2, 8 rows.)
 //
-// A warp takes 128 columns (64 bytes of each row of Q) in units of 64 rows, each
-// one TMA copy (and one of its scales) that the warp itself issues kStages units
-// ahead; groups' sums are scaled once a unit, or once each 32 rows where a group
-// may end there (kFolds).  The CTAs of a cluster split K and join their sums
-// through distributed shared memory, in rank order.
+// A CTA takes 512 columns in units of 64 rows, a warp 64 of them.  Units are
+// copied ahead by TMA, their codes, their scales and X's parts, each stage sent for
+// by the last warp to read what it held; groups' sums are
+// scaled once a unit, or once each 32 rows where a group may end there (kFolds).
+// 64 columns to a warp: at 128 their sums left room for 8 warps on an SM, and it
+// issued on 0.35 of the cycles.  K is split over CTAs; a warp leaves its sums in
+// the workspace and the last to arrive of those that share its columns adds them
+// up, in the order of k whichever that is.  (Clusters that joined through
+// distributed shared memory left a fifth of the places empty: 56 against XX us.)
 
-constexpr int kWarps = 4, kWarpCols = 128, kCtaCols = kWarps * kWarpCols;
+constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
-constexpr int kChunk = 256;                    // k that share a power of two
-constexpr int kCodes = kUnit * kWarpCols / 2;  // bytes of a unit's codes
+constexpr int kChunk = 256;                   // k that share a power of two
 constexpr int kSteps = kUnit / 16;
+constexpr int kBoxCols = 256;                 // columns of one TMA copy: rows of 128 bytes
+constexpr int kBox = kUnit * kBoxCols / 2;    // bytes of its codes
+constexpr int kCodes = kCtaCols / kBoxCols * kBox;
 
+// Units on their way or in use: 212 KB of shared memory for the CTAs of an SM.
 template <int NT>
-__host__ __device__ constexpr int matvec_per_sm() { return NT == 1 ? 4 : NT == 2 ? 2 : 2; }
+__host__ __device__ constexpr int stages() { return NT == 4 ? 8 : 5; }
 template <int NT>
-__host__ __device__ constexpr int stages() { return NT == 1 ? 2 : 3; }
-
-// Bytes of a unit's parts of X, and of a CTA's rings.
+__host__ __device__ constexpr int matvec_per_sm() { return NT == 4 ? 1 : 2; }
+// Bytes of a unit's parts of X, and of a stage: codes, scales, parts.
 template <int NT>
 __host__ __device__ constexpr int part_bytes() { return kSteps * NT * 256; }
 template <int NT, int kFolds>
-constexpr int matvec_smem() {
-    return kWarps * stages<NT>() * (kCodes + part_bytes<NT>() + kFolds * kWarpCols * 4) + 512;
-}
+__host__ __device__ constexpr int stage_bytes() { return kCodes + kFolds * kCtaCols * 4 + part_bytes<NT>(); }
+template <int NT, int kFolds>
+constexpr int matvec_smem() { return (kFolds == 2 ? stages<NT>() - 1 : stages<NT>()) * stage_bytes<NT, kFolds>() + 1024; }
 
-// The parts of X: [step of 16 k][NT][lane] pairs of registers, then the
-// exponents that chunks are raised by, [chunk][16].
+// The workspace: the parts of X, [step of 16 k][NT][lane] pairs of registers; the
+// exponents that chunks are raised by, [chunk][16]; a ticket for each 64 columns;
+// the splits' sums, [split][row][column].
 inline int64_t part_chunks(int64_t K) { return (K + kChunk - 1) / kChunk; }
 
 struct MatvecArgs {
     CUtensorMap q_map, s_map;  // where tma_q, tma_s
     const uint2 *parts;
     const int *up;
+    unsigned int *tickets;
+    float *sums;
+    int cols;  // of a row of sums
     const uint8_t *Q;
     int64_t ldq;
     const float *scale;
@@ -174,16 +183,18 @@ __device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, c
 }
 
 // X's parts: one CTA to a chunk, a row to a warp.  Lane 4s + t of a step holds, of
-// slot s, rows {0, 1, 4, 5}[t] + {0, 2, 8, 10} (see codes_at below).
+// slot s, rows 2t + {0, 1, 8, 9}.
 template <typename T, int NT>
 __global__ void __launch_bounds__(256)
     wgroups_parts_kernel(const T *__restrict__ X, int64_t ldx, int M, int K, uint2 *__restrict__ parts,
-                         int *__restrict__ up, int32_t *__restrict__ dstatus) {
+                         int *__restrict__ up, unsigned int *__restrict__ tickets, int n_tickets,
+                         int32_t *__restrict__ dstatus) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
     __shared__ uint2 x_s[kChunk / 16 * NT * 32];
     __half *xh = reinterpret_cast<__half *>(x_s);
     const int k0 = blockIdx.x * kChunk, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     griddep_launch_dependents();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n_tickets; i += gridDim.x * 256) tickets[i] = 0;
     for (int r = warp; r < 8 * NT / kParts; r += 8) {
         float x[kChunk / 32];
         uint32_t top = 0;
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(256)
             up[blockIdx.x * 16 + r] = e;
         }
         const int slot = r * kParts, kk = lane % 16;  // of step 2j + lane / 16
-        const int t = (kk & 1) | (kk >> 1 & 2), i = (kk >> 1 & 1) | (kk >> 2 & 2);
+        const int t = kk / 2 % 4, i = kk % 2 + kk / 8 * 2;
         const int at = ((lane / 16 * NT + slot / 8) * 32 + slot % 8 * 4 + t) * 4 + i;
 #pragma unroll
         for (int j = 0; j < kChunk / 32; ++j) {
@@ -218,103 +229,119 @@ __global__ void __launch_bounds__(256)
     for (int i = threadIdx.x; i < kChunk / 16 * NT * 16; i += 256) to[i] = from[i];
 }
 
-// grid (cluster, column tiles)
+template <typename T>
+__device__ __forceinline__ void store_pair(const MatvecArgs &a, int r, int c, float2 v) {
+    T *y = static_cast<T *>(a.Y) + r * a.ldy + c;
+    if (c < a.N) y[0] = from_f32<T>(a.relu && !(v.x > 0.0f) ? 0.0f : v.x);
+    if (c + 1 < a.N) y[1] = from_f32<T>(a.relu && !(v.y > 0.0f) ? 0.0f : v.y);
+}
+
+// grid (splits of K, column tiles)
 template <typename T, int NT, int kFolds>
 __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kScales = kFolds * kWarpCols;         // floats of a unit's scales
-    constexpr int kFoldSteps = kSteps / kFolds, kStages = stages<NT>();
+    constexpr int kFoldSteps = kSteps / kFolds, kStages = kFolds == 2 ? stages<NT>() - 1 : stages<NT>();
+    constexpr int kStage = stage_bytes<NT, kFolds>(), kScalesAt = kCodes, kPartsAt = kCodes + kFolds * kCtaCols * 4;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 511);  // the swizzle's period
-    float *scale_s = reinterpret_cast<float *>(smem + kWarps * kStages * kCodes);  // [warp][stage][fold][128]
-    __shared__ uint64_t full_s[kWarps][kStages];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023);  // the swizzle's period
+    __shared__ uint64_t full[kStages];
+    __shared__ int readers[kStages];  // warps that have yet to read a stage
     __shared__ volatile int gave_up, never;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int rank = blockIdx.x, ranks = gridDim.x;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int units = (a.K + kUnit - 1) / kUnit;
     const int u0 = (int)((int64_t)units * rank / ranks), u1 = (int)((int64_t)units * (rank + 1) / ranks);
-    const int col0 = blockIdx.y * kCtaCols + warp * kWarpCols;  // the warp's first column
+    const int tile0 = blockIdx.y * kCtaCols, col0 = tile0 + warp * kWarpCols;  // the warp's first column
     const bool busy = col0 < a.N;
-
-    // The ring.  A unit's rows are 64 bytes each, their 16-byte pieces permuted
-    // by the 64-byte swizzle.
-    uint8_t *codes_s = smem + warp * kStages * kCodes;
-    float *scales_s = scale_s + warp * kStages * kScales;
-    uint2 *parts_s = reinterpret_cast<uint2 *>(scale_s + kWarps * kStages * kScales) + warp * kStages * (part_bytes<NT>() / 8);
-    uint64_t *full = full_s[warp];
-    if (lane < kStages) mbar_init(&full[lane], 1);
+    const int boxes = a.N - tile0 > kBoxCols ? 2 : 1;
+    const int busy_warps = min(kWarps, (a.N - tile0 + kWarpCols - 1) / kWarpCols);
+    if (tid < kStages) {
+        mbar_init(&full[tid], 1);
+        readers[tid] = busy_warps;
+    }
     if (tid == 0) gave_up = never = 0;
     fence_mbar_init();
     __syncthreads();
-    const int copied = part_bytes<NT>() + (a.tma_q ? kCodes : 0) + (a.tma_s ? kScales * 4 : 0);
-    const int my_cols = min(kWarpCols, a.N - col0);
-    int f_unit = u0;
-    auto copy_parts = [&](int stage, int unit) {
-        bulk_load(parts_s + stage * (part_bytes<NT>() / 8), a.parts + (int64_t)unit * (part_bytes<NT>() / 8),
-                  part_bytes<NT>(), &full[stage]);
+
+    // One thread's copies of a unit: codes and scales (weights: there from the
+    // start), then X's parts.
+    const int copied = part_bytes<NT>() + (a.tma_q ? boxes * kBox : 0) + (a.tma_s ? boxes * kFolds * kBoxCols * 4 : 0);
+    auto copy_weights = [&](int unit, int stage) {
+        uint8_t *to = smem + stage * kStage;
+        mbar_arrive_expect_tx(&full[stage], copied);
+        for (int i = 0; i < boxes; ++i) {
+            if (a.tma_q)
+                tma_load_2d(&a.q_map, &full[stage], to + i * kBox, (tile0 + i * kBoxCols) / 2, unit * kUnit);
+            if (a.tma_s)
+#pragma unroll
+                for (int f = 0; f < kFolds; ++f)
+                    tma_load_2d(&a.s_map, &full[stage], to + kScalesAt + (f * kCtaCols + i * kBoxCols) * 4,
+                                tile0 + i * kBoxCols, (unit * kUnit + 32 * f) / a.group);
+        }
     };
-    auto fetch = [&](int stage, bool with_parts) {
+    auto copy_parts = [&](int unit, int stage) {
+        bulk_load(smem + stage * kStage + kPartsAt, a.parts + (int64_t)unit * (part_bytes<NT>() / 8), part_bytes<NT>(),
+                  &full[stage]);
+    };
+    // Rows that TMA does not take: each warp copies its own columns, in the
+    // places that TMA's 128-byte swizzle would give them.
+    int f_unit = u0;
+    auto copy_unaligned = [&](int stage) {
+        uint8_t *to = smem + stage * kStage;
         if (busy && f_unit < u1) {
             const int k0 = f_unit * kUnit;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], copied);
-                if (with_parts) copy_parts(stage, f_unit);
-                if (a.tma_q) tma_load_2d(&a.q_map, &full[stage], codes_s + stage * kCodes, col0 / 2, k0);
-                if (a.tma_s)
-#pragma unroll
-                    for (int f = 0; f < kFolds; ++f)
-                        tma_load_2d(&a.s_map, &full[stage], scales_s + stage * kScales + f * kWarpCols,
-                                    col0, (k0 + 32 * f) / a.group);
-            }
             if (!a.tma_q) {
-                const int half = (a.N + 1) / 2, c = lane % 4;
-                const int bytes = min(16, half - col0 / 2 - 16 * c);
+                const int half = (a.N + 1) / 2, c = lane % 2;
+                const int bytes = min(16, half - col0 / 2 - 16 * c), piece = warp % 4 * 2 + c;
                 const uint8_t *q_end = a.Q + (int64_t)(a.K - 1) * a.ldq + half;
-                const uint8_t *p = a.Q + (int64_t)(k0 + lane / 4) * a.ldq + col0 / 2 + 16 * c;
-#pragma unroll 4
-                for (int r = lane / 4; r < kUnit; r += 8, p += 8 * a.ldq)
+                const uint8_t *p = a.Q + (int64_t)(k0 + lane / 2) * a.ldq + col0 / 2 + 16 * c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 16 + lane / 2;
                     if (bytes > 0 && k0 + r < a.K)
-                        *reinterpret_cast<uint4 *>(codes_s + stage * kCodes + r * 64 + ((c ^ (r >> 1 & 3)) << 4)) =
-                            load_unaligned16(p, bytes, a.Q, q_end);
+                        *reinterpret_cast<uint4 *>(to + warp / 4 * kBox + r * 128 + ((piece ^ (r & 7)) << 4)) =
+                            load_unaligned16(p + i * 16 * a.ldq, bytes, a.Q, q_end);
+                }
             }
             if (!a.tma_s) {
 #pragma unroll
                 for (int f = 0; f < kFolds; ++f) {
                     const float *s = a.scale + (int64_t)(min(k0 + 32 * f, a.K - 1) / a.group) * a.lds + col0;
-                    const uint32_t at = smem_u32(scales_s + stage * kScales + f * kWarpCols);
+                    const uint32_t at = smem_u32(to + kScalesAt + (f * kCtaCols + warp * kWarpCols) * 4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = i * 32 + lane < my_cols;
+                    for (int i = 0; i < 2; ++i) {
+                        const bool in = col0 + i * 32 + lane < a.N;
                         copy_async4(at + (i * 32 + lane) * 4, in ? s + i * 32 + lane : s, in ? 4 : 0);
                     }
                 }
             }
         }
         ++f_unit;
-        if (!a.tma_s) asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(i, false);
+    const bool all_tma = a.tma_q && a.tma_s;
+    const int mine = warp < kStages && lane == 0 && u0 + warp < u1 ? warp : -1;  // the stage that this thread fills
+    if (mine >= 0) copy_weights(u0 + mine, mine);
+    if (!all_tma)
+        for (int i = 0; i < kStages; ++i) copy_unaligned(i);
     griddep_wait();  // X's parts are there
-    if (busy && lane == 0)
-        for (int i = 0; i < kStages && u0 + i < u1; ++i) copy_parts(i, u0 + i);
+    if (mine >= 0) copy_parts(u0 + mine, mine);
 
-    // The lane's 16 columns 16g .. 16g + 15, its slots 2t and 2t + 1 of each 8.
-    float acc[8][NT][4];
+    // The lane's 8 columns 8g .. 8g + 7, its slots 2t and 2t + 1 of each 8.
+    float acc[4][NT][4];
     int up[NT][2], up_next[NT][2];  // of its columns' rows: of the sums, of the coming chunk
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
-    // Where the lane finds its 16 columns' codes of rows {0, 1, 4, 5}[t] and, other
-    // swizzle, of 2 rows on: every four lanes' rows are on banks of their own.
-    const int row_t = (t & 1) | (t & 2) << 1;
-    const int codes_at = row_t * 64 + (((g >> 1) ^ (t & 2)) << 4) + (g & 1) * 8;
+    // Where the lane finds its columns' codes of rows 2t and 2t + 1 (+ 8): the
+    // swizzle puts the rows of four lanes on banks of their own.
+    const int piece = warp % 4 * 2 + (g >> 2), even_at = 2 * t * 128 + ((piece ^ 2 * t) << 4) + (g & 3) * 4;
+    const int odd_at = (2 * t + 1) * 128 + ((piece ^ (2 * t + 1)) << 4) + (g & 3) * 4;
     uint32_t parity = 0;
     int stage = 0;
     constexpr int kChunkUnits = kChunk / kUnit;
@@ -344,7 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                         if (!first && to != up[n][i]) {
                             const float f = exp2f((float)(to - up[n][i]));
 #pragma unroll
-                            for (int m = 0; m < 8; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
+                            for (int m = 0; m < 4; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
                         }
                         up[n][i] = to;
                     }
@@ -365,17 +392,19 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                 set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
                 break;
             }
-            if (!a.tma_s) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            if (!all_tma) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             __syncwarp();
+            const uint8_t *at = smem + stage * kStage;
 #pragma unroll
             for (int f = 0; f < kFolds; ++f) {
-                const float4 *scales = reinterpret_cast<const float4 *>(scales_s + stage * kScales + f * kWarpCols) + 4 * g;
-                const uint8_t *codes = codes_s + stage * kCodes + f * kFoldSteps * 1024;
-                const uint2 *xb = parts_s + stage * (part_bytes<NT>() / 8) + f * kFoldSteps * NT * 32 + lane;
-                float d[8][NT][4];  // this fold's sums: of the lane's column pairs
+                const float4 *scales =
+                    reinterpret_cast<const float4 *>(at + kScalesAt + (f * kCtaCols + warp * kWarpCols) * 4) + 2 * g;
+                const uint8_t *codes = at + warp / 4 * kBox + f * kFoldSteps * 2048;
+                const uint2 *xb = reinterpret_cast<const uint2 *>(at + kPartsAt) + f * kFoldSteps * NT * 32 + lane;
+                float d[4][NT][4];  // this fold's sums
 #pragma unroll
                 for (int s = 0; s < kFoldSteps; ++s) {
-                    uint2 x[NT], w[4];
+                    uint2 x[NT];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         x[n] = xb[(s * NT + n) * 32];
@@ -384,17 +413,15 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                             h[0] = __hmul2(h[0], lower[n]), h[1] = __hmul2(h[1], lower[n]);
                         }
                     }
+                    uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(
-                            codes + ((codes_at + s * 1024 + (i & 2) * 256 + (i & 1) * 128) ^ (i & 1) << 4));
-                        w[i] = make_uint2(v.x ^ 0x88888888u, v.y ^ 0x88888888u);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = *reinterpret_cast<const uint32_t *>(codes + (i % 2 ? odd_at : even_at) + s * 2048 +
+                                                                   i / 2 * 1024) ^ 0x88888888u;
 #pragma unroll
-                    for (int quad = 0; quad < 4; ++quad) {  // 4 columns: a 16-bit piece of a row
-                        const uint32_t sel = quad % 2 ? 0x7632 : 0x5410;
-                        const uint32_t p0 = quad < 2 ? __byte_perm(w[0].x, w[1].x, sel) : __byte_perm(w[0].y, w[1].y, sel);
-                        const uint32_t p1 = quad < 2 ? __byte_perm(w[2].x, w[3].x, sel) : __byte_perm(w[2].y, w[3].y, sel);
+                    for (int quad = 0; quad < 2; ++quad) {  // 4 columns: a 16-bit piece of a row
+                        const uint32_t sel = quad ? 0x7632 : 0x5410;
+                        const uint32_t p0 = __byte_perm(w[0], w[1], sel), p1 = __byte_perm(w[2], w[3], sel);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t v0 = p0 >> (8 * h), v1 = p1 >> (8 * h);
@@ -412,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                     }
                 }
 #pragma unroll
-                for (int quad = 0; quad < 4; ++quad) {
+                for (int quad = 0; quad < 2; ++quad) {
                     const float4 sc = scales[quad];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -425,106 +452,109 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                 }
             }
             __syncwarp();  // every lane has read the stage
-            fetch(stage, true);
-            if (++stage == kStages) stage = 0, parity ^= 1;
-        }
-    if (gave_up && busy) {  // its own copies in flight, with the same limit
-        const int done = f_unit - kStages;  // units waited for
-        for (int u = max(u0, done); u < min(u1, f_unit); ++u)
-            mbar_wait(&full[(u - u0) % kStages], (u - u0) / kStages & 1, &never);
-    }
-    if (!a.tma_s) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the rings are free
-
-    // This CTA's sums, [row][column], at their true size; then each CTA of the
-    // cluster adds up its share of the columns over all ranks.
-    float *y_s = reinterpret_cast<float *>(smem);
-    if (u0 < u1) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; i += kParts) {
-                const int r = (8 * n + 2 * t + i) / kParts;
-                if (r >= a.M) continue;
-                const float down = __uint_as_float((uint32_t)(max(1, min(254, 137 - up[n][i]))) << 23);  // 2^10 / 2^e
-#pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    float2 v = make_float2(acc[m][n][i], acc[m][n][i + 2]);
-                    if (kParts == 2)
-                        v = make_float2(fmaf(acc[m][n][1], 0x1p-11f, acc[m][n][0]),
-                                        fmaf(acc[m][n][3], 0x1p-11f, acc[m][n][2]));
-                    *reinterpret_cast<float2 *>(y_s + r * kCtaCols + warp * kWarpCols + 16 * g + 2 * m) =
-                        make_float2(v.x * down, v.y * down);
+            if (!all_tma) copy_unaligned(stage);
+            if (lane == 0) {  // the last warp to read a stage sends for its next unit
+                __threadfence_block();
+                if (atomicSub(&readers[stage], 1) == 1 && u + kStages < u1) {
+                    readers[stage] = busy_warps;
+                    __threadfence_block();
+                    copy_weights(u + kStages, stage);
+                    copy_parts(u + kStages, stage);
                 }
             }
-    } else {
-        for (int e = tid; e < a.M * kCtaCols; e += kWarps * 32) y_s[e] = 0.0f;
-    }
-    cluster.sync();
-    const int c0 = kCtaCols * rank / ranks, cols = kCtaCols * (rank + 1) / ranks - c0;
-    for (int e = tid; e < a.M * cols; e += kWarps * 32) {
-        const int r = e / cols, c = c0 + e - r * cols;
-        const int64_t n = (int64_t)blockIdx.y * kCtaCols + c;
-        if (n >= a.N) continue;
-        float part[16];  // all of them on their way at once
+            if (++stage == kStages) stage = 0, parity ^= 1;
+        }
+    if (gave_up)  // the copies in flight, with the same limit: a stage's last phase, if it has begun
+        for (int i = 0; i < kStages; ++i) mbar_wait(&full[i], parity ^ (i < stage ? 1u : 0u), &never);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!busy) return;
+
+    // The warp's sums at their true size: to Y, or to the workspace, where the last
+    // warp to arrive of those with these columns adds them up.
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            part[k] = k < ranks ? *cluster.map_shared_rank(y_s + r * kCtaCols + c, k) : 0.0f;
-        float y = 0.0f;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y += part[k];
-        if (a.relu && !(y > 0.0f)) y = 0.0f;
-        static_cast<T *>(a.Y)[r * a.ldy + n] = from_f32<T>(y);
+        for (int i = 0; i < 2; i += kParts) {
+            const int r = (8 * n + 2 * t + i) / kParts;
+            if (r >= a.M) continue;
+            const float down = __uint_as_float((uint32_t)(max(1, min(254, 137 - up[n][i]))) << 23);  // 2^10 / 2^e
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float2 v = make_float2(acc[m][n][i], acc[m][n][i + 2]);
+                if (kParts == 2)
+                    v = make_float2(fmaf(acc[m][n][1], 0x1p-11f, acc[m][n][0]),
+                                    fmaf(acc[m][n][3], 0x1p-11f, acc[m][n][2]));
+                v.x *= down, v.y *= down;
+                const int c = col0 + 8 * g + 2 * m;
+                if (ranks > 1)
+                    *reinterpret_cast<float2 *>(a.sums + ((int64_t)rank * a.M + r) * a.cols + c) = v;
+                else
+                    store_pair<T>(a, r, c, v);
+            }
+        }
+    if (ranks == 1) return;
+    __threadfence();
+    __syncwarp();
+    unsigned int arrived = 0;
+    if (lane == 0) arrived = atomicAdd(&a.tickets[blockIdx.y * kWarps + warp], 1u);
+    if (__shfl_sync(0xffffffffu, arrived, 0) + 1 != (unsigned)ranks) return;
+    __threadfence();
+    // four columns and every other row to a lane, eight splits on their way at once
+    for (int r = lane / 16; r < a.M; r += 2) {
+        const int c = col0 + lane % 16 * 4;
+        const float *from = a.sums + (int64_t)r * a.cols + c;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < ranks; k0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = k0 + k < ranks ? __ldcg(reinterpret_cast<const float4 *>(from + (int64_t)(k0 + k) * a.M * a.cols))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y.x += v[k].x, y.y += v[k].y, y.z += v[k].z, y.w += v[k].w;
+        }
+        store_pair<T>(a, r, c, make_float2(y.x, y.y));
+        store_pair<T>(a, r, c + 2, make_float2(y.z, y.w));
     }
-    cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+// The split of K that ends first: waves of CTAs times units of each, a CTA's
+// start and join counting as four units.
+inline int matvec_splits(int64_t N, int64_t K, int per_sm) {
+    const int64_t tiles = (N + kCtaCols - 1) / kCtaCols, units = (K + kUnit - 1) / kUnit;
+    const int64_t places = (int64_t)device_sm_count() * per_sm;
+    int splits = 1;
+    int64_t best = INT64_MAX;
+    for (int r = 1; r <= 32 && r <= units; ++r) {
+        const int64_t cost = (tiles * r + places - 1) / places * ((units + r - 1) / r + 4);
+        if (cost < best) best = cost, splits = r;
+    }
+    return splits;
 }
 
 template <typename T, int NT, int kFolds>
 cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
     constexpr int smem = matvec_smem<NT, kFolds>();
-    static_assert(BSG_MATVEC_MAX_M * kCtaCols * 4 <= kWarps * stages<NT>() * kCodes, "the sums fit where the codes were");
     auto *kernel = wgroups_matvec_kernel<T, NT, kFolds>;
-    static bool set[64] = {false};       // this kernel's attributes, on each device
-    static int clusters[64][17] = {{0}};  // how many clusters of each size fit the card
+    static bool set[64] = {false};  // this kernel's attribute, on each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const int tiles = (a.N + kCtaCols - 1) / kCtaCols, units = (a.K + kUnit - 1) / kUnit;
     if (!set[dev]) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        for (int r = 1; r <= 16 && e == cudaSuccess; ++r) {
-            attr[0].val.clusterDim.x = (unsigned)r;
-            cfg.gridDim = dim3((unsigned)r, 1);
-            e = cudaOccupancyMaxActiveClusters(&clusters[dev][r], kernel, &cfg);
-        }
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
-    // The split of K that ends first: waves of clusters times units of a CTA, its
-    // start and join counting as two units.
-    int ranks = 1;
-    int64_t best = INT64_MAX;
-    for (int r = 1; r <= 16 && r <= units; ++r) {
-        if (!clusters[dev][r]) continue;
-        const int64_t cost = (int64_t)((tiles + clusters[dev][r] - 1) / clusters[dev][r]) * ((units + r - 1) / r + 2);
-        if (cost < best) best = cost, ranks = r;
-    }
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside X's parts
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)tiles);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)matvec_splits(a.N, a.K, matvec_per_sm<NT>()), (unsigned)(a.cols / kCtaCols));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside X's parts
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
@@ -534,12 +564,16 @@ cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cuda
     const int64_t chunks = part_chunks(a.K);
     uint2 *parts = static_cast<uint2 *>(ws);
     int *up = reinterpret_cast<int *>(parts + chunks * (kChunk / 16 * NT * 32));
-    wgroups_parts_kernel<T, NT><<<(unsigned)chunks, 256, 0, st>>>(X, ldx, a.M, a.K, parts, up, a.dstatus);
+    a.parts = parts;
+    a.up = up;
+    a.cols = (int)round_up(a.N, kCtaCols);
+    a.tickets = reinterpret_cast<unsigned int *>(up + chunks * 16);
+    a.sums = reinterpret_cast<float *>(a.tickets + round_up(a.cols / kWarpCols, 64));
+    wgroups_parts_kernel<T, NT><<<(unsigned)chunks, 256, 0, st>>>(X, ldx, a.M, a.K, parts, up, a.tickets,
+                                                                 a.cols / kWarpCols, a.dstatus);
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    a.parts = parts;
-    a.up = up;
     return a.group % kUnit ? launch_matvec<T, NT, 2>(a, st) : launch_matvec<T, NT, 1>(a, st);
 }
 
@@ -556,10 +590,12 @@ cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t l
     return cudaGetLastError();
 }
 
-// Enough for f32 parts of M rows.
-size_t matvec_workspace_bytes(int64_t M, int64_t K) {
-    const int64_t nt = 2 * M <= 8 ? 1 : 2 * M <= 16 ? 2 : 4;
-    return (size_t)round_up(part_chunks(K) * (kChunk / 16 * nt * 256 + 64), 256);
+// Enough for X of any type.
+size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    const int64_t nt = 2 * M <= 8 ? 1 : 2 * M <= 16 ? 2 : 4, cols = round_up(N, kCtaCols);
+    const int64_t splits = std::max(matvec_splits(N, K, 1), matvec_splits(N, K, 2));
+    return (size_t)round_up(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) + round_up(cols / kWarpCols, 64) * 4 +
+                                (splits > 1 ? splits * M * cols * 4 : 0), 256);
 }
 
 cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const uint8_t *Q,
@@ -569,13 +605,13 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
     // one group to a column ends wherever it likes
     if (group >= K) group = round_up(K, kUnit);
     const int64_t groups = (K + group - 1) / group;
-    MatvecArgs a{{}, {}, nullptr, nullptr, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
+    MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, nullptr, 0, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
     if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)
         a.tma_q = make_tmap_2d(&a.q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Q, (uint64_t)(N + 1) / 2, (uint64_t)K,
-                               (uint64_t)ldq, kWarpCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_64B);
+                               (uint64_t)ldq, kBoxCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_128B);
     if (reinterpret_cast<uintptr_t>(scale) % 16 == 0 && lds % 4 == 0)
         a.tma_s = make_tmap_2d(&a.s_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scale, (uint64_t)N, (uint64_t)groups,
-                               (uint64_t)lds, kWarpCols, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+                               (uint64_t)lds, kBoxCols, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const int slots = (int)M * (sizeof(T) == 4 ? 2 : 1);

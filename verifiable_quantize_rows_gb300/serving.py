@@ -164,7 +164,7 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
     Y = _output(out, (M, N), X.dtype, dev, stream)
     lib = _bsg.load()
-    wp, wn = _bsg._ws(workspace, lib.bsg_wgroups_matvec_workspace_size(M, K))
+    wp, wn = _bsg._ws(workspace, lib.bsg_wgroups_matvec_workspace_size(M, N, K))
     _bsg._check(lib.bsg_wgroups_matvec(
         X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
         group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev),
