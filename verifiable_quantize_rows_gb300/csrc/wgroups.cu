@@ -79,10 +79,15 @@ __global__ void __launch_bounds__(128)
 // by the last warp to read what it held; groups' sums are
 // scaled once a unit, or once each 32 rows where a group may end there (kFolds).
 // 64 columns to a warp: at 128 their sums left room for 8 warps on an SM, and it
-// issued on 0.35 of the cycles.  K is split over CTAs; a warp leaves its sums in
-// the workspace and the last to arrive of those that share its columns adds them
-// up, in the order of k whichever that is.  (Clusters that joined through
-// distributed shared memory left a fifth of the places empty: 56 against XX us.)
+// issued on 0.35 of the cycles.  K is split over CTAs, whose sums a third launch
+// adds up in the order of k.  (Joined by clusters through distributed shared
+// memory, a fifth of the places stayed empty; by the last warp to arrive, its
+// loads alone took up to 13 us.)
+//
+// Measured on the device: 16384 x 16384, 8 f32 rows XX us; 1 row XX; 8191 x 12289, 5
+// bf16 rows XX.  What bounds it: the ALU pipe takes an instruction every other cycle,
+// and 7 of them for 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8
+// slots and shares the issue (measured: 16 together with 4 f16 multiply-adds).
 
 constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
@@ -106,15 +111,14 @@ template <int NT, int kFolds>
 constexpr int matvec_smem() { return (kFolds == 2 ? stages<NT>() - 1 : stages<NT>()) * stage_bytes<NT, kFolds>() + 1024; }
 
 // The workspace: the parts of X, [step of 16 k][NT][lane] pairs of registers; the
-// exponents that chunks are raised by, [chunk][16]; a ticket for each 64 columns;
-// the splits' sums, [split][row][column].
+// exponents that chunks are raised by, [chunk][16]; the splits' sums,
+// [split][row][column].
 inline int64_t part_chunks(int64_t K) { return (K + kChunk - 1) / kChunk; }
 
 struct MatvecArgs {
     CUtensorMap q_map, s_map;  // where tma_q, tma_s
     const uint2 *parts;
     const int *up;
-    unsigned int *tickets;
     float *sums;
     int cols;  // of a row of sums
     const uint8_t *Q;
@@ -187,14 +191,12 @@ __device__ __forceinline__ uint4 load_unaligned16(const uint8_t *p, int bytes, c
 template <typename T, int NT>
 __global__ void __launch_bounds__(256)
     wgroups_parts_kernel(const T *__restrict__ X, int64_t ldx, int M, int K, uint2 *__restrict__ parts,
-                         int *__restrict__ up, unsigned int *__restrict__ tickets, int n_tickets,
-                         int32_t *__restrict__ dstatus) {
+                         int *__restrict__ up, int32_t *__restrict__ dstatus) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
     __shared__ uint2 x_s[kChunk / 16 * NT * 32];
     __half *xh = reinterpret_cast<__half *>(x_s);
     const int k0 = blockIdx.x * kChunk, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     griddep_launch_dependents();
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n_tickets; i += gridDim.x * 256) tickets[i] = 0;
     for (int r = warp; r < 8 * NT / kParts; r += 8) {
         float x[kChunk / 32];
         uint32_t top = 0;
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     if (!all_tma)
         for (int i = 0; i < kStages; ++i) copy_unaligned(i);
     griddep_wait();  // X's parts are there
+    griddep_launch_dependents();
     if (mine >= 0) copy_parts(u0 + mine, mine);
 
     // The lane's 8 columns 8g .. 8g + 7, its slots 2t and 2t + 1 of each 8.
@@ -352,38 +355,30 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
             for (int i = 0; i < 2; ++i) up_next[n][i] = __ldg(a.up + chunk * 16 + (8 * n + 2 * t + i) / kParts);
     };
     bool first = true, held = false;
-    __half2 lower[NT];  // what the parts of slot g are multiplied by while held
+    float lower[NT][2];  // what the lane's columns of a chunk's sums are multiplied by while held
     if (u0 < u1) load_up(u0 / kChunkUnits);
     if (busy)
         for (int u = u0; u < u1; ++u) {
             if (first || u % kChunkUnits == 0) {
                 // Sums so far to this chunk's power of two.  Where that is over 2^60 more
                 // than theirs, no further: the chunk is small beside what they were made
-                // of, and its parts are lowered instead.
-                held = false;
+                // of, and its sums are lowered instead.
+                bool low = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    int low[2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int e = up_next[n][i], to = first ? e : min(e, up[n][i] + 60);
-                        low[i] = to - e;
                         if (!first && to != up[n][i]) {
                             const float f = exp2f((float)(to - up[n][i]));
 #pragma unroll
                             for (int m = 0; m < 4; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
                         }
                         up[n][i] = to;
+                        lower[n][i] = exp2f((float)(to - e));
+                        low |= to != e;
                     }
-                    if (__any_sync(0xffffffffu, (low[0] | low[1]) != 0)) {
-                        held = true;
-                        const int l0 = __shfl_sync(0xffffffffu, low[0], g >> 1);
-                        const int l1 = __shfl_sync(0xffffffffu, low[1], g >> 1);
-                        lower[n] = __float2half2_rn(exp2f((float)(g & 1 ? l1 : l0)));
-                    } else {
-                        lower[n] = __float2half2_rn(1.0f);
-                    }
-                }
+                held = __any_sync(0xffffffffu, low);
                 first = false;
                 if ((u / kChunkUnits + 1) * kChunkUnits < u1) load_up(u / kChunkUnits + 1);
             }
@@ -406,13 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                 for (int s = 0; s < kFoldSteps; ++s) {
                     uint2 x[NT];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        x[n] = xb[(s * NT + n) * 32];
-                        if (held) {
-                            __half2 *h = reinterpret_cast<__half2 *>(&x[n]);
-                            h[0] = __hmul2(h[0], lower[n]), h[1] = __hmul2(h[1], lower[n]);
-                        }
-                    }
+                    for (int n = 0; n < NT; ++n) x[n] = xb[(s * NT + n) * 32];
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -437,6 +426,14 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                             }
                         }
                     }
+                }
+                if (held) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) d[m][n][i] *= lower[n][i % 2];
                 }
 #pragma unroll
                 for (int quad = 0; quad < 2; ++quad) {
@@ -469,8 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!busy) return;
 
-    // The warp's sums at their true size: to Y, or to the workspace, where the last
-    // warp to arrive of those with these columns adds them up.
+    // The warp's sums at their true size, to Y or to the workspace.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -492,42 +488,44 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
                     store_pair<T>(a, r, c, v);
             }
         }
-    if (ranks == 1) return;
-    __threadfence();
-    __syncwarp();
-    unsigned int arrived = 0;
-    if (lane == 0) arrived = atomicAdd(&a.tickets[blockIdx.y * kWarps + warp], 1u);
-    if (__shfl_sync(0xffffffffu, arrived, 0) + 1 != (unsigned)ranks) return;
-    __threadfence();
-    // four columns and every other row to a lane, eight splits on their way at once
-    for (int r = lane / 16; r < a.M; r += 2) {
-        const int c = col0 + lane % 16 * 4;
-        const float *from = a.sums + (int64_t)r * a.cols + c;
-        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k0 = 0; k0 < ranks; k0 += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = k0 + k < ranks ? __ldcg(reinterpret_cast<const float4 *>(from + (int64_t)(k0 + k) * a.M * a.cols))
-                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y.x += v[k].x, y.y += v[k].y, y.z += v[k].z, y.w += v[k].w;
-        }
-        store_pair<T>(a, r, c, make_float2(y.x, y.y));
-        store_pair<T>(a, r, c + 2, make_float2(y.z, y.w));
-    }
 }
 
-// The split of K that ends first: waves of CTAs times units of each, a CTA's
-// start and join counting as four units.
-inline int matvec_splits(int64_t N, int64_t K, int per_sm) {
+// Y from the splits' sums: four columns of a row to a thread.
+template <typename T>
+__global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant__ MatvecArgs a, int splits) {
+    const int c = (blockIdx.x * 128 + threadIdx.x) * 4, r = blockIdx.y;
+    griddep_wait();
+    if (c >= a.N) return;
+    const float *from = a.sums + (int64_t)r * a.cols + c;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = 0; k0 < splits; k0 += 16) {
+        float4 v[16];  // all of them on their way at once
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            v[k] = k0 + k < splits ? __ldcg(reinterpret_cast<const float4 *>(from + (int64_t)(k0 + k) * a.M * a.cols))
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y.x += v[k].x, y.y += v[k].y, y.z += v[k].z, y.w += v[k].w;
+    }
+    store_pair<T>(a, r, c, make_float2(y.x, y.y));
+    store_pair<T>(a, r, c + 2, make_float2(y.z, y.w));
+}
+
+// The split of K that ends first, by what was measured: a unit takes a CTA
+// kUnitUs where it has its SM to itself and kSharedUs where it shares it with
+// another; a split costs its start, and the splits' sums are written and read
+// once through L2.
+inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt) {
     const int64_t tiles = (N + kCtaCols - 1) / kCtaCols, units = (K + kUnit - 1) / kUnit;
-    const int64_t places = (int64_t)device_sm_count() * per_sm;
+    const int64_t sms = device_sm_count(), places = nt == 4 ? sms : 2 * sms;
+    const double alone = nt == 1 ? 0.75 : nt == 2 ? 0.95 : 1.9, shared = nt == 1 ? 1.0 : 1.4;
     int splits = 1;
-    int64_t best = INT64_MAX;
+    double best = 1e30;
     for (int r = 1; r <= 32 && r <= units; ++r) {
-        const int64_t cost = (tiles * r + places - 1) / places * ((units + r - 1) / r + 4);
-        if (cost < best) best = cost, splits = r;
+        const double each = tiles * r <= sms || nt == 4 ? alone : shared;
+        const double us = (double)((tiles * r + places - 1) / places) * (3.0 + each * (double)((units + r - 1) / r)) +
+                          (r > 1 ? 2.0 + 8e-6 / 6.0 * (double)(r * M * N) : 0.0);
+        if (us < best) best = us, splits = r;
     }
     return splits;
 }
@@ -546,17 +544,24 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)matvec_splits(a.N, a.K, matvec_per_sm<NT>()), (unsigned)(a.cols / kCtaCols));
+    const int splits = matvec_splits(a.M, a.N, a.K, NT);
+    cfg.gridDim = dim3((unsigned)splits, (unsigned)(a.cols / kCtaCols));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside X's parts
+    cudaLaunchAttribute attr[1];  // each launch beside the end of the one before it
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess || splits == 1) return e;
+    cfg.gridDim = dim3((unsigned)((a.N + 511) / 512), (unsigned)a.M);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, wgroups_join_kernel<T>, a, splits);
 }
 
 template <typename T, int NT>
@@ -567,10 +572,8 @@ cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cuda
     a.parts = parts;
     a.up = up;
     a.cols = (int)round_up(a.N, kCtaCols);
-    a.tickets = reinterpret_cast<unsigned int *>(up + chunks * 16);
-    a.sums = reinterpret_cast<float *>(a.tickets + round_up(a.cols / kWarpCols, 64));
-    wgroups_parts_kernel<T, NT><<<(unsigned)chunks, 256, 0, st>>>(X, ldx, a.M, a.K, parts, up, a.tickets,
-                                                                 a.cols / kWarpCols, a.dstatus);
+    a.sums = reinterpret_cast<float *>(up + chunks * 16);
+    wgroups_parts_kernel<T, NT><<<(unsigned)chunks, 256, 0, st>>>(X, ldx, a.M, a.K, parts, up, a.dstatus);
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -592,10 +595,14 @@ cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t l
 
 // Enough for X of any type.
 size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    const int64_t nt = 2 * M <= 8 ? 1 : 2 * M <= 16 ? 2 : 4, cols = round_up(N, kCtaCols);
-    const int64_t splits = std::max(matvec_splits(N, K, 1), matvec_splits(N, K, 2));
-    return (size_t)round_up(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) + round_up(cols / kWarpCols, 64) * 4 +
-                                (splits > 1 ? splits * M * cols * 4 : 0), 256);
+    size_t most = 0;
+    for (int parts = 1; parts <= 2; ++parts) {
+        const int nt = parts * M <= 8 ? 1 : parts * M <= 16 ? 2 : 4;
+        const int64_t splits = matvec_splits(M, N, K, nt);
+        most = std::max(most, (size_t)(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) +
+                                       (splits > 1 ? splits * M * round_up(N, kCtaCols) * 4 : 0)));
+    }
+    return (size_t)round_up((int64_t)most, 256);
 }
 
 cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const uint8_t *Q,
@@ -605,7 +612,7 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
     // one group to a column ends wherever it likes
     if (group >= K) group = round_up(K, kUnit);
     const int64_t groups = (K + group - 1) / group;
-    MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, nullptr, 0, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
+    MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, 0, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
     if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)
         a.tma_q = make_tmap_2d(&a.q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Q, (uint64_t)(N + 1) / 2, (uint64_t)K,
                                (uint64_t)ldq, kBoxCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_128B);
