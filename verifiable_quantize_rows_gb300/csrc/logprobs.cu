@@ -4,126 +4,412 @@
 //   lse = m + log S,  S = sum_j e_j,  e_j = exp(x_j - m),  m = max_j x_j;
 //   entropy = log S - (sum_j e_j (x_j - m)) / S;
 //   dx_j = g_lp ([j = t] - p_j) - g_H p_j (x_j - lse + H).
+//
+// Forward: one read of the logits, which is what bounds it (HBM).  Each thread
+// keeps a running maximum with S and A = sum e (x - m) relative to it; a new
+// maximum m' scales S by f = e^(m - m') and makes A f (A + (m - m') S).
+//
+// The top alternatives come from the same read.  With T threads' maxima so far,
+// the 4th largest of each warp's 32, the least of that over 8 warps, has 32
+// values at least as large: what is not above it cannot be among the top 32.
+// What is goes to a list in shared memory, a few hundred entries a row, from which
+// the best 32 are sorted out at the end (and before the list would overflow, on
+// logits that keep rising).  Entries are 64-bit keys, the value's order above the
+// complement of the index, so that of equals the lowest index is the largest key.
+// Rounds go up in index, so after the first an equal value is never better.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "bsg_internal.h"
 #include "serve.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace bsg {
 namespace {
 
-// One CTA per row; one read for the maximum, one for the sums, and one for
-// each of the top alternatives.
+constexpr int kThreads = 256, kLpWarps = kThreads / 32;
+constexpr int kRound = 16;                          // elements of a thread in a round
+constexpr int kList = kThreads * kRound + 1024;     // entries that fit the list
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The 16-byte vectors that cover a row: vector v holds elements
+// [v kPer - off, (v + 1) kPer - off) of it, off the row's distance from 16 bytes.
 template <typename T>
-__global__ void __launch_bounds__(256)
-    logprobs_kernel(const T *__restrict__ logits, int64_t V, int64_t ldl,
-                    const int64_t *__restrict__ target, int top, float *__restrict__ logprob,
-                    float *__restrict__ entropy, float *__restrict__ lse,
-                    float *__restrict__ top_logprob, int32_t *__restrict__ top_id,
-                    int32_t *__restrict__ dstatus) {
-    __shared__ float red[8], red2[8];
-    __shared__ int redi[8];
-    const int64_t row = blockIdx.x;
-    const T *x = logits + row * ldl;
-    const int t = threadIdx.x, w = t / 32;
-    auto best = [&](float v, int i) {  // the largest value, then the lowest index
-        for (int o = 16; o; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, v, o);
-            const int oi = __shfl_xor_sync(0xffffffffu, i, o);
-            if (ov > v || (ov == v && oi < i)) v = ov, i = oi;
+struct RowVectors {
+    static constexpr int kPer = 16 / sizeof(T);
+    const T *row;
+    int64_t V, count;
+    int off;
+    __device__ RowVectors(const T *r, int64_t n) : row(r), V(n) {
+        off = (int)(reinterpret_cast<uintptr_t>(r) % 16 / sizeof(T));
+        count = (n + off + kPer - 1) / kPer;
+    }
+    // Elements of vector v, -inf outside the row; [j0, j0 + kPer) are their indexes.
+    __device__ __forceinline__ void load(int64_t v, float (&x)[kPer]) const {
+        const int64_t j0 = v * kPer - off;
+        if (j0 >= 0 && j0 + kPer <= V) {
+            uint4 w;
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "l"(row + j0));
+            const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = to_f32(e[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                x[i] = j0 + i >= 0 && j0 + i < V ? to_f32(row[j0 + i]) : -INFINITY;
         }
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Running maximum, S and A, of a thread or of several joined.
+struct Sums {
+    float m = -INFINITY, s = 0.0f, a = 0.0f;
+    // Relative to another maximum, not below this one.
+    __device__ __forceinline__ void raise(float to) {
+        if (m == -INFINITY || to == m) {  // nothing yet (s = a = 0), or nothing to do
+            m = to;
+            return;
+        }
+        const float d = fmaxf(m - to, -1e4f), f = ex2(d * kLog2e);  // e^-1e4 is 0
+        a = f * fmaf(d, s, a);
+        s *= f;
+        m = to;
+    }
+    __device__ __forceinline__ void join(Sums o) {
+        const float to = fmaxf(m, o.m);
+        raise(to);
+        o.raise(to);
+        s += o.s, a += o.a;
+    }
+};
+
+// A value and its index as a key: larger is better.  Values in order as unsigned
+// numbers, -0 as +0; no valid key is 0.
+__device__ __forceinline__ uint64_t key_of(float x, int64_t j) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    const uint32_t v = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return (uint64_t)v << 32 | (uint32_t)~(uint32_t)j;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+    const uint32_t v = (uint32_t)(k >> 32);
+    return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
+}
+__device__ __forceinline__ int32_t key_index(uint64_t k) { return (int32_t)~(uint32_t)k; }
+
+// One step of a bitonic network over a warp, larger keys first where `down`.
+__device__ __forceinline__ uint64_t exchange(uint64_t k, int distance, bool down) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, k, distance);
+    const bool low = (threadIdx.x & distance) == 0;
+    return (k > o) == (low == down) ? k : o;
+}
+__device__ __forceinline__ uint64_t warp_sort(uint64_t k) {  // descending
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d; d /= 2) k = exchange(k, d, size == 32 || (lane & size) == 0);
+    return k;
+}
+// The best 32 of two descending lists, descending.
+__device__ __forceinline__ uint64_t warp_merge(uint64_t k, uint64_t o) {
+    const uint64_t r = __shfl_sync(0xffffffffu, o, 31 - threadIdx.x % 32);
+    k = k > r ? k : r;
+#pragma unroll
+    for (int d = 16; d; d /= 2) k = exchange(k, d, true);
+    return k;
+}
+
+// Sorts the best 32 of list[0..n) to its front, by all threads; unused places 0.
+__device__ void sort_list(uint64_t *list, int n, uint64_t (*lists)[32]) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t best = 0;
+    for (int b = warp * 32; b < n; b += kThreads) {
+        uint64_t k = b + lane < n ? list[b + lane] : 0;
+        if (!__any_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, best, 31))) continue;
+        best = warp_merge(best, warp_sort(k));
+    }
+#pragma unroll
+    for (int half = kLpWarps / 2; half; half /= 2) {
+        if (warp >= half && warp < 2 * half) lists[warp][lane] = best;
         __syncthreads();
-        if (t % 32 == 0) red[w] = v, redi[w] = i;
-        __syncthreads();
-        v = red[0], i = redi[0];
-        for (int k = 1; k < 8; ++k)
-            if (red[k] > v || (red[k] == v && redi[k] < i)) v = red[k], i = redi[k];
-        return make_float2(v, __int_as_float(i));
-    };
-    float m = -INFINITY;
+        if (warp < half) best = warp_merge(best, lists[warp + half][lane]);
+    }
+    if (warp == 0) list[lane] = best;
+    __syncthreads();
+}
+
+struct LogprobsArgs {
+    const int64_t *target;
+    float *logprob, *entropy, *lse, *top_logprob;
+    int32_t *top_id, *dstatus;
+    int64_t V, ldl;
+    int top;
+};
+
+// A cluster of CTAs to a row (or one CTA), each a contiguous share of its vectors.
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4)
+    logprobs_kernel(const T *__restrict__ logits, const __grid_constant__ LogprobsArgs a) {
+    constexpr int kPer = RowVectors<T>::kPer, kVec = kRound / kPer;
+    __shared__ uint64_t list[kTop ? kList : 1];
+    __shared__ uint64_t lists[kTop ? kLpWarps : 1][32];
+    __shared__ float warp_least[2][kLpWarps];
+    __shared__ Sums warp_sums[kLpWarps];
+    __shared__ Sums cta_sums;
+    __shared__ int listed;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int64_t r = blockIdx.x / ranks;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const RowVectors<T> row(logits + r * a.ldl, a.V);
+    const int64_t v0 = row.count * rank / ranks, v1 = row.count * (rank + 1) / ranks;
+    if (tid == 0) listed = 0;
+    if (kTop) __syncthreads();
+
+    Sums sums;
     bool bad = false;
-    for (int64_t j = t; j < V; j += 256) {
-        const float v = to_f32(x[j]);
-        bad |= !(v < INFINITY);
-        m = fmaxf(m, v);
+    float least = -INFINITY;  // what is not above it is not among the top
+    auto push = [&](float (&x)[kVec][kPer], int64_t v, bool first) {
+        bool full = false;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int64_t j = (v + i * kThreads) * kPer - row.off + e;
+                if ((first ? x[i][e] >= least : x[i][e] > least) && j >= 0 && j < a.V && v + i * kThreads < v1) {
+                    const int at = atomicAdd(&listed, 1);
+                    list[at] = key_of(x[i][e], j);
+                    full |= at >= kList - kThreads * kRound - 1;
+                }
+            }
+        return full;
+    };
+    auto load = [&](float (&x)[kVec][kPer], int64_t v) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            if (v + i * kThreads < v1)
+                row.load(v + i * kThreads, x[i]);
+            else
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) x[i][e] = -INFINITY;
+        }
+    };
+    float x[kVec][kPer], next[kVec][kPer];
+    load(next, v0 + tid);
+    int side = 0;
+    for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads, side ^= 1) {
+        const bool first = v - tid == v0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[i][e] = next[i][e];
+        load(next, v + kVec * kThreads);
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                bad |= !(x[i][e] < INFINITY);
+                most = fmaxf(most, x[i][e]);
+            }
+        if (most > sums.m) sums.raise(most);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                // -inf, and -inf less -inf, count as far below: 0 in both sums
+                const float d = fmaxf(x[i][e] - sums.m, -1e4f), p = ex2(d * kLog2e);
+                sums.s += p;
+                sums.a = fmaf(p, d, sums.a);
+            }
+        if (kTop) {
+            bool full = false;
+            if (!first && most > least) full = push(x, v, false);
+            // the 4th largest of the warp's maxima
+            float mine = sums.m, fourth = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float w = mine;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+                const uint32_t has = __ballot_sync(0xffffffffu, mine == w);
+                if (lane == __ffs(has) - 1) mine = -INFINITY;
+                fourth = w;
+            }
+            if (lane == 0) warp_least[side][warp] = fourth;
+            const bool any_full = __syncthreads_or(full);
+            float l = warp_least[side][0];
+#pragma unroll
+            for (int w = 1; w < kLpWarps; ++w) l = fminf(l, warp_least[side][w]);
+            least = fmaxf(least, l);
+            bool again = any_full;
+            if (first) again = __syncthreads_or(push(x, v, true));
+            if (again) {
+                sort_list(list, min(listed, kList), lists);
+                if (tid == 0) listed = min(listed, 32);
+                if (list[31]) least = fmaxf(least, key_value(list[31]));
+                __syncthreads();
+            }
+        }
     }
-    if (bad) set_status(dstatus, BSG_DSTATUS_NONFINITE);
-    m = best(m, 0).x;
-    float s = 0.0f, a = 0.0f;
-    for (int64_t j = t; j < V; j += 256) {
-        const float d = to_f32(x[j]) - m, e = expf(d);
-        s += e;
-        if (e > 0.0f) a = fmaf(e, d, a);
-    }
+    if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+
+    // Join the threads, the warps and the cluster, in that order.
+#pragma unroll
     for (int o = 16; o; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        a += __shfl_xor_sync(0xffffffffu, a, o);
+        Sums other;
+        other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
+        other.s = __shfl_xor_sync(0xffffffffu, sums.s, o);
+        other.a = __shfl_xor_sync(0xffffffffu, sums.a, o);
+        sums.join(other);
     }
+    if (lane == 0) warp_sums[warp] = sums;
     __syncthreads();
-    if (t % 32 == 0) red[w] = s, red2[w] = a;
-    __syncthreads();
-    s = a = 0.0f;
-    for (int k = 0; k < 8; ++k) s += red[k], a += red2[k];
-    const bool none = m == -INFINITY;  // every logit is -inf
-    const float logs = none ? 0.0f : logf(s);
-    if (t == 0) {
-        if (lse) lse[row] = m + logs;
-        if (entropy) entropy[row] = none ? 0.0f : logs - a / s;
-        if (logprob) {
-            const int64_t g = target ? target[row] : -1;
-            if (g >= V) set_status(dstatus, BSG_DSTATUS_RANGE);
-            logprob[row] = g < 0 ? 0.0f
-                                 : g >= V ? NAN : none ? -INFINITY : to_f32(x[g]) - m - logs;
+    if (kTop) sort_list(list, min(listed, kList), lists);
+    Sums all = warp_sums[0];
+#pragma unroll
+    for (int w = 1; w < kLpWarps; ++w) all.join(warp_sums[w]);
+    if (ranks > 1) {
+        if (tid == 0) cta_sums = all;
+        cluster.sync();
+        if (rank == 0 && warp == 0) {
+            all = Sums();
+            uint64_t best = 0;
+            for (int k = 0; k < ranks; ++k) {
+                all.join(*cluster.map_shared_rank(&cta_sums, k));
+                if (kTop) best = warp_merge(best, cluster.map_shared_rank(list, k)[lane]);
+            }
+            if (kTop) list[lane] = best;
         }
+        cluster.sync();  // no CTA leaves while its results are read
+        if (rank > 0) return;
     }
-    float lv = INFINITY;
-    int li = -1;
-    for (int k = 0; k < top; ++k) {
-        float v = -INFINITY;
-        int i = INT32_MAX;
-        for (int64_t j = t; j < V; j += 256) {
-            const float y = to_f32(x[j]);
-            if (y < lv || (y == lv && j > li))
-                if (y > v || i == INT32_MAX) v = y, i = (int)j;
-        }
-        const float2 r = best(v, i);
-        lv = r.x;
-        li = __float_as_int(r.y);
-        if (t == 0) {
-            top_logprob[row * top + k] = none ? -INFINITY : lv - m - logs;
-            top_id[row * top + k] = li;
-        }
+    if (warp > 0) return;
+
+    const bool none = all.m == -INFINITY;  // every logit is -inf
+    const float log_s = none ? 0.0f : logf(all.s);
+    if (lane == 0) {
+        if (a.lse) a.lse[r] = all.m + log_s;
+        if (a.entropy) a.entropy[r] = none ? 0.0f : log_s - all.a / all.s;
+        const int64_t g = a.target ? a.target[r] : -1;
+        if (g >= a.V) set_status(a.dstatus, BSG_DSTATUS_RANGE);
+        if (a.logprob)
+            a.logprob[r] = g < 0        ? 0.0f
+                           : g >= a.V   ? NAN
+                           : none       ? -INFINITY
+                                        : to_f32(row.row[g]) - all.m - log_s;
+    }
+    if (kTop && lane < a.top) {
+        const uint64_t k = list[lane];
+        a.top_logprob[r * a.top + lane] = none ? -INFINITY : key_value(k) - all.m - log_s;
+        a.top_id[r * a.top + lane] = key_index(k);
     }
 }
 
+// ---- gradient: one read and one write of a row's elements -------------------
+constexpr int kGradVec = 4;  // vectors of a thread
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
     logprobs_backward_kernel(const T *logits, int64_t V, int64_t ldl,
                              const int64_t *__restrict__ target, const float *__restrict__ lse,
                              const float *__restrict__ entropy,
                              const float *__restrict__ g_logprob,
                              const float *__restrict__ g_entropy, T *dlogits, int64_t ldd,
-                             int32_t *__restrict__ dstatus) {
-    const int64_t row = blockIdx.x;
-    const T *x = logits + row * ldl;
-    T *dx = dlogits + row * ldd;
-    const int64_t g = target ? target[row] : -1;
-    const float L = lse[row], H = g_entropy ? entropy[row] : 0.0f;
-    const float gl = g_logprob && g >= 0 ? g_logprob[row] : 0.0f;
-    const float gh = g_entropy ? g_entropy[row] : 0.0f;
-    if (g >= V && threadIdx.x == 0) set_status(dstatus, BSG_DSTATUS_RANGE);
+                             int blocks, int32_t *__restrict__ dstatus) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int64_t r = blockIdx.x / blocks;
+    const T *x = logits + r * ldl;
+    T *dx = dlogits + r * ldd;
+    const int64_t t = target ? target[r] : -1;
+    const float L = lse[r], H = g_entropy ? entropy[r] : 0.0f;
+    const float gl = g_logprob && t >= 0 ? g_logprob[r] : 0.0f;
+    const float gh = g_entropy ? g_entropy[r] : 0.0f;
+    const bool bad_target = t >= V;
+    if (bad_target && threadIdx.x == 0) set_status(dstatus, BSG_DSTATUS_RANGE);
+    // vectors by the logits' alignment; the gradient's may be another
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+    const bool same = reinterpret_cast<uintptr_t>(dx) % 16 == reinterpret_cast<uintptr_t>(x) % 16;
+    const int64_t j_first = ((int64_t)(blockIdx.x % blocks) * kGradVec * kThreads + threadIdx.x) * kPer - off;
     bool bad = false;
-    for (int64_t j = threadIdx.x; j < V; j += 256) {
-        const float v = to_f32(x[j]), lp = v - L, p = expf(lp);
+    auto gradient = [&](float v, int64_t j) {
         bad |= !(v < INFINITY);
+        const float lp = v - L, p = ex2(lp * kLog2e);
         float d = p > 0.0f ? -p * fmaf(gh, lp + H, gl) : 0.0f;
-        if (j == g) d += gl;
+        if (j == t) d += gl;
         if (L == -INFINITY) d = 0.0f;
-        if (g >= V) d = NAN;
-        dx[j] = from_f32<T>(d);
+        return bad_target ? NAN : d;
+    };
+    uint4 w[kGradVec];
+#pragma unroll
+    for (int i = 0; i < kGradVec; ++i) {
+        const int64_t j = j_first + (int64_t)i * kThreads * kPer;
+        // not the read-only path: the gradient may take the logits' place
+        if (j >= 0 && j + kPer <= V)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "l"(x + j)
+                         : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < kGradVec; ++i) {
+        const int64_t j = j_first + (int64_t)i * kThreads * kPer;
+        if (j >= 0 && j + kPer <= V) {
+            T *e = reinterpret_cast<T *>(&w[i]);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) e[k] = from_f32<T>(gradient(to_f32(e[k]), j + k));
+            if (same)
+                __stcs(reinterpret_cast<uint4 *>(dx + j), w[i]);
+            else
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) dx[j + k] = e[k];
+        } else {
+            for (int k = 0; k < kPer; ++k)
+                if (j + k >= 0 && j + k < V) dx[j + k] = from_f32<T>(gradient(to_f32(x[j + k]), j + k));
+        }
     }
     if (bad) set_status(dstatus, BSG_DSTATUS_NONFINITE);
+}
+
+template <typename T, bool kTop>
+cudaError_t launch_forward(const T *logits, const LogprobsArgs &a, int64_t M, cudaStream_t st) {
+    auto *kernel = logprobs_kernel<T, kTop>;
+    static bool set[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    // A row to one CTA where there are rows for every SM, else to a cluster, with a
+    // round for each of its CTAs at least.
+    int ranks = 1;
+    while (ranks < 16 && M * ranks < device_sm_count() && a.V > (int64_t)ranks * kThreads * kRound) ranks *= 2;
+    if (M * ranks > INT32_MAX) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(M * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, logits, a);
 }
 
 }  // namespace
@@ -132,13 +418,11 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t M, int64_t V,
                             const int64_t *target, int top, float *logprob, float *entropy,
                             float *lse, float *top_logprob, int32_t *top_id, int32_t *dstatus,
                             cudaStream_t st) {
+    const LogprobsArgs a{target, logprob, entropy, lse, top_logprob, top_id, dstatus, V, ldl, top};
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        logprobs_kernel<T><<<(unsigned)M, 256, 0, st>>>((const T *)logits, V, ldl, target, top,
-                                                        logprob, entropy, lse, top_logprob, top_id,
-                                                        dstatus);
-        count_launches(1);
-        return cudaGetLastError();
+        const T *x = static_cast<const T *>(logits);
+        return top ? launch_forward<T, true>(x, a, M, st) : launch_forward<T, false>(x, a, M, st);
     });
 }
 
@@ -149,9 +433,12 @@ cudaError_t launch_logprobs_backward(const void *logits, int dtype, int64_t M, i
                                      int32_t *dstatus, cudaStream_t st) {
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        logprobs_backward_kernel<T><<<(unsigned)M, 256, 0, st>>>(
-            (const T *)logits, V, ldl, target, lse, entropy, g_logprob, g_entropy, (T *)dlogits,
-            ldd, dstatus);
+        const int64_t per = kGradVec * kThreads * (16 / (int64_t)sizeof(T));
+        const int64_t blocks = (V + 16 / (int64_t)sizeof(T) - 1 + per - 1) / per;  // with a shifted start
+        if (M > INT32_MAX / blocks) return cudaErrorInvalidValue;
+        logprobs_backward_kernel<T><<<(unsigned)(M * blocks), kThreads, 0, st>>>(
+            static_cast<const T *>(logits), V, ldl, target, lse, entropy, g_logprob, g_entropy,
+            static_cast<T *>(dlogits), ldd, (int)blocks, dstatus);
         count_launches(1);
         return cudaGetLastError();
     });
