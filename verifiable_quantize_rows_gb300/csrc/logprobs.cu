@@ -2,7 +2,7 @@
 // alternatives of logits, and their gradient.
 //
 //   lse = m + log S,  S = sum_j e_j,  e_j = exp(x_j - m),  m = max_j x_j;
-//   entropy = log S - (sum_j e_j (x_j - m)) / S;
+//   entropy = log S - A / S,  A = sum_j e_j (x_j - m);
 //   dx_j = g_lp ([j = t] - p_j) - g_H p_j (x_j - lse + H).
 //
 // Forward: one read of the logits, which is what bounds it (HBM).  Each thread
@@ -13,10 +13,11 @@
 // the 4th largest of each warp's 32, the least of that over 8 warps, has 32
 // values at least as large: what is not above it cannot be among the top 32.
 // What is goes to a list in shared memory, a few hundred entries a row, from which
-// the best 32 are sorted out at the end (and before the list would overflow, on
-// logits that keep rising).  Entries are 64-bit keys, the value's order above the
-// complement of the index, so that of equals the lowest index is the largest key.
-// Rounds go up in index, so after the first an equal value is never better.
+// the best 32 are sorted out at the end.  Entries are 64-bit keys, the value's order
+// above the complement of the index, so that of equals the lowest index is the
+// largest key.  Rounds go up in index, so after the first an equal value is never
+// better.  Where the list overflows (logits that keep rising), a second read in
+// steps of one round sorts it whenever it is full.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -71,7 +72,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Running maximum, S and A, of a thread or of several joined.
+// Larger of the two, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Running maximum, S and A / ln 2, of a thread or of several joined.
 struct Sums {
     float m = -INFINITY, s = 0.0f, a = 0.0f;
     // Relative to another maximum, not below this one.
@@ -80,8 +88,8 @@ struct Sums {
             m = to;
             return;
         }
-        const float d = fmaxf(m - to, -1e4f), f = ex2(d * kLog2e);  // e^-1e4 is 0
-        a = f * fmaf(d, s, a);
+        const float y = fmaxf((m - to) * kLog2e, -1e4f), f = ex2(y);  // 2^-1e4 is 0
+        a = f * fmaf(y, s, a);
         s *= f;
         m = to;
     }
@@ -129,6 +137,18 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t k, uint64_t o) {
     return k;
 }
 
+// The best 32 of the warps' descending lists, in warp 0.
+__device__ __forceinline__ uint64_t join_warps(uint64_t best, uint64_t (*lists)[32]) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+    for (int half = kLpWarps / 2; half; half /= 2) {
+        if (warp >= half && warp < 2 * half) lists[warp][lane] = best;
+        __syncthreads();
+        if (warp < half) best = warp_merge(best, lists[warp + half][lane]);
+    }
+    return best;
+}
+
 // Sorts the best 32 of list[0..n) to its front, by all threads; unused places 0.
 __device__ void sort_list(uint64_t *list, int n, uint64_t (*lists)[32]) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -138,12 +158,7 @@ __device__ void sort_list(uint64_t *list, int n, uint64_t (*lists)[32]) {
         if (!__any_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, best, 31))) continue;
         best = warp_merge(best, warp_sort(k));
     }
-#pragma unroll
-    for (int half = kLpWarps / 2; half; half /= 2) {
-        if (warp >= half && warp < 2 * half) lists[warp][lane] = best;
-        __syncthreads();
-        if (warp < half) best = warp_merge(best, lists[warp + half][lane]);
-    }
+    best = join_warps(best, lists);
     if (warp == 0) list[lane] = best;
     __syncthreads();
 }
@@ -163,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     constexpr int kPer = RowVectors<T>::kPer, kVec = kRound / kPer;
     __shared__ uint64_t list[kTop ? kList : 1];
     __shared__ uint64_t lists[kTop ? kLpWarps : 1][32];
-    __shared__ float warp_least[2][kLpWarps];
+    __shared__ float warp_least[kLpWarps];
     __shared__ Sums warp_sums[kLpWarps];
     __shared__ Sums cta_sums;
     __shared__ int listed;
@@ -179,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     Sums sums;
     bool bad = false;
     float least = -INFINITY;  // what is not above it is not among the top
+    // True where the list has less than a round's room left (or none).
     auto push = [&](float (&x)[kVec][kPer], int64_t v, bool first) {
         bool full = false;
 #pragma unroll
@@ -188,11 +204,32 @@ __global__ void __launch_bounds__(kThreads, 4)
                 const int64_t j = (v + i * kThreads) * kPer - row.off + e;
                 if ((first ? x[i][e] >= least : x[i][e] > least) && j >= 0 && j < a.V && v + i * kThreads < v1) {
                     const int at = atomicAdd(&listed, 1);
-                    list[at] = key_of(x[i][e], j);
+                    if (at < kList) list[at] = key_of(x[i][e], j);
                     full |= at >= kList - kThreads * kRound - 1;
                 }
             }
         return full;
+    };
+    // The least that 32 of the values read so far reach: of each warp's maxima the
+    // 4th largest, and of those the smallest.  All threads together.
+    auto find_least = [&]() {
+        float mine = sums.m, fourth = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float w = mine;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+            const uint32_t has = __ballot_sync(0xffffffffu, mine == w);
+            if (lane == __ffs(has) - 1) mine = -INFINITY;
+            fourth = w;
+        }
+        __syncthreads();  // the last one's have been read
+        if (lane == 0) warp_least[warp] = fourth;
+        __syncthreads();
+        float l = warp_least[0];
+#pragma unroll
+        for (int w = 1; w < kLpWarps; ++w) l = fminf(l, warp_least[w]);
+        least = fmaxf(least, l);
     };
     auto load = [&](float (&x)[kVec][kPer], int64_t v) {
 #pragma unroll
@@ -206,9 +243,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     };
     float x[kVec][kPer], next[kVec][kPer];
     load(next, v0 + tid);
-    int side = 0;
-    for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads, side ^= 1) {
-        const bool first = v - tid == v0;
+    int round = 0;
+    for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads, ++round) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
@@ -218,46 +254,40 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                bad |= !(x[i][e] < INFINITY);
-                most = fmaxf(most, x[i][e]);
-            }
+            for (int e = 0; e < kPer; ++e) most = max_nan(most, x[i][e]);
+        bad |= !(most < INFINITY);
         if (most > sums.m) sums.raise(most);
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 // -inf, and -inf less -inf, count as far below: 0 in both sums
-                const float d = fmaxf(x[i][e] - sums.m, -1e4f), p = ex2(d * kLog2e);
+                const float y = fmaxf((x[i][e] - sums.m) * kLog2e, -1e4f), p = ex2(y);
                 sums.s += p;
-                sums.a = fmaf(p, d, sums.a);
+                sums.a = fmaf(p, y, sums.a);
             }
         if (kTop) {
-            bool full = false;
-            if (!first && most > least) full = push(x, v, false);
-            // the 4th largest of the warp's maxima
-            float mine = sums.m, fourth = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float w = mine;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-                const uint32_t has = __ballot_sync(0xffffffffu, mine == w);
-                if (lane == __ffs(has) - 1) mine = -INFINITY;
-                fourth = w;
+            if (round == 0) {
+                find_least();
+                push(x, v, true);
+            } else {
+                if (most > least) push(x, v, false);
+                if ((round & (round + 1)) == 0) find_least();  // after 2, 4, 8 ... rounds
             }
-            if (lane == 0) warp_least[side][warp] = fourth;
-            const bool any_full = __syncthreads_or(full);
-            float l = warp_least[side][0];
-#pragma unroll
-            for (int w = 1; w < kLpWarps; ++w) l = fminf(l, warp_least[side][w]);
-            least = fmaxf(least, l);
-            bool again = any_full;
-            if (first) again = __syncthreads_or(push(x, v, true));
-            if (again) {
-                sort_list(list, min(listed, kList), lists);
-                if (tid == 0) listed = min(listed, 32);
-                if (list[31]) least = fmaxf(least, key_value(list[31]));
+        }
+    }
+    if (kTop && __syncthreads_or(listed > kList)) {
+        // the list has overflowed: again, round by round
+        __syncthreads();
+        if (tid == 0) listed = 0;
+        least = -INFINITY;
+        __syncthreads();
+        for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads) {
+            load(x, v);
+            if (__syncthreads_or(push(x, v, v - tid == v0))) {
+                sort_list(list, listed, lists);
+                if (list[31]) least = key_value(list[31]);
+                if (tid == 0) listed = 32;
                 __syncthreads();
             }
         }
@@ -275,21 +305,31 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     if (lane == 0) warp_sums[warp] = sums;
     __syncthreads();
-    if (kTop) sort_list(list, min(listed, kList), lists);
+    if (kTop) sort_list(list, listed, lists);
     Sums all = warp_sums[0];
 #pragma unroll
     for (int w = 1; w < kLpWarps; ++w) all.join(warp_sums[w]);
     if (ranks > 1) {
         if (tid == 0) cta_sums = all;
         cluster.sync();
-        if (rank == 0 && warp == 0) {
-            all = Sums();
-            uint64_t best = 0;
-            for (int k = 0; k < ranks; ++k) {
-                all.join(*cluster.map_shared_rank(&cta_sums, k));
-                if (kTop) best = warp_merge(best, cluster.map_shared_rank(list, k)[lane]);
+        if (rank == 0) {
+            if (kTop) {  // two CTAs' lists to a warp
+                const int k = 2 * warp;
+                uint64_t best = k < ranks ? cluster.map_shared_rank(list, k)[lane] : 0;
+                const uint64_t more = k + 1 < ranks ? cluster.map_shared_rank(list, k + 1)[lane] : 0;
+                best = join_warps(warp_merge(best, more), lists);
+                if (warp == 0) list[lane] = best;  // warp 0 has read its own
             }
-            if (kTop) list[lane] = best;
+            all = Sums();
+            if (lane < ranks) all = *cluster.map_shared_rank(&cta_sums, lane);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                Sums other;
+                other.m = __shfl_xor_sync(0xffffffffu, all.m, o);
+                other.s = __shfl_xor_sync(0xffffffffu, all.s, o);
+                other.a = __shfl_xor_sync(0xffffffffu, all.a, o);
+                all.join(other);
+            }
         }
         cluster.sync();  // no CTA leaves while its results are read
         if (rank > 0) return;
@@ -300,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const float log_s = none ? 0.0f : logf(all.s);
     if (lane == 0) {
         if (a.lse) a.lse[r] = all.m + log_s;
-        if (a.entropy) a.entropy[r] = none ? 0.0f : log_s - all.a / all.s;
+        if (a.entropy) a.entropy[r] = none ? 0.0f : log_s - all.a * 0.69314718055994531f / all.s;
         const int64_t g = a.target ? a.target[r] : -1;
         if (g >= a.V) set_status(a.dstatus, BSG_DSTATUS_RANGE);
         if (a.logprob)
