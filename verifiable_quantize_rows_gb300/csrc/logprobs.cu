@@ -9,9 +9,9 @@
 // keeps a running maximum with S and A = sum e (x - m) relative to it; a new
 // maximum m' scales S by f = e^(m - m') and makes A f (A + (m - m') S).
 //
-// The top alternatives come from the same read.  With T threads' maxima so far,
-// the 4th largest of each warp's 32, the least of that over 8 warps, has 32
-// values at least as large: what is not above it cannot be among the top 32.
+// The top alternatives come from the same read.  Of the threads' maxima so far, the
+// n-th largest of each warp's 32 and of those the least over 8 warps has 8 n
+// values at least as large: what is not above it cannot be among the top 8 n.
 // What is goes to a list in shared memory, a few hundred entries a row, from which
 // the best 32 are sorted out at the end.  Entries are 64-bit keys, the value's order
 // above the complement of the index, so that of equals the lowest index is the
@@ -47,17 +47,20 @@ struct RowVectors {
         off = (int)(reinterpret_cast<uintptr_t>(r) % 16 / sizeof(T));
         count = (n + off + kPer - 1) / kPer;
     }
-    // Elements of vector v, -inf outside the row; [j0, j0 + kPer) are their indexes.
+    static __device__ __forceinline__ void load_whole(const T *at, float (&x)[kPer]) {
+        uint4 w;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "l"(at));
+        const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = to_f32(e[i]);
+    }
+    // Elements of vector v, -inf outside the row.
     __device__ __forceinline__ void load(int64_t v, float (&x)[kPer]) const {
         const int64_t j0 = v * kPer - off;
         if (j0 >= 0 && j0 + kPer <= V) {
-            uint4 w;
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "l"(row + j0));
-            const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = to_f32(e[i]);
+            load_whole(row + j0, x);
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
@@ -194,44 +197,59 @@ __global__ void __launch_bounds__(kThreads, 4)
     Sums sums;
     bool bad = false;
     float least = -INFINITY;  // what is not above it is not among the top
-    // True where the list has less than a round's room left (or none).
-    auto push = [&](float (&x)[kVec][kPer], int64_t v, bool first) {
+    // Lists what is not `<= above` (NaN: everything).  True where the list has less
+    // than a round's room left, or none.
+    auto push = [&](float (&x)[kVec][kPer], int64_t v, float above) {
         bool full = false;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
+        for (int i = 0; i < kVec; ++i) {
+            float most = x[i][0];
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int64_t j = (v + i * kThreads) * kPer - row.off + e;
-                if ((first ? x[i][e] >= least : x[i][e] > least) && j >= 0 && j < a.V && v + i * kThreads < v1) {
+            for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[i][e]);
+            if (most <= above) continue;
+            const int64_t j0 = (v + i * kThreads) * kPer - row.off;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (!(x[i][e] <= above) && j0 + e >= 0 && j0 + e < a.V && v + i * kThreads < v1) {
                     const int at = atomicAdd(&listed, 1);
-                    if (at < kList) list[at] = key_of(x[i][e], j);
+                    if (at < kList) list[at] = key_of(x[i][e], j0 + e);
                     full |= at >= kList - kThreads * kRound - 1;
                 }
-            }
+        }
         return full;
     };
-    // The least that 32 of the values read so far reach: of each warp's maxima the
-    // 4th largest, and of those the smallest.  All threads together.
+    // The least that `top` of the values read so far reach: of each warp's maxima the
+    // n-th largest, 8 n >= top, and of those the smallest.  All threads together.
     auto find_least = [&]() {
-        float mine = sums.m, fourth = -INFINITY;
+        float mine = sums.m, nth = -INFINITY;
+        for (int k = 0; k < a.top; k += kLpWarps) {
+            nth = mine;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float w = mine;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
-            const uint32_t has = __ballot_sync(0xffffffffu, mine == w);
+            for (int o = 16; o; o >>= 1) nth = fmaxf(nth, __shfl_xor_sync(0xffffffffu, nth, o));
+            const uint32_t has = __ballot_sync(0xffffffffu, mine == nth);
             if (lane == __ffs(has) - 1) mine = -INFINITY;
-            fourth = w;
         }
         __syncthreads();  // the last one's have been read
-        if (lane == 0) warp_least[warp] = fourth;
+        if (lane == 0) warp_least[warp] = nth;
         __syncthreads();
         float l = warp_least[0];
 #pragma unroll
         for (int w = 1; w < kLpWarps; ++w) l = fminf(l, warp_least[w]);
         least = fmaxf(least, l);
     };
+    // Just below x, so that x itself is above it.
+    auto below = [](float x) {
+        const uint32_t b = __float_as_uint(x + 0.0f);
+        return x == -INFINITY ? NAN : b == 0 ? -1.4e-45f : __uint_as_float(b & 0x80000000u ? b + 1 : b - 1);
+    };
     auto load = [&](float (&x)[kVec][kPer], int64_t v) {
+        const int64_t base = v - tid, j0 = base * kPer - row.off;  // the round's, of all threads
+        if (j0 >= 0 && j0 + kThreads * kRound <= a.V && base + kVec * kThreads <= v1) {
+            const T *at = row.row + j0 + tid * kPer;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) RowVectors<T>::load_whole(at + i * kThreads * kPer, x[i]);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             if (v + i * kThreads < v1)
@@ -267,13 +285,11 @@ __global__ void __launch_bounds__(kThreads, 4)
                 sums.a = fmaf(p, y, sums.a);
             }
         if (kTop) {
-            if (round == 0) {
-                find_least();
-                push(x, v, true);
-            } else {
-                if (most > least) push(x, v, false);
-                if ((round & (round + 1)) == 0) find_least();  // after 2, 4, 8 ... rounds
-            }
+            // after 1, 2, 4, 8 ... rounds; what equals the least of this round counts
+            const bool due = (round & (round + 1)) == 0;
+            if (due) find_least();
+            const float above = due ? below(least) : least;
+            if (!(most <= above)) push(x, v, above);
         }
     }
     if (kTop && __syncthreads_or(listed > kList)) {
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         __syncthreads();
         for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads) {
             load(x, v);
-            if (__syncthreads_or(push(x, v, v - tid == v0))) {
+            if (__syncthreads_or(push(x, v, v - tid == v0 ? NAN : least))) {
                 sort_list(list, listed, lists);
                 if (list[31]) least = key_value(list[31]);
                 if (tid == 0) listed = 32;
