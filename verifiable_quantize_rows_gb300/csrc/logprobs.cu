@@ -10,8 +10,8 @@
 // maximum m' scales S by f = e^(m - m') and makes A f (A + (m - m') S).
 //
 // The top alternatives come from the same read.  Of the threads' maxima so far, the
-// n-th largest of each warp's 32 and of those the least over 8 warps has 8 n
-// values at least as large: what is not above it cannot be among the top 8 n.
+// n-th largest of each warp's 32 and of those the least over W warps has W n
+// values at least as large: what is not above it cannot be among the top W n.
 // What is goes to a list in shared memory, a few hundred entries a row, from which
 // the best 32 are sorted out at the end.  Entries are 64-bit keys, the value's order
 // above the complement of the index, so that of equals the lowest index is the
@@ -30,9 +30,11 @@ namespace cg = cooperative_groups;
 namespace bsg {
 namespace {
 
-constexpr int kThreads = 256, kLpWarps = kThreads / 32;
-constexpr int kRound = 16;                          // elements of a thread in a round
-constexpr int kList = kThreads * kRound + 1024;     // entries that fit the list
+constexpr int kRound = 16;        // elements of a thread in a round
+constexpr int kGradThreads = 256;
+// Entries that fit the list of a CTA: a round's, and some.
+__host__ __device__ constexpr int list_size(int threads) { return threads * kRound + 512; }
+constexpr int kMaxRanks = 16;     // CTAs of a row
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The 16-byte vectors that cover a row: vector v holds elements
@@ -75,10 +77,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Larger of the two, NaN where one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// Largest of the three, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
@@ -141,10 +143,11 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t k, uint64_t o) {
 }
 
 // The best 32 of the warps' descending lists, in warp 0.
+template <int kWarps>
 __device__ __forceinline__ uint64_t join_warps(uint64_t best, uint64_t (*lists)[32]) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-    for (int half = kLpWarps / 2; half; half /= 2) {
+    for (int half = kWarps / 2; half; half /= 2) {
         if (warp >= half && warp < 2 * half) lists[warp][lane] = best;
         __syncthreads();
         if (warp < half) best = warp_merge(best, lists[warp + half][lane]);
@@ -153,15 +156,16 @@ __device__ __forceinline__ uint64_t join_warps(uint64_t best, uint64_t (*lists)[
 }
 
 // Sorts the best 32 of list[0..n) to its front, by all threads; unused places 0.
+template <int kWarps>
 __device__ void sort_list(uint64_t *list, int n, uint64_t (*lists)[32]) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint64_t best = 0;
-    for (int b = warp * 32; b < n; b += kThreads) {
+    for (int b = warp * 32; b < n; b += kWarps * 32) {
         uint64_t k = b + lane < n ? list[b + lane] : 0;
         if (!__any_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, best, 31))) continue;
         best = warp_merge(best, warp_sort(k));
     }
-    best = join_warps(best, lists);
+    best = join_warps<kWarps>(best, lists);
     if (warp == 0) list[lane] = best;
     __syncthreads();
 }
@@ -175,10 +179,11 @@ struct LogprobsArgs {
 };
 
 // A cluster of CTAs to a row (or one CTA), each a contiguous share of its vectors.
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4)
+template <typename T, bool kTop, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     logprobs_kernel(const T *__restrict__ logits, const __grid_constant__ LogprobsArgs a) {
     constexpr int kPer = RowVectors<T>::kPer, kVec = kRound / kPer;
+    constexpr int kLpWarps = kThreads / 32, kList = list_size(kThreads);
     __shared__ uint64_t list[kTop ? kList : 1];
     __shared__ uint64_t lists[kTop ? kLpWarps : 1][32];
     __shared__ float warp_least[kLpWarps];
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         return full;
     };
     // The least that `top` of the values read so far reach: of each warp's maxima the
-    // n-th largest, 8 n >= top, and of those the smallest.  All threads together.
+    // n-th largest, n kLpWarps >= top, and of those the smallest.  All threads together.
     auto find_least = [&]() {
         float mine = sums.m, nth = -INFINITY;
         for (int k = 0; k < a.top; k += kLpWarps) {
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) most = max_nan(most, x[i][e]);
+            for (int e = 0; e < kPer; e += 2) most = max_nan(most, x[i][e], x[i][e + 1]);
         bad |= !(most < INFINITY);
         if (most > sums.m) sums.raise(most);
 #pragma unroll
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int64_t v = v0 + tid; v - tid < v1; v += kVec * kThreads) {
             load(x, v);
             if (__syncthreads_or(push(x, v, v - tid == v0 ? NAN : least))) {
-                sort_list(list, listed, lists);
+                sort_list<kLpWarps>(list, listed, lists);
                 if (list[31]) least = key_value(list[31]);
                 if (tid == 0) listed = 32;
                 __syncthreads();
@@ -311,41 +316,39 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
 
     // Join the threads, the warps and the cluster, in that order.
+    auto join_lanes = [](Sums x) {  // of all lanes, in each
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        Sums other;
-        other.m = __shfl_xor_sync(0xffffffffu, sums.m, o);
-        other.s = __shfl_xor_sync(0xffffffffu, sums.s, o);
-        other.a = __shfl_xor_sync(0xffffffffu, sums.a, o);
-        sums.join(other);
-    }
+        for (int o = 16; o; o /= 2) {
+            Sums other;
+            other.m = __shfl_xor_sync(0xffffffffu, x.m, o);
+            other.s = __shfl_xor_sync(0xffffffffu, x.s, o);
+            other.a = __shfl_xor_sync(0xffffffffu, x.a, o);
+            x.join(other);
+        }
+        return x;
+    };
+    sums = join_lanes(sums);
     if (lane == 0) warp_sums[warp] = sums;
     __syncthreads();
-    if (kTop) sort_list(list, listed, lists);
-    Sums all = warp_sums[0];
-#pragma unroll
-    for (int w = 1; w < kLpWarps; ++w) all.join(warp_sums[w]);
+    if (kTop) sort_list<kLpWarps>(list, listed, lists);
+    Sums all;
+    if (warp == 0) all = join_lanes(lane < kLpWarps ? warp_sums[lane] : Sums());
     if (ranks > 1) {
         if (tid == 0) cta_sums = all;
         cluster.sync();
         if (rank == 0) {
-            if (kTop) {  // two CTAs' lists to a warp
-                const int k = 2 * warp;
-                uint64_t best = k < ranks ? cluster.map_shared_rank(list, k)[lane] : 0;
-                const uint64_t more = k + 1 < ranks ? cluster.map_shared_rank(list, k + 1)[lane] : 0;
-                best = join_warps(warp_merge(best, more), lists);
+            if (kTop) {  // a few CTAs' lists to a warp, all on their way at once
+                constexpr int kEach = kMaxRanks / kLpWarps;
+                uint64_t best = 0, more[kEach];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    more[i] = warp + i * kLpWarps < ranks ? cluster.map_shared_rank(list, warp + i * kLpWarps)[lane] : 0;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) best = warp_merge(best, more[i]);
+                best = join_warps<kLpWarps>(best, lists);
                 if (warp == 0) list[lane] = best;  // warp 0 has read its own
             }
-            all = Sums();
-            if (lane < ranks) all = *cluster.map_shared_rank(&cta_sums, lane);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                Sums other;
-                other.m = __shfl_xor_sync(0xffffffffu, all.m, o);
-                other.s = __shfl_xor_sync(0xffffffffu, all.s, o);
-                other.a = __shfl_xor_sync(0xffffffffu, all.a, o);
-                all.join(other);
-            }
+            all = join_lanes(lane < ranks ? *cluster.map_shared_rank(&cta_sums, lane) : Sums());
         }
         cluster.sync();  // no CTA leaves while its results are read
         if (rank > 0) return;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 constexpr int kGradVec = 4;  // vectors of a thread
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kGradThreads)
     logprobs_backward_kernel(const T *logits, int64_t V, int64_t ldl,
                              const int64_t *__restrict__ target, const float *__restrict__ lse,
                              const float *__restrict__ entropy,
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kThreads)
     // vectors by the logits' alignment; the gradient's may be another
     const int off = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
     const bool same = reinterpret_cast<uintptr_t>(dx) % 16 == reinterpret_cast<uintptr_t>(x) % 16;
-    const int64_t j_first = ((int64_t)(blockIdx.x % blocks) * kGradVec * kThreads + threadIdx.x) * kPer - off;
+    const int64_t j_first = ((int64_t)(blockIdx.x % blocks) * kGradVec * kGradThreads + threadIdx.x) * kPer - off;
     bool bad = false;
     auto gradient = [&](float v, int64_t j) {
         bad |= !(v < INFINITY);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kThreads)
     uint4 w[kGradVec];
 #pragma unroll
     for (int i = 0; i < kGradVec; ++i) {
-        const int64_t j = j_first + (int64_t)i * kThreads * kPer;
+        const int64_t j = j_first + (int64_t)i * kGradThreads * kPer;
         // not the read-only path: the gradient may take the logits' place
         if (j >= 0 && j + kPer <= V)
             asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int i = 0; i < kGradVec; ++i) {
-        const int64_t j = j_first + (int64_t)i * kThreads * kPer;
+        const int64_t j = j_first + (int64_t)i * kGradThreads * kPer;
         if (j >= 0 && j + kPer <= V) {
             T *e = reinterpret_cast<T *>(&w[i]);
 #pragma unroll
@@ -437,9 +440,9 @@ __global__ void __launch_bounds__(kThreads)
     if (bad) set_status(dstatus, BSG_DSTATUS_NONFINITE);
 }
 
-template <typename T, bool kTop>
-cudaError_t launch_forward(const T *logits, const LogprobsArgs &a, int64_t M, cudaStream_t st) {
-    auto *kernel = logprobs_kernel<T, kTop>;
+template <typename T, bool kTop, int kThreads>
+cudaError_t launch_forward(const T *logits, const LogprobsArgs &a, int64_t M, int ranks, cudaStream_t st) {
+    auto *kernel = logprobs_kernel<T, kTop, kThreads>;
     static bool set[64] = {false};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -449,10 +452,6 @@ cudaError_t launch_forward(const T *logits, const LogprobsArgs &a, int64_t M, cu
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
-    // A row to one CTA where there are rows for every SM, else to a cluster, with a
-    // round for each of its CTAs at least.
-    int ranks = 1;
-    while (ranks < 16 && M * ranks < device_sm_count() && a.V > (int64_t)ranks * kThreads * kRound) ranks *= 2;
     if (M * ranks > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(M * ranks));
@@ -468,6 +467,17 @@ cudaError_t launch_forward(const T *logits, const LogprobsArgs &a, int64_t M, cu
     return cudaLaunchKernelEx(&cfg, kernel, logits, a);
 }
 
+// A row to one CTA of 128 threads where there are rows for every SM (256: 349 against
+// 297 us at 8192 x 50304, since a row's sorting and joining are per warp), else
+// to a cluster of 256-thread ones, with a round for each of them at least.
+template <typename T, bool kTop>
+cudaError_t launch_rows(const T *logits, const LogprobsArgs &a, int64_t M, cudaStream_t st) {
+    int ranks = 1;
+    while (ranks < kMaxRanks && M * ranks < device_sm_count() && a.V > (int64_t)ranks * 256 * kRound) ranks *= 2;
+    return ranks == 1 && M >= device_sm_count() ? launch_forward<T, kTop, 128>(logits, a, M, 1, st)
+                                                : launch_forward<T, kTop, 256>(logits, a, M, ranks, st);
+}
+
 }  // namespace
 
 cudaError_t launch_logprobs(const void *logits, int dtype, int64_t M, int64_t V, int64_t ldl,
@@ -478,7 +488,7 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t M, int64_t V,
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const T *x = static_cast<const T *>(logits);
-        return top ? launch_forward<T, true>(x, a, M, st) : launch_forward<T, false>(x, a, M, st);
+        return top ? launch_rows<T, true>(x, a, M, st) : launch_rows<T, false>(x, a, M, st);
     });
 }
 
@@ -489,10 +499,10 @@ cudaError_t launch_logprobs_backward(const void *logits, int dtype, int64_t M, i
                                      int32_t *dstatus, cudaStream_t st) {
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        const int64_t per = kGradVec * kThreads * (16 / (int64_t)sizeof(T));
+        const int64_t per = kGradVec * kGradThreads * (16 / (int64_t)sizeof(T));
         const int64_t blocks = (V + 16 / (int64_t)sizeof(T) - 1 + per - 1) / per;  // with a shifted start
         if (M > INT32_MAX / blocks) return cudaErrorInvalidValue;
-        logprobs_backward_kernel<T><<<(unsigned)(M * blocks), kThreads, 0, st>>>(
+        logprobs_backward_kernel<T><<<(unsigned)(M * blocks), kGradThreads, 0, st>>>(
             static_cast<const T *>(logits), V, ldl, target, lse, entropy, g_logprob, g_entropy,
             static_cast<T *>(dlogits), ldd, (int)blocks, dstatus);
         count_launches(1);
