@@ -7,6 +7,7 @@
 // place of a row; the scale is one f32 product with f32(1/127).
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "bsg_internal.h"
 #include "bsg_ptx.cuh"
@@ -19,6 +20,7 @@ template <int N>
 __device__ __forceinline__ float block_max(float x, float *red) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (N == 32) return x;
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
     __syncthreads();
     x = red[0];
@@ -41,62 +43,174 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
     return x;
 }
 
-// One CTA per touched page of a sequence, head, and side (keys or values).
+// ---- append -----------------------------------------------------------------
+//
+// One CTA per touched page of a sequence, some of the heads, and side (keys or
+// values); a warp where the new tokens are few.  A head's tokens are on their way
+// while the one before it is stored.  A thread takes 8 values at a time and keeps kKept
+// such pieces in registers between the maximum and the codes, so that new tokens
+// are read once (up to 64 x 128 values a page; larger ones are read again, from
+// L2), and sends for them before it knows where they go.  HBM bounds prompts, a
+// launch's latency single tokens.
+
+// 8 values as they are stored.
 template <typename T>
-__global__ void __launch_bounds__(128)
-    kv8_append_kernel(bsg_kv8_cache c, const int32_t *__restrict__ table, int64_t table_ld,
-                      const int32_t *__restrict__ starts, const int32_t *__restrict__ counts,
-                      bsg_tokens tk, bsg_tokens tv, int blocks, int tokens,
-                      int32_t *__restrict__ dstatus) {
-    __shared__ float red[4];
-    const int b = blockIdx.x / blocks, h = blockIdx.y, t = threadIdx.x;
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p, bool aligned) {
+        if (aligned) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        } else {
+            T e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = p[i];
+            memcpy(w, e, sizeof(w));
+        }
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        T e[8];
+        memcpy(e, w, sizeof(w));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+    }
+    // Raises `top`, the largest |x| so far as bits (of 16-bit types, of the values
+    // in each half): magnitudes are in order as whole numbers, Inf and NaN above all.
+    __device__ __forceinline__ void raise(uint32_t &top) const {
+        const uint32_t *b = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i)
+            top = sizeof(T) == 2 ? __vmaxu2(top, b[i] & 0x7fff7fffu) : max(top, b[i] & 0x7fffffffu);
+    }
+    static __device__ __forceinline__ float absmax(uint32_t top) {
+        if (sizeof(T) == 4) return __uint_as_float(top);
+        const unsigned short m = (unsigned short)max(top & 0xffffu, top >> 16);
+        T e;
+        memcpy(&e, &m, 2);
+        return to_f32(e);
+    }
+};
+
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __byte_perm(unit_code(x[4 * i], inv), unit_code(x[4 * i + 1], inv), 0x0040);
+        const uint32_t hi = __byte_perm(unit_code(x[4 * i + 2], inv), unit_code(x[4 * i + 3], inv), 0x0040);
+        w[i] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 32 ? 1 : sizeof(T) == 2 ? 4 : 3)
+    kv8_append_kernel(const __grid_constant__ bsg_kv8_cache c, const int32_t *__restrict__ table,
+                      int64_t table_ld, const int32_t *__restrict__ starts,
+                      const int32_t *__restrict__ counts, const __grid_constant__ bsg_tokens tk,
+                      const __grid_constant__ bsg_tokens tv, int blocks, int tokens, int aligned,
+                      int heads, int32_t *__restrict__ dstatus) {
+    constexpr int kKept = kThreads == 32 ? 4 : 8;
+    __shared__ float red[kThreads / 32];
+    const int b = blockIdx.x / blocks, t = threadIdx.x;
+    const int h0 = blockIdx.y * heads, h1 = min(c.heads, h0 + heads);
     const int start = starts[b], count = counts ? counts[b] : tokens;
     if (start < 0 || count < 0 || count > tokens) {
         if (t == 0) set_status(dstatus, BSG_DSTATUS_RANGE);
         return;
     }
-    const int P = c.page_tokens, D = c.dim;
+    const int P = c.page_tokens, D = c.dim, per = D / 8;  // pieces of a token
     const int64_t end = (int64_t)start + count;
     const int64_t j = start / P + blockIdx.x % blocks;  // the sequence's page
     if (j * P >= end) return;
+    const int lo = (int)(start > j * P ? start - j * P : 0);  // new tokens: [lo, hi)
+    const int hi = (int)(end < (j + 1) * P ? end - j * P : P);
+    const bsg_tokens &tok = blockIdx.z ? tv : tk;
+    const T *x = (const T *)tok.data + b * tok.stride_batch + (j * P - start) * tok.stride_token;
+    const bool vec = aligned >> blockIdx.z & 1;
+    // The thread's pieces: e0, e0 + kThreads ... (which is step_tokens tokens and
+    // step_pieces pieces on).
+    const int e0 = lo * per + t, e1 = hi * per;
+    const int step_tokens = kThreads / per, step_pieces = kThreads % per;
+    const int64_t step = step_tokens * tok.stride_token;
+    auto each = [&](int h, int skip, auto &&f) {  // f(piece, its address), after the first `skip`
+        int e = e0 + skip * kThreads, p = e % per;
+        const T *at = x + h * tok.stride_head + (e / per) * tok.stride_token + p * 8;
+        for (; e < e1; e += kThreads) {
+            f(e, at);
+            at += step + step_pieces * 8;
+            if ((p += step_pieces) >= per) p -= per, at += tok.stride_token - per * 8;
+        }
+    };
+    Raw8<T> kept[kKept], next[kKept];
+    auto load = [&](int h) {
+        int p = e0 % per;
+        const T *at = x + h * tok.stride_head + (e0 / per) * tok.stride_token + p * 8;
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) {
+            if (e0 + i * kThreads < e1) next[i].load(at, vec);
+            at += step + step_pieces * 8;
+            if ((p += step_pieces) >= per) p -= per, at += tok.stride_token - per * 8;
+        }
+    };
+    load(h0);
+
     int page = -1;
     if (j < table_ld) page = table[b * table_ld + j];
     if (page < 0 || page >= c.pages) {
         if (t == 0) set_status(dstatus, BSG_DSTATUS_RANGE);
         return;
     }
-    const bsg_tokens &tok = blockIdx.z ? tv : tk;
-    const int64_t ph = (int64_t)page * c.heads + h;
-    int8_t *codes = (blockIdx.z ? c.v : c.k) + ph * P * D;
-    float *scale = (blockIdx.z ? c.v_scale : c.k_scale) + ph;
-    const int lo = (int)(start > j * P ? start - j * P : 0);              // new tokens: [lo, hi)
-    const int hi = (int)(end < (j + 1) * P ? end - j * P : P);
-    const T *x = (const T *)tok.data + b * tok.stride_batch + h * tok.stride_head +
-                 (j * P - start) * tok.stride_token;
-    float m = 0.0f;
-    bool bad = false;
-    for (int i = lo * D + t; i < hi * D; i += 128) {
-        const float v = to_f32(x[(i / D) * tok.stride_token + i % D]);
-        bad |= !isfinite(v);
-        m = fmaxf(m, fabsf(v));
-    }
-    if (bad) set_status(dstatus, BSG_DSTATUS_NONFINITE);
-    m = block_max<128>(m, red);
-    float s = kv8_scale(m);
-    if (lo > 0) {
-        const float old = *scale;
+    for (int h = h0; h < h1; ++h) {
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) kept[i] = next[i];
+        if (h + 1 < h1) load(h + 1);
+        const int64_t ph = (int64_t)page * c.heads + h;
+        uint2 *codes = reinterpret_cast<uint2 *>((blockIdx.z ? c.v : c.k) + ph * P * D);
+        float *scale = (blockIdx.z ? c.v_scale : c.k_scale) + ph;
+        const float old = lo > 0 ? *scale : 0.0f;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            if (e0 + i * kThreads < e1) kept[i].raise(top);
+        each(h, kKept, [&](int, const T *at) {
+            Raw8<T> raw;
+            raw.load(at, vec);
+            raw.raise(top);
+        });
+        const float most = Raw8<T>::absmax(top);
+        if (!(most < INFINITY)) set_status(dstatus, BSG_DSTATUS_NONFINITE);
+        float s = kv8_scale(block_max<kThreads>(most, red));
+        __syncwarp();  // all have read the old scale
         if (old < s) {
-            const float r = __fdiv_rn(old, s);
-            for (int i = t; i < lo * D; i += 128) codes[i] = (int8_t)unit_code(codes[i], r);
+            if (lo > 0) {
+                const float r = __fdiv_rn(old, s);
+                for (int e = t; e < lo * per; e += kThreads) {
+                    const uint2 w = codes[e];
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)((k < 4 ? w.x : w.y) >> (k % 4 * 8));
+                    codes[e] = codes8(v, r);
+                }
+            }
+            if (t == 0) *scale = s;
         } else {
             s = old;
         }
+        const float inv = __fdiv_rn(1.0f, s);
+        auto store = [&](const Raw8<T> &raw, int e) {
+            float v[8];
+            raw.values(v);
+            codes[e] = codes8(v, inv);
+        };
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            if (e0 + i * kThreads < e1) store(kept[i], e0 + i * kThreads);
+        each(h, kKept, [&](int e, const T *at) {
+            Raw8<T> raw;
+            raw.load(at, vec);
+            store(raw, e);
+        });
     }
-    const float inv = __fdiv_rn(1.0f, s);
-    for (int i = lo * D + t; i < hi * D; i += 128)
-        codes[i] = (int8_t)unit_code(to_f32(x[(i / D) * tok.stride_token + i % D]), inv);
-    __syncthreads();  // every thread has read the old scale
-    if (t == 0) *scale = s;
 }
 
 // ---- attention ----------------------------------------------------------------
@@ -764,9 +878,26 @@ cudaError_t launch_kv8_append(const bsg_kv8_cache &c, const int32_t *table, int6
     if (B * blocks > INT32_MAX) return cudaErrorInvalidValue;
     return with_dtype(dtype, [&](auto t) {
         using E = decltype(t);
-        const dim3 grid((unsigned)(B * blocks), (unsigned)c.heads, 2);
-        kv8_append_kernel<E><<<grid, 128, 0, st>>>(c, table, table_ld, starts, counts, k, v,
-                                                   (int)blocks, (int)T, dstatus);
+        auto on16 = [](const bsg_tokens &x) {
+            return (reinterpret_cast<uintptr_t>(x.data) | (uintptr_t)(x.stride_batch * (int64_t)sizeof(E)) |
+                    (uintptr_t)(x.stride_token * (int64_t)sizeof(E)) |
+                    (uintptr_t)(x.stride_head * (int64_t)sizeof(E))) % 16 == 0;
+        };
+        const int aligned = (int)on16(k) | (int)on16(v) << 1;
+        // few tokens: a warp to a head; prompts: as many heads as leave four CTAs for
+        // each of four places on an SM
+        const bool few = T * c.dim <= 1024;
+        int64_t heads = few ? 1 : 2 * B * blocks * c.heads / (16 * (int64_t)device_sm_count());
+        heads = heads < 1 ? 1 : heads > c.heads ? c.heads : heads;
+        const int64_t groups = (c.heads + heads - 1) / heads;
+        heads = (c.heads + groups - 1) / groups;  // alike
+        const dim3 grid((unsigned)(B * blocks), (unsigned)groups, 2);
+        if (few)
+            kv8_append_kernel<E, 32><<<grid, 32, 0, st>>>(c, table, table_ld, starts, counts, k, v, (int)blocks,
+                                                          (int)T, aligned, 1, dstatus);
+        else
+            kv8_append_kernel<E, 128><<<grid, 128, 0, st>>>(c, table, table_ld, starts, counts, k, v, (int)blocks,
+                                                            (int)T, aligned, (int)heads, dstatus);
         count_launches(1);
         return cudaGetLastError();
     });
