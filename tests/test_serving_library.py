@@ -1,7 +1,5 @@
 """The serving calls without a GPU: exported, and every bad argument refused
 before anything touches CUDA; the binding refuses what is no CUDA tensor."""
-import ctypes
-
 import pytest
 import torch
 
@@ -54,7 +52,7 @@ def test_wgroups_matvec(lib):
 
 def cache(**kw):
     c = dict(k=D, v=D, k_scale=D, v_scale=D, pages=10, heads=2, page_tokens=16, dim=64)
-    return ctypes.byref(serving._CacheStruct(*dict(c, **kw).values()))
+    return serving._CACHE.pack(*(0 if x is None else x for x in dict(c, **kw).values()))
 
 
 BAD_CACHES = [dict(k=None), dict(v=None), dict(k=D + 8), dict(v=D + 1), dict(k_scale=None), dict(v_scale=D + 2),
@@ -63,7 +61,7 @@ BAD_CACHES = [dict(k=None), dict(v=None), dict(k=D + 8), dict(v=D + 1), dict(k_s
 
 
 def tokens(data=D):
-    return ctypes.byref(serving._TokensStruct(data, 128, 128, 64))
+    return serving._TOKENS.pack(data or 0, 128, 128, 64)
 
 
 def test_kv8_append(lib):

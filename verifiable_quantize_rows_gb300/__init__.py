@@ -54,6 +54,7 @@ _lock = threading.Lock()
 _lib = None
 
 _i64, _vp, _sz, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_cp = ctypes.c_char_p  # a C struct, packed into bytes
 
 
 class GemmItem(ctypes.Structure):
@@ -123,9 +124,9 @@ def _declare(lib):
         "bsg_wgroups_matvec": ([_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64,
                                 _i32, _vp, _i64, _vp, _sz, _vp, _vp], _i32),
         "bsg_wgroups_matvec_workspace_size": ([_i64, _i64, _i64], _sz),
-        "bsg_kv8_append": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp], _i32),
-        "bsg_kv8_attend_workspace_size": ([_vp, _i64, _i64, _i64, _i32], _sz),
-        "bsg_kv8_attend": ([_vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i32, ctypes.c_float,
+        "bsg_kv8_append": ([_cp, _vp, _i64, _vp, _vp, _cp, _cp, _i32, _i64, _i64, _vp, _vp], _i32),
+        "bsg_kv8_attend_workspace_size": ([_cp, _i64, _i64, _i64, _i32], _sz),
+        "bsg_kv8_attend": ([_cp, _vp, _i64, _vp, _cp, _cp, _i32, _i64, _i64, _i32, ctypes.c_float,
                             _vp, _vp, _sz, _vp, _vp], _i32),
         "bsg_logprobs": ([_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                           _vp], _i32),

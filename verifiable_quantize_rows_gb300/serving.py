@@ -12,7 +12,8 @@ CPU fallback and no autograd: gradients have calls of their own.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
+import struct
 from typing import NamedTuple
 
 import torch
@@ -29,17 +30,10 @@ MAX_TOP = 32
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-class _CacheStruct(ctypes.Structure):
-    """The C struct bsg_kv8_cache."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int),
-                ("page_tokens", ctypes.c_int), ("dim", ctypes.c_int)]
-
-
-class _TokensStruct(ctypes.Structure):
-    """The C struct bsg_tokens."""
-    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
-                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+# The C structs bsg_kv8_cache and bsg_tokens, packed (a call takes microseconds; a
+# ctypes structure would be one of them).
+_CACHE = struct.Struct("@PPPPqiii4x")
+_TOKENS = struct.Struct("@Pqqq")
 
 
 class Kv8Cache(NamedTuple):
@@ -70,23 +64,26 @@ class Logprobs(NamedTuple):
     top_id: torch.Tensor
 
 
+# The checks below cost a decode step as much as its small kernels take, so each
+# is one condition that a good argument passes; what is wrong is said after.
 def _activation(t, dim: int, name: str) -> int:
     """The C dtype of an activation tensor, checked."""
     code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if code is None or not t.is_cuda:
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 CUDA tensor")
-    if t.dim() != dim or t.numel() == 0 or (t.stride(-1) != 1 and t.shape[-1] != 1):
+    if t.dim() != dim or not t.numel() or (t.stride(-1) != 1 and t.shape[-1] != 1):
         raise ValueError(f"{name} must be a non-empty {dim}-D tensor with a contiguous last dimension")
     return code
 
 
 def _exact(t, dtype, shape, name: str, device) -> int:
     """The address of a contiguous tensor of this dtype and shape, on `device`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index \
+            and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
         raise TypeError(f"{name} must be a tensor of dtype {dtype} on {device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
 
 
 def _rows(t) -> int:
@@ -101,23 +98,48 @@ def _made(shape, dtype, device, stream):
     return t
 
 
-def _output(out, shape, dtype, device, stream):
-    """`out`, checked, or a new tensor."""
+def _output(out, like, shape, stream):
+    """`out`, checked, or a new tensor of `like`'s dtype."""
     if out is None:
-        return _made(shape, dtype, device, stream)
-    if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.device != device:
-        raise TypeError(f"out must be a tensor of dtype {dtype} on {device}")
+        return _made(shape, like.dtype, like.device, stream)
+    if not isinstance(out, torch.Tensor) or out.dtype != like.dtype or out.device != like.device:
+        raise TypeError(f"out must be a tensor of dtype {like.dtype} on {like.device}")
     if out.shape != shape or (out.stride(-1) != 1 and out.shape[-1] != 1):
         raise ValueError(f"out must have shape {tuple(shape)} and a contiguous last dimension")
     return out
 
 
+# The current stream's handle: the stream object that torch.cuda.current_stream
+# makes takes 2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _status(dstatus, device):
     return None if dstatus is None else _exact(dstatus, torch.int32, (1,), "dstatus", device)
+
+
+def _lib():
+    return _bsg._lib or _bsg.load()
+
+
+def _workspace(workspace, need: int, device):
+    """(address, size) of the workspace given, or of the package's default one."""
+    if workspace is None:
+        workspace = _bsg._default_ws.get(device.index)
+        if workspace is None:
+            workspace = _bsg._default_ws.setdefault(device.index, _bsg.Workspace(device))
+    buf = workspace.buf
+    if buf is None or buf.numel() < need:
+        buf = workspace.get(need)
+    return buf.data_ptr(), buf.numel()
 
 
 # ---------------------------------------------------------------------------
@@ -134,10 +156,15 @@ def wquant_groups(W, group: int = 64, dstatus=None, stream=None):
     half = (N + 1) // 2
     Q = _made((K, (half + 15) // 16 * 16), torch.uint8, W.device, stream)
     scale = _made(((K + group - 1) // group if group else 1, N), torch.float32, W.device, stream)
-    _bsg._check(_bsg.load().bsg_wquant_groups(
+    _bsg._check(_lib().bsg_wquant_groups(
         W.data_ptr(), K, N, _rows(W), group, Q.data_ptr(), Q.shape[1], scale.data_ptr(), N,
         _status(dstatus, W.device), _stream(stream, W.device)), "bsg_wquant_groups")
     return Q[:, :half], scale
+
+
+@functools.lru_cache(maxsize=1024)
+def _matvec_bytes(M: int, N: int, K: int) -> int:
+    return _lib().bsg_wgroups_matvec_workspace_size(M, N, K)
 
 
 def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, dstatus=None,
@@ -152,20 +179,19 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
         raise ValueError(f"at most {MATVEC_MAX_M} rows: X has {M} (use bsgemm_i8 for more)")
     if group < 0 or group % 32:
         raise ValueError("group must be a multiple of 32, or 0")
-    if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.device != dev:
+    if not isinstance(scale, torch.Tensor) or scale.dtype is not torch.float32 or scale.get_device() != dev.index:
         raise TypeError(f"scale must be a float32 tensor on {dev}")
     if scale.dim() != 2 or scale.stride(1) != 1 and scale.shape[1] != 1 \
             or scale.shape[0] != ((K + group - 1) // group if group else 1):
         raise ValueError("scale must be (groups, N), one row per group of rows of the weight")
     N = scale.shape[1]
-    if not isinstance(Q, torch.Tensor) or Q.dtype != torch.uint8 or Q.device != dev:
+    if not isinstance(Q, torch.Tensor) or Q.dtype is not torch.uint8 or Q.get_device() != dev.index:
         raise TypeError(f"Q must be a uint8 tensor on {dev}")
     if Q.shape != (K, (N + 1) // 2) or Q.stride(1) != 1 and Q.shape[1] != 1:
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
-    Y = _output(out, (M, N), X.dtype, dev, stream)
-    lib = _bsg.load()
-    wp, wn = _bsg._ws(workspace, lib.bsg_wgroups_matvec_workspace_size(M, N, K))
-    _bsg._check(lib.bsg_wgroups_matvec(
+    Y = _output(out, X, (M, N), stream)
+    wp, wn = _workspace(workspace, _matvec_bytes(M, N, K), dev)
+    _bsg._check(_lib().bsg_wgroups_matvec(
         X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
         group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev),
         _stream(stream, dev)), "bsg_wgroups_matvec")
@@ -173,21 +199,22 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
 
 
 # ---------------------------------------------------------------------------
-def _cache_struct(cache, device):
+def _cache(cache, device):
+    """(bsg_kv8_cache, heads, page_tokens, dim), checked."""
     k, v, ks, vs = cache
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("the cache's k must be (pages, heads, page_tokens, dim)")
     pages, heads, page_tokens, dim = shape = k.shape
-    return _CacheStruct(_exact(k, torch.int8, shape, "k", device),
-                        _exact(v, torch.int8, shape, "v", device),
-                        _exact(ks, torch.float32, shape[:2], "k_scale", device),
-                        _exact(vs, torch.float32, shape[:2], "v_scale", device),
-                        pages, heads, page_tokens, dim)
+    per_page = (pages, heads)
+    packed = _CACHE.pack(_exact(k, torch.int8, shape, "k", device), _exact(v, torch.int8, shape, "v", device),
+                         _exact(ks, torch.float32, per_page, "k_scale", device),
+                         _exact(vs, torch.float32, per_page, "v_scale", device), pages, heads, page_tokens, dim)
+    return packed, heads, page_tokens, dim
 
 
-def _tokens_struct(t):
+def _tokens(t):
     s = t.stride()
-    return _TokensStruct(t.data_ptr(), s[0], s[1], s[2])
+    return _TOKENS.pack(t.data_ptr(), s[0], s[1], s[2])
 
 
 def _table(table, B: int, device):
@@ -206,15 +233,19 @@ def kv8_append(k, v, cache, table, starts, counts=None, dstatus=None, stream=Non
     if _activation(v, 4, "v") != code or v.shape != k.shape or v.device != dev:
         raise ValueError("k and v must have the same shape, dtype and device")
     B, T, H, D = k.shape
-    c = _cache_struct(cache, dev)
-    if (H, D) != (c.heads, c.dim):
-        raise ValueError(f"the cache has {c.heads} heads of {c.dim}")
-    _bsg._check(_bsg.load().bsg_kv8_append(
-        ctypes.byref(c), _table(table, B, dev), table.shape[1],
-        _exact(starts, torch.int32, (B,), "starts", dev),
-        None if counts is None else _exact(counts, torch.int32, (B,), "counts", dev),
-        ctypes.byref(_tokens_struct(k)), ctypes.byref(_tokens_struct(v)), code, B, T,
-        _status(dstatus, dev), _stream(stream, dev)), "bsg_kv8_append")
+    c, heads, _, dim = _cache(cache, dev)
+    if H != heads or D != dim:
+        raise ValueError(f"the cache has {heads} heads of {dim}")
+    _bsg._check(_lib().bsg_kv8_append(
+        c, _table(table, B, dev), table.shape[1], _exact(starts, torch.int32, (B,), "starts", dev),
+        None if counts is None else _exact(counts, torch.int32, (B,), "counts", dev), _tokens(k),
+        _tokens(v), code, B, T, _status(dstatus, dev), _stream(stream, dev)), "bsg_kv8_append")
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_bytes(pages: int, heads: int, page_tokens: int, dim: int, width: int, B: int, T: int, H: int) -> int:
+    anything = _CACHE.pack(256, 256, 256, 256, pages, heads, page_tokens, dim)  # its addresses do not matter
+    return _lib().bsg_kv8_attend_workspace_size(anything, width, B, T, H)
 
 
 def kv8_attend(q, cache, table, lens, scale: float | None = None, out=None, lse=None,
@@ -228,19 +259,16 @@ def kv8_attend(q, cache, table, lens, scale: float | None = None, out=None, lse=
     code = _activation(q, 4, "q")
     dev = q.device
     B, T, H, D = q.shape
-    c = _cache_struct(cache, dev)
-    if D != c.dim or H % c.heads:
-        raise ValueError(f"the cache has {c.heads} heads of {c.dim}")
+    c, heads, page_tokens, dim = _cache(cache, dev)
+    if D != dim or H % heads:
+        raise ValueError(f"the cache has {heads} heads of {dim}")
     if T > KV8_MAX_T:
         raise ValueError(f"at most {KV8_MAX_T} tokens a sequence: q has {T}")
-    O = _output(out, q.shape, q.dtype, dev, stream)
-    lib = _bsg.load()
+    O = _output(out, q, q.shape, stream)
     tp, width = _table(table, B, dev), table.shape[1]
-    need = lib.bsg_kv8_attend_workspace_size(ctypes.byref(c), width, B, T, H)
-    wp, wn = _bsg._ws(workspace, need)
-    _bsg._check(lib.bsg_kv8_attend(
-        ctypes.byref(c), tp, width, _exact(lens, torch.int32, (B,), "lens", dev),
-        ctypes.byref(_tokens_struct(q)), ctypes.byref(_tokens_struct(O)), code, B, T, H,
+    wp, wn = _workspace(workspace, _attend_bytes(cache[0].shape[0], heads, page_tokens, dim, width, B, T, H), dev)
+    _bsg._check(_lib().bsg_kv8_attend(
+        c, tp, width, _exact(lens, torch.int32, (B,), "lens", dev), _tokens(q), _tokens(O), code, B, T, H,
         D ** -0.5 if scale is None else scale,
         None if lse is None else _exact(lse, torch.float32, (B, T, H), "lse", dev), wp, wn,
         _status(dstatus, dev), _stream(stream, dev)), "bsg_kv8_attend")
@@ -259,10 +287,10 @@ def logprobs(logits, target=None, top: int = 0, dstatus=None, stream=None) -> Lo
     if not 0 <= top <= min(MAX_TOP, V):
         raise ValueError(f"top must be 0 to {min(MAX_TOP, V)}")
     tp = None if target is None else _exact(target, torch.int64, (M,), "target", dev)
-    lp, ent, lse = (_made((M,), torch.float32, dev, stream) for _ in range(3))
+    lp, ent, lse = _made((3, M), torch.float32, dev, stream).unbind()
     tl = _made((M, top), torch.float32, dev, stream)
     ti = _made((M, top), torch.int32, dev, stream)
-    _bsg._check(_bsg.load().bsg_logprobs(
+    _bsg._check(_lib().bsg_logprobs(
         logits.data_ptr(), code, M, V, _rows(logits), tp, top, lp.data_ptr(), ent.data_ptr(),
         lse.data_ptr(), tl.data_ptr(), ti.data_ptr(), _status(dstatus, dev),
         _stream(stream, dev)), "bsg_logprobs")
@@ -284,8 +312,8 @@ def logprobs_backward(logits, target, lse, entropy=None, g_logprob=None, g_entro
                for t, name in ((lse, "lse"), (entropy, "entropy"), (g_logprob, "g_logprob"),
                                (g_entropy, "g_entropy"))]
     tp = None if target is None else _exact(target, torch.int64, (M,), "target", dev)
-    D = _output(out, (M, V), logits.dtype, dev, stream)
-    _bsg._check(_bsg.load().bsg_logprobs_backward(
+    D = _output(out, logits, (M, V), stream)
+    _bsg._check(_lib().bsg_logprobs_backward(
         logits.data_ptr(), code, M, V, _rows(logits), tp, *per_row, D.data_ptr(), _rows(D),
         _status(dstatus, dev), _stream(stream, dev)), "bsg_logprobs_backward")
     return D
