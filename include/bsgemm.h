@@ -352,7 +352,8 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
  * Y: M x N (ldy >= N), of X's type.  Inf or NaN in X sets
  * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  N <= 2^25, K <=
  * 2^30.  `workspace`: bsg_wgroups_matvec_workspace_size(M, N, K) bytes,
- * 256-byte aligned.  Fastest with Q 16-byte aligned and ldq a multiple of
+ * 256-byte aligned (small products need none: 0, and any pointer; 0 too for sizes
+ * that the call refuses).  Fastest with Q 16-byte aligned and ldq a multiple of
  * 16, and scale likewise (lds a multiple of 4). */
 #define BSG_MATVEC_MAX_M 16
 size_t bsg_wgroups_matvec_workspace_size(int64_t M, int64_t N, int64_t K);

@@ -134,6 +134,30 @@ def test_unaligned_and_strided_operands(offset):
     assert (out[:, :offset] == 7).all() and (out[:, offset + N:] == 7).all()
 
 
+@pytest.mark.parametrize("K", [1, 15, 16, 17, 31, 33, 64, 127, 255, 256, 257, 1023])
+@pytest.mark.parametrize("N", [1, 63, 130, 513])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_five_rows(K, N, offset):
+    """The tails again with more rows than the small form takes, whose products
+    run on the tensor cores at any size."""
+    Q, sc = bsg.wquant_groups(dev(weight(K, N, K + N)), 32)
+    half = (N + 1) // 2
+    wide = torch.full((K, half + offset + 3), 0x5A, dtype=torch.uint8, device="cuda")
+    wide[:, offset:offset + half] = Q
+    X = torch.full((5, K + 9), float("nan"), device="cuda")
+    X[:, offset:offset + K] = activations(5, K, torch.float32, K)
+    check(X[:, offset:offset + K], wide[:, offset:offset + half], sc, 32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 2048), (1, 4096, 2049), (1, 4097, 2048), (2, 2048, 2048),
+                                   (2, 2047, 2051), (3, 1031, 2035), (4, 1031, 2033), (4, 9001, 233),
+                                   (1, 65537, 128), (1, 65537, 127), (1, 1, 70001), (1, 7, 1198372)])
+def test_either_side_of_small(dtype, M, K, N):
+    Q, sc = bsg.wquant_groups(dev(weight(K, N, K + N)), 96)
+    check(activations(M, K, dtype, M), Q, sc, 96)
+
+
 def test_column_storage_is_group_zero():
     """A weight that wquant_cols stored in 4 bits goes in as it is."""
     W = dev(weight(700, 131, 8))

@@ -46,6 +46,8 @@ def test_wgroups_matvec(lib):
             [("X", None), ("X", D + 2), ("dtype", 3), ("dtype", -1), ("ldx", 99), ("Q", None), ("ldq", 3), ("scale", None),
              ("lds", 6), ("group", 48), ("M", 0), ("M", 17), ("N", 0), ("K", 0), ("relu", 2), ("Y", None), ("ldy", 6),
              ("N", (1 << 25) + 1), ("K", (1 << 30) + 1)])
+    assert good["n"] == 0  # small products need none
+    good.update(M=5, n=lib.bsg_wgroups_matvec_workspace_size(5, 7, 100))
     refused(lib.bsg_wgroups_matvec, good, [("ws", None), ("ws", D + 16), ("n", good["n"] - 1)], WORKSPACE)
     assert lib.bsg_wgroups_matvec_workspace_size(0, 5, 5) == lib.bsg_wgroups_matvec_workspace_size(17, 5, 5) == 0
 

@@ -16,7 +16,7 @@ cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 bool ws_ok(const void *ws, size_t have, size_t need) {
-    return ws != nullptr && aligned(ws, 256) && have >= need;
+    return need == 0 || (ws != nullptr && aligned(ws, 256) && have >= need);
 }
 
 // A known type, and a pointer on one of its elements.

@@ -4,6 +4,7 @@
 // The storage is wquant.cu's scheme ("Precision" manual, section "Integer
 // weights") on blocks of `group` rows: s = absmax / 7 rounded to f32, codes
 // the integer nearest w / s, ties to even, all-zero blocks s = 0.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,6 +14,8 @@
 #include "bsg_ptx.cuh"
 #include "serve.cuh"
 #include "wq_round.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace bsg {
 namespace {
@@ -511,6 +514,185 @@ __global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant
     store_pair<T>(a, r, c + 2, make_float2(y.z, y.w));
 }
 
+// ---- small products ---------------------------------------------------------
+//
+// Where the weights are few, the three launches above cost more than the products.
+// This is one launch on the CUDA cores, without a workspace: 8 lanes take 64
+// columns (a word of 8 codes each), the 32 such parts of a CTA and the CTAs of a
+// cluster split K evenly, so that a lane has a few rows, loaded at once; their sums
+// meet by shuffles and in (distributed) shared memory, always in one order.  A code
+// becomes a float by the magic number 2^23, exactly, and X is used as it is, in f32.
+//
+// What bounds it: the launch, one round of loads and the cluster's two barriers at
+// the small end; 4 + M instructions per weight beyond.  Measured on the device, this
+// against the three launches: 768 x 2304, 1 f32 row 4.8 and 6.0 us; 768 x 768, 1 row
+// 4.4 and 5.8, 4 rows 5.9 and 6.1; 2048 x 2048 bf16, 1 row 6.3 and 7.4, 2 rows 7.4
+// and 7.9, 4 rows 8.3 and 8.0; 4096 x 2048 f16, 1 row 8.4 and 8.1, 2 rows 9.8 and
+// 8.6; 4096 x 4096 f16, 1 row 15.7 and 9.1.  The host's part is 3 us against 7.5.
+// So it is taken up to 2^23 products, rows counted as 1, 2 or 4.
+// (256 columns to a CTA, a quarter of the lanes on K: 6.5 us at 768 x 2304, 17.1
+// against 6.8 at 3072 x 768.)
+constexpr int kSmallWarps = 8, kSmallCols = 64, kSmallX = 8192;  // floats of X that a CTA stages
+
+struct SmallArgs {
+    const void *X;
+    int64_t ldx;
+    const uint8_t *Q;
+    int64_t ldq;
+    const float *scale;
+    int64_t lds;
+    void *Y;
+    int64_t ldy;
+    int32_t *dstatus;
+    int group, M, N, K, relu, ranks;
+    bool words;  // Q's rows start on words
+};
+
+// A word of codes, of which the first `bytes` are wanted.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *p, int bytes, bool words) {
+    if (words && bytes >= 4) return __ldg(reinterpret_cast<const uint32_t *>(p));
+    uint32_t w = 0;
+    for (int i = 0; i < min(bytes, 4); ++i) w |= (uint32_t)p[i] << (8 * i);
+    return w;
+}
+
+// grid: column tiles x CTAs of a cluster; MT >= M rows
+template <typename T, int MT>
+__global__ void __launch_bounds__(kSmallWarps * 32) wgroups_small_kernel(const __grid_constant__ SmallArgs a) {
+    __shared__ float x_s[kSmallX];
+    __shared__ float sum_s[kSmallWarps][MT][kSmallCols];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = a.ranks;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int k0 = (int)((int64_t)a.K * rank / ranks), k1 = (int)((int64_t)a.K * (rank + 1) / ranks), n = k1 - k0;
+    const int tile0 = (int)(blockIdx.x / ranks) * kSmallCols, col = tile0 + lane % 8 * 8;  // the lane's first column
+    const int part = tid / 8;                                               // its rows
+    constexpr int kParts = kSmallWarps * 4;
+    const int ks = k0 + n * part / kParts, ke = k0 + n * (part + 1) / kParts;
+    const int bytes = (a.N + 1) / 2 - col / 2;  // of its columns and those after them
+    const uint8_t *q = a.Q + (int64_t)ks * a.ldq + col / 2;
+    constexpr int kAhead = 12;
+    uint32_t w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        w[i] = ks + i < ke && bytes > 0 ? load_codes(q + i * a.ldq, bytes, a.words) : 0x88888888u;
+    int g = ks / a.group;
+    int64_t g_end = (int64_t)(g + 1) * a.group;
+    float sc[8];
+    auto load_scales = [&]() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = col + i < a.N ? __ldg(a.scale + g * a.lds + col + i) : 0.0f;
+    };
+    load_scales();
+    bool bad = false;
+    for (int e = tid; e < MT * n; e += kSmallWarps * 32) {
+        const int m = e / n, k = e % n;
+        const float x = m < a.M ? to_f32(static_cast<const T *>(a.X)[m * a.ldx + k0 + k]) : 0.0f;
+        bad |= !isfinite(x);
+        x_s[e] = x;
+    }
+    if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+    __syncthreads();
+
+    float acc[MT][8], sum[MT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[m][i] = sum[m][i] = 0.0f;
+    for (int kb = ks; kb < ke; kb += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = kb + i;
+            if (k >= ke) break;
+            if (k >= g_end) {  // a group ends: its sums at its scales
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) sum[m][c] = fmaf(acc[m][c], sc[c], sum[m][c]), acc[m][c] = 0.0f;
+                ++g;
+                g_end += a.group;
+                load_scales();
+            }
+            const uint32_t u = w[i] ^ 0x88888888u;
+            if (k + kAhead < ke && bytes > 0)
+                w[i] = load_codes(q + (int64_t)(k + kAhead - ks) * a.ldq, bytes, a.words);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {  // 2^23 + code + 8, less 2^23 + 8
+                const float v = __fadd_rn(__uint_as_float((u >> (4 * c) & 15u) | 0x4b000000u), -8388616.0f);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[m][c] = fmaf(x_s[m * n + k - k0], v, acc[m][c]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float y = fmaf(acc[m][c], sc[c], sum[m][c]);
+            y += __shfl_xor_sync(0xffffffffu, y, 8);
+            y += __shfl_xor_sync(0xffffffffu, y, 16);
+            if (lane < 8) sum_s[warp][m][lane * 8 + c] = y;
+        }
+    __syncthreads();
+    auto store = [&](int m, int c, float y) {
+        if (m < a.M && tile0 + c < a.N)
+            static_cast<T *>(a.Y)[m * a.ldy + tile0 + c] = from_f32<T>(a.relu && !(y > 0.0f) ? 0.0f : y);
+    };
+    for (int e = tid; e < MT * kSmallCols; e += kSmallWarps * 32) {  // a thread's own element: written after it is read
+        const int m = e / kSmallCols, c = e % kSmallCols;
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSmallWarps; ++i) y += sum_s[i][m][c];
+        if (ranks == 1)
+            store(m, c, y);
+        else
+            sum_s[0][m][c] = y;
+    }
+    if (ranks == 1) return;
+    cluster.sync();
+    const int c0 = kSmallCols * rank / ranks, cols = kSmallCols * (rank + 1) / ranks - c0;
+    for (int e = tid; e < MT * cols; e += kSmallWarps * 32) {
+        const int m = e / cols, c = c0 + e % cols;
+        float of[8], y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) of[i] = i < ranks ? *cluster.map_shared_rank(&sum_s[0][m][c], i) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y += of[i];
+        store(m, c, y);
+    }
+    cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+inline int small_rows(int64_t M) { return M <= 2 ? (int)M : 4; }
+
+// CTAs that split K in the small form: up to 8, until two CTAs to an SM are there or
+// a lane has two rows left; 0 where the products are not small.
+inline int small_ranks(int64_t M, int64_t N, int64_t K) {
+    if (M > 4 || small_rows(M) * N * K > (1 << 23)) return 0;
+    const int64_t tiles = (N + kSmallCols - 1) / kSmallCols, xs = small_rows(M) * K;
+    int ranks = 1;
+    while (ranks < 8 && (tiles * ranks < 2 * device_sm_count() || xs > ranks * kSmallX) &&
+           K >= ranks * kSmallWarps * 16)
+        ranks *= 2;
+    return small_rows(M) * ((K + ranks - 1) / ranks) > kSmallX ? 0 : ranks;
+}
+
+template <typename T, int MT>
+cudaError_t launch_small(const SmallArgs &a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.N + kSmallCols - 1) / kSmallCols * a.ranks));
+    cfg.blockDim = dim3(kSmallWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, wgroups_small_kernel<T, MT>, a);
+}
+
 // The split of K that ends first, by what was measured: a unit takes a CTA
 // kUnitUs where it has its SM to itself and kSharedUs where it shares it with
 // another; a split costs its start, and the splits' sums are written and read
@@ -593,8 +775,9 @@ cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t l
     return cudaGetLastError();
 }
 
-// Enough for X of any type.
+// Enough for X of any type; none where the products are small.
 size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (small_ranks(M, N, K)) return 0;
     size_t most = 0;
     for (int parts = 1; parts <= 2; ++parts) {
         const int nt = parts * M <= 8 ? 1 : parts * M <= 16 ? 2 : 4;
@@ -611,6 +794,16 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
                                   void *ws, int32_t *dstatus, cudaStream_t st) {
     // one group to a column ends wherever it likes
     if (group >= K) group = round_up(K, kUnit);
+    if (const int ranks = small_ranks(M, N, K)) {
+        const SmallArgs s{X, ldx, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, ranks,
+                          (reinterpret_cast<uintptr_t>(Q) | (uintptr_t)ldq) % 4 == 0};
+        return with_dtype(dtype, [&](auto t) {
+            using T = decltype(t);
+            return M == 1   ? launch_small<T, 1>(s, st)
+                   : M == 2 ? launch_small<T, 2>(s, st)
+                            : launch_small<T, 4>(s, st);
+        });
+    }
     const int64_t groups = (K + group - 1) / group;
     MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, 0, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
     if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)

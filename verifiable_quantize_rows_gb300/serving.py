@@ -190,7 +190,8 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     if Q.shape != (K, (N + 1) // 2) or Q.stride(1) != 1 and Q.shape[1] != 1:
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
     Y = _output(out, X, (M, N), stream)
-    wp, wn = _workspace(workspace, _matvec_bytes(M, N, K), dev)
+    need = _matvec_bytes(M, N, K)
+    wp, wn = _workspace(workspace, need, dev) if need else (None, 0)
     _bsg._check(_lib().bsg_wgroups_matvec(
         X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
         group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev),
