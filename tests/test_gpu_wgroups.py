@@ -44,6 +44,27 @@ def test_storage_is_the_column_storage_of_each_block(orc, shape, group):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("K,N", [(5000, 130), (2049, 131), (129, 517)])
+@pytest.mark.parametrize("group", [0, 64, 128, 160, 1056, 2048])
+def test_storage_of_halves_and_tiny_scales(orc, K, N, group):
+    """Quotients on and next to half-integers, and columns whose scale is near
+    or below the least normal number (there the oracle says that it had to clamp)."""
+    rng = np.random.default_rng(K + group)
+    s = np.float32(rng.random((1, N)) + 0.5)
+    n = rng.integers(-7, 7, (K, N))
+    W = np.float32(s * (n + 0.5))
+    W = np.nextafter(W, np.float32(W * rng.integers(0, 3, W.shape)), dtype=np.float32)
+    W[0::32] = 7 * s
+    W[:, 3::7] *= np.float32(2.0 ** -125)
+    W[:, 4::7] *= np.float32(2.0 ** -147)
+    Q, sc = bsg.wquant_groups(dev(W), group)
+    G = group or K
+    for g in range(sc.shape[0]):
+        Qo, so, _ = orc.wquant_cols(np.ascontiguousarray(W[g * G:(g + 1) * G]), 4, False)
+        assert_bits_equal(host(sc[g]), so, "scales")
+        assert (host(Q[g * G:(g + 1) * G].contiguous()) == orc.pack_int4(Qo)).all()
+
+
 def test_storage_reads_strided_weights_and_reports_nonfinite(orc):
     W = weight(100, 50, 1)
     wide = dev(np.concatenate([W, W], 1))

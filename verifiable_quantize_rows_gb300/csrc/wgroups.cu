@@ -20,37 +20,128 @@ namespace cg = cooperative_groups;
 namespace bsg {
 namespace {
 
-// One thread per byte column (two weight columns) of one group: the maxima of
-// its rows, then the codes from a second read (L2).
-__global__ void __launch_bounds__(128)
-    wquant_groups_kernel(const float *__restrict__ W, int64_t K, int64_t N, int64_t ldw,
-                         int64_t group, uint8_t *__restrict__ Q, int64_t ldq,
-                         float *__restrict__ scale, int64_t lds, int32_t *__restrict__ dstatus) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (2 * c >= N) return;
-    const bool two = 2 * c + 1 < N;
-    const int64_t groups = (K + group - 1) / group;
+// ---- storage ------------------------------------------------------------------
+//
+// One read of W and one write of the codes: HBM bounds it.  A CTA takes 128 columns
+// of a group, a warp every 8th row of it, a lane 4 columns; a lane's rows stay in
+// registers between the maximum and the codes (kKept of them: groups up to 8 kKept
+// rows are read once).  Longer groups go to a cluster of up to 8 CTAs, what does not
+// fit the registers is read twice.
+//
+// A code is RN(w RN(1/s)) where that lies more than 2^-14 from a half-integer, as
+// wq_round.cuh shows, and the exact quotient's otherwise; a magic number rounds
+// it, and the sum's low bits are the code.  |w RN(1/s)| <= 7 (1 + 2^-22), so there is
+// nothing to clamp, but for scales near or below the least normal number: those
+// columns take the exact path throughout.
+//
+// Measured: 16384 x 16384 in groups of 64 343 us (0.52 of the floor's rate; a thread
+// to two columns that read them twice 519), of 128 364 (643), the whole column 828
+// (12009); 8191 x 12289 (unaligned rows) in groups of 32 140 (171; 213 with the same 8
+// warps, which have half as many rows to hold), 768 x 50304 57 (94).  What bounds it:
+// a CTA's loads, barrier and stores follow one another, and 24 warps an SM overlap
+// them by half; at 32 warps the rows spill (365 us).
+constexpr int kStoreCols = 128;
+
+struct StoreArgs {
+    const float *W;
+    uint8_t *Q;
+    float *scale;
+    int32_t *dstatus;
+    int64_t K, N, ldw, group, ldq, lds;
+    int ranks;
+    bool vec, pairs;  // rows of W on 16 bytes, of Q on 2
+};
+
+__device__ __noinline__ uint32_t exact_code(float w, float s) { return (uint32_t)wq_round_quotient_exact(w, s, 7); }
+
+template <int kWarps, int kKept>
+__global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
+    wquant_groups_kernel(const __grid_constant__ StoreArgs a) {
+    __shared__ uint32_t max_s[kWarps][kStoreCols], top_s[kStoreCols];
+    __shared__ float scale_s[kStoreCols];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = a.ranks;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t tile0 = (int64_t)(blockIdx.x / ranks) * kStoreCols, col = tile0 + lane * 4;
+    const int64_t groups = (a.K + a.group - 1) / a.group;
+    auto load = [&](int64_t k) {
+        const float *p = a.W + k * a.ldw + col;
+        if (a.vec && col + 4 <= a.N) return __ldg(reinterpret_cast<const float4 *>(p));
+        return make_float4(col < a.N ? p[0] : 0.0f, col + 1 < a.N ? p[1] : 0.0f, col + 2 < a.N ? p[2] : 0.0f,
+                           col + 3 < a.N ? p[3] : 0.0f);
+    };
     for (int64_t g = blockIdx.y; g < groups; g += gridDim.y) {
-        const int64_t k0 = g * group, k1 = k0 + group < K ? k0 + group : K;
-        uint32_t m0 = 0, m1 = 0;
-        for (int64_t k = k0; k < k1; ++k) {
-            const float *row = W + k * ldw + 2 * c;
-            m0 = max(m0, __float_as_uint(row[0]) & 0x7fffffffu);
-            if (two) m1 = max(m1, __float_as_uint(row[1]) & 0x7fffffffu);
+        const int64_t g0 = g * a.group, rows = (a.K - g0 < a.group ? a.K - g0 : a.group);
+        const int64_t first = g0 + rows * rank / ranks + warp, end = g0 + rows * (rank + 1) / ranks;
+        const int64_t rest = first + kKept * kWarps;
+        float4 v[kKept];
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            v[i] = first + i * kWarps < end ? load(first + i * kWarps) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        uint32_t top[4] = {0, 0, 0, 0};
+        auto raise = [&](const float4 &x) {
+            top[0] = max(top[0], __float_as_uint(x.x) & 0x7fffffffu);
+            top[1] = max(top[1], __float_as_uint(x.y) & 0x7fffffffu);
+            top[2] = max(top[2], __float_as_uint(x.z) & 0x7fffffffu);
+            top[3] = max(top[3], __float_as_uint(x.w) & 0x7fffffffu);
+        };
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) raise(v[i]);
+#pragma unroll 4
+        for (int64_t k = rest; k < end; k += kWarps) raise(load(k));
+        *reinterpret_cast<uint4 *>(&max_s[warp][lane * 4]) = make_uint4(top[0], top[1], top[2], top[3]);
+        __syncthreads();
+        uint32_t m = 0;
+        if (tid < kStoreCols) {
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) m = max(m, max_s[i][tid]);
+            top_s[tid] = m;
         }
-        if (m0 >= 0x7f800000u || m1 >= 0x7f800000u) set_status(dstatus, BSG_DSTATUS_NONFINITE);
-        const float s0 = __fdiv_rn(__uint_as_float(m0), 7.0f);
-        const float s1 = __fdiv_rn(__uint_as_float(m1), 7.0f);
-        scale[g * lds + 2 * c] = s0;
-        if (two) scale[g * lds + 2 * c + 1] = s1;
-        const bool u0 = s0 != 0.0f && isfinite(s0), u1 = s1 != 0.0f && isfinite(s1);
-        const float r0 = u0 ? __frcp_rn(s0) : 0.0f, r1 = u1 ? __frcp_rn(s1) : 0.0f;
-        for (int64_t k = k0; k < k1; ++k) {
-            const float *row = W + k * ldw + 2 * c;
-            const int q0 = u0 ? wq_round_quotient(row[0], s0, r0, 7) : 0;
-            const int q1 = u1 && two ? wq_round_quotient(row[1], s1, r1, 7) : 0;
-            Q[k * ldq + c] = (uint8_t)((q0 & 15) | ((q1 & 15) << 4));
+        if (ranks > 1) {
+            cluster.sync();
+            if (tid < kStoreCols)
+                for (int i = 0; i < ranks; ++i) m = max(m, *cluster.map_shared_rank(&top_s[tid], i));
         }
+        if (tid < kStoreCols) {
+            if (m >= 0x7f800000u) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+            const float s = __fdiv_rn(__uint_as_float(m), 7.0f);
+            scale_s[tid] = s;
+            if (rank == 0 && tile0 + tid < a.N) a.scale[g * a.lds + tile0 + tid] = s;
+        }
+        __syncthreads();
+        float s[4], r[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s[c] = scale_s[lane * 4 + c];
+            r[c] = s[c] == 0.0f || !isfinite(s[c]) ? 0.0f : s[c] < 0x1p-120f ? NAN : __frcp_rn(s[c]);
+        }
+        auto code = [&](float w, int c) -> uint32_t {
+            const float x = __fmul_rn(w, r[c]), y = __fadd_rn(x, 12582912.0f);  // 1.5 2^23
+            const float off = fabsf(__fsub_rn(x, __fsub_rn(y, 12582912.0f)));
+            return off <= 0.5f - 0x1p-14f ? __float_as_uint(y) : exact_code(w, s[c]);
+        };
+        auto put = [&](int64_t k, const float4 &x) {
+            const uint32_t even = __byte_perm(code(x.x, 0), code(x.z, 2), 0x0040);
+            const uint32_t odd = __byte_perm(code(x.y, 1), code(x.w, 3), 0x0040);
+            const uint32_t w = (even & 0x0f0fu) | (odd << 4 & 0xf0f0u);
+            uint8_t *q = a.Q + k * a.ldq + col / 2;
+            if (a.pairs && col + 2 < a.N) {
+                *reinterpret_cast<uint16_t *>(q) = (uint16_t)w;
+            } else {
+                if (col < a.N) q[0] = (uint8_t)w;
+                if (col + 2 < a.N) q[1] = (uint8_t)(w >> 8);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            if (first + i * kWarps < end) put(first + i * kWarps, v[i]);
+#pragma unroll 4
+        for (int64_t k = rest; k < end; k += kWarps) put(k, load(k));
+        // nobody writes the maxima again, or leaves, while another reads them
+        if (ranks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
     }
 }
 
@@ -75,7 +166,7 @@ __global__ void __launch_bounds__(128)
 // the row, so that f16's range holds them.  A first, small launch lays them out
 // as the B operand; it runs beside the start of the second, whose weights are
 // on their way meanwhile.  (With each CTA making its own parts in shared memory
-// its warps met at a barrier every kChunk: 62 against XX us at 16384^2, 8 rows.)
+// its warps met at a barrier every kChunk: 62 against 53 us at 16384^2, 8 rows.)
 //
 // A CTA takes 512 columns in units of 64 rows, a warp 64 of them.  Units are
 // copied ahead by TMA, their codes, their scales and X's parts, each stage sent for
@@ -87,8 +178,9 @@ __global__ void __launch_bounds__(128)
 // memory, a fifth of the places stayed empty; by the last warp to arrive, its
 // loads alone took up to 13 us.)
 //
-// Measured on the device: 16384 x 16384, 8 f32 rows XX us; 1 row XX; 8191 x 12289, 5
-// bf16 rows XX.  What bounds it: the ALU pipe takes an instruction every other cycle,
+// Measured on the device: 16384 x 16384, 8 f32 rows 53 us (0.42 of the
+// floor's rate), 1 row 46; 8191 x 12289, 5 bf16 rows 23 (0.34); 8192 x 8192, 16 bf16
+// rows 23; 4096 x 4096, 16 f32 rows 14.  What bounds it: the ALU pipe takes an instruction every other cycle,
 // and 7 of them for 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8
 // slots and shares the issue (measured: 16 together with 4 f16 multiply-adds).
 
@@ -767,12 +859,27 @@ cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cuda
 cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, int64_t group,
                                  uint8_t *Q, int64_t ldq, float *scale, int64_t lds,
                                  int32_t *dstatus, cudaStream_t st) {
-    const int64_t groups = (K + group - 1) / group;
-    const dim3 grid((unsigned)(((N + 1) / 2 + 127) / 128),
-                    (unsigned)(groups < 65535 ? groups : 65535));
-    wquant_groups_kernel<<<grid, 128, 0, st>>>(W, K, N, ldw, group, Q, ldq, scale, lds, dstatus);
+    group = std::min(group, K);
+    const int64_t groups = (K + group - 1) / group, tiles = (N + kStoreCols - 1) / kStoreCols;
+    int ranks = 1;
+    while (ranks < 8 && group > ranks * 128) ranks *= 2;
+    const StoreArgs a{W, Q, scale, dstatus, K, N, ldw, group, ldq, lds, ranks,
+                      reinterpret_cast<uintptr_t>(W) % 16 == 0 && ldw % 4 == 0,
+                      (reinterpret_cast<uintptr_t>(Q) | (uintptr_t)ldq) % 2 == 0};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * ranks), (unsigned)std::min<int64_t>(groups, 65535));
+    cfg.blockDim = dim3(group <= 32 ? 128 : 256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     count_launches(1);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, group <= 32   ? wquant_groups_kernel<4, 8>
+                                    : group <= 64 ? wquant_groups_kernel<8, 8>
+                                                  : wquant_groups_kernel<8, 16>, a);
 }
 
 // Enough for X of any type; none where the products are small.
