@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // loads alone took up to 13 us.)
 //
 // Measured on the device: 16384 x 16384, 8 f32 rows 53 us (0.42 of the
-// floor's rate), 1 row 46; 8191 x 12289, 5 bf16 rows 23 (0.34); 8192 x 8192, 16 bf16
-// rows 23; 4096 x 4096, 16 f32 rows 14.  What bounds it: the ALU pipe takes an instruction every other cycle,
+// floor's rate), 1 row or 8 bf16 rows 43 (0.52); 8191 x 12289, 5 bf16 rows 24
+// (0.34); 8192 x 8192, 16 bf16 rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it: the ALU pipe takes an instruction every other cycle,
 // and 7 of them for 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8
 // slots and shares the issue (measured: 16 together with 4 f16 multiply-adds).
 
@@ -192,18 +192,21 @@ constexpr int kBoxCols = 256;                 // columns of one TMA copy: rows o
 constexpr int kBox = kUnit * kBoxCols / 2;    // bytes of its codes
 constexpr int kCodes = kCtaCols / kBoxCols * kBox;
 
-// Units on their way or in use: 212 KB of shared memory for the CTAs of an SM.
-template <int NT>
-__host__ __device__ constexpr int stages() { return NT == 4 ? 8 : 5; }
-template <int NT>
-__host__ __device__ constexpr int matvec_per_sm() { return NT == 4 ? 1 : 2; }
+// CTAs on an SM: three of one slot tile where a group ends once a unit (80 registers a
+// thread; 42.7 us against 46.0 with two at 16384 x 16384, 44.2 against 49.3 with 8 bf16
+// rows), two else (with the scales of 32-row groups they would spill), one of four tiles.
+__host__ __device__ constexpr int matvec_per_sm(int nt, int folds) { return nt == 4 ? 1 : nt == 1 && folds == 1 ? 3 : 2; }
+// Units on their way or in use: 180 to 212 KB of shared memory for the CTAs of an SM.
+__host__ __device__ constexpr int stages(int nt, int folds) {
+    return (nt == 4 ? 8 : nt == 1 && folds == 1 ? 3 : 5) - (folds == 2 ? 1 : 0);
+}
 // Bytes of a unit's parts of X, and of a stage: codes, scales, parts.
 template <int NT>
 __host__ __device__ constexpr int part_bytes() { return kSteps * NT * 256; }
 template <int NT, int kFolds>
 __host__ __device__ constexpr int stage_bytes() { return kCodes + kFolds * kCtaCols * 4 + part_bytes<NT>(); }
 template <int NT, int kFolds>
-constexpr int matvec_smem() { return (kFolds == 2 ? stages<NT>() - 1 : stages<NT>()) * stage_bytes<NT, kFolds>() + 1024; }
+constexpr int matvec_smem() { return stages(NT, kFolds) * stage_bytes<NT, kFolds>() + 1024; }
 
 // The workspace: the parts of X, [step of 16 k][NT][lane] pairs of registers; the
 // exponents that chunks are raised by, [chunk][16]; the splits' sums,
@@ -335,10 +338,10 @@ __device__ __forceinline__ void store_pair(const MatvecArgs &a, int r, int c, fl
 
 // grid (splits of K, column tiles)
 template <typename T, int NT, int kFolds>
-__global__ void __launch_bounds__(kWarps * 32, matvec_per_sm<NT>())
+__global__ void __launch_bounds__(kWarps * 32, matvec_per_sm(NT, kFolds))
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kFoldSteps = kSteps / kFolds, kStages = kFolds == 2 ? stages<NT>() - 1 : stages<NT>();
+    constexpr int kFoldSteps = kSteps / kFolds, kStages = stages(NT, kFolds);
     constexpr int kStage = stage_bytes<NT, kFolds>(), kScalesAt = kCodes, kPartsAt = kCodes + kFolds * kCtaCols * 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023);  // the swizzle's period
@@ -785,19 +788,21 @@ cudaError_t launch_small(const SmallArgs &a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, wgroups_small_kernel<T, MT>, a);
 }
 
-// The split of K that ends first, by what was measured: a unit takes a CTA
-// kUnitUs where it has its SM to itself and kSharedUs where it shares it with
-// another; a split costs its start, and the splits' sums are written and read
-// once through L2.
-inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt) {
+// The split of K that ends first, by what was measured: what a CTA takes to start
+// and for a unit, alone on its SM or with one or two others; a split's sums are
+// written and read once through L2.
+inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int folds) {
     const int64_t tiles = (N + kCtaCols - 1) / kCtaCols, units = (K + kUnit - 1) / kUnit;
-    const int64_t sms = device_sm_count(), places = nt == 4 ? sms : 2 * sms;
-    const double alone = nt == 1 ? 0.75 : nt == 2 ? 0.95 : 1.9, shared = nt == 1 ? 1.0 : 1.4;
+    const int per_sm = matvec_per_sm(nt, folds);
+    const int64_t sms = device_sm_count(), places = per_sm * sms;
+    const double unit_us[3] = {per_sm == 1 ? 1.9 : nt == 2 ? 0.95 : per_sm == 3 ? 0.85 : 0.75,
+                               nt == 2 ? 1.4 : per_sm == 3 ? 1.2 : 1.0, 1.45};
     int splits = 1;
     double best = 1e30;
     for (int r = 1; r <= 32 && r <= units; ++r) {
-        const double each = tiles * r <= sms || nt == 4 ? alone : shared;
-        const double us = (double)((tiles * r + places - 1) / places) * (3.0 + each * (double)((units + r - 1) / r)) +
+        const int with = tiles * r <= sms ? 0 : tiles * r <= 2 * sms ? 1 : 2, among = std::min(with, per_sm - 1);
+        const double us = (double)((tiles * r + places - 1) / places) *
+                              ((among == 2 ? 3.5 : 3.0) + unit_us[among] * (double)((units + r - 1) / r)) +
                           (r > 1 ? 2.0 + 8e-6 / 6.0 * (double)(r * M * N) : 0.0);
         if (us < best) best = us, splits = r;
     }
@@ -818,7 +823,7 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    const int splits = matvec_splits(a.M, a.N, a.K, NT);
+    const int splits = matvec_splits(a.M, a.N, a.K, NT, kFolds);
     cfg.gridDim = dim3((unsigned)splits, (unsigned)(a.cols / kCtaCols));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
@@ -882,13 +887,13 @@ cudaError_t launch_wquant_groups(const float *W, int64_t K, int64_t N, int64_t l
                                                   : wquant_groups_kernel<8, 16>, a);
 }
 
-// Enough for X of any type; none where the products are small.
+// Enough for X of any type and any groups; none where the products are small.
 size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (small_ranks(M, N, K)) return 0;
     size_t most = 0;
     for (int parts = 1; parts <= 2; ++parts) {
         const int nt = parts * M <= 8 ? 1 : parts * M <= 16 ? 2 : 4;
-        const int64_t splits = matvec_splits(M, N, K, nt);
+        const int64_t splits = std::max(matvec_splits(M, N, K, nt, 1), matvec_splits(M, N, K, nt, 2));
         most = std::max(most, (size_t)(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) +
                                        (splits > 1 ? splits * M * round_up(N, kCtaCols) * 4 : 0)));
     }
