@@ -180,9 +180,12 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 //
 // Measured on the device: 16384 x 16384, 8 f32 rows 53 us (0.42 of the
 // floor's rate), 1 row or 8 bf16 rows 43 (0.52); 8191 x 12289, 5 bf16 rows 24
-// (0.34); 8192 x 8192, 16 bf16 rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it: the ALU pipe takes an instruction every other cycle,
-// and 7 of them for 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8
-// slots and shares the issue (measured: 16 together with 4 f16 multiply-adds).
+// (0.35); 8192 x 8192, 16 bf16 rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it:
+// no pipe alone.  The ALU pipe takes an instruction every other cycle, and 7 of them for
+// 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8 slots and shares the issue
+// (measured: 16 together with 4 f16 multiply-adds); four warps on a scheduler, which is
+// what the registers leave, issue on 0.42 of the cycles.  Weights that lie in L2 are no
+// faster.  Below some 4096 x 4096 it is the launches and the first copies, about 9 us.
 
 constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
