@@ -249,6 +249,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
           "f"(c3));
 }
 
+// v & mask ^ flip, in one instruction
+__device__ __forceinline__ uint32_t masked_flip(uint32_t v, uint32_t mask, uint32_t flip) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(v), "r"(mask), "r"(flip));
+    return r;
+}
+
 // The codes in the low (high) nibbles of bytes 0 and 2, as u = q + 8, as f16 q 2^-10.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
     const uint32_t minus8 = 0xa000a000u;  // -8 2^-10
@@ -257,10 +264,10 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ uint32_t low_codes(uint32_t v) {
-    return codes_f16(v & 0x000f000fu, 0x74007400u);  // u 2^-24 times 2^14
+    return codes_f16(masked_flip(v, 0x000f000fu, 0x00080008u), 0x74007400u);  // u 2^-24 times 2^14
 }
 __device__ __forceinline__ uint32_t high_codes(uint32_t v) {
-    return codes_f16(v & 0x00f000f0u, 0x64006400u);  // u 2^-20 times 2^10
+    return codes_f16(masked_flip(v, 0x00f000f0u, 0x00800080u), 0x64006400u);  // u 2^-20 times 2^10
 }
 
 // 16 bytes at any address, of which the first `bytes` are wanted; whole words
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32, matvec_per_sm(NT, kFolds))
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         w[i] = *reinterpret_cast<const uint32_t *>(codes + (i % 2 ? odd_at : even_at) + s * 2048 +
-                                                                   i / 2 * 1024) ^ 0x88888888u;
+                                                                   i / 2 * 1024);
 #pragma unroll
                     for (int quad = 0; quad < 2; ++quad) {  // 4 columns: a 16-bit piece of a row
                         const uint32_t sel = quad ? 0x7632 : 0x5410;
