@@ -152,12 +152,12 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // operations to a byte: HBM bounds it, provided a weight costs the SM less than
 // 2.7 instructions per lane.  So the products run on the tensor cores
 // (m16n8k16, the weights as the 16-row operand, X's rows as the 8 columns), and
-// a weight is unpacked with one and a quarter:
+// a weight is unpacked with one and an eighth:
 //
-//   Every nibble's top bit flipped (8 codes at once) is u = q + 8.  Two rows'
-//   16-bit pieces of 4 codes side by side (a byte permute), masked to one nibble
-//   each, are two f16 subnormals, u 2^-24 (low nibble of a byte) or u 2^-20
-//   (high); one f16 multiply-add makes them q 2^-10.
+//   Two rows' 16-bit pieces of 4 codes side by side (a byte permute), masked to one
+//   nibble each with its top bit flipped (u = q + 8; one LOP3), are two f16
+//   subnormals, u 2^-24 (low nibble of a byte) or u 2^-20 (high); one f16
+//   multiply-add makes them q 2^-10.
 //   (Left subnormal, with 8 sum_k x taken off the sums, they cost a third less
 //   and lost ten bits: the tensor cores align products by the exponent field.)
 //
@@ -178,14 +178,15 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // memory, a fifth of the places stayed empty; by the last warp to arrive, its
 // loads alone took up to 13 us.)
 //
-// Measured on the device: 16384 x 16384, 8 f32 rows 53 us (0.42 of the
-// floor's rate), 1 row or 8 bf16 rows 43 (0.52); 8191 x 12289, 5 bf16 rows 24
-// (0.35); 8192 x 8192, 16 bf16 rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it:
-// no pipe alone.  The ALU pipe takes an instruction every other cycle, and 7 of them for
-// 256 weights are 14 cycles; m16n8k16 takes 8 more for each 8 slots and shares the issue
-// (measured: 16 together with 4 f16 multiply-adds); four warps on a scheduler, which is
-// what the registers leave, issue on 0.42 of the cycles.  Weights that lie in L2 are no
-// faster.  Below some 4096 x 4096 it is the launches and the first copies, about 9 us.
+// Measured on the device: 16384 x 16384, 8 f32 rows 54 us (0.42 of the floor's rate), 1
+// row 42, 8 bf16 rows 43 (0.52); 8191 x 12289, 5 bf16 rows 23 (0.34); 8192 x 8192, 16 bf16
+// rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it: the issue of the tensor and
+// ALU pipes together.  The ALU takes an instruction every other cycle, and 6 of them for 256
+// weights are 12 cycles (8 more, the flip by itself: 42 -> 48 us); m16n8k16 takes 8 more
+// for each 8 slots and overlaps them only in part (measured: 16 together with 4 f16
+// multiply-adds).  Weights that lie in L2 are no faster.  Below some 4096 x 4096 it
+// is the launches and the first copies, about 9 us.  (The shift of a 16-bit piece as a
+// product on the FMA pipe: 44.)
 
 constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
@@ -196,7 +197,7 @@ constexpr int kBox = kUnit * kBoxCols / 2;    // bytes of its codes
 constexpr int kCodes = kCtaCols / kBoxCols * kBox;
 
 // CTAs on an SM: three of one slot tile where a group ends once a unit (80 registers a
-// thread; 42.7 us against 46.0 with two at 16384 x 16384, 44.2 against 49.3 with 8 bf16
+// thread; 42.6 us against 46.0 with two at 16384 x 16384, 44.2 against 49.3 with 8 bf16
 // rows), two else (with the scales of 32-row groups they would spill), one of four tiles.
 __host__ __device__ constexpr int matvec_per_sm(int nt, int folds) { return nt == 4 ? 1 : nt == 1 && folds == 1 ? 3 : 2; }
 // Units on their way or in use: 180 to 212 KB of shared memory for the CTAs of an SM.
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant
 // What bounds it: the launch, one round of loads and the cluster's two barriers at
 // the small end; 4 + M instructions per weight beyond.  Measured on the device, this
 // against the three launches: 768 x 2304, 1 f32 row 4.8 and 6.0 us; 768 x 768, 1 row
-// 4.4 and 5.8, 4 rows 5.9 and 6.1; 2048 x 2048 bf16, 1 row 6.3 and 7.4, 2 rows 7.4
+// 4.4 and 5.8, 4 rows 5.6 and 6.1; 2048 x 2048 bf16, 1 row 6.3 and 7.4, 2 rows 7.4
 // and 7.9, 4 rows 8.3 and 8.0; 4096 x 2048 f16, 1 row 8.4 and 8.1, 2 rows 9.8 and
 // 8.6; 4096 x 4096 f16, 1 row 15.7 and 9.1.  The host's part is 3 us against 7.5.
 // So it is taken up to 2^23 products, rows counted as 1, 2 or 4.
