@@ -257,7 +257,7 @@ __device__ __forceinline__ uint32_t masked_flip(uint32_t v, uint32_t mask, uint3
     return r;
 }
 
-// The codes in the low (high) nibbles of bytes 0 and 2, as u = q + 8, as f16 q 2^-10.
+// The codes in the low (high) nibbles of bytes 0 and 2 as f16 q 2^-10.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t up) {
     const uint32_t minus8 = 0xa000a000u;  // -8 2^-10
     const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&up),
