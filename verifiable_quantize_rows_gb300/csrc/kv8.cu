@@ -52,11 +52,12 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
 // are read once (up to 64 x 128 values a page; larger ones are read again, from
 // L2), and sends for them before it knows where they go.
 //
-// Measured: prompts of 168 MB of bf16 keys and values 58 us (0.64 of the floor's rate), 64
-// sequences' single tokens 3.8 us.  What bounds prompts: the issue (0.64 of the cycles,
-// at 16 warps an SM; a value costs its share of the maximum, the code and the packing);
-// single tokens: the launch and two dependent reads (table, then the page's old scale).
-// (256 threads that read every token twice: 210 us.)
+// Measured: prompts of 168 MB of bf16 keys and values 52 us (0.72 of the floor's rate; 58
+// with a floor by comparison), 64 sequences' single tokens 3.6 us.  What bounds prompts:
+// the issue at 16 warps an SM (a value costs its share of the maximum, the conversion, the
+// code and the packing); single tokens: the launch and two dependent reads (the table,
+// then the page's old scale).  (256 threads of 4 pieces: 55 to 61 us, the registers of 32
+// warps spill; reading every token twice: 210.)
 
 // 8 values as they are stored.
 template <typename T>
