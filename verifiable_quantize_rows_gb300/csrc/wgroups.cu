@@ -196,21 +196,26 @@ constexpr int kBoxCols = 256;                 // columns of one TMA copy: rows o
 constexpr int kBox = kUnit * kBoxCols / 2;    // bytes of its codes
 constexpr int kCodes = kCtaCols / kBoxCols * kBox;
 
-// CTAs on an SM: three of one slot tile where a group ends once a unit (80 registers a
-// thread; 42.6 us against 46.0 with two at 16384 x 16384, 44.2 against 49.3 with 8 bf16
-// rows), two else (with the scales of 32-row groups they would spill), one of four tiles.
-__host__ __device__ constexpr int matvec_per_sm(int nt, int folds) { return nt == 4 ? 1 : nt == 1 && folds == 1 ? 3 : 2; }
+// CTAs on an SM: two; one of four slot tiles; three (80 registers a thread, fewer units
+// each) of one slot tile where a group ends once a unit (with the scales of 32-row
+// groups they would spill) and the weights are many: 16384 x 16384, 8 bf16 rows 44.2
+// against 49.3 us with two, 8191 x 12289, 5 rows 23.8 against 25.6; but 8192 x 8192, 8
+// f16 rows 21.1 against 17.8 and 4096 x 12288 15.5 against 15.0, since three split K
+// further and the splits' sums have to be joined.
+inline int matvec_per_sm(int nt, int folds, int64_t N, int64_t K) {
+    return nt == 4 ? 1 : nt == 1 && folds == 1 && N * K >= 5 << 24 ? 3 : 2;
+}
 // Units on their way or in use: 180 to 212 KB of shared memory for the CTAs of an SM.
-__host__ __device__ constexpr int stages(int nt, int folds) {
-    return (nt == 4 ? 8 : nt == 1 && folds == 1 ? 3 : 5) - (folds == 2 ? 1 : 0);
+__host__ __device__ constexpr int stages(int folds, int per_sm) {
+    return (per_sm == 1 ? 8 : per_sm == 2 ? 5 : 3) - (folds == 2 ? 1 : 0);
 }
 // Bytes of a unit's parts of X, and of a stage: codes, scales, parts.
 template <int NT>
 __host__ __device__ constexpr int part_bytes() { return kSteps * NT * 256; }
 template <int NT, int kFolds>
 __host__ __device__ constexpr int stage_bytes() { return kCodes + kFolds * kCtaCols * 4 + part_bytes<NT>(); }
-template <int NT, int kFolds>
-constexpr int matvec_smem() { return stages(NT, kFolds) * stage_bytes<NT, kFolds>() + 1024; }
+template <int NT, int kFolds, int kPerSm>
+constexpr int matvec_smem() { return stages(kFolds, kPerSm) * stage_bytes<NT, kFolds>() + 1024; }
 
 // The workspace: the parts of X, [step of 16 k][NT][lane] pairs of registers; the
 // exponents that chunks are raised by, [chunk][16]; the splits' sums,
@@ -348,11 +353,11 @@ __device__ __forceinline__ void store_pair(const MatvecArgs &a, int r, int c, fl
 }
 
 // grid (splits of K, column tiles)
-template <typename T, int NT, int kFolds>
-__global__ void __launch_bounds__(kWarps * 32, matvec_per_sm(NT, kFolds))
+template <typename T, int NT, int kFolds, int kPerSm>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm)
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
     constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kFoldSteps = kSteps / kFolds, kStages = stages(NT, kFolds);
+    constexpr int kFoldSteps = kSteps / kFolds, kStages = stages(kFolds, kPerSm);
     constexpr int kStage = stage_bytes<NT, kFolds>(), kScalesAt = kCodes, kPartsAt = kCodes + kFolds * kCtaCols * 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023);  // the swizzle's period
@@ -631,13 +636,14 @@ __global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant
 //
 // What bounds it: the launch, one round of loads and the cluster's two barriers at
 // the small end; 4 + M instructions per weight beyond.  Measured on the device, this
-// against the three launches: 768 x 2304, 1 f32 row 4.8 and 6.0 us; 768 x 768, 1 row
-// 4.4 and 5.8, 4 rows 5.6 and 6.1; 2048 x 2048 bf16, 1 row 6.3 and 7.4, 2 rows 7.4
-// and 7.9, 4 rows 8.3 and 8.0; 4096 x 2048 f16, 1 row 8.4 and 8.1, 2 rows 9.8 and
-// 8.6; 4096 x 4096 f16, 1 row 15.7 and 9.1.  The host's part is 3 us against 7.5.
-// So it is taken up to 2^23 products, rows counted as 1, 2 or 4.
-// (256 columns to a CTA, a quarter of the lanes on K: 6.5 us at 768 x 2304, 17.1
-// against 6.8 at 3072 x 768.)
+// against the three launches: 768 x 2304 f32, 1 row 4.3 and 6.7 us, 4 rows 6.0 and 7.1;
+// 768 x 768, 1 row 3.9 and 6.3; 2048 x 2048 bf16, 1 row 5.1 and 9.3, 4 rows 7.6 and 9.6;
+// 4096 x 2048 f16, 1 row 7.1 and 9.9, 2 rows 8.4 and 10.0; 4096 x 4096 f16 before the loop
+// was short, 1 row 15.7 and 9.1.  The host's part is 3 us against 7.5.  So it is taken up
+// to 2^23 weights and 2^24 products, rows counted as 1, 2 or 4.
+// (12 rows' instructions in a line, most of them run once: 4.7 us at 768 x 2304, 7.0
+// against 5.7 at 3072 x 768, waiting for instructions.  256 columns to a CTA, a quarter of
+// the lanes on K: 6.5 and 17.1.)
 constexpr int kSmallWarps = 8, kSmallCols = 64, kSmallX = 8192;  // floats of X that a CTA stages
 
 struct SmallArgs {
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) wgroups_small_kernel(const _
     const int ks = k0 + n * part / kParts, ke = k0 + n * (part + 1) / kParts;
     const int bytes = (a.N + 1) / 2 - col / 2;  // of its columns and those after them
     const uint8_t *q = a.Q + (int64_t)ks * a.ldq + col / 2;
-    constexpr int kAhead = 12;
+    constexpr int kAhead = 8;
     uint32_t w[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
@@ -705,29 +711,28 @@ __global__ void __launch_bounds__(kSmallWarps * 32) wgroups_small_kernel(const _
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[m][i] = sum[m][i] = 0.0f;
-    for (int kb = ks; kb < ke; kb += kAhead) {
+    // a row at a time: the words move up, so that one row's instructions serve all
+#pragma unroll 1
+    for (int k = ks; k < ke; ++k) {
+        if (k >= g_end) {  // a group ends: its sums at its scales
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int k = kb + i;
-            if (k >= ke) break;
-            if (k >= g_end) {  // a group ends: its sums at its scales
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int c = 0; c < 8; ++c) sum[m][c] = fmaf(acc[m][c], sc[c], sum[m][c]), acc[m][c] = 0.0f;
+            ++g;
+            g_end += a.group;
+            load_scales();
+        }
+        const uint32_t u = w[0] ^ 0x88888888u;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) sum[m][c] = fmaf(acc[m][c], sc[c], sum[m][c]), acc[m][c] = 0.0f;
-                ++g;
-                g_end += a.group;
-                load_scales();
-            }
-            const uint32_t u = w[i] ^ 0x88888888u;
-            if (k + kAhead < ke && bytes > 0)
-                w[i] = load_codes(q + (int64_t)(k + kAhead - ks) * a.ldq, bytes, a.words);
+        for (int i = 0; i + 1 < kAhead; ++i) w[i] = w[i + 1];
+        if (k + kAhead < ke && bytes > 0)
+            w[kAhead - 1] = load_codes(q + (int64_t)(k + kAhead - ks) * a.ldq, bytes, a.words);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 2^23 + code + 8, less 2^23 + 8
-                const float v = __fadd_rn(__uint_as_float((u >> (4 * c) & 15u) | 0x4b000000u), -8388616.0f);
+        for (int c = 0; c < 8; ++c) {  // 2^23 + code + 8, less 2^23 + 8
+            const float v = __fadd_rn(__uint_as_float((u >> (4 * c) & 15u) | 0x4b000000u), -8388616.0f);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[m][c] = fmaf(x_s[m * n + k - k0], v, acc[m][c]);
-            }
+            for (int m = 0; m < MT; ++m) acc[m][c] = fmaf(x_s[m * n + k - k0], v, acc[m][c]);
         }
     }
 #pragma unroll
@@ -774,7 +779,7 @@ inline int small_rows(int64_t M) { return M <= 2 ? (int)M : 4; }
 // CTAs that split K in the small form: up to 8, until two CTAs to an SM are there or
 // a lane has two rows left; 0 where the products are not small.
 inline int small_ranks(int64_t M, int64_t N, int64_t K) {
-    if (M > 4 || small_rows(M) * N * K > (1 << 23)) return 0;
+    if (M > 4 || N * K > (1 << 23) || small_rows(M) * N * K > (1 << 24)) return 0;
     const int64_t tiles = (N + kSmallCols - 1) / kSmallCols, xs = small_rows(M) * K;
     int ranks = 1;
     while (ranks < 8 && (tiles * ranks < 2 * device_sm_count() || xs > ranks * kSmallX) &&
@@ -802,9 +807,8 @@ cudaError_t launch_small(const SmallArgs &a, cudaStream_t st) {
 // The split of K that ends first, by what was measured: what a CTA takes to start
 // and for a unit, alone on its SM or with one or two others; a split's sums are
 // written and read once through L2.
-inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int folds) {
+inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int per_sm) {
     const int64_t tiles = (N + kCtaCols - 1) / kCtaCols, units = (K + kUnit - 1) / kUnit;
-    const int per_sm = matvec_per_sm(nt, folds);
     const int64_t sms = device_sm_count(), places = per_sm * sms;
     const double unit_us[3] = {per_sm == 1 ? 1.9 : nt == 2 ? 0.95 : per_sm == 3 ? 0.85 : 0.75,
                                nt == 2 ? 1.4 : per_sm == 3 ? 1.2 : 1.0, 1.45};
@@ -820,10 +824,10 @@ inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int folds) {
     return splits;
 }
 
-template <typename T, int NT, int kFolds>
+template <typename T, int NT, int kFolds, int kPerSm>
 cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
-    constexpr int smem = matvec_smem<NT, kFolds>();
-    auto *kernel = wgroups_matvec_kernel<T, NT, kFolds>;
+    constexpr int smem = matvec_smem<NT, kFolds, kPerSm>();
+    auto *kernel = wgroups_matvec_kernel<T, NT, kFolds, kPerSm>;
     static bool set[64] = {false};  // this kernel's attribute, on each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -834,7 +838,7 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    const int splits = matvec_splits(a.M, a.N, a.K, NT, kFolds);
+    const int splits = matvec_splits(a.M, a.N, a.K, NT, kPerSm);
     cfg.gridDim = dim3((unsigned)splits, (unsigned)(a.cols / kCtaCols));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
@@ -867,7 +871,11 @@ cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cuda
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return a.group % kUnit ? launch_matvec<T, NT, 2>(a, st) : launch_matvec<T, NT, 1>(a, st);
+    constexpr int kPerSm = NT == 4 ? 1 : 2;
+    if (a.group % kUnit) return launch_matvec<T, NT, 2, kPerSm>(a, st);
+    if constexpr (NT == 1)
+        if (matvec_per_sm(NT, 1, a.N, a.K) == 3) return launch_matvec<T, NT, 1, 3>(a, st);
+    return launch_matvec<T, NT, 1, kPerSm>(a, st);
 }
 
 }  // namespace
@@ -904,7 +912,8 @@ size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     size_t most = 0;
     for (int parts = 1; parts <= 2; ++parts) {
         const int nt = parts * M <= 8 ? 1 : parts * M <= 16 ? 2 : 4;
-        const int64_t splits = std::max(matvec_splits(M, N, K, nt, 1), matvec_splits(M, N, K, nt, 2));
+        const int64_t splits = std::max(matvec_splits(M, N, K, nt, matvec_per_sm(nt, 1, N, K)),
+                                        matvec_splits(M, N, K, nt, matvec_per_sm(nt, 2, N, K)));
         most = std::max(most, (size_t)(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) +
                                        (splits > 1 ? splits * M * round_up(N, kCtaCols) * 4 : 0)));
     }
