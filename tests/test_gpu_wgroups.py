@@ -247,3 +247,25 @@ def test_offsets_past_32_bits():
     small, sc = bsg.wquant_groups(dev(weight(K, N, 2)), group)
     rows[:, :4] = small
     check(activations(2, K, torch.float32, 2), rows[:, :4], sc, group)
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["current", "given"])
+def test_calls_on_two_streams(given):
+    """Calls that overlap on two streams, each with its stream's own workspace."""
+    K, N = 2048, 5000
+    sides = []
+    for i in range(2):
+        Q, sc = bsg.wquant_groups(dev(weight(K, N, i)), 64)
+        X = activations(8, K, torch.float32, i)
+        sides.append((X, Q, sc, check(X, Q, sc, 64), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(50):
+        for X, Q, sc, want, stream in sides:
+            if given:
+                out.append((bsg.wgroups_matvec(X, Q, sc, stream=stream), want))
+            else:
+                with torch.cuda.stream(stream):
+                    out.append((bsg.wgroups_matvec(X, Q, sc), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y, want in out)

@@ -7,7 +7,10 @@ call checks and marshals its arguments and launches the library's kernels on
 the current PyTorch stream (or the ``stream`` given).  Activations are
 float32, float16 or bfloat16 CUDA tensors whose last dimension is contiguous;
 their other strides are free.  Data-dependent conditions are OR-ed into
-``dstatus`` (an int32 CUDA tensor, or None) as DSTATUS_* bits.  There is no
+``dstatus`` (an int32 CUDA tensor, or None) as DSTATUS_* bits.  A call given no
+``workspace`` uses one of its stream's own, so calls on different streams may
+overlap; a graph keeps the one of the stream it was captured on, and graphs that
+may overlap need workspaces of their own.  There is no
 CPU fallback and no autograd: gradients have calls of their own.
 """
 from __future__ import annotations
@@ -130,15 +133,21 @@ def _lib():
     return _bsg._lib or _bsg.load()
 
 
-def _workspace(workspace, need: int, device):
-    """(address, size) of the workspace given, or of the package's default one."""
+# The default workspaces, one for each stream of a device: calls on different
+# streams may overlap.
+_default_ws: dict = {}
+
+
+def _workspace(workspace, need: int, device, stream, handle: int):
+    """(address, size) of the workspace given, or of the stream's default one."""
     if workspace is None:
-        workspace = _bsg._default_ws.get(device.index)
+        workspace = _default_ws.get((device.index, handle))
         if workspace is None:
-            workspace = _bsg._default_ws.setdefault(device.index, _bsg.Workspace(device))
+            workspace = _default_ws.setdefault((device.index, handle), _bsg.Workspace(device))
     buf = workspace.buf
     if buf is None or buf.numel() < need:
-        buf = workspace.get(need)
+        with torch.cuda.stream(stream):  # whose memory it is to be (None: the current one's)
+            buf = workspace.get(need)
     return buf.data_ptr(), buf.numel()
 
 
@@ -191,11 +200,12 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
     Y = _output(out, X, (M, N), stream)
     need = _matvec_bytes(M, N, K)
-    wp, wn = _workspace(workspace, need, dev) if need else (None, 0)
+    on = _stream(stream, dev)
+    wp, wn = _workspace(workspace, need, dev, stream, on) if need else (None, 0)
     _bsg._check(_lib().bsg_wgroups_matvec(
         X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
-        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev),
-        _stream(stream, dev)), "bsg_wgroups_matvec")
+        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev), on),
+        "bsg_wgroups_matvec")
     return Y
 
 
@@ -267,12 +277,14 @@ def kv8_attend(q, cache, table, lens, scale: float | None = None, out=None, lse=
         raise ValueError(f"at most {KV8_MAX_T} tokens a sequence: q has {T}")
     O = _output(out, q, q.shape, stream)
     tp, width = _table(table, B, dev), table.shape[1]
-    wp, wn = _workspace(workspace, _attend_bytes(cache[0].shape[0], heads, page_tokens, dim, width, B, T, H), dev)
+    on = _stream(stream, dev)
+    wp, wn = _workspace(workspace, _attend_bytes(cache[0].shape[0], heads, page_tokens, dim, width, B, T, H), dev,
+                        stream, on)
     _bsg._check(_lib().bsg_kv8_attend(
         c, tp, width, _exact(lens, torch.int32, (B,), "lens", dev), _tokens(q), _tokens(O), code, B, T, H,
         D ** -0.5 if scale is None else scale,
         None if lse is None else _exact(lse, torch.float32, (B, T, H), "lse", dev), wp, wn,
-        _status(dstatus, dev), _stream(stream, dev)), "bsg_kv8_attend")
+        _status(dstatus, dev), on), "bsg_kv8_attend")
     return O
 
 
