@@ -833,11 +833,11 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
     __shared__ float4 o_s[kSides][kCols];
     const int r = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int all = (length_of(a, b, false) + 15) / 16;
-    if (all <= chunk_begin(a, 1)) return;  // finished where it was computed
-    int n = 0;                             // chunks that begin within the length
+    int n = 0;  // chunks that begin within the length
     for (int i0 = 0; i0 < a.splits; i0 += kJoin)
         n += __syncthreads_count(i0 + tid < a.splits && chunk_begin(a, i0 + tid) < all);
-    griddep_wait();
+    griddep_wait();  // every block, so that this grid never ends before the one it joins
+    if (all <= chunk_begin(a, 1)) return;  // finished where it was computed
     const int64_t part = (((int64_t)b * a.c.heads + hk) * a.rows + r) * a.splits;
     const float2 *ml = a.part_ml + part;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + part * D);
