@@ -174,6 +174,8 @@ def test_five_rows(K, N, offset):
 @pytest.mark.parametrize("M,K,N", [(1, 4096, 2048), (1, 4096, 2049), (1, 4097, 2048), (2, 2048, 2048),
                                    (2, 2047, 2051), (3, 1031, 2035), (4, 1031, 2033), (4, 9001, 233),
                                    (2, 4096, 2048), (2, 2049, 4096), (4, 2048, 2048), (3, 2048, 2049),
+                                   (1, 2048, 2048), (1, 2049, 2048), (2, 1024, 2048), (2, 1024, 2049),
+                                   (4, 1024, 1024), (3, 1024, 1025),
                                    (1, 65537, 128), (1, 65537, 127), (1, 1, 70001), (1, 7, 1198372)])
 def test_either_side_of_small(dtype, M, K, N):
     Q, sc = bsg.wquant_groups(dev(weight(K, N, K + N)), 96)

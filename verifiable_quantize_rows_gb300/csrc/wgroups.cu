@@ -178,15 +178,15 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // memory, a fifth of the places stayed empty; by the last warp to arrive, its
 // loads alone took up to 13 us.)
 //
-// Measured on the device: 16384 x 16384, 8 f32 rows 54 us (0.42 of the floor's rate), 1
-// row 42, 8 bf16 rows 43 (0.52); 8191 x 12289, 5 bf16 rows 23 (0.34); 8192 x 8192, 16 bf16
-// rows 24; 4096 x 4096, 16 f32 rows 14.  What bounds it: the issue of the tensor and
-// ALU pipes together.  The ALU takes an instruction every other cycle, and 6 of them for 256
-// weights are 12 cycles (8 more, the flip by itself: 42 -> 48 us); m16n8k16 takes 8 more
-// for each 8 slots and overlaps them only in part (measured: 16 together with 4 f16
-// multiply-adds).  Weights that lie in L2 are no faster.  Below some 4096 x 4096 it
-// is the launches and the first copies, about 9 us.  (The shift of a 16-bit piece as a
-// product on the FMA pipe: 44.)
+// Measured on the device: 16384 x 16384, 8 f32 rows 52 us (0.43 of the floor's rate), 1
+// row 39, 8 bf16 rows 41 (0.55); 8191 x 12289, 5 bf16 rows 21.5 (0.37); 8192 x 8192, 8 f16
+// rows 16, 16 bf16 rows 22; 4096 x 4096, 8 f16 rows 9.3.  What bounds it: the issue of the
+// tensor and ALU pipes together.  The ALU takes an instruction every other cycle, and 6 of
+// them for 256 weights are 12 cycles (8 more, the flip by itself, cost 6 us of 42);
+// m16n8k16 takes 8 more for each 8 slots and overlaps them only in part (measured: 16
+// together with 4 f16 multiply-adds).  Weights that lie in L2 are no faster.  Below some
+// 4096 x 4096 it is the three launches and the first copies, about 5 us.  (The shift of a
+// 16-bit piece as a product on the FMA pipe: 44 us.)
 
 constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
@@ -197,14 +197,11 @@ constexpr int kBox = kUnit * kBoxCols / 2;    // bytes of its codes
 constexpr int kCodes = kCtaCols / kBoxCols * kBox;
 
 // CTAs on an SM: two; one of four slot tiles; three (80 registers a thread, fewer units
-// each) of one slot tile where a group ends once a unit (with the scales of 32-row
-// groups they would spill) and the weights are many: 16384 x 16384, 8 bf16 rows 44.2
-// against 49.3 us with two, 8191 x 12289, 5 rows 23.8 against 25.6; but 8192 x 8192, 8
-// f16 rows 21.1 against 17.8 and 4096 x 12288 15.5 against 15.0, since three split K
-// further and the splits' sums have to be joined.
-inline int matvec_per_sm(int nt, int folds, int64_t N, int64_t K) {
-    return nt == 4 ? 1 : nt == 1 && folds == 1 && N * K >= 5 << 24 ? 3 : 2;
-}
+// each) of one slot tile where a group ends once a unit; with the scales of 32-row
+// groups they would spill.  Three against two: 16384 x 16384, 1 row 42.6 and 46.0 us, 8 bf16
+// rows 44.2 and 49.3 (before the join was quicker); 8 x 4096 x 4096 9.3 and 9.4; 8 x
+// 8192 x 8192 16.4 and 15.9.
+constexpr int matvec_per_sm(int nt, int folds) { return nt == 4 ? 1 : nt == 1 && folds == 1 ? 3 : 2; }
 // Units on their way or in use: 180 to 212 KB of shared memory for the CTAs of an SM.
 __host__ __device__ constexpr int stages(int folds, int per_sm) {
     return (per_sm == 1 ? 8 : per_sm == 2 ? 5 : 3) - (folds == 2 ? 1 : 0);
@@ -604,25 +601,36 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
         }
 }
 
-// Y from the splits' sums: four columns of a row to a thread.
+constexpr int kMaxMatvecSplits = 32, kJoinSides = 8, kJoinCols = 64;
+
+// Adds the splits' sums: grid (column tiles, rows), kJoinSides warps with a share of the
+// splits each, whose loads are all on their way at once.  (A thread to all splits of
+// four columns: 12.5 against 9.4 us for 8 x 4096 x 4096 in all, 54.6 against 52.2 for
+// 8 x 16384 x 16384.)
 template <typename T>
-__global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant__ MatvecArgs a, int splits) {
-    const int c = (blockIdx.x * 128 + threadIdx.x) * 4, r = blockIdx.y;
+__global__ void __launch_bounds__(kJoinSides * 32) wgroups_join_kernel(const __grid_constant__ MatvecArgs a, int splits) {
+    constexpr int kEach = kMaxMatvecSplits / kJoinSides;
+    __shared__ float2 part_s[kJoinSides][32];
+    const int side = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int c = blockIdx.x * kJoinCols + lane * 2, r = blockIdx.y;
+    const int each = (splits + kJoinSides - 1) / kJoinSides, k0 = side * each, k1 = min(splits, k0 + each);
+    const int64_t step = (int64_t)a.M * a.cols;
     griddep_wait();
-    if (c >= a.N) return;
     const float *from = a.sums + (int64_t)r * a.cols + c;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k0 = 0; k0 < splits; k0 += 16) {
-        float4 v[16];  // all of them on their way at once
+    float2 y = make_float2(0.0f, 0.0f), v[kEach];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            v[k] = k0 + k < splits ? __ldcg(reinterpret_cast<const float4 *>(from + (int64_t)(k0 + k) * a.M * a.cols))
-                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) y.x += v[k].x, y.y += v[k].y, y.z += v[k].z, y.w += v[k].w;
+    for (int k = 0; k < kEach; ++k) {
+        v[k] = make_float2(0.0f, 0.0f);
+        if (k0 + k < k1 && c < a.N) v[k] = __ldcg(reinterpret_cast<const float2 *>(from + (k0 + k) * step));
     }
-    store_pair<T>(a, r, c, make_float2(y.x, y.y));
-    store_pair<T>(a, r, c + 2, make_float2(y.z, y.w));
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) y.x += v[k].x, y.y += v[k].y;
+    part_s[side][lane] = y;
+    __syncthreads();
+    if (side || c >= a.N) return;
+#pragma unroll
+    for (int i = 1; i < kJoinSides; ++i) y.x += part_s[i][lane].x, y.y += part_s[i][lane].y;
+    store_pair<T>(a, r, c, y);
 }
 
 // ---- small products ---------------------------------------------------------
@@ -636,11 +644,10 @@ __global__ void __launch_bounds__(128) wgroups_join_kernel(const __grid_constant
 //
 // What bounds it: the launch, one round of loads and the cluster's two barriers at
 // the small end; 4 + M instructions per weight beyond.  Measured on the device, this
-// against the three launches: 768 x 2304 f32, 1 row 4.3 and 6.7 us, 4 rows 6.0 and 7.1;
-// 768 x 768, 1 row 3.9 and 6.3; 2048 x 2048 bf16, 1 row 5.1 and 9.3, 4 rows 7.6 and 9.6;
-// 4096 x 2048 f16, 1 row 7.1 and 9.9, 2 rows 8.4 and 10.0; 4096 x 4096 f16 before the loop
-// was short, 1 row 15.7 and 9.1.  The host's part is 3 us against 7.5.  So it is taken up
-// to 2^23 weights and 2^24 products, rows counted as 1, 2 or 4.
+// against the three launches: 768 x 2304 f32, 1 row 4.3 and 5.0 us, 2 rows 4.8 and 5.0, 4
+// rows 5.8 and 5.4; 768 x 768, 1 row 4.0 and 4.8, 4 rows 5.0 and 5.3; 2048 x 2048 bf16, 1
+// row 5.2 and 5.1, 2 rows 6.2 and 5.5; 3072 x 768, 1 row 5.9 and 5.5.  The host's part is
+// 3 us against 7.5.  So it is taken up to 2^22 products, rows counted as 1, 2 or 4.
 // (12 rows' instructions in a line, most of them run once: 4.7 us at 768 x 2304, 7.0
 // against 5.7 at 3072 x 768, waiting for instructions.  256 columns to a CTA, a quarter of
 // the lanes on K: 6.5 and 17.1.)
@@ -779,7 +786,7 @@ inline int small_rows(int64_t M) { return M <= 2 ? (int)M : 4; }
 // CTAs that split K in the small form: up to 8, until two CTAs to an SM are there or
 // a lane has two rows left; 0 where the products are not small.
 inline int small_ranks(int64_t M, int64_t N, int64_t K) {
-    if (M > 4 || N * K > (1 << 23) || small_rows(M) * N * K > (1 << 24)) return 0;
+    if (M > 4 || small_rows(M) * N * K > (1 << 22)) return 0;
     const int64_t tiles = (N + kSmallCols - 1) / kSmallCols, xs = small_rows(M) * K;
     int ranks = 1;
     while (ranks < 8 && (tiles * ranks < 2 * device_sm_count() || xs > ranks * kSmallX) &&
@@ -814,7 +821,7 @@ inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int per_sm) {
                                nt == 2 ? 1.4 : per_sm == 3 ? 1.2 : 1.0, 1.45};
     int splits = 1;
     double best = 1e30;
-    for (int r = 1; r <= 32 && r <= units; ++r) {
+    for (int r = 1; r <= kMaxMatvecSplits && r <= units; ++r) {
         const int with = tiles * r <= sms ? 0 : tiles * r <= 2 * sms ? 1 : 2, among = std::min(with, per_sm - 1);
         const double us = (double)((tiles * r + places - 1) / places) *
                               ((among == 2 ? 3.5 : 3.0) + unit_us[among] * (double)((units + r - 1) / r)) +
@@ -851,8 +858,8 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
     count_launches(1);
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || splits == 1) return e;
-    cfg.gridDim = dim3((unsigned)((a.N + 511) / 512), (unsigned)a.M);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)((a.N + kJoinCols - 1) / kJoinCols), (unsigned)a.M);
+    cfg.blockDim = dim3(kJoinSides * 32);
     cfg.dynamicSmemBytes = 0;
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, wgroups_join_kernel<T>, a, splits);
@@ -871,11 +878,8 @@ cudaError_t launch_matvec(MatvecArgs &a, const T *X, int64_t ldx, void *ws, cuda
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    constexpr int kPerSm = NT == 4 ? 1 : 2;
-    if (a.group % kUnit) return launch_matvec<T, NT, 2, kPerSm>(a, st);
-    if constexpr (NT == 1)
-        if (matvec_per_sm(NT, 1, a.N, a.K) == 3) return launch_matvec<T, NT, 1, 3>(a, st);
-    return launch_matvec<T, NT, 1, kPerSm>(a, st);
+    return a.group % kUnit ? launch_matvec<T, NT, 2, matvec_per_sm(NT, 2)>(a, st)
+                           : launch_matvec<T, NT, 1, matvec_per_sm(NT, 1)>(a, st);
 }
 
 }  // namespace
@@ -912,8 +916,8 @@ size_t matvec_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     size_t most = 0;
     for (int parts = 1; parts <= 2; ++parts) {
         const int nt = parts * M <= 8 ? 1 : parts * M <= 16 ? 2 : 4;
-        const int64_t splits = std::max(matvec_splits(M, N, K, nt, matvec_per_sm(nt, 1, N, K)),
-                                        matvec_splits(M, N, K, nt, matvec_per_sm(nt, 2, N, K)));
+        const int64_t splits = std::max(matvec_splits(M, N, K, nt, matvec_per_sm(nt, 1)),
+                                        matvec_splits(M, N, K, nt, matvec_per_sm(nt, 2)));
         most = std::max(most, (size_t)(part_chunks(K) * (kChunk / 16 * nt * 256 + 64) +
                                        (splits > 1 ? splits * M * round_up(N, kCtaCols) * 4 : 0)));
     }
