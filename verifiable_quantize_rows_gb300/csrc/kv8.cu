@@ -231,9 +231,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 1 : sizeof(T) == 2 
 //   O^T (dim x 8 slots) += V^T (dim x 16) . P'^T (16 x 8 slots),  l += p' / value scale
 //
 // The value scale rides in the exponent, so the second product adds up in the
-// tensor cores' own accumulators; `ref` is then a maximum of p v's size, and
-// what f16 drops of a p' is small beside the row's output.  Value scales below
-// 1e-30 count as 1e-30.
+// tensor cores' own accumulators; `ref` is then 2^-11 of a maximum of p v's size.  Value
+// scales below 1e-30 count as 1e-30.
 //
 // Each warp copies its own tiles ahead into a ring of shared memory (cp.async,
 // kStages tiles of 32 dim bytes) and takes them from there to the tensor cores
@@ -246,13 +245,20 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 1 : sizeof(T) == 2 
 //
 // A slot is one column of the 8: a row, or (kParts = 2, f32) one of a row's two
 // f16 parts hi + 2^-11 lo.  Queries are taken relative to their largest |q|
-// (a power of two), so two parts keep 2^-22 of it; probabilities keep 2^-22 of
-// themselves.  16-bit types have one part: their queries are exact in it, and
-// their probabilities keep 11 bits, as many as the output can show.
+// (a power of two), so two parts keep 2^-22 of it.  16-bit types have one part: their
+// queries are exact in it, down to 2^-38 of the row's largest.
 //
-// The running reference `ref` follows a row's maximum only when that is more
-// than 2^8 above it: probabilities stay below 2^8 (f16 holds 2^15) and the
-// outputs are rescaled a few times per row instead of at every tile.
+// A p' goes to the second product as two f16 parts for every type, f32's as a slot
+// each, 16-bit types' as p' = hi + lo in one accumulator, by a second multiplication with
+// the same codes.  hi + lo leaves out 2^-24 of p' at most, or 2^-25 where that is more (the
+// least f16 step is 2^-24), 2^-36 of the largest.  (By hi alone, as an output in 16 bits
+// might seem to allow, a sum of many positions that cancel is off by more than its own
+// rounding: f16 outputs 2.9e-4 off 64 bits in place of 2.1e-4; and below 2^-14 of the
+// largest p' a position lost bit after bit.)
+//
+// The running reference `ref` is 2^-11 of a row's maximum, and follows it only when that
+// is more than 2^4 above: a p' stays below 2^15, which f16 holds, the largest is at
+// least 2^11, and the outputs are rescaled a few times per row instead of at every tile.
 
 // The positions are cut into chunks, a CTA each, several for each place on the
 // card, so that the hardware's own scheduling evens out what SMs and lengths
@@ -264,16 +270,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 32 ? 1 : sizeof(T) == 2 
 // joins the chunks.  (As a cluster that joins its chunks itself, one launch: 7.1 against
 // 6.2 us at 12 heads and 1021 positions, 13.4 against 10.2 at 8 heads and 4000.)
 //
-// Measured: 64 ragged sequences of up to 8190, 8 heads of 128 (538 MB) 93 us, 0.85 of the
-// floor's rate; two of up to 262143 with 4 query tokens 146 us, 0.82; 1001 positions of
-// 12 heads of 64 6.7 us.  What bounds it: HBM (0.74 of its peak over the whole launch,
-// start and last chunks among it); the short ones their two launches.
+// Measured: 64 ragged sequences of up to 8190, 8 heads of 128 (538 MB) 94 us, 0.84 of the
+// floor's rate; two of up to 262143 with 4 query tokens 164 us, 0.73; 1001 positions of
+// 12 heads of 64 6.4 us.  What bounds it: HBM with few rows; with 16 and more the tensor
+// cores beside the unpacking (probabilities in one part, whose outputs were not good to
+// their last bit: 146 us, and 92 with one query token); the short ones their two launches.
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kMaxSplits = 1024;
 constexpr float kRefNone = -3.0e38f;  // the reference of a row that has seen nothing
-constexpr float kSlack = 8.0f;
+constexpr float kTop = 11.0f, kMost = 15.0f;  // exponents of a new reference's largest p', and of any
 
 // 16 bytes from global to shared memory, asynchronously, past L1.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
@@ -310,10 +317,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return bits(__floats2half2_rn(lo, hi)); }
 
 // Two codes, already + 128 (unsigned bytes `sel` picks of x), as f16.
 template <uint32_t SEL>
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
                 }
         };
         exponents();
-        if (__any_sync(0xffffffffu, most > kSlack || fresh || edge)) {
+        if (__any_sync(0xffffffffu, most > kMost || fresh || edge)) {
             fresh = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -699,9 +705,9 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
                     keep[u] = 1.0f;
                     // each row by itself: no other row's values move its reference
                     const uint32_t bit = 1u << (2 * n + u);
-                    if (none & bit ? m > -INFINITY : m > kSlack) {
-                        ref[n][u] += m;
-                        keep[u] = none & bit ? 0.0f : exp2_fast(-m);
+                    if (none & bit ? m > -INFINITY : m > kMost) {
+                        ref[n][u] += m - kTop;
+                        keep[u] = none & bit ? 0.0f : exp2_fast(kTop - m);
                         sum[n][u] *= keep[u];
                         none &= ~bit;
                     }
@@ -715,7 +721,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
             exponents();
         }
         // Probabilities, as the B operand of the second product.
-        uint32_t p01[NT], p89[NT];
+        uint32_t p01[NT], p89[NT], lo01[NT], lo89[NT];  // lo: of 16-bit types
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (kParts == 2) {
@@ -731,8 +737,12 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
                 for (int u = 0; u < 4; ++u) p[u] = exp2_fast(x[n][u]);
                 sum[n][0] = fmaf(p[0] + p[2], of_tile.z, sum[n][0]);
                 sum[n][1] = fmaf(p[1] + p[3], of_tile.z, sum[n][1]);
-                p01[n] = transpose8(pack_half2(p[0], p[1]));
-                p89[n] = transpose8(pack_half2(p[2], p[3]));
+                const __half2 h01 = __floats2half2_rn(p[0], p[1]), h89 = __floats2half2_rn(p[2], p[3]);
+                const float2 f01 = __half22float2(h01), f89 = __half22float2(h89);
+                p01[n] = transpose8(bits(h01));
+                p89[n] = transpose8(bits(h89));
+                lo01[n] = transpose8(pack_half2(p[0] - f01.x, p[1] - f01.y));
+                lo89[n] = transpose8(pack_half2(p[2] - f89.x, p[3] - f89.y));
             }
         }
         uint32_t vr[4][D / 32];
@@ -754,6 +764,10 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     mma_16816(acc[n][2 * w + h], a0, a1, a2, a3, p01[n], p89[n]);
+                if (kParts == 1)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_16816(acc[n][2 * w + h], a0, a1, a2, a3, lo01[n], lo89[n]);
             }
         }
         __syncwarp();  // every lane has read the stage
@@ -942,7 +956,8 @@ static AttendPlan attend_plan(const bsg_kv8_cache &c, int64_t table_ld, int64_t 
                                  : per_sm<256>(p.nt);
     const int64_t places = (int64_t)device_sm_count() * n, groups = B * c.heads * p.row_tiles;
     const int64_t most = table_ld * (c.page_tokens / 16);  // tiles of a sequence
-    // 3 and 6 chunks a place: 99 and 96 us against 94 (64 ragged sequences), 145 and 154 against 146 (two long ones)
+    // 3 and 6 chunks a place: 99 and 96 us against 94 (64 ragged sequences), 145 and 154 against 146 (two long
+    // ones; then with probabilities in one part)
     constexpr int kPerPlace = 4;
     int64_t splits = (kPerPlace * places + groups - 1) / groups;
     if (splits > kMaxSplits) splits = kMaxSplits;
