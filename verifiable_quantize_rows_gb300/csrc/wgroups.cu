@@ -163,7 +163,12 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 //
 // f32 rows are two f16 parts, hi + 2^-11 lo (two columns), 16-bit rows one, all
 // relative to a power of two near the largest |x| of kChunk consecutive k of
-// the row, so that f16's range holds them.  A first, small launch lays them out
+// the row, so that f16's range holds them.  What they add up to is brought to 2^-10 of
+// its true size before it is scaled and added (f32 holds that of any 64 finite x, below
+// 2^128 2^3 2^6 2^-10), so that chunks of any sizes, zeros among them, meet in one sum as
+// they would in plain f32.  (Sums kept at their chunks' sizes and moved from one to the next
+// ran over where chunks of zeros followed large ones, and took 52 against 50 us at 8 f32 rows
+// of 16384 x 16384.)  A first, small launch lays the parts out
 // as the B operand; it runs beside the start of the second, whose weights are
 // on their way meanwhile.  (With each CTA making its own parts in shared memory
 // its warps met at a barrier every kChunk: 62 against 53 us at 16384^2, 8 rows.)
@@ -178,9 +183,9 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // memory, a fifth of the places stayed empty; by the last warp to arrive, its
 // loads alone took up to 13 us.)
 //
-// Measured on the device: 16384 x 16384, 8 f32 rows 52 us (0.43 of the floor's rate), 1
-// row 39, 8 bf16 rows 41 (0.55); 8191 x 12289, 5 bf16 rows 21.5 (0.37); 8192 x 8192, 8 f16
-// rows 16, 16 bf16 rows 22; 4096 x 4096, 8 f16 rows 9.3.  What bounds it: the issue of the
+// Measured on the device: 16384 x 16384, 8 f32 rows 50 us (0.45 of the floor's rate), 1
+// row 38, 8 bf16 rows 40 (0.56); 8191 x 12289, 5 bf16 rows 21.2 (0.37); 8192 x 8192, 8 f16
+// rows 15.7, 16 bf16 rows 22; 4096 x 4096, 8 f16 rows 9.2.  What bounds it: the issue of the
 // tensor and ALU pipes together.  The ALU takes an instruction every other cycle, and 6 of
 // them for 256 weights are 12 cycles (8 more, the flip by itself, cost 6 us of 42);
 // m16n8k16 takes 8 more for each 8 slots and overlaps them only in part (measured: 16
@@ -442,15 +447,18 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     griddep_launch_dependents();
     if (mine >= 0) copy_parts(u0 + mine, mine);
 
-    // The lane's 8 columns 8g .. 8g + 7, its slots 2t and 2t + 1 of each 8.
-    float acc[4][NT][4];
-    int up[NT][2], up_next[NT][2];  // of its columns' rows: of the sums, of the coming chunk
+    // The lane's 8 columns 8g .. 8g + 7, its slots 2t and 2t + 1 of each 8: sums of 2^-10
+    // of their true size, of the rows in those slots.
+    constexpr int kRows = 2 / kParts;  // rows of two slots
+    float acc[4][NT][2 * kRows];
+    float by[NT][kRows];       // the parts' sums, 2^e too large, times this
+    int up_next[NT][kRows];    // e of the coming chunk
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+            for (int i = 0; i < 2 * kRows; ++i) acc[m][n][i] = 0.0f;
 
     // Where the lane finds its columns' codes of rows 2t and 2t + 1 (+ 8): the
     // swizzle puts the rows of four lanes on banks of their own.
@@ -463,34 +471,17 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) up_next[n][i] = __ldg(a.up + chunk * 16 + (8 * n + 2 * t + i) / kParts);
+            for (int i = 0; i < kRows; ++i) up_next[n][i] = __ldg(a.up + chunk * 16 + (8 * n + 2 * t) / kParts + i);
     };
-    bool first = true, held = false;
-    float lower[NT][2];  // what the lane's columns of a chunk's sums are multiplied by while held
     if (u0 < u1) load_up(u0 / kChunkUnits);
     if (busy)
         for (int u = u0; u < u1; ++u) {
-            if (first || u % kChunkUnits == 0) {
-                // Sums so far to this chunk's power of two.  Where that is over 2^60 more
-                // than theirs, no further: the chunk is small beside what they were made
-                // of, and its sums are lowered instead.
-                bool low = false;
+            if (u == u0 || u % kChunkUnits == 0) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int e = up_next[n][i], to = first ? e : min(e, up[n][i] + 60);
-                        if (!first && to != up[n][i]) {
-                            const float f = exp2f((float)(to - up[n][i]));
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) acc[m][n][i] *= f, acc[m][n][i + 2] *= f;
-                        }
-                        up[n][i] = to;
-                        lower[n][i] = exp2f((float)(to - e));
-                        low |= to != e;
-                    }
-                held = __any_sync(0xffffffffu, low);
-                first = false;
+                    for (int i = 0; i < kRows; ++i)
+                        by[n][i] = __uint_as_float((uint32_t)(127 - up_next[n][i]) << 23);  // |e| <= 126
                 if ((u / kChunkUnits + 1) * kChunkUnits < u1) load_up(u / kChunkUnits + 1);
             }
             if (!mbar_wait(&full[stage], parity, &gave_up)) {
@@ -538,24 +529,25 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
                         }
                     }
                 }
-                if (held) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) d[m][n][i] *= lower[n][i % 2];
-                }
 #pragma unroll
                 for (int quad = 0; quad < 2; ++quad) {
                     const float4 sc = scales[quad];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[2 * quad][n][i] = fmaf(d[2 * quad][n][i], i < 2 ? sc.x : sc.y, acc[2 * quad][n][i]);
-                            acc[2 * quad + 1][n][i] =
-                                fmaf(d[2 * quad + 1][n][i], i < 2 ? sc.z : sc.w, acc[2 * quad + 1][n][i]);
+                        for (int n = 0; n < NT; ++n) {
+                            const float(&y)[4] = d[2 * quad + half][n];
+                            float(&to)[2 * kRows] = acc[2 * quad + half][n];
+                            const float s0 = half ? sc.z : sc.x, s1 = half ? sc.w : sc.y;
+                            if constexpr (kParts == 2) {
+                                const float low = by[n][0] * 0x1p-11f;
+                                to[0] = fmaf(fmaf(y[1], low, y[0] * by[n][0]), s0, to[0]);
+                                to[1] = fmaf(fmaf(y[3], low, y[2] * by[n][0]), s1, to[1]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    to[i] = fmaf(y[i] * by[n][i % 2], i < 2 ? s0 : s1, to[i]);
+                            }
                         }
                 }
             }
@@ -581,17 +573,12 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; i += kParts) {
-            const int r = (8 * n + 2 * t + i) / kParts;
+        for (int i = 0; i < kRows; ++i) {
+            const int r = (8 * n + 2 * t) / kParts + i;
             if (r >= a.M) continue;
-            const float down = __uint_as_float((uint32_t)(max(1, min(254, 137 - up[n][i]))) << 23);  // 2^10 / 2^e
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                float2 v = make_float2(acc[m][n][i], acc[m][n][i + 2]);
-                if (kParts == 2)
-                    v = make_float2(fmaf(acc[m][n][1], 0x1p-11f, acc[m][n][0]),
-                                    fmaf(acc[m][n][3], 0x1p-11f, acc[m][n][2]));
-                v.x *= down, v.y *= down;
+                const float2 v = make_float2(acc[m][n][i] * 1024.0f, acc[m][n][i + kRows] * 1024.0f);
                 const int c = col0 + 8 * g + 2 * m;
                 if (ranks > 1)
                     *reinterpret_cast<float2 *>(a.sums + ((int64_t)rank * a.M + r) * a.cols + c) = v;
