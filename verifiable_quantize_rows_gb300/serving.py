@@ -4,7 +4,9 @@ Products of a few rows with int4 weights that carry group scales, an int8
 key/value cache with the attention over it, and log probabilities of the
 logits with their gradient.  A thin binding like the rest of the package: each
 call checks and marshals its arguments and launches the library's kernels on
-the current PyTorch stream (or the ``stream`` given).  Activations are
+the current PyTorch stream (or the ``stream`` given, which waits for no other: its
+arguments have to be there and to stay; what the call makes is of that stream's
+memory).  Activations are
 float32, float16 or bfloat16 CUDA tensors whose last dimension is contiguous;
 their other strides are free.  Data-dependent conditions are OR-ed into
 ``dstatus`` (an int32 CUDA tensor, or None) as DSTATUS_* bits.  A call given no
@@ -95,9 +97,12 @@ def _rows(t) -> int:
 
 
 def _made(shape, dtype, device, stream):
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    # of `stream`'s memory: what the current stream has freed it may still be using
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
