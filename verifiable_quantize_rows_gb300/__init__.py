@@ -197,17 +197,25 @@ def _need(t, dtype, name):
 
 class Workspace:
     """A growable device byte buffer (256-byte aligned, from PyTorch).  One
-    per stream of concurrent calls; see the module notes on workspaces."""
+    per stream of concurrent calls; see the module notes on workspaces.  A
+    buffer that a call took while a graph was being captured is kept as long
+    as the Workspace, larger ones after it or not: the graph writes to it."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self.captured = False  # whether a graph may hold `buf`
+        self._kept = []        # earlier buffers that one may hold
 
     def get(self, nbytes: int):
         torch = _torch()
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.captured:
+                self._kept.append(self.buf)
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
+            self.captured = False
+        self.captured = self.captured or torch.cuda.is_current_stream_capturing()
         return self.buf
 
     def ptr_size(self, nbytes: int):

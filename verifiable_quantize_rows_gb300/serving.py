@@ -11,8 +11,9 @@ float32, float16 or bfloat16 CUDA tensors whose last dimension is contiguous;
 their other strides are free.  Data-dependent conditions are OR-ed into
 ``dstatus`` (an int32 CUDA tensor, or None) as DSTATUS_* bits.  A call given no
 ``workspace`` uses one of its stream's own, so calls on different streams may
-overlap; a graph keeps the one of the stream it was captured on, and graphs that
-may overlap need workspaces of their own.  There is no
+overlap; a graph uses the one of the stream it was captured on (whose buffer is kept
+for it when a later call needs a larger one), so graphs that may overlap with one another
+or with calls on that stream need workspaces of their own.  There is no
 CPU fallback and no autograd: gradients have calls of their own.
 """
 from __future__ import annotations
@@ -120,6 +121,7 @@ def _output(out, like, shape, stream):
 # The current stream's handle: the stream object that torch.cuda.current_stream
 # makes takes 2 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _stream(stream, device) -> int:
@@ -150,7 +152,7 @@ def _workspace(workspace, need: int, device, stream, handle: int):
         if workspace is None:
             workspace = _default_ws.setdefault((device.index, handle), _bsg.Workspace(device))
     buf = workspace.buf
-    if buf is None or buf.numel() < need:
+    if buf is None or buf.numel() < need or not workspace.captured and (stream is not None or _capturing()):
         with torch.cuda.stream(stream):  # whose memory it is to be (None: the current one's)
             buf = workspace.get(need)
     return buf.data_ptr(), buf.numel()
