@@ -1,0 +1,22 @@
+"""The serving calls at the largest sizes that they take."""
+import pytest
+import torch
+
+import verifiable_quantize_rows_gb300 as bsg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("N", [65535 * 512, 65535 * 512 + 1, (1 << 25) - 1, 1 << 25])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_products_of_the_most_columns(N, dtype):
+    """Each column's bits are those of a call on a few columns (65 rows of K are two units in one split)."""
+    K, M = 65, 5
+    g = torch.Generator("cuda").manual_seed(1)
+    Q, sc = bsg.wquant_groups(torch.randn((K, N), generator=g, device="cuda"), 32)
+    X = torch.randn((M, K), generator=g, device="cuda").to(dtype)
+    Y = bsg.wgroups_matvec(X, Q, sc, group=32)
+    for c in (0, 512 * 40000, 512 * 65534, N // 512 * 512 - 512):
+        part = slice(c, min(N, c + 1024))
+        q = Q[:, c // 2:(part.stop + 1) // 2]
+        assert torch.equal(Y[:, part], bsg.wgroups_matvec(X, q, sc[:, part], group=32))

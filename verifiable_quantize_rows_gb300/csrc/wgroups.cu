@@ -230,6 +230,7 @@ struct MatvecArgs {
     const int *up;
     float *sums;
     int cols;  // of a row of sums
+    int splits;  // of K
     const uint8_t *Q;
     int64_t ldq;
     const float *scale;
@@ -354,7 +355,8 @@ __device__ __forceinline__ void store_pair(const MatvecArgs &a, int r, int c, fl
     if (c + 1 < a.N) y[1] = from_f32<T>(a.relu && !(v.y > 0.0f) ? 0.0f : v.y);
 }
 
-// grid (splits of K, column tiles)
+// grid: splits of K x column tiles, the splits of a tile side by side (in one dimension:
+// 2^25 columns are one tile more than a grid's others hold)
 template <typename T, int NT, int kFolds, int kPerSm>
 __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     wgroups_matvec_kernel(const __grid_constant__ MatvecArgs a) {
@@ -366,11 +368,11 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     __shared__ uint64_t full[kStages];
     __shared__ int readers[kStages];  // warps that have yet to read a stage
     __shared__ volatile int gave_up, never;
-    const int rank = blockIdx.x, ranks = gridDim.x;
+    const int ranks = a.splits, rank = blockIdx.x % ranks;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
     const int units = (a.K + kUnit - 1) / kUnit;
     const int u0 = (int)((int64_t)units * rank / ranks), u1 = (int)((int64_t)units * (rank + 1) / ranks);
-    const int tile0 = blockIdx.y * kCtaCols, col0 = tile0 + warp * kWarpCols;  // the warp's first column
+    const int tile0 = (int)(blockIdx.x / ranks) * kCtaCols, col0 = tile0 + warp * kWarpCols;  // the warp's first column
     const bool busy = col0 < a.N;
     const int boxes = a.N - tile0 > kBoxCols ? 2 : 1;
     const int busy_warps = min(kWarps, (a.N - tile0 + kWarpCols - 1) / kWarpCols);
@@ -819,7 +821,7 @@ inline int matvec_splits(int64_t M, int64_t N, int64_t K, int nt, int per_sm) {
 }
 
 template <typename T, int NT, int kFolds, int kPerSm>
-cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
+cudaError_t launch_matvec(MatvecArgs &a, cudaStream_t st) {
     constexpr int smem = matvec_smem<NT, kFolds, kPerSm>();
     auto *kernel = wgroups_matvec_kernel<T, NT, kFolds, kPerSm>;
     static bool set[64] = {false};  // this kernel's attribute, on each device
@@ -832,8 +834,8 @@ cudaError_t launch_matvec(const MatvecArgs &a, cudaStream_t st) {
         set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    const int splits = matvec_splits(a.M, a.N, a.K, NT, kPerSm);
-    cfg.gridDim = dim3((unsigned)splits, (unsigned)(a.cols / kCtaCols));
+    const int splits = a.splits = matvec_splits(a.M, a.N, a.K, NT, kPerSm);
+    cfg.gridDim = dim3((unsigned)(a.cols / kCtaCols * splits));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -928,7 +930,7 @@ cudaError_t launch_wgroups_matvec(const void *X, int dtype, int64_t ldx, const u
         });
     }
     const int64_t groups = (K + group - 1) / group;
-    MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, 0, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
+    MatvecArgs a{{}, {}, nullptr, nullptr, nullptr, 0, 1, Q, ldq, scale, lds, Y, ldy, dstatus, (int)group, (int)M, (int)N, (int)K, relu, 0, 0};
     if (reinterpret_cast<uintptr_t>(Q) % 16 == 0 && ldq % 16 == 0)
         a.tma_q = make_tmap_2d(&a.q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Q, (uint64_t)(N + 1) / 2, (uint64_t)K,
                                (uint64_t)ldq, kBoxCols / 2, kUnit, CU_TENSOR_MAP_SWIZZLE_128B);
