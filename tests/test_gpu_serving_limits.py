@@ -20,3 +20,19 @@ def test_products_of_the_most_columns(N, dtype):
         part = slice(c, min(N, c + 1024))
         q = Q[:, c // 2:(part.stop + 1) // 2]
         assert torch.equal(Y[:, part], bsg.wgroups_matvec(X, q, sc[:, part], group=32))
+
+
+@pytest.mark.parametrize("T,heads", [(16, 40000), (1, 65535)])
+def test_attention_of_the_most_heads(T, heads):
+    """Each head's bits are those of a call on a few heads (one page: one chunk)."""
+    D, page, length = 256 if T > 1 else 32, 16, 16
+    g = torch.Generator("cuda").manual_seed(1)
+    codes = [torch.randint(-127, 128, (1, heads, page, D), generator=g, device="cuda").to(torch.int8) for _ in range(2)]
+    scales = [torch.rand((1, heads), generator=g, device="cuda") + 0.1 for _ in range(2)]
+    q = torch.randn((1, T, heads, D), generator=g, device="cuda") * 0.01
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.full((1,), length, dtype=torch.int32, device="cuda")
+    o = bsg.kv8_attend(q, bsg.Kv8Cache(*codes, *scales), table, lens)
+    for h in (0, heads // 2, 32760, heads - 8):
+        few = slice(h, h + 8)
+        cache = bsg.Kv8Cache(*[c[:, few].contiguous() for c in (*codes, *scales)])
+        assert torch.equal(o[:, :, few], bsg.kv8_attend(q[:, :, few], cache, table, lens))

@@ -1035,7 +1035,6 @@ cudaError_t launch_kv8_attend(const bsg_kv8_cache &c, const int32_t *table, int6
                               int dtype, int64_t B, int64_t T, int heads, float scale, float *lse,
                               void *ws, int32_t *dstatus, cudaStream_t st) {
     const AttendPlan p = attend_plan(c, table_ld, B, T, heads, dtype == BSG_F32 ? 2 : 1);
-    if ((int64_t)c.heads * p.row_tiles > 65535) return cudaErrorInvalidValue;
     AttendArgs a{c, table, table_ld, lens, q, out, dtype, (int)T, heads, p.rows, p.row_tiles,
                  p.width, p.splits, scale, lse, nullptr, nullptr, dstatus};
     a.part_o = static_cast<float *>(ws);
