@@ -36,3 +36,10 @@ def test_attention_of_the_most_heads(T, heads):
         few = slice(h, h + 8)
         cache = bsg.Kv8Cache(*[c[:, few].contiguous() for c in (*codes, *scales)])
         assert torch.equal(o[:, :, few], bsg.kv8_attend(q[:, :, few], cache, table, lens))
+
+
+def test_more_rows_than_a_call_takes():
+    """The refusal names no other call: none takes codes with group scales."""
+    Q, sc = bsg.wquant_groups(torch.randn((64, 40), device="cuda"), 32)
+    with pytest.raises(ValueError, match=r"at most 16 rows a call: X has 17$"):
+        bsg.wgroups_matvec(torch.ones((17, 64), device="cuda"), Q, sc, group=32)

@@ -192,7 +192,7 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     dev = X.device
     M, K = X.shape
     if M > MATVEC_MAX_M:
-        raise ValueError(f"at most {MATVEC_MAX_M} rows: X has {M} (use bsgemm_i8 for more)")
+        raise ValueError(f"at most {MATVEC_MAX_M} rows a call: X has {M}")
     if group < 0 or group % 32:
         raise ValueError("group must be a multiple of 32, or 0")
     if not isinstance(scale, torch.Tensor) or scale.dtype is not torch.float32 or scale.get_device() != dev.index:
