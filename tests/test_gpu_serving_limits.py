@@ -43,3 +43,19 @@ def test_more_rows_than_a_call_takes():
     Q, sc = bsg.wquant_groups(torch.randn((64, 40), device="cuda"), 32)
     with pytest.raises(ValueError, match=r"at most 16 rows a call: X has 17$"):
         bsg.wgroups_matvec(torch.ones((17, 64), device="cuda"), Q, sc, group=32)
+
+
+def test_rows_that_overlap_are_refused_by_name():
+    Q, sc = bsg.wquant_groups(torch.randn((64, 40), device="cuda"), 32)
+    x, row = torch.ones((3, 64), device="cuda"), torch.ones((1, 64), device="cuda").expand(3, 64)
+    close = torch.ones(200, device="cuda").as_strided((3, 64), (63, 1))
+    lse, out = torch.zeros(3, device="cuda"), torch.empty((1, 40), device="cuda").expand(3, 40)
+    for name, call in (("W", lambda: bsg.wquant_groups(row)), ("X", lambda: bsg.wgroups_matvec(row, Q, sc, group=32)),
+                       ("X", lambda: bsg.wgroups_matvec(close, Q, sc, group=32)),
+                       ("Q", lambda: bsg.wgroups_matvec(x, Q[:1].expand(64, 20), sc, group=32)),
+                       ("scale", lambda: bsg.wgroups_matvec(x, Q, sc[:1].expand(2, 40), group=32)),
+                       ("out", lambda: bsg.wgroups_matvec(x, Q, sc, group=32, out=out)),
+                       ("logits", lambda: bsg.logprobs(row)), ("logits", lambda: bsg.logprobs_backward(row, None, lse)),
+                       ("out", lambda: bsg.logprobs_backward(x, None, lse, out=row))):
+        with pytest.raises(ValueError, match=f"the rows of {name} must not overlap"):
+            call()

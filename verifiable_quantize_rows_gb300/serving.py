@@ -8,7 +8,8 @@ the current PyTorch stream (or the ``stream`` given, which waits for no other: i
 arguments have to be there and to stay; what the call makes is of that stream's
 memory).  Activations are
 float32, float16 or bfloat16 CUDA tensors whose last dimension is contiguous;
-their other strides are free.  Data-dependent conditions are OR-ed into
+their other strides are free, but for 2-D ones, whose rows must not overlap (an
+expanded row is refused).  Data-dependent conditions are OR-ed into
 ``dstatus`` (an int32 CUDA tensor, or None) as DSTATUS_* bits.  A call given no
 ``workspace`` uses one of its stream's own, so calls on different streams may
 overlap; a graph uses the one of the stream it was captured on (whose buffer is kept
@@ -92,9 +93,15 @@ def _exact(t, dtype, shape, name: str, device) -> int:
     raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
 
 
-def _rows(t) -> int:
+def _rows(t, name: str) -> int:
     """The leading dimension of a 2-D tensor (its row stride; one row has any)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    n = t.shape[1]
+    if t.shape[0] == 1:
+        return n
+    ld = t.stride(0)
+    if ld < n:
+        raise ValueError(f"the rows of {name} must not overlap: they are {ld} apart and {n} long")
+    return ld
 
 
 def _made(shape, dtype, device, stream):
@@ -173,7 +180,7 @@ def wquant_groups(W, group: int = 64, dstatus=None, stream=None):
     Q = _made((K, (half + 15) // 16 * 16), torch.uint8, W.device, stream)
     scale = _made(((K + group - 1) // group if group else 1, N), torch.float32, W.device, stream)
     _bsg._check(_lib().bsg_wquant_groups(
-        W.data_ptr(), K, N, _rows(W), group, Q.data_ptr(), Q.shape[1], scale.data_ptr(), N,
+        W.data_ptr(), K, N, _rows(W, "W"), group, Q.data_ptr(), Q.shape[1], scale.data_ptr(), N,
         _status(dstatus, W.device), _stream(stream, W.device)), "bsg_wquant_groups")
     return Q[:, :half], scale
 
@@ -210,8 +217,8 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     on = _stream(stream, dev)
     wp, wn = _workspace(workspace, need, dev, stream, on) if need else (None, 0)
     _bsg._check(_lib().bsg_wgroups_matvec(
-        X.data_ptr(), code, _rows(X), Q.data_ptr(), _rows(Q), scale.data_ptr(), _rows(scale),
-        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y), wp, wn, _status(dstatus, dev), on),
+        X.data_ptr(), code, _rows(X, "X"), Q.data_ptr(), _rows(Q, "Q"), scale.data_ptr(), _rows(scale, "scale"),
+        group, M, N, K, bool(relu), Y.data_ptr(), _rows(Y, "out"), wp, wn, _status(dstatus, dev), on),
         "bsg_wgroups_matvec")
     return Y
 
@@ -311,7 +318,7 @@ def logprobs(logits, target=None, top: int = 0, dstatus=None, stream=None) -> Lo
     tl = _made((M, top), torch.float32, dev, stream)
     ti = _made((M, top), torch.int32, dev, stream)
     _bsg._check(_lib().bsg_logprobs(
-        logits.data_ptr(), code, M, V, _rows(logits), tp, top, lp.data_ptr(), ent.data_ptr(),
+        logits.data_ptr(), code, M, V, _rows(logits, "logits"), tp, top, lp.data_ptr(), ent.data_ptr(),
         lse.data_ptr(), tl.data_ptr(), ti.data_ptr(), _status(dstatus, dev),
         _stream(stream, dev)), "bsg_logprobs")
     return Logprobs(lp, ent, lse, tl, ti)
@@ -334,6 +341,6 @@ def logprobs_backward(logits, target, lse, entropy=None, g_logprob=None, g_entro
     tp = None if target is None else _exact(target, torch.int64, (M,), "target", dev)
     D = _output(out, logits, (M, V), stream)
     _bsg._check(_lib().bsg_logprobs_backward(
-        logits.data_ptr(), code, M, V, _rows(logits), tp, *per_row, D.data_ptr(), _rows(D),
+        logits.data_ptr(), code, M, V, _rows(logits, "logits"), tp, *per_row, D.data_ptr(), _rows(D, "out"),
         _status(dstatus, dev), _stream(stream, dev)), "bsg_logprobs_backward")
     return D
