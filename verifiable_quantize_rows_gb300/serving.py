@@ -95,13 +95,13 @@ def _exact(t, dtype, shape, name: str, device) -> int:
 
 def _rows(t, name: str) -> int:
     """The leading dimension of a 2-D tensor (its row stride; one row has any)."""
-    n = t.shape[1]
-    if t.shape[0] == 1:
+    rows, n = t.shape
+    if rows == 1:
         return n
     ld = t.stride(0)
-    if ld < n:
-        raise ValueError(f"the rows of {name} must not overlap: they are {ld} apart and {n} long")
-    return ld
+    if ld >= n:
+        return ld
+    raise ValueError(f"the rows of {name} must not overlap: they are {ld} apart and {n} long")
 
 
 def _made(shape, dtype, device, stream):
@@ -128,7 +128,7 @@ def _output(out, like, shape, stream):
 # The current stream's handle: the stream object that torch.cuda.current_stream
 # makes takes 2 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_capturing = torch.cuda.is_current_stream_capturing
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _stream(stream, device) -> int:
