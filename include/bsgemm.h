@@ -349,7 +349,9 @@ bsg_status bsg_wquant_groups(const float *W, int64_t K, int64_t N, int64_t ldw, 
  *   Y[m][n] = sum over groups g of scale[g][n] * sum over k in g of X[m][k] q[k][n],
  * then max(., 0) with relu != 0.  Q, scale, group: as written by
  * bsg_wquant_groups, or by bsg_wquant_cols with bits = 4 and group = 0.
- * Y: M x N (ldy >= N), of X's type.  Inf or NaN in X sets
+ * Y: M x N (ldy >= N), of X's type; not X's memory.  Sums are f32; large products take f32
+ * activations to 22 bits, and those of 16 bits exactly, down to 2^-38 of the largest of
+ * 256 consecutive ones.  Inf or NaN in X sets
  * BSG_DSTATUS_NONFINITE (that row of Y is then unspecified).  N <= 2^25, K <=
  * 2^30.  `workspace`: bsg_wgroups_matvec_workspace_size(M, N, K) bytes,
  * 256-byte aligned (small products need none: 0, and any pointer; 0 too for sizes
@@ -411,6 +413,8 @@ bsg_status bsg_kv8_append(const bsg_kv8_cache *cache, const int32_t *table, int6
  * the positions up to its own:
  *   out = sum_j p_j v_j,  p = softmax_j(scale * q . k_j),  k_j, v_j = code * page scale.
  * A query at a negative position sees nothing: its output is 0, its lse -inf.
+ * Scores and sums are f32; f32 queries keep 22 bits of their row's largest,
+ * probabilities 22 bits of themselves, or 2^-36 of the largest.
  * q, out: B x T x heads x cache->dim; `heads` a multiple of cache->heads, query
  * head h reading key/value head h / (heads / cache->heads).  lse (may be NULL):
  * f32 [B][T][heads], the natural log of the softmax's denominator.  `workspace`:

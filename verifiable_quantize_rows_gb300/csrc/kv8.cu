@@ -54,8 +54,8 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
 //
 // Measured: prompts of 168 MB of bf16 keys and values 52 us (0.72 of the floor's rate; 58
 // with a floor by comparison), 64 sequences' single tokens 3.6 us.  What bounds prompts:
-// the issue at 16 warps an SM (a value costs its share of the maximum, the conversion, the
-// code and the packing); single tokens: the launch and two dependent reads (the table,
+// some 14 instructions a value (its share of the maximum, the conversion, the code and the
+// packing) at 16 warps an SM, which issue in 0.64 of the cycles; single tokens: the launch and two dependent reads (the table,
 // then the page's old scale).  (256 threads of 4 pieces: 55 to 61 us, the registers of 32
 // warps spill; reading every token twice: 210.)
 

@@ -28,7 +28,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
 }
 
 // The cache's scale of an absmax, one product where the unit of rows has a
-// quotient (the codes stay within +-127: m / s <= 127 (1 + 2^-22)).
+// quotient: by this operator's definition, and at times a last place beside the unit's,
+// so that a page's codes need not be the unit's of the same block (they stay within
+// +-127: m / s <= 127 (1 + 2^-22)).
 __device__ __forceinline__ float kv8_scale(float absmax) {
     return fmaxf(__fmul_rn(absmax, 1.0f / 127.0f), 1e-8f);
 }

@@ -184,14 +184,18 @@ __global__ void __launch_bounds__(kWarps * 32, kKept == 8 ? 24 / kWarps : 2)
 // loads alone took up to 13 us.)
 //
 // Measured on the device: 16384 x 16384, 8 f32 rows 50 us (0.45 of the floor's rate), 1
-// row 38, 8 bf16 rows 40 (0.56); 8191 x 12289, 5 bf16 rows 21.2 (0.37); 8192 x 8192, 8 f16
-// rows 15.7, 16 bf16 rows 22; 4096 x 4096, 8 f16 rows 9.2.  What bounds it: the issue of the
-// tensor and ALU pipes together.  The ALU takes an instruction every other cycle, and 6 of
-// them for 256 weights are 12 cycles (8 more, the flip by itself, cost 6 us of 42);
-// m16n8k16 takes 8 more for each 8 slots and overlaps them only in part (measured: 16
-// together with 4 f16 multiply-adds).  Weights that lie in L2 are no faster.  Below some
-// 4096 x 4096 it is the three launches and the first copies, about 5 us.  (The shift of a
-// 16-bit piece as a product on the FMA pipe: 44 us.)
+// row 38, 8 bf16 rows 40 (0.56); 8191 x 12289, 5 bf16 rows 21.0 (0.38); 8192 x 8192, 8 f16
+// rows 15.5, 16 bf16 rows 20; 4096 x 4096, 8 f16 rows 8.8.  What bounds it is no one thing: at
+// 8 f32 rows of 16384 x 16384 the tensor pipe is busy for 33 % of the cycles, ALU 31, FMA
+// 26, and an instruction issues in 0.47 of them.  The copies without the products took
+// 38 of 55 us when that was measured, the products without the copies 42: each well over the
+// floor, and overlapping in part.  What counts of the products: the ALU takes an
+// instruction every other cycle, and 6 of them for 256 weights are 12 cycles (8 more,
+// the flip by itself, cost 6 us of 42); m16n8k16 takes 8 more for each 8 slots (measured: 16
+// together with 4 f16 multiply-adds).  Weights that lie in L2 are no faster.  The parts'
+// launch and the join are 1 to 2 us each.  Below some 4096 x 4096 it is the three launches and
+// the first copies, about 5 us.  (The shift of a 16-bit piece as a product on the FMA
+// pipe: 44 us.)
 
 constexpr int kWarps = 8, kWarpCols = 64, kCtaCols = kWarps * kWarpCols;
 constexpr int kUnit = 64;
@@ -633,10 +637,12 @@ __global__ void __launch_bounds__(kJoinSides * 32) wgroups_join_kernel(const __g
 //
 // What bounds it: the launch, one round of loads and the cluster's two barriers at
 // the small end; 4 + M instructions per weight beyond.  Measured on the device, this
-// against the three launches: 768 x 2304 f32, 1 row 4.3 and 5.0 us, 2 rows 4.8 and 5.0, 4
-// rows 5.8 and 5.4; 768 x 768, 1 row 4.0 and 4.8, 4 rows 5.0 and 5.3; 2048 x 2048 bf16, 1
-// row 5.2 and 5.1, 2 rows 6.2 and 5.5; 3072 x 768, 1 row 5.9 and 5.5.  The host's part is
-// 3 us against 7.5.  So it is taken up to 2^22 products, rows counted as 1, 2 or 4.
+// against the three launches: 768 x 2304 f32, 1 row 4.1 and 4.5 us, 2 rows 4.4 and 4.6, 4
+// rows 5.0 and 4.9; 768 x 768, 1 row 3.9 and 4.2, 4 rows 4.8 and 4.6; 2048 x 2048 bf16, 1
+// row 5.0 and 4.6, 2 rows 4.8 (both the three launches); 3000 x 768, 1 row 5.6 and 4.7.  The
+// host's part is 3 us against 7.5.  So it is taken up to 2^22 products, rows counted as 1, 2
+// or 4: what it loses on the device at the upper end, which is all that a graph sees, is
+// less than what a call by itself saves.
 // (12 rows' instructions in a line, most of them run once: 4.7 us at 768 x 2304, 7.0
 // against 5.7 at 3072 x 768, waiting for instructions.  256 columns to a CTA, a quarter of
 // the lanes on K: 6.5 and 17.1.)

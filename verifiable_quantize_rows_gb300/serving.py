@@ -194,7 +194,8 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
                    stream=None, workspace=None):
     """Y = X . W_hat (+ReLU) for up to MATVEC_MAX_M rows of X (M x K) and a
     weight stored by wquant_groups -- or by wquant_cols with bits=4, with
-    group=0 and scale viewed as (1, N).  Y: M x N of X's dtype."""
+    group=0 and scale viewed as (1, N).  Y: M x N of X's dtype; `out` must not
+    share X's memory."""
     code = _activation(X, 2, "X")
     dev = X.device
     M, K = X.shape
