@@ -59,3 +59,11 @@ def test_rows_that_overlap_are_refused_by_name():
                        ("out", lambda: bsg.logprobs_backward(x, None, lse, out=row))):
         with pytest.raises(ValueError, match=f"the rows of {name} must not overlap"):
             call()
+
+
+def test_products_do_not_go_where_their_rows_are():
+    Q, sc = bsg.wquant_groups(torch.randn((64, 64), device="cuda"), 32)
+    x = torch.ones((2, 64), device="cuda")
+    with pytest.raises(ValueError, match="out must not share X's memory"):
+        bsg.wgroups_matvec(x, Q, sc, group=32, out=x)
+    assert (x == 1).all()

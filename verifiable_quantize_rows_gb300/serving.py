@@ -214,6 +214,8 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     if Q.shape != (K, (N + 1) // 2) or Q.stride(1) != 1 and Q.shape[1] != 1:
         raise ValueError("Q must be (K, ceil(N/2)) with contiguous rows")
     Y = _output(out, X, (M, N), stream)
+    if Y.data_ptr() == X.data_ptr():  # one CTA's columns of Y would be another's X
+        raise ValueError("out must not share X's memory")
     need = _matvec_bytes(M, N, K)
     on = _stream(stream, dev)
     wp, wn = _workspace(workspace, need, dev, stream, on) if need else (None, 0)
