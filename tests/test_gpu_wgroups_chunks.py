@@ -87,3 +87,14 @@ def test_a_large_sum_before_zeros_is_kept():
     want = X.double().sum(1, keepdim=True) * float(sc[0, 0]) * 7
     assert torch.isfinite(Y).all()
     assert ((Y.double() - want).abs() <= 2.0 ** -20 * want.abs()).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 768, 2304), (2, 768, 768), (4, 300, 1000), (3, 300, 1001)])
+def test_values_near_the_largest_in_the_small_form(M, K, N):
+    """X times a code is beyond f32 here; X times the weight is not."""
+    X = torch.zeros((M, K), device="cuda")
+    X[:, 5], X[:, K - 1] = 3e38, -1e38
+    Q, sc = bsg.wquant_groups(torch.full((K, N), 0.02, device="cuda"), 64)
+    Y = bsg.wgroups_matvec(X, Q, sc)
+    want = X.double().sum(1, keepdim=True) * float(sc[0, 0]) * 7
+    assert ((Y.double() - want).abs() <= 2.0 ** -20 * 4e38 * float(sc[0, 0]) * 7).all()

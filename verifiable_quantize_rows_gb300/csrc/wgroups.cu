@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(kJoinSides * 32) wgroups_join_kernel(const __g
 // columns (a word of 8 codes each), the 32 such parts of a CTA and the CTAs of a
 // cluster split K evenly, so that a lane has a few rows, loaded at once; their sums
 // meet by shuffles and in (distributed) shared memory, always in one order.  A code
-// becomes a float by the magic number 2^23, exactly, and X is used as it is, in f32.
+// becomes a float by the magic number 2^23, exactly, and X is used in f32, as 2^-10 of what
+// it is, so that a group's sum before its scale does not run over where Y would not.
 //
 // What bounds it: the launch, one round of loads and the cluster's two barriers at
 // the small end; 4 + M instructions per weight beyond.  Measured on the device, this
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) wgroups_small_kernel(const _
         const int m = e / n, k = e % n;
         const float x = m < a.M ? to_f32(static_cast<const T *>(a.X)[m * a.ldx + k0 + k]) : 0.0f;
         bad |= !isfinite(x);
-        x_s[e] = x;
+        x_s[e] = x * 0x1p-10f;
     }
     if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
     __syncthreads();
@@ -748,6 +749,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32) wgroups_small_kernel(const _
         }
     __syncthreads();
     auto store = [&](int m, int c, float y) {
+        y *= 1024.0f;
         if (m < a.M && tile0 + c < a.N)
             static_cast<T *>(a.Y)[m * a.ldy + tile0 + c] = from_f32<T>(a.relu && !(y > 0.0f) ? 0.0f : y);
     };
