@@ -321,8 +321,8 @@ bsg_status bsg_wdequant_cols(const void *Q, int64_t K, int64_t N, int64_t ldq, i
 
 /* ---- serving a model stored in codes ------------------------------------------ */
 
-/* The calls of a token-by-token decode step: products with weights stored as
- * int4 codes, an int8 key/value cache with the attention over it, and what is
+/* The calls of a prompt and of a token-by-token decode step: products with weights stored
+ * as int4 or int8 codes, an int8 key/value cache with the attention over it, and what is
  * reported of the logits.  Activations are f32, f16 or bf16 (`dtype` names the
  * type of every activation argument of a call); codes and scales are as
  * stored; sums, softmax statistics and scales are f32.  The results are the
@@ -363,6 +363,24 @@ bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const
                               int64_t ldq, const float *scale, int64_t lds, int group, int64_t M,
                               int64_t N, int64_t K, int relu, void *Y, int64_t ldy,
                               void *workspace, size_t ws_bytes, int32_t *dstatus, void *stream);
+
+/* Y = X . W_hat in 8-bit integers for any number of rows (tokens), with a scale for
+ * each token and each column: a weight stored by bsg_wquant_cols with bits = 8, and X
+ * quantized row by row by the unit's step 1,
+ *   q = floor(RN(RN(x * inv) + 0.5)), scale and inv as for bsg_quantize_rows (x: X's
+ *   value as f32);   S = sum_k q[m][k] Q[k][n], exact;
+ *   y = RN(RN(f32(S) * scale_m) * scale[n]), (y > 0 ? y : +0) with relu, rounded to X's type.
+ * X: M x K (ldx >= K); Q: K x N int8 (ldq >= N); scale: f32[N]; Y: M x N (ldy >= N), of X's
+ * type, not X's memory.  The same bits on every run and for any M: a token's row of Y
+ * does not depend on the others'.  Inf or NaN in X sets BSG_DSTATUS_NONFINITE (that row of Y
+ * is then unspecified).  M, N < 2^31, M N <= 2^40; K <= BSG_MAX_K.  `workspace`:
+ * bsg_wcols_matmul_workspace_size(M, N, K) bytes, 256-byte aligned (0 for sizes that the
+ * call refuses).  Fastest with Q 16-byte aligned and ldq a multiple of 16. */
+size_t bsg_wcols_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
+bsg_status bsg_wcols_matmul(const void *X, bsg_dtype dtype, int64_t ldx, const int8_t *Q,
+                            int64_t ldq, const float *scale, int64_t M, int64_t N, int64_t K,
+                            int relu, void *Y, int64_t ldy, void *workspace, size_t ws_bytes,
+                            int32_t *dstatus, void *stream);
 
 /* A key/value cache in int8 codes: a pool of pages of `page_tokens` tokens,
  * with one scale for each page and head.  Layout: k, v int8
@@ -430,6 +448,46 @@ bsg_status bsg_kv8_attend(const bsg_kv8_cache *cache, const int32_t *table, int6
                           bsg_dtype dtype, int64_t B, int64_t T, int heads, float scale,
                           float *lse, void *workspace, size_t ws_bytes, int32_t *dstatus,
                           void *stream);
+
+/* Attention of any number of new tokens over the cache, through a sliding window with
+ * a few first tokens that stay visible.  counts[b] (int32, DEVICE; NULL: T for all) of q's T
+ * tokens of sequence b are there, the newest of its lens[b] cached ones: query t stands at
+ * position i = lens[b] - counts[b] + t and sees
+ *   j <= i   with   j > i - window or j < sinks      (window 0: every j <= i).
+ * The rest is as for bsg_kv8_attend: a query that sees no position gives 0 and lse -inf;
+ * scores and sums are f32, f32 queries keep 22 bits of their row's largest, and
+ * probabilities keep 22 bits (of 16 tokens or fewer, and of f32 and f16) or 11 (of longer bf16
+ * ones) of themselves, or 2^-36 of the largest.  Tokens t >= counts[b] are not read, and
+ * nothing is written for them.  A count that is not in 0..T leaves its sequence out and sets
+ * BSG_DSTATUS_RANGE; lengths and pages out of range as for bsg_kv8_attend (of pages that some
+ * query sees).  T * (heads / cache->heads) < 2^31.  window, sinks >= 0.
+ * `workspace`: bsg_kv8_attend_window_workspace_size bytes. */
+size_t bsg_kv8_attend_window_workspace_size(const bsg_kv8_cache *cache, int64_t table_ld,
+                                            int64_t B, int64_t T, int heads, int window, int sinks);
+bsg_status bsg_kv8_attend_window(const bsg_kv8_cache *cache, const int32_t *table,
+                                 int64_t table_ld, const int32_t *lens, const int32_t *counts,
+                                 const bsg_tokens *q, const bsg_tokens *out, bsg_dtype dtype,
+                                 int64_t B, int64_t T, int heads, int window, int sinks,
+                                 float scale, float *lse, void *workspace, size_t ws_bytes,
+                                 int32_t *dstatus, void *stream);
+
+/* bsg_kv8_attend for sequences that all begin with the same tokens, whose codes are read
+ * once for all of them: the prefix's *prefix_len tokens (int32, DEVICE) lie in the pages
+ * prefix[0..prefix_pages-1] (int32, DEVICE), a sequence's own ones, lens[b] with the new,
+ * in its table's pages from the start of the first.  Query t of sequence b sees the whole
+ * prefix and its own positions up to lens[b] - T + t; one whose position is negative is
+ * none: it sees nothing, not the prefix either (a slot of length 0 is idle).  A prefix
+ * length out of range is cut to the pages' and sets BSG_DSTATUS_RANGE.  The rest is as
+ * for bsg_kv8_attend.  `workspace`: bsg_kv8_attend_shared_workspace_size bytes. */
+size_t bsg_kv8_attend_shared_workspace_size(const bsg_kv8_cache *cache, int64_t prefix_pages,
+                                            int64_t table_ld, int64_t B, int64_t T, int heads);
+bsg_status bsg_kv8_attend_shared(const bsg_kv8_cache *cache, const int32_t *prefix,
+                                 int64_t prefix_pages, const int32_t *prefix_len,
+                                 const int32_t *table, int64_t table_ld, const int32_t *lens,
+                                 const bsg_tokens *q, const bsg_tokens *out, bsg_dtype dtype,
+                                 int64_t B, int64_t T, int heads, float scale, float *lse,
+                                 void *workspace, size_t ws_bytes, int32_t *dstatus,
+                                 void *stream);
 
 /* What is reported of logits x (M x V, ldl >= V), per row:
  *   lse = log sum_j exp x_j;  logprob = x_target - lse;  entropy = -sum_j p_j log p_j;

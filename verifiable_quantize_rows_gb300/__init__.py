@@ -27,8 +27,8 @@ __all__ = ["BsgError", "load", "exported_symbols", "quantize_rows", "quantize_co
            "gemm_s32", "epilogue", "bsgemm_i8", "bsgemm_i8_ex", "bsgemm_i8_host",
            "bsgemm_i8_quantize", "bsgemm_i8_contract", "launch_count", "selftest_scales", "gemm_tile_width", "hash_f32", "probe_hash", "probe_hash_async", "workspace_size", "Workspace",
            "DSTATUS_NONFINITE", "DSTATUS_TIMEOUT", "DSTATUS_RANGE", "MAX_K",
-           "Kv8Cache", "wquant_groups", "wgroups_matvec", "kv8_append", "kv8_attend", "logprobs",
-           "logprobs_backward"]
+           "Kv8Cache", "wquant_groups", "wgroups_matvec", "wcols_matmul", "kv8_append", "kv8_attend",
+           "kv8_attend_window", "kv8_attend_shared", "logprobs", "logprobs_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libbsgemm.so")
@@ -128,6 +128,15 @@ def _declare(lib):
         "bsg_kv8_attend_workspace_size": ([_cp, _i64, _i64, _i64, _i32], _sz),
         "bsg_kv8_attend": ([_cp, _vp, _i64, _vp, _cp, _cp, _i32, _i64, _i64, _i32, ctypes.c_float,
                             _vp, _vp, _sz, _vp, _vp], _i32),
+        "bsg_wcols_matmul_workspace_size": ([_i64, _i64, _i64], _sz),
+        "bsg_wcols_matmul": ([_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp,
+                              _sz, _vp, _vp], _i32),
+        "bsg_kv8_attend_window_workspace_size": ([_cp, _i64, _i64, _i64, _i32, _i32, _i32], _sz),
+        "bsg_kv8_attend_window": ([_cp, _vp, _i64, _vp, _vp, _cp, _cp, _i32, _i64, _i64, _i32, _i32, _i32,
+                                   ctypes.c_float, _vp, _vp, _sz, _vp, _vp], _i32),
+        "bsg_kv8_attend_shared_workspace_size": ([_cp, _i64, _i64, _i64, _i64, _i32], _sz),
+        "bsg_kv8_attend_shared": ([_cp, _vp, _i64, _vp, _vp, _i64, _vp, _cp, _cp, _i32, _i64, _i64, _i32,
+                                   ctypes.c_float, _vp, _vp, _sz, _vp, _vp], _i32),
         "bsg_logprobs": ([_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                           _vp], _i32),
         "bsg_logprobs_backward": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
@@ -629,8 +638,8 @@ def probe_hash(seed: int, M: int = 1024, N: int = 1024, K: int = 1024, stream=No
 # ---------------------------------------------------------------------------
 # The serving calls live in serving.py, which imports torch at its top; they
 # load on first use, so that importing this package still does not.
-_SERVING = ("Kv8Cache", "Logprobs", "wquant_groups", "wgroups_matvec", "kv8_append", "kv8_attend",
-            "logprobs", "logprobs_backward", "MATVEC_MAX_M", "KV8_MAX_T", "MAX_TOP")
+_SERVING = ("Kv8Cache", "Logprobs", "wquant_groups", "wgroups_matvec", "wcols_matmul", "kv8_append",
+            "kv8_attend", "kv8_attend_window", "kv8_attend_shared", "logprobs", "logprobs_backward", "MATVEC_MAX_M", "KV8_MAX_T", "MAX_TOP")
 
 
 def __getattr__(name):

@@ -125,6 +125,25 @@ cudaError_t launch_kv8_attend(const bsg_kv8_cache &c, const int32_t *table, int6
                               const int32_t *lens, const bsg_tokens &q, const bsg_tokens &out,
                               int dtype, int64_t B, int64_t T, int heads, float scale, float *lse,
                               void *ws, int32_t *dstatus, cudaStream_t st);
+size_t wcols_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int8_t *Q, int64_t ldq,
+                                const float *scale, int64_t M, int64_t N, int64_t K, int relu,
+                                void *Y, int64_t ldy, void *ws, int32_t *dstatus, cudaStream_t st);
+size_t kv8_window_workspace_bytes(const bsg_kv8_cache &c, int64_t table_ld, int64_t B, int64_t T,
+                                  int heads, int window, int sinks);
+cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
+                                     const int32_t *lens, const int32_t *counts, const bsg_tokens &q,
+                                     const bsg_tokens &out, int dtype, int64_t B, int64_t T,
+                                     int heads, int window, int sinks, float scale, float *lse,
+                                     void *ws, int32_t *dstatus, cudaStream_t st);
+size_t kv8_shared_workspace_bytes(const bsg_kv8_cache &c, int64_t prefix_pages, int64_t table_ld,
+                                  int64_t B, int64_t T, int heads);
+cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *prefix,
+                                     int64_t prefix_pages, const int32_t *prefix_len,
+                                     const int32_t *table, int64_t table_ld, const int32_t *lens,
+                                     const bsg_tokens &q, const bsg_tokens &out, int dtype,
+                                     int64_t B, int64_t T, int heads, float scale, float *lse,
+                                     void *ws, int32_t *dstatus, cudaStream_t st);
 cudaError_t launch_logprobs(const void *logits, int dtype, int64_t M, int64_t V, int64_t ldl,
                             const int64_t *target, int top, float *logprob, float *entropy,
                             float *lse, float *top_logprob, int32_t *top_id, int32_t *dstatus,
@@ -155,8 +174,9 @@ int gemm_group_m();
 int gemm_snake();
 // The tensor-core GEMM.  Aop: M x ldk f16, Bop: N x ldk f16 (both K-major,
 // ldk = operand_ld(K)).  mode 0: C = epi(S, sa, sb) (+ReLU) as float;
-// mode 1: S stored as int32.  sa / sb must hold round_up(M, kBM) /
-// round_up(N, kBN) + kBN floats (mode 0).  `tile_width` 64/128/192/256
+// mode 1: S stored as int32; modes 2 and 3: as mode 0, C rounded once more, to f16 or
+// bf16 (a single GEMM only).  sa / sb must hold round_up(M, kBM) /
+// round_up(N, kBN) + kBN floats (but for mode 1).  `tile_width` 64/128/192/256
 // fixes the tile width, 0 leaves it to gemm_tile_width.  `ticket`: two unsigned ints of
 // device memory, the tile counter: zero before the first launch on it (the
 // quantize step that fills a unit workspace zeroes it), and zero again after

@@ -54,6 +54,7 @@
 // BSG_DSTATUS_TIMEOUT, drains its copies and MMAs, frees tensor memory and
 // returns.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <stdint.h>
@@ -170,7 +171,7 @@ struct Params {
     Prob prob[NP];
     int nprob;
     int num_units;  // tiles of the launch, all GEMMs
-    int mode;       // 0: f32 epilogue, 1: int32 accumulators
+    int mode;       // 0: f32 epilogue, 1: int32 accumulators, 2, 3: f32 rounded to f16, bf16
     int group_m;    // tile raster: m-units per group
     int snake;      // 1: odd raster groups take their n-tiles in reverse
     int32_t *dstatus;
@@ -314,7 +315,64 @@ __device__ __forceinline__ void emit_box(const Prob &p, const CUtensorMap *tmap_
     }
 }
 
-template <int BN, bool PAIR, int NP>
+// The same for 16-bit outputs: the 32 values of a thread's row, rounded once more,
+// in a box of 64-byte rows (64-byte swizzle; the first half of a staging box).
+template <int NBOX>
+__device__ __forceinline__ void emit_half_box(const Prob &p, const CUtensorMap *tmap_c, uint8_t *boxes,
+                                              const uint32_t (&v)[32], bool bf16, int row0, int col0,
+                                              int lane, int &nstored) {
+    if (nstored >= NBOX) {  // TMA stores only
+        if (lane == 0) {
+            if (NBOX == 1)
+                bulk_wait_read0();
+            else
+                bulk_wait_read1();
+        }
+        __syncwarp();
+    }
+    uint8_t *box = boxes + (nstored % NBOX) * kEpiBufBytes;
+    uint32_t h[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float x = __uint_as_float(v[2 * j]), y = __uint_as_float(v[2 * j + 1]);
+        if (bf16) {
+            const __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
+            h[j] = *reinterpret_cast<const uint32_t *>(&r);
+        } else {
+            const __half2 r = __floats2half2_rn(x, y);
+            h[j] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) =
+            make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+    if (p.tma_store) {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tmap_c, box, col0, row0);
+            bulk_commit();
+        }
+        ++nstored;
+        return;
+    }
+    __syncwarp();  // rows not 16-byte aligned: 32 columns of a row at a time
+    const int col = col0 + lane;
+    if (col < p.N) {
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + (int64_t)row0 * p.ldo + col;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            if (row0 + r >= p.M) break;
+            dst[(int64_t)r * p.ldo] = *reinterpret_cast<const uint16_t *>(
+                box + r * 64 + ((lane >> 3 ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2);
+        }
+    }
+    __syncwarp();
+}
+
+// HALF: modes 2 and 3.
+template <int BN, bool PAIR, int NP, bool HALF>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_tc_kernel(const __grid_constant__ Maps<NP> maps, const __grid_constant__ Params<NP> p) {
     using K = Cfg<BN, PAIR>;
@@ -625,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float bl[K::kPieces];
 #pragma unroll
             for (int piece = 0; piece < K::kPieces; ++piece) bl[piece] = 0.0f;
-            if (p.mode == 0 && rows_here) {
+            if ((HALF || p.mode == 0) && rows_here) {
                 a = __ldg(pr.sa + row0 + lane);
 #pragma unroll
                 for (int piece = 0; piece < K::kPieces; ++piece)
@@ -636,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The f32 epilogue then needs no conversion (float->int and back
             // run at a fraction of the ALU rate); adding +0 turns a -0 sum
             // (all products -0) into f32(0) = +0.
-            const bool f32_sums = num_chunks == 1 && p.mode == 0;
+            const bool f32_sums = num_chunks == 1 && (HALF || p.mode == 0);
             // ---- drain every chunk into int32 sums (or, f32_sums, f32(S))
             uint32_t acc[K::kWarpCols];  // int32 or f32 bit patterns
             for (int c = 0; c < num_chunks; ++c) {
@@ -693,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int piece = 0; piece < K::kPieces; ++piece) {
                 uint32_t(&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(&acc[piece * 32]);
                 const int col0 = colh + piece * 32;
-                if (p.mode == 0) {
+                if (HALF || p.mode == 0) {
                     // in place: the sums become the output bits
                     if (f32_sums)
                         epi_piece<true>(v, bl[piece], a, pr.relu);
@@ -705,7 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (col0 + j < pr.N) rmax = max(rmax, v[j] & 0x7fffffffu);
                     }
                 }
-                emit_box<K::kBoxes>(pr, &maps.c[pi], boxes, v, row0, col0, lane, nstored);
+                if (HALF)
+                    emit_half_box<K::kBoxes>(pr, &maps.c[pi], boxes, v, p.mode == 3, row0, col0, lane, nstored);
+                else
+                    emit_box<K::kBoxes>(pr, &maps.c[pi], boxes, v, row0, col0, lane, nstored);
             }
             // exact in any order: the max of non-negative bit patterns
             if (pr.rowmax && row0 + lane < pr.M) atomicMax(pr.rowmax + row0 + lane, rmax);
@@ -728,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ host side
-template <int BN, bool PAIR, int NP>
+template <int BN, bool PAIR, int NP, bool HALF>
 cudaError_t launch_bn(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, cudaStream_t st) {
     using C = Cfg<BN, PAIR>;
     // per device: the shared-memory attribute, and how many CTAs (pairs)
@@ -754,7 +815,7 @@ cudaError_t launch_bn(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
     if (!ready[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_tc_kernel<BN, PAIR, NP>,
+        cudaError_t e = cudaFuncSetAttribute(gemm_tc_kernel<BN, PAIR, NP, HALF>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)C::kSmemBytes);
         if (e != cudaSuccess) return e;
@@ -762,7 +823,7 @@ cudaError_t launch_bn(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, cudaSt
         if (PAIR) {
             cfg.gridDim = dim3((unsigned)(2 * units), 1, 1);
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, gemm_tc_kernel<BN, PAIR, NP>, &cfg) == cudaSuccess &&
+            if (cudaOccupancyMaxActiveClusters(&n, gemm_tc_kernel<BN, PAIR, NP, HALF>, &cfg) == cudaSuccess &&
                 n > 0 && n < units)
                 units = n;
             cudaGetLastError();
@@ -787,7 +848,7 @@ cudaError_t launch_bn(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, cudaSt
     p.num_units = units_total;
     const int units = p.num_units < max_units[dev] ? p.num_units : max_units[dev];
     cfg.gridDim = dim3((unsigned)(units * (PAIR ? 2 : 1)), 1, 1);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_tc_kernel<BN, PAIR, NP>, maps, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_tc_kernel<BN, PAIR, NP, HALF>, maps, p);
     count_launches(1);
     return e;
 }
@@ -795,8 +856,12 @@ cudaError_t launch_bn(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, cudaSt
 template <int BN, int NP>
 cudaError_t launch_width(Maps<NP> &maps, Params<NP> &p, const GemmJob *jobs, bool pair,
                          cudaStream_t st) {
-    if (pair) return launch_bn<BN, true, NP>(maps, p, jobs, st);
-    return launch_bn<BN, false, NP>(maps, p, jobs, st);
+    if constexpr (NP == 1)
+        if (p.mode >= 2)
+            return pair ? launch_bn<BN, true, NP, true>(maps, p, jobs, st)
+                        : launch_bn<BN, false, NP, true>(maps, p, jobs, st);
+    if (pair) return launch_bn<BN, true, NP, false>(maps, p, jobs, st);
+    return launch_bn<BN, false, NP, false>(maps, p, jobs, st);
 }
 
 }  // namespace
@@ -891,16 +956,18 @@ cudaError_t launch_group_np(const GemmJob *jobs, int n, int mode, int32_t *dstat
             return cudaErrorInvalidValue;
         // TMA stores need 16-byte aligned rows, and a row length that is a
         // whole number of 16-byte chunks: at the right edge the store writes
-        // whole chunks, so with N % 4 != 0 it would write up to 3 elements
+        // whole chunks, so with N % 4 != 0 it would write up to 3 elements (of f32)
         // past column N - 1 into the caller's row padding (ldc > N)
-        const bool aligned = ((j.ldo * 4) % 16 == 0) && ((j.N * 4) % 16 == 0) &&
+        const int esz = mode >= 2 ? 2 : 4;
+        const bool aligned = ((j.ldo * esz) % 16 == 0) && ((j.N * esz) % 16 == 0) &&
                              (reinterpret_cast<uintptr_t>(j.out) % 16 == 0);
         Prob &q = p.prob[i];
         q.tma_store = aligned && make_tmap_2d(&maps.c[i],
-                                              mode == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                        : CU_TENSOR_MAP_DATA_TYPE_INT32,
-                                              4, j.out, (uint64_t)j.N, (uint64_t)j.M,
-                                              (uint64_t)j.ldo, 32, 32)
+                                              mode == 0   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                              : mode == 1 ? CU_TENSOR_MAP_DATA_TYPE_INT32
+                                                          : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                                              esz, j.out, (uint64_t)j.N, (uint64_t)j.M, (uint64_t)j.ldo, 32, 32,
+                                              mode >= 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)
                           ? 1
                           : 0;
         q.M = (int)j.M;
@@ -931,7 +998,7 @@ cudaError_t launch_group_np(const GemmJob *jobs, int n, int mode, int32_t *dstat
 
 cudaError_t launch_gemm_tc_group(const GemmJob *jobs, int n, int mode, int32_t *dstatus,
                                  unsigned int *ticket, cudaStream_t st, int tile_width) {
-    if (n < 1 || n > kMaxGroup) return cudaErrorInvalidValue;
+    if (n < 1 || n > kMaxGroup || (mode >= 2 && n > 1)) return cudaErrorInvalidValue;
     // a single GEMM gets the kernel compiled for one
     if (n == 1) return launch_group_np<1>(jobs, n, mode, dstatus, ticket, st, tile_width);
     return launch_group_np<kMaxGroup>(jobs, n, mode, dstatus, ticket, st, tile_width);

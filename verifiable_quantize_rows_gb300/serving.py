@@ -27,8 +27,8 @@ import torch
 
 import verifiable_quantize_rows_gb300 as _bsg
 
-__all__ = ["Kv8Cache", "wquant_groups", "wgroups_matvec", "kv8_append", "kv8_attend", "logprobs",
-           "logprobs_backward", "Logprobs", "MATVEC_MAX_M", "KV8_MAX_T", "MAX_TOP"]
+__all__ = ["Kv8Cache", "wquant_groups", "wgroups_matvec", "wcols_matmul", "kv8_append", "kv8_attend",
+           "kv8_attend_window", "kv8_attend_shared", "logprobs", "logprobs_backward", "Logprobs", "MATVEC_MAX_M", "KV8_MAX_T", "MAX_TOP"]
 
 MATVEC_MAX_M = 16
 KV8_MAX_T = 16
@@ -226,6 +226,39 @@ def wgroups_matvec(X, Q, scale, group: int = 64, relu: bool = False, out=None, d
     return Y
 
 
+@functools.lru_cache(maxsize=1024)
+def _matmul_bytes(M: int, N: int, K: int) -> int:
+    return _lib().bsg_wcols_matmul_workspace_size(M, N, K)
+
+
+def wcols_matmul(X, Q, scale, relu: bool = False, out=None, dstatus=None, stream=None, workspace=None):
+    """Y = X . W_hat (+ReLU) in 8-bit integers for any number of rows of X (M x K)
+    and a weight stored by wquant_cols with bits=8: Q int8 (K, N), scale float32
+    (N,).  Each row of X is quantized by itself, by quantize_rows' rule; the sums of
+    code products are exact.  Y: M x N of X's dtype; `out` must not share X's
+    memory."""
+    code = _activation(X, 2, "X")
+    dev = X.device
+    M, K = X.shape
+    if not isinstance(Q, torch.Tensor) or Q.dtype is not torch.int8 or Q.get_device() != dev.index:
+        raise TypeError(f"Q must be an int8 tensor on {dev}")
+    if Q.dim() != 2 or Q.shape[0] != K or not Q.shape[1] or Q.stride(1) != 1 and Q.shape[1] != 1:
+        raise ValueError("Q must be (K, N) with contiguous rows")
+    if K > _bsg.MAX_K:
+        raise ValueError(f"at most {_bsg.MAX_K} columns of X")
+    N = Q.shape[1]
+    sp = _exact(scale, torch.float32, (N,), "scale", dev)
+    Y = _output(out, X, (M, N), stream)
+    if Y.data_ptr() == X.data_ptr():
+        raise ValueError("out must not share X's memory")
+    on = _stream(stream, dev)
+    wp, wn = _workspace(workspace, _matmul_bytes(M, N, K), dev, stream, on)
+    _bsg._check(_lib().bsg_wcols_matmul(
+        X.data_ptr(), code, _rows(X, "X"), Q.data_ptr(), _rows(Q, "Q"), sp, M, N, K, bool(relu), Y.data_ptr(),
+        _rows(Y, "out"), wp, wn, _status(dstatus, dev), on), "bsg_wcols_matmul")
+    return Y
+
+
 # ---------------------------------------------------------------------------
 def _cache(cache, device):
     """(bsg_kv8_cache, heads, page_tokens, dim), checked."""
@@ -302,6 +335,95 @@ def kv8_attend(q, cache, table, lens, scale: float | None = None, out=None, lse=
         D ** -0.5 if scale is None else scale,
         None if lse is None else _exact(lse, torch.float32, (B, T, H), "lse", dev), wp, wn,
         _status(dstatus, dev), on), "bsg_kv8_attend")
+    return O
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_bytes(pages: int, heads: int, page_tokens: int, dim: int, width: int, B: int, T: int, H: int,
+                  window: int, sinks: int) -> int:
+    anything = _CACHE.pack(256, 256, 256, 256, pages, heads, page_tokens, dim)
+    return _lib().bsg_kv8_attend_window_workspace_size(anything, width, B, T, H, window, sinks)
+
+
+def _apart(O, q):
+    if O.data_ptr() == q.data_ptr():
+        raise ValueError("out must not share q's memory")
+
+
+def kv8_attend_window(q, cache, table, lens, window: int = 0, sinks: int = 0, counts=None,
+                      scale: float | None = None, out=None, lse=None, dstatus=None, stream=None,
+                      workspace=None):
+    """Attention of any number of new tokens of each sequence over the cache: a
+    query at position i sees the positions j <= i with j > i - window or j < sinks
+    (window 0: all of them).  q: (batch, T, heads, dim), heads a multiple of the
+    cache's; counts: int32 (batch,), how many of the T tokens of each sequence are
+    there (None: all); lens: int32 (batch,), tokens cached with the new ones.
+    Returns out, of q's shape and dtype (not q's memory), in which tokens past a
+    sequence's count are left as they were; a query that sees no position gives
+    zeros.  lse: float32 (batch, T, heads) to be filled, or None."""
+    code = _activation(q, 4, "q")
+    dev = q.device
+    B, T, H, D = q.shape
+    c, heads, page_tokens, dim = _cache(cache, dev)
+    if D != dim or H % heads:
+        raise ValueError(f"the cache has {heads} heads of {dim}")
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError("window and sinks must be 0 or more, and below 2^31")
+    O = _output(out, q, q.shape, stream)
+    _apart(O, q)
+    tp, width = _table(table, B, dev), table.shape[1]
+    on = _stream(stream, dev)
+    wp, wn = _workspace(workspace, _window_bytes(cache[0].shape[0], heads, page_tokens, dim, width, B, T, H,
+                                                 window, sinks), dev, stream, on)
+    _bsg._check(_lib().bsg_kv8_attend_window(
+        c, tp, width, _exact(lens, torch.int32, (B,), "lens", dev),
+        None if counts is None else _exact(counts, torch.int32, (B,), "counts", dev), _tokens(q), _tokens(O),
+        code, B, T, H, window, sinks, D ** -0.5 if scale is None else scale,
+        None if lse is None else _exact(lse, torch.float32, (B, T, H), "lse", dev), wp, wn,
+        _status(dstatus, dev), on), "bsg_kv8_attend_window")
+    return O
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_bytes(pages: int, heads: int, page_tokens: int, dim: int, prefix: int, width: int, B: int, T: int,
+                  H: int) -> int:
+    anything = _CACHE.pack(256, 256, 256, 256, pages, heads, page_tokens, dim)
+    return _lib().bsg_kv8_attend_shared_workspace_size(anything, prefix, width, B, T, H)
+
+
+def kv8_attend_shared(q, cache, prefix, prefix_len, table, lens, scale: float | None = None, out=None,
+                      lse=None, dstatus=None, stream=None, workspace=None):
+    """kv8_attend for sequences that begin with the same tokens, whose part of the
+    cache is read once for all of them.  prefix: int32 (pages,), the pages of the
+    common tokens; prefix_len: int32 (1,), how many there are.  table, lens: each
+    sequence's own tokens behind them, which begin a page of their own; lens counts
+    these alone, with the new ones.  A query sees the whole prefix and its own
+    sequence up to itself; one before its sequence's first own token (lens below T; a
+    slot of length 0 is idle) gives zeros.  q, out (not q's memory) and lse are
+    kv8_attend's."""
+    code = _activation(q, 4, "q")
+    dev = q.device
+    B, T, H, D = q.shape
+    c, heads, page_tokens, dim = _cache(cache, dev)
+    if D != dim or H % heads:
+        raise ValueError(f"the cache has {heads} heads of {dim}")
+    if T > KV8_MAX_T:
+        raise ValueError(f"at most {KV8_MAX_T} tokens a sequence: q has {T}")
+    if not isinstance(prefix, torch.Tensor) or prefix.dim() != 1 or not prefix.numel():
+        raise ValueError("prefix must be (pages of the prefix,), one page at least")
+    O = _output(out, q, q.shape, stream)
+    _apart(O, q)
+    tp, width, pages = _table(table, B, dev), table.shape[1], prefix.shape[0]
+    on = _stream(stream, dev)
+    wp, wn = _workspace(workspace, _shared_bytes(cache[0].shape[0], heads, page_tokens, dim, pages, width, B, T, H),
+                        dev, stream, on)
+    _bsg._check(_lib().bsg_kv8_attend_shared(
+        c, _exact(prefix, torch.int32, (pages,), "prefix", dev), pages,
+        _exact(prefix_len, torch.int32, (1,), "prefix_len", dev), tp, width,
+        _exact(lens, torch.int32, (B,), "lens", dev), _tokens(q), _tokens(O), code, B, T, H,
+        D ** -0.5 if scale is None else scale,
+        None if lse is None else _exact(lse, torch.float32, (B, T, H), "lse", dev), wp, wn,
+        _status(dstatus, dev), on), "bsg_kv8_attend_shared")
     return O
 
 
