@@ -1,122 +1,197 @@
 // kv8_more.cu -- attention over the int8 cache for any number of query tokens through a
-// window with sinks, and behind a prefix that all sequences share.
+// window with sinks, and behind a prefix that all sequences share: how a call is cut into
+// chunks, its launches, and the join of the chunks.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "bsg_internal.h"
-#include "serve.cuh"
+#include <type_traits>
+
+#include "kv8_tiles.cuh"
 
 namespace bsg {
 namespace {
 
-struct Args {
-    bsg_kv8_cache c;
-    const int32_t *table, *lens, *counts, *prefix, *prefix_len;
-    int64_t table_ld, prefix_pages;
-    bsg_tokens q, out;
-    int tokens, heads, window, sinks;
-    float scale;
-    float *lse;
-    int32_t *dstatus;
+// ---- the join ---------------------------------------------------------------
+//
+// A row's output from the partial ones of one or two lists of chunks (its own positions',
+// and the prefix's): each relative to its own reference, in units of log 2.  A chunk whose
+// sum is 0 saw nothing, and its output is not read.
+struct JoinArgs {
+    bsg_tokens out;
+    int kv_heads, heads, tokens, B;
+    const int32_t *lens, *counts;  // counts: window; lens: shared, whose idle rows give 0
+    int64_t most;                  // positions of a table
+    const float *o[2];
+    const float2 *ml[2];
+    int splits[2];                 // of [0]: own chunks, [sequence][head][token, head of the group][split]; [1]: the
+    float *lse;                    // prefix's, [head][sequence, token, head of the group][split], or 0
 };
 
-// A warp to a query row, a running maximum and sum.
+constexpr int kJoinThreads = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Args a, int64_t rows) {
-    const int lane = threadIdx.x % 32, P = a.c.page_tokens;
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    if (row >= rows) return;
-    const int h = (int)(row % a.heads), t = (int)(row / a.heads % a.tokens);
-    const int64_t b = row / a.heads / a.tokens;
-    const int hk = h / (a.heads / a.c.heads);
-    const int count = a.counts ? a.counts[b] : a.tokens;
-    if (count < 0 || count > a.tokens) {
-        if (lane == 0) set_status(a.dstatus, BSG_DSTATUS_RANGE);
-        return;
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __grid_constant__ JoinArgs a) {
+    constexpr int kCols = D / 4, kSides = kJoinThreads / kCols;
+    __shared__ float4 o_s[kSides][kCols];
+    const int share = a.heads / a.kv_heads, tid = threadIdx.x;
+    const int h = blockIdx.x % a.heads, t = blockIdx.x / a.heads % a.tokens, b = blockIdx.x / a.heads / a.tokens;
+    const int hk = h / share;
+    bool idle = false;
+    if (a.counts) {
+        const int count = __ldg(a.counts + b);
+        if (t >= count || count > a.tokens) return;
     }
-    if (t >= count) return;
-    const int64_t most = a.table_ld * P;
-    int64_t len = a.lens[b];
-    if (len < 0 || len > most) {
-        if (lane == 0) set_status(a.dstatus, BSG_DSTATUS_RANGE);
-        len = len < 0 ? 0 : most;
+    if (a.lens) {
+        int64_t len = __ldg(a.lens + b);
+        idle = min(len, a.most) - a.tokens + t < 0;
     }
-    const int64_t pos = len - count + t;
-    float q[D / 32], o[D / 32];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        q[i] = to_f32(static_cast<const T *>(a.q.data)[b * a.q.stride_batch + t * a.q.stride_token +
-                                                       h * a.q.stride_head + lane + 32 * i]);
-        bad |= !isfinite(q[i]);
-        o[i] = 0.0f;
-    }
-    if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
-    float m = -INFINITY, l = 0.0f;
-    auto see = [&](const int32_t *table, int64_t from, int64_t to) {
-        for (int64_t j = from; j < to; ++j) {
-            const int page = table[j / P];
-            if (page < 0 || page >= a.c.pages) {
-                if (lane == 0) set_status(a.dstatus, BSG_DSTATUS_RANGE);
-                continue;
-            }
-            const int64_t ph = (int64_t)page * a.c.heads + hk, at = (ph * P + j % P) * D + lane;
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) s = fmaf(q[i], (float)a.c.k[at + 32 * i], s);
-#pragma unroll
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            s *= a.scale * a.c.k_scale[ph];
-            const float n = fmaxf(m, s), keep = expf(m - n), p = expf(s - n), vs = a.c.v_scale[ph];
-            m = n;
-            l = fmaf(l, keep, p);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], keep, p * vs * (float)a.c.v[at + 32 * i]);
-        }
+    const int64_t row[2] = {((int64_t)b * a.kv_heads + hk) * a.tokens * share + t * share + h % share,
+                            (((int64_t)hk * a.B + b) * a.tokens + t) * share + h % share};
+    griddep_wait();
+    const int n = a.splits[0] + a.splits[1];
+    auto at = [&](int i) {  // chunk i: its list's place
+        return i < a.splits[0] ? row[0] * a.splits[0] + i : row[1] * a.splits[1] + i - a.splits[0];
     };
-    if (pos >= 0) {
-        if (a.prefix) {
-            int64_t n = *a.prefix_len;
-            if (n < 0 || n > a.prefix_pages * P) {
-                if (lane == 0) set_status(a.dstatus, BSG_DSTATUS_RANGE);
-                n = n < 0 ? 0 : a.prefix_pages * P;
-            }
-            see(a.prefix, 0, n);
-        }
-        const int64_t low = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-        see(a.table + b * a.table_ld, 0, low < a.sinks ? low : a.sinks);
-        see(a.table + b * a.table_ld, low, pos + 1);
+    float m = -3.0e38f;
+    for (int i = tid % 32; i < n; i += 32) {
+        const float2 x = a.ml[i >= a.splits[0]][at(i)];
+        if (x.y != 0.0f) m = fmaxf(m, x.x);
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        static_cast<T *>(a.out.data)[b * a.out.stride_batch + t * a.out.stride_token + h * a.out.stride_head +
-                                     lane + 32 * i] = from_f32<T>(l > 0.0f || l != l ? o[i] / l : 0.0f);
-    if (lane == 0 && a.lse)
-        a.lse[row] = l > 0.0f || l != l ? m + logf(l) : -INFINITY;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int col = tid % kCols, side = tid / kCols;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    if (side < kSides && !idle)
+        for (int i = side; i < n; i += kSides) {
+            const int list = i >= a.splits[0];
+            const float2 x = a.ml[list][at(i)];
+            if (x.y == 0.0f) continue;
+            const float f = tile_exp2(x.x - m);
+            const float4 v = *reinterpret_cast<const float4 *>(a.o[list] + at(i) * D + 4 * col);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+            l = fmaf(x.y, f, l);
+        }
+    __shared__ float l_s[kSides];
+    if (side < kSides) {
+        o_s[side][col] = o;
+        if (col == 0) l_s[side] = l;
+    }
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSides; ++i) l += l_s[i];
+    const bool some = l > 0.0f || l != l;
+    const float inv = some ? 1.0f / l : 0.0f;
+    T *out = static_cast<T *>(a.out.data) + b * a.out.stride_batch + t * a.out.stride_token + h * a.out.stride_head;
+    for (int d = tid; d < D; d += kJoinThreads) {
+        float y = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSides; ++i) y += reinterpret_cast<const float *>(&o_s[i][d / 4])[d % 4];
+        out[d] = from_f32<T>(some ? y * inv : 0.0f);
+    }
+    if (tid == 0 && a.lse) a.lse[blockIdx.x] = some ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-cudaError_t launch(const Args &a, int dtype, int64_t B, cudaStream_t st) {
-    const int64_t rows = B * a.tokens * a.heads;
-    if ((rows + 3) / 4 > INT32_MAX) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
+template <typename F>
+cudaError_t with_dim(int dim, F &&f) {
+    switch (dim) {
+        case 32: return f(std::integral_constant<int, 32>{});
+        case 64: return f(std::integral_constant<int, 64>{});
+        case 96: return f(std::integral_constant<int, 96>{});
+        case 128: return f(std::integral_constant<int, 128>{});
+        default: return f(std::integral_constant<int, 256>{});
+    }
+}
+
+cudaError_t launch_join(const JoinArgs &a, int dim, int dtype, cudaStream_t st) {
+    const int64_t rows = (int64_t)a.B * a.tokens * a.heads;
+    if (rows > INT32_MAX) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return with_dtype(dtype, [&](auto t) {
-        using T = decltype(t);
-        switch (a.c.dim) {
-            case 32: rows_kernel<T, 32><<<grid, 128, 0, st>>>(a, rows); break;
-            case 64: rows_kernel<T, 64><<<grid, 128, 0, st>>>(a, rows); break;
-            case 96: rows_kernel<T, 96><<<grid, 128, 0, st>>>(a, rows); break;
-            case 128: rows_kernel<T, 128><<<grid, 128, 0, st>>>(a, rows); break;
-            default: rows_kernel<T, 256><<<grid, 128, 0, st>>>(a, rows);
-        }
-        count_launches(1);
-        return cudaGetLastError();
+        return with_dim(dim, [&](auto d) {
+            count_launches(1);
+            return cudaLaunchKernelEx(&cfg, kv8_join_lists_kernel<decltype(t), decltype(d)::value>, a);
+        });
     });
 }
 
+// ---- the tiles ----------------------------------------------------------------
+
+struct TilePlan {
+    int row_blocks, splits;
+    int64_t groups;
+    size_t floats, parts;  // of partial outputs, and their count
+};
+
+int64_t most_tiles(const bsg_kv8_cache &c, int64_t table_ld, int64_t tokens, int window, int sinks) {
+    const int64_t all = table_ld * c.page_tokens, n = c.dim == 256 ? 64 : 128;
+    int64_t see = all;
+    if (window && window + tokens + sinks < all) see = window + tokens + sinks;
+    return (see + n - 1) / n + (window ? 2 : 0);
+}
+
+// As many chunks as fill the card once, of two tiles at least.
+TilePlan tile_plan(const bsg_kv8_cache &c, int64_t rows, int64_t groups, int64_t tiles, bool later) {
+    TilePlan p;
+    const int64_t block = c.dim == 256 ? 128 : 256;
+    p.row_blocks = (int)((rows + block - 1) / block);
+    p.groups = groups;
+    int64_t splits = device_sm_count() / (p.row_blocks * groups);
+    if (splits > tiles / 2) splits = tiles / 2;
+    p.splits = (int)(splits < 1 ? 1 : splits);
+    p.parts = p.splits > 1 || later ? (size_t)groups * rows * p.splits : 0;
+    p.floats = p.parts * (c.dim + 2);
+    return p;
+}
+
+template <int D, int kQ, int kP, bool PREFIX>
+cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
+    using C = TileCfg<D, kQ>;
+    static bool set[64] = {false};  // this kernel's shared memory, on each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(kv8_tiles_kernel<D, kQ, kP, PREFIX>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
+    }
+    const int64_t blocks = a.row_blocks * a.groups;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), C::kThreads, C::kBytes, st>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <bool PREFIX>
+cudaError_t launch_tiles(TileArgs a, const TilePlan &p, int dtype, cudaStream_t st) {
+    a.row_blocks = p.row_blocks, a.groups = p.groups, a.splits = p.splits;
+    return with_dim(a.c.dim, [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (dtype == BSG_F32) return launch_tiles_as<D, 2, 2, PREFIX>(a, st);
+        if (dtype == BSG_F16) return launch_tiles_as<D, 1, 2, PREFIX>(a, st);
+        return launch_tiles_as<D, 1, 1, PREFIX>(a, st);
+    });
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
 }  // namespace
 
-size_t kv8_window_workspace_bytes(const bsg_kv8_cache &, int64_t, int64_t, int64_t, int, int, int) {
-    return 256;
+size_t kv8_window_workspace_bytes(const bsg_kv8_cache &c, int64_t table_ld, int64_t B, int64_t T,
+                                  int heads, int window, int sinks) {
+    const TilePlan p = tile_plan(c, T * (heads / c.heads), B * c.heads, most_tiles(c, table_ld, T, window, sinks), false);
+    return up256(p.floats * 4 + 1);
 }
 
 cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
@@ -124,13 +199,25 @@ cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *tabl
                                      const bsg_tokens &out, int dtype, int64_t B, int64_t T,
                                      int heads, int window, int sinks, float scale, float *lse,
                                      void *ws, int32_t *dstatus, cudaStream_t st) {
-    return launch({c, table, lens, counts, nullptr, nullptr, table_ld, 0, q, out, (int)T, heads, window,
-                   sinks, scale, lse, dstatus},
-                  dtype, B, st);
+    const int64_t rows = T * (heads / c.heads);
+    const TilePlan p = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, window, sinks), false);
+    float *part_o = static_cast<float *>(ws);
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + p.parts * c.dim);
+    const TileArgs a{c, table, table_ld, lens, counts, q, out, (int)T, heads, window, sinks, (int)rows, 0, 0, 0, 0,
+                     scale, lse, part_o, part_ml, dstatus};
+    cudaError_t e = launch_tiles<false>(a, p, dtype, st);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_join({out, c.heads, heads, (int)T, (int)B, nullptr, counts, 0, {part_o, nullptr},
+                        {part_ml, nullptr}, {p.splits, 0}, lse},
+                       c.dim, dtype, st);
 }
 
-size_t kv8_shared_workspace_bytes(const bsg_kv8_cache &, int64_t, int64_t, int64_t, int64_t, int) {
-    return 256;
+size_t kv8_shared_workspace_bytes(const bsg_kv8_cache &c, int64_t prefix_pages, int64_t table_ld,
+                                  int64_t B, int64_t T, int heads) {
+    const int64_t rows = T * (heads / c.heads);
+    const TilePlan own = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, 0, 0), true);
+    const TilePlan pre = tile_plan(c, B * rows, c.heads, most_tiles(c, prefix_pages, 0, 0, 0), true);
+    return up256((own.floats + pre.floats) * 4);
 }
 
 cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *prefix,
@@ -139,9 +226,23 @@ cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *pref
                                      const bsg_tokens &q, const bsg_tokens &out, int dtype,
                                      int64_t B, int64_t T, int heads, float scale, float *lse,
                                      void *ws, int32_t *dstatus, cudaStream_t st) {
-    return launch({c, table, lens, nullptr, prefix, prefix_len, table_ld, prefix_pages, q, out, (int)T,
-                   heads, 0, 0, scale, lse, dstatus},
-                  dtype, B, st);
+    const int64_t rows = T * (heads / c.heads);
+    if (B * rows > INT32_MAX) return cudaErrorInvalidValue;
+    const TilePlan own = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, 0, 0), true);
+    const TilePlan pre = tile_plan(c, B * rows, c.heads, most_tiles(c, prefix_pages, 0, 0, 0), true);
+    float *own_o = static_cast<float *>(ws), *pre_o = own_o + own.parts * c.dim;
+    float2 *own_ml = reinterpret_cast<float2 *>(pre_o + pre.parts * c.dim), *pre_ml = own_ml + own.parts;
+    TileArgs a{c, table, table_ld, lens, nullptr, q, out, (int)T, heads, 0, 0, (int)rows, 0, 0, 0, 1,
+               scale, lse, own_o, own_ml, dstatus};
+    cudaError_t e = launch_tiles<false>(a, own, dtype, st);
+    if (e != cudaSuccess) return e;
+    a.table = prefix, a.table_ld = prefix_pages, a.lens = prefix_len, a.rows = (int)(B * rows);
+    a.part_o = pre_o, a.part_ml = pre_ml;
+    e = launch_tiles<true>(a, pre, dtype, st);
+    if (e != cudaSuccess) return e;
+    return launch_join({out, c.heads, heads, (int)T, (int)B, lens, nullptr, table_ld * c.page_tokens, {own_o, pre_o},
+                        {own_ml, pre_ml}, {own.splits, pre.splits}, lse},
+                       c.dim, dtype, st);
 }
 
 }  // namespace bsg
