@@ -168,7 +168,7 @@ cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
     }
     const int64_t blocks = a.row_blocks * a.groups;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), C::kThreads, C::kBytes, st>>>(a);
+    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), kTileThreads, C::kBytes, st>>>(a);
     count_launches(1);
     return cudaGetLastError();
 }

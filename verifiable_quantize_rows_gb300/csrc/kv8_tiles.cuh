@@ -12,10 +12,14 @@
 // Codes are exact in f16, so K and V are too; queries are relative to a power of two near
 // their row's largest, f32's as two f16 parts (22 bits).
 //
-// Roles: warps 0-3 (and 4-7 for the second 128 rows) softmax, one row a thread; 4 warps
-// turn codes into f16 operands in a ring of shared memory, their loads a tile ahead in
-// registers; one thread issues the MMAs.  The two groups of rows alternate: while one's
-// softmax runs, the tensor cores work for the other.
+// Roles, four warps each, the registers split among them (setmaxnreg):
+//   0-3, 4-7   softmax, a row to a thread (4-7: the second 128 rows), the row's scores of a
+//              tile in registers;
+//   8-11       codes into f16 operands, in a ring of shared memory that K and V tiles take
+//              in turn; each tile's loads are sent two fills ahead;
+//   12         one thread issues the MMAs: P V of a tile, then S of the next, for one group
+//              of rows while the other's softmax runs;
+//   13         finds where the tiles' pages lie, and their scales, some tiles at a time.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -46,13 +50,36 @@ struct TileArgs {
 };
 
 constexpr float kTileTop = 11.0f, kTileMost = 15.0f;
-constexpr int kScaleSlots = 6;
+constexpr int kAtSlots = 4;
 
 __device__ __forceinline__ float tile_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// x f + off for two values; f and off twice in a pair each.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t f, uint64_t off) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(f), "l"(off));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 // What a CTA of some rows sees: `sink_tiles` tiles from the first, then those from `first`.
 struct Seen {
@@ -83,38 +110,60 @@ struct TileCfg {
     static constexpr int kQBytes = kBlocks * 128 * 128;       // one part of 128 rows
     static constexpr int kStageBytes = kBlocks * kN * 128;    // a K or V tile
     static constexpr int kRoom = 229376 - kM * kQParts * kQBytes;
-    static constexpr int kStages = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
+    static constexpr int kStages = kRoom / kStageBytes >= 6 ? 6 : kRoom / kStageBytes == 5 ? 4 : kRoom / kStageBytes;
     static constexpr int kGroups = kN / 16;
-    static constexpr int kSoftWarps = 4 * kM, kConvWarps = 4;
-    static constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
     static constexpr int kOffStage = kM * kQParts * kQBytes;
-    static constexpr int kOffScale = kOffStage + kStages * kStageBytes;
-    static constexpr int kOffMul = kOffScale + kScaleSlots * kGroups * 16;
+    static constexpr int kOffAt = kOffStage + kStages * kStageBytes;
+    static constexpr int kOffMul = kOffAt + kAtSlots * kGroups * 16;
     static constexpr int kOffBar = kOffMul + kM * 128 * 4;
-    static constexpr int kBars = 2 * kStages + kScaleSlots + 3 * kM;
+    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 3 * kM;
     static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     static constexpr int kBytes = (kUsed > 118000 ? kUsed : 118000) + 1024;  // one CTA on an SM (all its tensor memory)
     static_assert(kStages >= 2 && kBytes <= 232448, "shared memory");
-    static_assert(kScaleSlots >= kStages / 2 + 3, "a slot is free before it is written again");
     static __device__ constexpr int kS(int m) { return m * kN; }               // columns of tensor memory
     static __device__ constexpr int kO(int m) { return kM * kN + m * D; }
 };
+
+constexpr int kTileThreads = 512;
+// Registers of a softmax, a converting and another thread; together no more than four
+// times the 128 that the block is launched with.
+constexpr int kSoftRegs = 168, kConvRegs = 112, kOtherRegs = 64;
+static_assert(2 * kSoftRegs + kConvRegs + kOtherRegs <= 4 * 128, "register split");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 bytes of codes, in the order of the program.
+__device__ __forceinline__ uint4 load_codes(const int8_t *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
 
 // PREFIX: rows are those of all sequences (rows = B x tokens x heads of a group), every one
 // sees the positions below *lens; what a CTA finds is joined later.  The report of bad lengths
 // is the first CTA's.
 template <int D, int kQParts, int kPParts, bool PREFIX>
-__global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
+__global__ void __launch_bounds__(kTileThreads, 1)
     kv8_tiles_kernel(const __grid_constant__ TileArgs a) {
     using C = TileCfg<D, kQParts>;
     constexpr int kM = C::kM, kN = C::kN, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    float4 *scale_s = reinterpret_cast<float4 *>(smem + C::kOffScale);
+    // of a tile's groups of 16 positions: key scale, log2 of the value scale, its reciprocal,
+    // and the place in the pool (in groups; -1: nowhere)
+    float4 *at_s = reinterpret_cast<float4 *>(smem + C::kOffAt);
     float *mul_s = reinterpret_cast<float *>(smem + C::kOffMul);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *kv_full = bars, *kv_empty = bars + kStages, *sc_full = bars + 2 * kStages;
-    uint64_t *s_full = sc_full + kScaleSlots, *p_full = s_full + kM, *o_full = p_full + kM;
+    uint64_t *kv_full = bars, *kv_empty = bars + kStages, *at_full = bars + 2 * kStages;
+    uint64_t *at_empty = at_full + kAtSlots, *s_full = at_empty + kAtSlots, *p_full = s_full + kM, *o_full = p_full + kM;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
 
@@ -162,10 +211,13 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&kv_full[s], C::kConvWarps);
+            mbar_init(&kv_full[s], 4);
             mbar_init(&kv_empty[s], 1);
         }
-        for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sc_full[s], 1);
+        for (int s = 0; s < kAtSlots; ++s) {
+            mbar_init(&at_full[s], 1);
+            mbar_init(&at_empty[s], 4 + 4 * groups);  // the warps that read a slot
+        }
         for (int m = 0; m < kM; ++m) {
             mbar_init(&s_full[m], 1);
             mbar_init(&p_full[m], 4);
@@ -174,7 +226,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    constexpr int kMmaWarp = C::kSoftWarps + C::kConvWarps;
+    constexpr int kMmaWarp = 12;
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_ptr, 512);
         tmem_relinquish();
@@ -186,7 +238,8 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
     auto load_queries = [&](auto type) {
         using T = decltype(type);
         constexpr int kAhead = 4;
-        for (int rr = warp * kAhead; rr < groups * 128; rr += C::kThreads / 32 * kAhead) {
+#pragma unroll 1
+        for (int rr = warp * kAhead; rr < groups * 128; rr += kTileThreads / 32 * kAhead) {
             float q[kAhead][D / 32];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
@@ -208,8 +261,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
                     m = fmaxf(m, fabsf(q[i][j]));
                 }
                 if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
                 // 2^e with m 2^e in [2^13, 2^14); e <= 126 leaves subnormal rows their small error
                 const int e = max(-126, min(126, 13 + 127 - (int)(__float_as_uint(m) >> 23)));
                 const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
@@ -245,60 +297,71 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
         *abort_flag = 1;
         set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
     };
+    // a whole warp's wait
+    auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        if (!ok && lane == 0) give_up();
+        return ok;
+    };
 
-    if (warp == kMmaWarp) {
-        // ---------------------------------------------------- MMA issuer
-        if (lane == 0 && tiles > 0) {
+    if (warp >= 12) {
+        fewer_registers<kOtherRegs>();
+        if (warp == kMmaWarp && lane == 0 && tiles > 0) {
+            // ------------------------------------------------ MMA issuer
             constexpr uint32_t kIdescS = idesc_f16_f32(128, kN), kIdescO = idesc_f16_f32(128, D) | kIdescBMn;
             const uint32_t stage0 = smem_u32(smem + C::kOffStage);
+            const uint64_t q_desc = sdesc_k128(smem_u32(smem)), k_desc = sdesc_k128(stage0);
+            const uint64_t v_desc = sdesc_mn128(stage0, kN * 128);
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (ok && !mbar_wait(bar, parity, abort_flag)) {
                     give_up();
                     ok = false;
                 }
-                tc_fence_after();
             };
-            auto products = [&](int m, int i) {  // S of rows m and tile i
-                const uint32_t k = stage0 + 2 * i % kStages * C::kStageBytes;
+            int stage = 0;
+            uint32_t phase = 0;  // of the next fill that is waited for
+#pragma unroll 1
+            for (int i = -1; i < tiles && ok; ++i) {
+                const int vs = stage;  // V of tile i, then K of the next
+                const uint32_t vphase = phase;
+                if (i >= 0 && ++stage == kStages) stage = 0, phase ^= 1;
+                const int ks = stage;
+                const uint32_t kphase = phase;
+                if (i + 1 < tiles && ++stage == kStages) stage = 0, phase ^= 1;
+#pragma unroll 1
+                for (int m = 0; m < groups && ok; ++m) {
+                    if (i >= 0) {
+                        wait(&p_full[m], i & 1);
+                        if (m == 0) wait(&kv_full[vs], vphase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t v = v_desc + vs * (C::kStageBytes / 16);
+                        const uint32_t p_at = tmem + C::kS(m), o_at = tmem + C::kO(m);
 #pragma unroll
-                for (int part = 0; part < kQParts; ++part)
+                        for (int j = 0; j < kN / 16; ++j)
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        mma_f16_ss(tmem + C::kS(m),
-                                   sdesc_k128(smem_u32(smem) + (m * kQParts + part) * C::kQBytes + j / 4 * 16384) + 2 * (j % 4),
-                                   sdesc_k128(k + j / 4 * (kN * 128)) + 2 * (j % 4), kIdescS, part + j > 0);
-                mma_commit(&s_full[m]);
-            };
-            wait(&kv_full[0], 0);
-            if (ok) {
-                products(0, 0);
-                if (groups > 1) products(kM - 1, 0);
-                mma_commit(&kv_empty[0]);
-            }
-            for (int i = 0; i < tiles && ok; ++i) {
-                const int vs = (2 * i + 1) % kStages, ks = (2 * i + 2) % kStages;
-                const uint32_t vphase = (2 * i + 1) / kStages & 1, kphase = (2 * i + 2) / kStages & 1;
-                for (int m = 0; m < groups; ++m) {
-                    wait(&p_full[m], i & 1);
-                    if (m == 0) wait(&kv_full[vs], vphase);
-                    if (!ok) break;
-                    const uint32_t v = stage0 + vs * C::kStageBytes;
-#pragma unroll
-                    for (int j = 0; j < kN / 16; ++j)
-#pragma unroll
-                        for (int part = 0; part < kPParts; ++part)
-                            mma_f16_ts(tmem + C::kO(m), tmem + C::kS(m) + j / 2 * 32 + j % 2 * 8 + part * 16,
-                                       sdesc_mn128(v + j * 2048, kN * 128), kIdescO, i + j + part > 0);
-                    if (m == groups - 1) mma_commit(&kv_empty[vs]);
-                    if (i + 1 == tiles) {
-                        mma_commit(&o_full[m]);
-                        continue;
+                            for (int part = 0; part < kPParts; ++part)
+                                mma_f16_ts(o_at, p_at + j / 2 * 32 + j % 2 * 8 + part * 16, v + j * 128, kIdescO,
+                                           j + part > 0 ? 1 : i > 0);
+                        if (m == groups - 1) mma_commit(&kv_empty[vs]);
+                        if (i + 1 == tiles) mma_commit(&o_full[m]);
                     }
-                    if (m == 0) wait(&kv_full[ks], kphase);
-                    if (!ok) break;
-                    products(m, i + 1);
-                    if (m == groups - 1) mma_commit(&kv_empty[ks]);
+                    if (i + 1 < tiles) {  // S of the next tile, in P's place
+                        if (m == 0) wait(&kv_full[ks], kphase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t k = k_desc + ks * (C::kStageBytes / 16);
+                        const uint64_t q = q_desc + m * (kQParts * C::kQBytes / 16);
+#pragma unroll
+                        for (int part = 0; part < kQParts; ++part)
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j)
+                                mma_f16_ss(tmem + C::kS(m), q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                                           k + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
+                        mma_commit(&s_full[m]);
+                        if (m == groups - 1) mma_commit(&kv_empty[ks]);
+                    }
                 }
             }
             if (!ok) {  // wait until every MMA issued so far has finished
@@ -307,102 +370,120 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
                 while (!mbar_try_wait(&o_full[0], 0) && clock64() - t0 < kWaitLimitCycles) {
                 }
             }
+        } else if (warp == 13) {
+            // ------------------------------------------------ pages and scales
+            constexpr int kBatch = 32 / C::kGroups;  // tiles at a time, a lane to each group of 16 positions
+            const int32_t *table = a.table + b * a.table_ld;
+            bool ok = true;
+#pragma unroll 1
+            for (int i0 = 0; i0 < tiles && ok; i0 += kBatch) {
+                const int i = i0 + lane / C::kGroups;
+                float4 at = make_float4(0.0f, -INFINITY, 0.0f, __int_as_float(-1));
+                if (i < tiles) {
+                    const int pos = position(i) + lane % C::kGroups * 16;
+                    // a page that no row sees is not looked up
+                    if (pos < seen.see && (pos + 16 > seen.low || pos < a.sinks)) {
+                        const int page = __ldg(table + pos / P);
+                        if (page < 0 || page >= a.c.pages) {
+                            set_status(a.dstatus, BSG_DSTATUS_RANGE);
+                        } else {
+                            const int64_t ph = (int64_t)page * a.c.heads + hk;
+                            const float v = fmaxf(__ldg(a.c.v_scale + ph), 1e-30f);
+                            at = make_float4(__ldg(a.c.k_scale + ph), log2f(v), __frcp_rn(v),
+                                             __int_as_float((int)(ph * (P / 16) + pos % P / 16)));
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (int u = 0; u < kBatch && i0 + u < tiles; ++u) {
+                    const int slot = (i0 + u) % kAtSlots;
+                    if (!(ok = all_wait(&at_empty[slot], ((i0 + u) / kAtSlots & 1) ^ 1))) break;
+                    if (lane / C::kGroups == u) at_s[slot * C::kGroups + lane % C::kGroups] = at;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&at_full[slot]);
+                }
+            }
         }
         __syncwarp();
-    } else if (warp >= C::kSoftWarps) {
+    } else if (warp >= 8) {
         // ---------------------------------------------------- codes to f16 operands
-        constexpr int kChunks = D / 16;                             // 16-byte pieces of a row
-        constexpr int kPer = kN * kChunks / (C::kConvWarps * 32);   // of a thread and tile
-        const int ctid = tid - C::kSoftWarps * 32;
-        const int32_t *table = a.table + b * a.table_ld;
-        uint4 kbuf[kPer], vbuf[kPer];
-        int64_t at = -1, at_next = -1;  // of group `lane` of a tile, in bytes of the pool; -1: nowhere
-        float4 sc, sc_next;
-        // Where the groups of tile i lie, a lane each.  A page that no row sees is not looked up.
-        auto look_up = [&](int i) {
-            at_next = -1;
-            sc_next = make_float4(0.0f, -INFINITY, 0.0f, 1.0f);
-            if (i >= tiles || lane >= C::kGroups) return;
-            const int pos = position(i) + lane * 16;
-            if (pos >= seen.see || (pos + 16 <= seen.low && pos >= a.sinks)) return;
-            const int page = __ldg(table + pos / P);
-            if (page < 0 || page >= a.c.pages) {
-                set_status(a.dstatus, BSG_DSTATUS_RANGE);
-                return;
-            }
-            const int64_t ph = (int64_t)page * a.c.heads + hk;
-            at_next = (ph * P + pos % P) * D;
-            const float ks = __ldg(a.c.k_scale + ph), vs = __ldg(a.c.v_scale + ph), v = fmaxf(fabsf(vs), 1e-30f);
-            // w: the signs, which go to the codes
-            sc_next = make_float4(fabsf(ks), log2f(v), __frcp_rn(v),
-                                  __uint_as_float((ks < 0.0f ? 1u : 0u) | (vs < 0.0f ? 2u : 0u)));
+        fewer_registers<kConvRegs>();
+        constexpr int kChunks = D / 16;           // 16-byte pieces of a row
+        constexpr int kPer = kN * kChunks / 128;  // of a thread and tile
+        const int ctid = tid - 256;
+        // Piece j of a thread.  Eight lanes store to two rows, of either parity, so that the
+        // swizzle spreads them over all banks.
+        auto row_of = [&](int j) {
+            const int e = ctid + j * 128;
+            return kChunks % 4 ? e / kChunks : e / (2 * kChunks) * 2 + e % 8 / 4;
         };
-        auto load = [&](uint4 (&buf)[kPer], const int8_t *codes, int64_t where) {
+        auto chunk_of = [&](int j) {
+            const int e = ctid + j * 128;
+            return kChunks % 4 ? e % kChunks : e % 4 + e / 8 % (kChunks / 4 ? kChunks / 4 : 1) * 4;
+        };
+        uint4 buf[2][kPer];  // of K and V tiles
+        auto load = [&](uint4 (&x)[kPer], const int8_t *codes, int i) {
+            const float4 *at = at_s + i % kAtSlots * C::kGroups;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                const int e = ctid + j * (C::kConvWarps * 32), row = e / kChunks;
-                const int64_t base = __shfl_sync(0xffffffffu, where, row / 16);
-                buf[j] = make_uint4(0x0u, 0x0u, 0x0u, 0x0u);
-                if (base >= 0)
-                    buf[j] = __ldg(reinterpret_cast<const uint4 *>(codes + base + row % 16 * D) + e % kChunks);
+                const int place = __float_as_int(at[row_of(j) / 16].w);
+                x[j] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                if (place >= 0)
+                    x[j] = load_codes(codes + (int64_t)place * (16 * D) + row_of(j) % 16 * D + chunk_of(j) * 16);
             }
         };
-        auto convert = [&](const uint4 (&buf)[kPer], int fill, uint32_t bit, float4 of) {
-            const int stage = fill % kStages;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], (fill / kStages & 1) ^ 1, abort_flag));
-            if (!ok) {
-                if (lane == 0) give_up();
-                return false;
-            }
-            uint8_t *tile = smem + C::kOffStage + stage * C::kStageBytes;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int e = ctid + j * (C::kConvWarps * 32), row = e / kChunks, chunk = e % kChunks;
-                const uint32_t signs = __float_as_uint(__shfl_sync(0xffffffffu, of.w, row / 16));
-                const __half2 sign = __float2half2_rn(signs & bit ? -1.0f : 1.0f);
-                const __half2 bias = __float2half2_rn(signs & bit ? 1152.0f : -1152.0f);
-                uint32_t h[8];
-                const uint32_t w[4] = {buf[j].x, buf[j].y, buf[j].z, buf[j].w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t x = w[u] ^ 0x80808080u;
-                    const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140), hi = __byte_perm(x, 0x64646464u, 0x4342);
-                    const __half2 l = __hfma2(*reinterpret_cast<const __half2 *>(&lo), sign, bias);
-                    const __half2 g = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sign, bias);
-                    h[2 * u] = *reinterpret_cast<const uint32_t *>(&l);
-                    h[2 * u + 1] = *reinterpret_cast<const uint32_t *>(&g);
-                }
-                uint8_t *line = tile + chunk / 4 * (kN * 128) + row * 128;
-                const int c = chunk % 4 * 2;
-                *reinterpret_cast<uint4 *>(line + ((c ^ row % 8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(line + ((c + 1 ^ row % 8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-            fence_async_shared();
+        bool ok = true;
+        if (tiles > 0 && (ok = all_wait(&at_full[0], 0))) {
+            load(buf[0], a.c.k, 0);
+            load(buf[1], a.c.v, 0);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&kv_full[stage]);
-            return true;
-        };
-        look_up(0);
-        at = at_next, sc = sc_next;
-        load(kbuf, a.c.k, at);
-        for (int i = 0; i < tiles; ++i) {
-            load(vbuf, a.c.v, at);
-            look_up(i + 1);
-            // the scales' slot was read by the softmax of tile i - kScaleSlots, whose P V a
-            // value tile filled earlier has waited for
-            if (warp == C::kSoftWarps) {
-                if (lane < C::kGroups) scale_s[i % kScaleSlots * C::kGroups + lane] = sc;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[i % kScaleSlots]);
-            }
-            if (!convert(kbuf, 2 * i, 1u, sc)) break;
-            load(kbuf, a.c.k, at_next);
-            if (!convert(vbuf, 2 * i + 1, 2u, sc)) break;
-            at = at_next, sc = sc_next;
+            if (lane == 0) mbar_arrive(&at_empty[0]);
         }
-    } else if (warp / 4 < groups) {
+        int stage = 0;
+        uint32_t phase = 0;
+#pragma unroll 1
+        for (int i = 0; i < tiles && ok; ++i) {
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                if (!ok || !(ok = all_wait(&kv_empty[stage], phase ^ 1))) break;
+                uint8_t *tile = smem + C::kOffStage + stage * C::kStageBytes;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int row = row_of(j), chunk = chunk_of(j);
+                    uint32_t h[8];
+                    const uint32_t w[4] = {buf[side][j].x, buf[side][j].y, buf[side][j].z, buf[side][j].w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {  // code + 128, as f16 1024 + that, less 1152
+                        const uint32_t x = w[u] ^ 0x80808080u, bias = 0x64806480u;
+                        const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140), hi = __byte_perm(x, 0x64646464u, 0x4342);
+                        const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), *reinterpret_cast<const __half2 *>(&bias));
+                        const __half2 g = __hsub2(*reinterpret_cast<const __half2 *>(&hi), *reinterpret_cast<const __half2 *>(&bias));
+                        h[2 * u] = *reinterpret_cast<const uint32_t *>(&l);
+                        h[2 * u + 1] = *reinterpret_cast<const uint32_t *>(&g);
+                    }
+                    uint8_t *line = tile + chunk / 4 * (kN * 128) + row * 128;
+                    const int c = chunk % 4 * 2;
+                    *reinterpret_cast<uint4 *>(line + ((c ^ row % 8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(line + ((c + 1 ^ row % 8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[stage]);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+                if (i + 1 < tiles) {  // the next tile's, into the registers that are free
+                    const int slot = (i + 1) % kAtSlots;
+                    if (side == 0 && !(ok = all_wait(&at_full[slot], (i + 1) / kAtSlots & 1))) break;
+                    load(buf[side], side ? a.c.v : a.c.k, i + 1);
+                    __syncwarp();
+                    if (side == 1 && lane == 0) mbar_arrive(&at_empty[slot]);
+                }
+            }
+        }
+    } else {
         // ---------------------------------------------------- softmax, a row a thread
+        more_registers<kSoftRegs>();
         const int m = warp / 4, r = tid;
+        if (m < groups) {
         const uint32_t quad = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t s_at = tmem + C::kS(m) + quad, o_at = tmem + C::kO(m) + quad;
         const int pos = PREFIX ? len - 1 : pos0 + (r0 + r) / share;
@@ -416,41 +497,38 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
         const float mul = mul_s[r];
         float ref = 0.0f, sum = 0.0f;
         bool none = true, ok = true;
-        uint32_t v[2][32];
+#pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
-            const int tile = position(i);
-            const float4 *sc = scale_s + i % kScaleSlots * C::kGroups;
-            ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[i % kScaleSlots], i / kScaleSlots & 1, abort_flag) &&
-                                             mbar_wait(&s_full[m], i & 1, abort_flag));
-            if (!ok) {
-                if (lane == 0) give_up();
-                break;
-            }
+            const int tile = position(i), slot = i % kAtSlots;
+            const float4 *of_s = at_s + slot * C::kGroups;
+            if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
             tc_fence_after();
+            uint32_t v[kN / 32][32];  // the row's scores
+#pragma unroll
+            for (int c = 0; c < kN / 32; ++c) tmem_ld32(s_at + 32 * c, v[c]);
+#pragma unroll
+            for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
             const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
-            auto hidden = [&](int j) { return j >= see || (j < low && j >= a.sinks); };
+            if (edge) {  // what the row does not see
+#pragma unroll
+                for (int c = 0; c < kN / 32; ++c) {
+                    const int j = tile + 32 * c;
+                    const uint32_t mask = below(see - j) & (~below(low - j) | below(a.sinks - j));
+#pragma unroll
+                    for (int u = 0; u < 32; ++u)
+                        if (!(mask & 1u << u)) v[c][u] = 0xff800000u;
+                }
+            }
             // the largest exponent, relative to the reference
             float top = -INFINITY;
-            tmem_ld32(s_at, v[0]);
 #pragma unroll
-            for (int c = 0; c < kN / 32; ++c) {
-                tmem_ld_wait32(v[c % 2]);
-                if (c + 1 < kN / 32) tmem_ld32(s_at + 32 * (c + 1), v[(c + 1) % 2]);
+            for (int g = 0; g < C::kGroups; ++g) {
+                const float2 of = *reinterpret_cast<const float2 *>(of_s + g);
+                const uint32_t *x = v[g / 2] + g % 2 * 16;
+                float y = __uint_as_float(x[0]);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 of = sc[2 * c + g];
-                    const float f = of.x * mul, off = of.y - ref;
-                    float x = -INFINITY;
-                    if (edge) {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u)
-                            if (!hidden(tile + 32 * c + 16 * g + u)) x = fmaxf(x, __uint_as_float(v[c % 2][16 * g + u]));
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) x = fmaxf(x, __uint_as_float(v[c % 2][16 * g + u]));
-                    }
-                    if (x > -INFINITY) top = fmaxf(top, fmaf(x, f, off));
-                }
+                for (int u = 1; u < 16; ++u) y = fmaxf(y, __uint_as_float(x[u]));
+                if (y > -INFINITY) top = fmaxf(top, fmaf(y, of.x * mul, of.y - ref));
             }
             const bool move = none ? top > -INFINITY : top > kTileMost;
             if (__any_sync(0xffffffffu, move)) {
@@ -463,58 +541,66 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
                 }
                 if (i > 0) {
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        tmem_ld32(o_at + 32 * c, v[0]);
-                        tmem_ld_wait32(v[0]);
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + 16 * c, o);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) v[0][u] = __float_as_uint(__uint_as_float(v[0][u]) * keep);
-                        tmem_st32(o_at + 32 * c, v[0]);
+                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                        tmem_st16(o_at + 16 * c, o);
                     }
                 }
             }
-            tmem_ld32(s_at, v[0]);
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-                tmem_ld_wait32(v[c % 2]);
-                if (c + 1 < kN / 32) tmem_ld32(s_at + 32 * (c + 1), v[(c + 1) % 2]);
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float4 of = sc[2 * c + g];
-                    const float f = of.x * mul, off = of.y - ref;
-                    float part = 0.0f;
+                    const float4 of = of_s[2 * c + g];
+                    // (a score of -inf times 0 would be no number)
+                    const float f = fmaxf(of.x * mul, 1e-37f), off = of.y - ref;
+                    const uint64_t ff = pair_of(f, f), oo = pair_of(off, off);
+                    const uint32_t *x = v[c] + 16 * g;
+                    float p[16];
 #pragma unroll
                     for (int u = 0; u < 16; u += 2) {
-                        float x[2], p[2];
+                        unpair(fma2(pair_of(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), ff, oo), p[u], p[u + 1]);
+                        p[u] = tile_exp2(p[u]), p[u + 1] = tile_exp2(p[u + 1]);
+                    }
+                    uint64_t part = pair_of(p[0], p[1]);
 #pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            x[w] = fmaf(__uint_as_float(v[c % 2][16 * g + u + w]), f, off);
-                            if (edge && hidden(tile + 32 * c + 16 * g + u + w)) x[w] = -INFINITY;
-                            p[w] = tile_exp2(x[w]);
-                        }
-                        part += p[0] + p[1];
-                        const __half2 h = __floats2half2_rn(p[0], p[1]);
-                        hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
-                        if (kPParts == 2) {
-                            const float2 back = __half22float2(h);
-                            const __half2 rest = __floats2half2_rn(p[0] - back.x, p[1] - back.y);
+                    for (int u = 2; u < 16; u += 2) part = add2(part, pair_of(p[u], p[u + 1]));
+                    float even, odd;
+                    unpair(part, even, odd);
+                    sum = fmaf(even + odd, of.z, sum);
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) {
+                        if (kPParts == 1) {
+                            const __half2 h = __floats2half2_rn(p[u], p[u + 1]);
+                            hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                        } else {  // the first 11 bits, and 11 of the rest
+                            const float a0 = __uint_as_float(__float_as_uint(p[u]) & 0xffffe000u);
+                            const float a1 = __uint_as_float(__float_as_uint(p[u + 1]) & 0xffffe000u);
+                            const __half2 h = __floats2half2_rn(a0, a1);
+                            const __half2 rest = __floats2half2_rn(p[u] - a0, p[u + 1] - a1);
+                            hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
                             lo[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&rest);
                         }
                     }
-                    sum = fmaf(part, of.z, sum);
                 }
-                // in the place of the 32 columns of S that were read
                 tmem_st16(s_at + 32 * c, hi);
                 if (kPParts == 2) tmem_st16(s_at + 32 * c + 16, lo);
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[m]);
+            if (lane == 0) {
+                mbar_arrive(&p_full[m]);
+                mbar_arrive(&at_empty[slot]);
+            }
         }
         if (ok && tiles > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[m], 0, abort_flag));
-            if (!ok && lane == 0) give_up();
+            ok = all_wait(&o_full[m], 0);
             tc_fence_after();
         }
         // ---- the row's outputs
@@ -527,17 +613,16 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
         const float inv = some ? __frcp_rn(sum) : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
             __syncwarp();
             if (tiles > 0) {
-                tmem_ld32(o_at + 32 * c, v[0]);
-                tmem_ld_wait32(v[0]);
+                tmem_ld32(o_at + 32 * c, v);
+                tmem_ld_wait32(v);
             }
             if (!there) continue;
-            float *o = reinterpret_cast<float *>(v[0]);
-            if (tiles == 0 || (!some && direct)) {
+            float o[32];
 #pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = 0.0f;
-            }
+            for (int u = 0; u < 32; ++u) o[u] = tiles == 0 || (!some && direct) ? 0.0f : __uint_as_float(v[u]);
             if (direct) {
                 auto store = [&](auto type) {
                     using T = decltype(type);
@@ -573,6 +658,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQParts>::kThreads, 1)
             a.lse[((int64_t)b * a.tokens + n) * a.heads + head] =
                 some ? (ref + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         tc_fence_before();
+        }
     }
     __syncthreads();
     if (warp == kMmaWarp) {
