@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
 
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
     const int64_t group = blockIdx.x % a.groups;
     const int hk = (int)(group % a.c.heads), b = (int)(group / a.c.heads), split = blockIdx.y;
     const int share = a.heads / a.c.heads, P = a.c.page_tokens;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_ptr;
+    // all 512 columns are this CTA's: they begin at column 0
     auto give_up = [&]() {
         *abort_flag = 1;
         set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
@@ -306,65 +306,79 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     if (warp >= 12) {
         fewer_registers<kOtherRegs>();
-        if (warp == kMmaWarp && lane == 0 && tiles > 0) {
+        if (warp == kMmaWarp && tiles > 0) {
             // ------------------------------------------------ MMA issuer
+            // The whole warp goes along, so that descriptors stay in uniform registers (one
+            // lane alone took 90 clocks to issue an MMA of 64); one lane issues.
             constexpr uint32_t kIdescS = idesc_f16_f32(128, kN), kIdescO = idesc_f16_f32(128, D) | kIdescBMn;
             const uint32_t stage0 = smem_u32(smem + C::kOffStage);
             const uint64_t q_desc = sdesc_k128(smem_u32(smem)), k_desc = sdesc_k128(stage0);
             const uint64_t v_desc = sdesc_mn128(stage0, kN * 128);
+            const int n = __reduce_max_sync(0xffffffffu, tiles);
+            const bool two = __reduce_max_sync(0xffffffffu, groups) > 1;
+            const bool one = elect_one();
             bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (ok && !mbar_wait(bar, parity, abort_flag)) {
-                    give_up();
-                    ok = false;
-                }
-            };
             int stage = 0;
             uint32_t phase = 0;  // of the next fill that is waited for
+            auto outputs = [&](int m, int i, int vs) {  // P V of tile i
+                const uint64_t v = v_desc + vs * (C::kStageBytes / 16);
+                if (one) {
+#pragma unroll
+                    for (int j = 0; j < kN / 16; ++j)
+#pragma unroll
+                        for (int part = 0; part < kPParts; ++part)
+                            mma_f16_ts(C::kO(m), C::kS(m) + j / 2 * 32 + j % 2 * 8 + part * 16, v + j * 128, kIdescO,
+                                       j + part > 0 ? 1 : i > 0);
+                    if (i + 1 == n) mma_commit(&o_full[m]);
+                }
+            };
+            auto scores = [&](int m, int ks) {  // S of a tile
+                const uint64_t k = k_desc + ks * (C::kStageBytes / 16);
+                const uint64_t q = q_desc + m * (kQParts * C::kQBytes / 16);
+                if (one) {
+#pragma unroll
+                    for (int part = 0; part < kQParts; ++part)
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j)
+                            mma_f16_ss(C::kS(m), q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                                       k + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
+                    mma_commit(&s_full[m]);
+                }
+            };
 #pragma unroll 1
-            for (int i = -1; i < tiles && ok; ++i) {
+            for (int i = -1; i < n; ++i) {
                 const int vs = stage;  // V of tile i, then K of the next
                 const uint32_t vphase = phase;
                 if (i >= 0 && ++stage == kStages) stage = 0, phase ^= 1;
                 const int ks = stage;
                 const uint32_t kphase = phase;
-                if (i + 1 < tiles && ++stage == kStages) stage = 0, phase ^= 1;
-#pragma unroll 1
-                for (int m = 0; m < groups && ok; ++m) {
+                if (++stage == kStages) stage = 0, phase ^= 1;
+                if (i >= 0) {
+                    if (!(ok = all_wait(&p_full[0], i & 1) && all_wait(&kv_full[vs], vphase))) break;
+                    tc_fence_after();
+                    outputs(0, i, vs);
+                    if (!two && one) mma_commit(&kv_empty[vs]);
+                }
+                if (i + 1 < n) {  // S of the next tile, in P's place
+                    if (!(ok = all_wait(&kv_full[ks], kphase))) break;
+                    tc_fence_after();
+                    scores(0, ks);
+                    if (!two && one) mma_commit(&kv_empty[ks]);
+                }
+                if (kM == 2 && two) {
                     if (i >= 0) {
-                        wait(&p_full[m], i & 1);
-                        if (m == 0) wait(&kv_full[vs], vphase);
-                        if (!ok) break;
+                        if (!(ok = all_wait(&p_full[kM - 1], i & 1))) break;
                         tc_fence_after();
-                        const uint64_t v = v_desc + vs * (C::kStageBytes / 16);
-                        const uint32_t p_at = tmem + C::kS(m), o_at = tmem + C::kO(m);
-#pragma unroll
-                        for (int j = 0; j < kN / 16; ++j)
-#pragma unroll
-                            for (int part = 0; part < kPParts; ++part)
-                                mma_f16_ts(o_at, p_at + j / 2 * 32 + j % 2 * 8 + part * 16, v + j * 128, kIdescO,
-                                           j + part > 0 ? 1 : i > 0);
-                        if (m == groups - 1) mma_commit(&kv_empty[vs]);
-                        if (i + 1 == tiles) mma_commit(&o_full[m]);
+                        outputs(kM - 1, i, vs);
+                        if (one) mma_commit(&kv_empty[vs]);
                     }
-                    if (i + 1 < tiles) {  // S of the next tile, in P's place
-                        if (m == 0) wait(&kv_full[ks], kphase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t k = k_desc + ks * (C::kStageBytes / 16);
-                        const uint64_t q = q_desc + m * (kQParts * C::kQBytes / 16);
-#pragma unroll
-                        for (int part = 0; part < kQParts; ++part)
-#pragma unroll
-                            for (int j = 0; j < D / 16; ++j)
-                                mma_f16_ss(tmem + C::kS(m), q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
-                                           k + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
-                        mma_commit(&s_full[m]);
-                        if (m == groups - 1) mma_commit(&kv_empty[ks]);
+                    if (i + 1 < n) {
+                        scores(kM - 1, ks);
+                        if (one) mma_commit(&kv_empty[ks]);
                     }
                 }
             }
-            if (!ok) {  // wait until every MMA issued so far has finished
+            if (!ok && one) {  // wait until every MMA issued so far has finished
                 mma_commit(&o_full[0]);
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&o_full[0], 0) && clock64() - t0 < kWaitLimitCycles) {
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int m = warp / 4, r = tid;
         if (m < groups) {
         const uint32_t quad = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t s_at = tmem + C::kS(m) + quad, o_at = tmem + C::kO(m) + quad;
+        const uint32_t s_at = C::kS(m) + quad, o_at = C::kO(m) + quad;
         const int pos = PREFIX ? len - 1 : pos0 + (r0 + r) / share;
         const int see = r < rows ? pos + 1 : 0;
         const int low = !PREFIX && a.window && pos >= a.window ? pos - a.window + 1 : 0;
@@ -663,7 +677,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(0, 512);
     }
 }
 
