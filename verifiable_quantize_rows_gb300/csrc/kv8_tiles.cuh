@@ -3,12 +3,13 @@
 //
 // A CTA takes up to kM x 128 rows (queries of one key/value head: the heads of its group
 // times tokens) and walks the tiles of kN positions that some of them see:
-//   S = Q K^T          one accumulator of 128 x kN per 128 rows, in tensor memory
-//   p' = 2^(S ks mul + log2 vs - ref)   a thread to a row, in f16, in S's place
+//   S = Q K^T          128 x kN, in tensor memory, one place that the groups of 128 rows use in turn
+//   p' = 2^(S ks mul + log2 vs - ref)   a thread to a row, in f16, half a tile at a time
 //   O += P V           P read from tensor memory, O stays there
 // with ks, vs the page's scales (one for each 16 positions of a tile), mul the row's
 // multiplier, ref the row's running reference, which follows the maximum only when that is
-// more than 2^4 above it (O is then rescaled where it lies); sums of p = p' / vs in f32.
+// above 2^15 (what f16 holds) and makes it 2^9 then: O is rescaled where it lies, a few times
+// in a row's life.  Sums of p = p' / vs in f32.
 // Codes are exact in f16, so K and V are too; queries are relative to a power of two near
 // their row's largest, f32's as two f16 parts (22 bits).
 //
@@ -17,8 +18,8 @@
 //              tile in registers;
 //   8-11       codes into f16 operands, in a ring of shared memory that K and V tiles take
 //              in turn; each tile's loads are sent two fills ahead;
-//   12         one thread issues the MMAs: P V of a tile, then S of the next, for one group
-//              of rows while the other's softmax runs;
+//   12         issues the MMAs: S of a tile as soon as the one before it has been read into
+//              registers, P V of each half tile as it comes;
 //   13         finds where the tiles' pages lie, and their scales, some tiles at a time.
 #pragma once
 
@@ -49,7 +50,7 @@ struct TileArgs {
     int32_t *dstatus;
 };
 
-constexpr float kTileTop = 11.0f, kTileMost = 15.0f;
+constexpr float kTileTop = 9.0f, kTileMost = 15.0f;  // exponents of a new reference's largest p', and of any
 constexpr int kAtSlots = 4;
 
 __device__ __forceinline__ float tile_exp2(float x) {
@@ -78,10 +79,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     return r;
 }
 
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) { tmem_st32(at, r); }
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) { tmem_st16(at, r); }
+
 // The lowest n bits.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// What a CTA of some rows sees: `sink_tiles` tiles from the first, then those from `first`.
+// What a CTA of some rows sees: the tiles from `first`, then (whose few positions would
+// begin with a low reference) `sink_tiles` from the sequence's start.
 struct Seen {
     int tiles, sink_tiles, first;
     int low, see;  // the lowest position of the window part, and the end
@@ -116,18 +121,21 @@ struct TileCfg {
     static constexpr int kOffAt = kOffStage + kStages * kStageBytes;
     static constexpr int kOffMul = kOffAt + kAtSlots * kGroups * 16;
     static constexpr int kOffBar = kOffMul + kM * 128 * 4;
-    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 3 * kM;
+    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 1 + 6 * kM;
     static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     static constexpr int kBytes = (kUsed > 118000 ? kUsed : 118000) + 1024;  // one CTA on an SM (all its tensor memory)
     static_assert(kStages >= 2 && kBytes <= 232448, "shared memory");
-    static __device__ constexpr int kS(int m) { return m * kN; }               // columns of tensor memory
-    static __device__ constexpr int kO(int m) { return kM * kN + m * D; }
+    // columns of tensor memory: S (the groups of rows in turn), P's and O's
+    static constexpr int kPCols = kN / 2;  // one part of a tile, or two of half a tile
+    static __device__ constexpr int kP(int m) { return kN + m * kPCols; }
+    static __device__ constexpr int kO(int m) { return kN + kM * kPCols + m * D; }
+    static_assert(kN + kM * (kPCols + D) <= 512, "tensor memory");
 };
 
 constexpr int kTileThreads = 512;
 // Registers of a softmax, a converting and another thread; together no more than four
 // times the 128 that the block is launched with.
-constexpr int kSoftRegs = 168, kConvRegs = 112, kOtherRegs = 64;
+constexpr int kSoftRegs = 176, kConvRegs = 112, kOtherRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kOtherRegs <= 4 * 128, "register split");
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -158,12 +166,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     // of a tile's groups of 16 positions: key scale, log2 of the value scale, its reciprocal,
-    // and the place in the pool (in groups; -1: nowhere)
+    // and the place in the pool (in groups; unseen: exponents of -inf, any place)
     float4 *at_s = reinterpret_cast<float4 *>(smem + C::kOffAt);
     float *mul_s = reinterpret_cast<float *>(smem + C::kOffMul);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *kv_full = bars, *kv_empty = bars + kStages, *at_full = bars + 2 * kStages;
-    uint64_t *at_empty = at_full + kAtSlots, *s_full = at_empty + kAtSlots, *p_full = s_full + kM, *o_full = p_full + kM;
+    uint64_t *at_empty = at_full + kAtSlots, *s_empty = at_empty + kAtSlots, *s_full = s_empty + 1;
+    uint64_t *o_full = s_full + kM, *p_full = o_full + kM, *p_empty = p_full + 2 * kM;  // [m][slot]
+    // P goes to the tensor cores by halves of a tile: one part has room for both, two parts for one
+    constexpr int kSlots = kPParts == 1 ? 2 : 1, kHalf = kN / 2;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
 
@@ -206,7 +217,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int groups = rows > 128 ? kM : 1;  // of 128 rows
     auto position = [&](int i) {  // of the CTA's tile i
         const int v = begin + i;
-        return (v < seen.sink_tiles ? v : v - seen.sink_tiles + seen.first) * kN;
+        const int near = seen.tiles - seen.sink_tiles;
+        return (v < near ? seen.first + v : v - near) * kN;
     };
 
     if (tid == 0) {
@@ -220,9 +232,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int m = 0; m < kM; ++m) {
             mbar_init(&s_full[m], 1);
-            mbar_init(&p_full[m], 4);
             mbar_init(&o_full[m], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&p_full[2 * m + u], 4);
+                mbar_init(&p_empty[2 * m + u], 1);
+            }
         }
+        mbar_init(s_empty, 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -237,17 +253,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // the scale), in f16 parts, rows of 64 dims in the 128-byte swizzle.
     auto load_queries = [&](auto type) {
         using T = decltype(type);
-        constexpr int kAhead = 4;
+        constexpr int kAhead = 4, kMine = kM * 128 / (kTileThreads / 32);  // rows of a warp
+        // where row `lane` of the warp's is
+        const int n = (r0 + warp * kMine + lane) / share, h = (r0 + warp * kMine + lane) % share;
+        const int64_t where = (PREFIX ? n / a.tokens * a.q.stride_batch + n % a.tokens * a.q.stride_token
+                                      : b * a.q.stride_batch + n * a.q.stride_token) + (hk * share + h) * a.q.stride_head;
 #pragma unroll 1
-        for (int rr = warp * kAhead; rr < groups * 128; rr += kTileThreads / 32 * kAhead) {
+        for (int r1 = 0; r1 < kMine; r1 += kAhead) {
+            const int rr = warp * kMine + r1;
+            if (rr >= groups * 128) break;
             float q[kAhead][D / 32];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int r = r0 + rr + i;
-                const int64_t n = r / share;
-                const int64_t at = PREFIX ? n / a.tokens * a.q.stride_batch + n % a.tokens * a.q.stride_token
-                                          : b * a.q.stride_batch + n * a.q.stride_token;
-                const T *row = static_cast<const T *>(a.q.data) + at + (hk * share + r % share) * a.q.stride_head + lane;
+                const T *row = static_cast<const T *>(a.q.data) + __shfl_sync(0xffffffffu, where, r1 + i) + lane;
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) q[i][j] = rr + i < rows ? to_f32(row[32 * j]) : 0.0f;
             }
@@ -299,7 +317,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     // a whole warp's wait
     auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        bool ok = mbar_sleep_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        const long long t0 = clock64();
+#pragma unroll 1
+        while (!ok) {
+            if (*abort_flag || clock64() - t0 > kWaitLimitCycles) break;
+            ok = mbar_sleep_wait(bar, parity);
+        }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) give_up();
         return ok;
     };
@@ -318,18 +344,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const bool two = __reduce_max_sync(0xffffffffu, groups) > 1;
             const bool one = elect_one();
             bool ok = true;
-            int stage = 0;
-            uint32_t phase = 0;  // of the next fill that is waited for
-            auto outputs = [&](int m, int i, int vs) {  // P V of tile i
+            // P V of tile i, by halves
+            auto outputs = [&](int m, int i, int vs) {
                 const uint64_t v = v_desc + vs * (C::kStageBytes / 16);
-                if (one) {
 #pragma unroll
-                    for (int j = 0; j < kN / 16; ++j)
+                for (int half = 0; half < 2; ++half) {
+                    const int slot = 2 * m + half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
+                    if (!(ok = all_wait(&p_full[slot], use & 1))) return;
+                    tc_fence_after();
+                    if (one) {
 #pragma unroll
-                        for (int part = 0; part < kPParts; ++part)
-                            mma_f16_ts(C::kO(m), C::kS(m) + j / 2 * 32 + j % 2 * 8 + part * 16, v + j * 128, kIdescO,
-                                       j + part > 0 ? 1 : i > 0);
-                    if (i + 1 == n) mma_commit(&o_full[m]);
+                        for (int j = 0; j < kHalf / 16; ++j)
+#pragma unroll
+                            for (int part = 0; part < kPParts; ++part)
+                                mma_f16_ts(C::kO(m),
+                                           C::kP(m) + half % kSlots * (kHalf / 2) + part * (kHalf / 2) + 8 * j,
+                                           v + (half * (kHalf / 16) + j) * 128, kIdescO, half + j + part > 0 ? 1 : i > 0);
+                        mma_commit(&p_empty[slot]);
+                        if (half == 1 && i + 1 == n) mma_commit(&o_full[m]);
+                    }
                 }
             };
             auto scores = [&](int m, int ks) {  // S of a tile
@@ -340,43 +373,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int part = 0; part < kQParts; ++part)
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
-                            mma_f16_ss(C::kS(m), q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                            mma_f16_ss(0, q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
                                        k + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
                     mma_commit(&s_full[m]);
                 }
             };
+            // S(0), S(1), ... of rows and tiles in turn take one place, each when the one before
+            // it has been read; P V of a tile follows the S that is `groups` places ahead of it.
+            int s_uses = 0, k_stage = 0, v_stage = 1;  // fills K 0, V 0, K 1, V 1, ...
+            uint32_t k_phase = 0, v_phase = 0;
+            auto step = [&](int &stage, uint32_t &phase) {
+                stage += 2;
+                if (stage >= kStages) stage -= kStages, phase ^= 1;
+            };
+            auto next_scores = [&](int m, bool first, bool last) {
+                if (first && !(ok = all_wait(&kv_full[k_stage], k_phase))) return;
+                if (s_uses > 0 && !(ok = all_wait(s_empty, (s_uses - 1) & 1))) return;
+                ++s_uses;
+                tc_fence_after();
+                scores(m, k_stage);
+                if (last) {
+                    if (one) mma_commit(&kv_empty[k_stage]);
+                    step(k_stage, k_phase);
+                }
+            };
+            next_scores(0, true, !two);
+            if (ok && kM == 2 && two) next_scores(kM - 1, false, true);
+            if (ok && n > 1) next_scores(0, true, !two);
 #pragma unroll 1
-            for (int i = -1; i < n; ++i) {
-                const int vs = stage;  // V of tile i, then K of the next
-                const uint32_t vphase = phase;
-                if (i >= 0 && ++stage == kStages) stage = 0, phase ^= 1;
-                const int ks = stage;
-                const uint32_t kphase = phase;
-                if (++stage == kStages) stage = 0, phase ^= 1;
-                if (i >= 0) {
-                    if (!(ok = all_wait(&p_full[0], i & 1) && all_wait(&kv_full[vs], vphase))) break;
-                    tc_fence_after();
-                    outputs(0, i, vs);
-                    if (!two && one) mma_commit(&kv_empty[vs]);
-                }
-                if (i + 1 < n) {  // S of the next tile, in P's place
-                    if (!(ok = all_wait(&kv_full[ks], kphase))) break;
-                    tc_fence_after();
-                    scores(0, ks);
-                    if (!two && one) mma_commit(&kv_empty[ks]);
-                }
+            for (int i = 0; i < n && ok; ++i) {
+                if (!(ok = all_wait(&kv_full[v_stage], v_phase))) break;
+                outputs(0, i, v_stage);
                 if (kM == 2 && two) {
-                    if (i >= 0) {
-                        if (!(ok = all_wait(&p_full[kM - 1], i & 1))) break;
-                        tc_fence_after();
-                        outputs(kM - 1, i, vs);
-                        if (one) mma_commit(&kv_empty[vs]);
-                    }
-                    if (i + 1 < n) {
-                        scores(kM - 1, ks);
-                        if (one) mma_commit(&kv_empty[ks]);
-                    }
+                    if (ok && i + 1 < n) next_scores(kM - 1, false, true);
+                    if (ok) outputs(kM - 1, i, v_stage);
                 }
+                if (one) mma_commit(&kv_empty[v_stage]);
+                step(v_stage, v_phase);
+                if (ok && i + 2 < n) next_scores(0, true, !two);
             }
             if (!ok && one) {  // wait until every MMA issued so far has finished
                 mma_commit(&o_full[0]);
@@ -392,7 +426,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
             for (int i0 = 0; i0 < tiles && ok; i0 += kBatch) {
                 const int i = i0 + lane / C::kGroups;
-                float4 at = make_float4(0.0f, -INFINITY, 0.0f, __int_as_float(-1));
+                float4 at = make_float4(0.0f, -INFINITY, 0.0f, __int_as_float(0));
                 if (i < tiles) {
                     const int pos = position(i) + lane % C::kGroups * 16;
                     // a page that no row sees is not looked up
@@ -424,26 +458,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fewer_registers<kConvRegs>();
         constexpr int kChunks = D / 16;           // 16-byte pieces of a row
         constexpr int kPer = kN * kChunks / 128;  // of a thread and tile
-        const int ctid = tid - 256;
-        // Piece j of a thread.  Eight lanes store to two rows, of either parity, so that the
-        // swizzle spreads them over all banks.
-        auto row_of = [&](int j) {
-            const int e = ctid + j * 128;
-            return kChunks % 4 ? e / kChunks : e / (2 * kChunks) * 2 + e % 8 / 4;
+        const uint32_t ctid = tid - 256;
+        // Piece j of a thread: which 16 bytes of which row.  Eight lanes store to two rows, of
+        // either parity, so that the swizzle spreads them over all banks; a thread's pieces
+        // are whole groups of 16 rows apart, or even parts of one (but for 96 dims).
+        constexpr uint32_t kStep = D == 96 ? 0 : 2048 / D;  // rows
+        const uint32_t row0 = kChunks % 4 ? ctid / kChunks : ctid / (2 * kChunks) * 2 + ctid % 8 / 4;
+        const uint32_t chunk0 = kChunks % 4 ? ctid % kChunks : ctid % 4 + ctid / 8 % (kChunks / 4 ? kChunks / 4 : 1) * 4;
+        auto group_of = [&](uint32_t j) {
+            return D == 96 ? (ctid + j * 128) / kChunks / 16 : kStep >= 16 ? row0 / 16 + j * (kStep / 16) : j / (16 / (kStep ? kStep : 1));
         };
-        auto chunk_of = [&](int j) {
-            const int e = ctid + j * 128;
-            return kChunks % 4 ? e % kChunks : e % 4 + e / 8 % (kChunks / 4 ? kChunks / 4 : 1) * 4;
+        auto row_of = [&](uint32_t j) {  // of the group
+            return D == 96 ? (ctid + j * 128) / kChunks % 16 : kStep >= 16 ? row0 % 16 : row0 + j % (16 / (kStep ? kStep : 1)) * kStep;
         };
+        auto chunk_of = [&](uint32_t j) { return D == 96 ? (ctid + j * 128) % kChunks : chunk0; };
         uint4 buf[2][kPer];  // of K and V tiles
         auto load = [&](uint4 (&x)[kPer], const int8_t *codes, int i) {
             const float4 *at = at_s + i % kAtSlots * C::kGroups;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                const int place = __float_as_int(at[row_of(j) / 16].w);
-                x[j] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                if (place >= 0)
-                    x[j] = load_codes(codes + (int64_t)place * (16 * D) + row_of(j) % 16 * D + chunk_of(j) * 16);
+                const int place = __float_as_int(at[group_of(j)].w);
+                x[j] = load_codes(codes + (row_of(j) * D + chunk_of(j) * 16) + (int64_t)place * (16 * D));
             }
         };
         bool ok = true;
@@ -463,7 +498,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 uint8_t *tile = smem + C::kOffStage + stage * C::kStageBytes;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
-                    const int row = row_of(j), chunk = chunk_of(j);
+                    const uint32_t row = row_of(j), chunk = chunk_of(j);
                     uint32_t h[8];
                     const uint32_t w[4] = {buf[side][j].x, buf[side][j].y, buf[side][j].z, buf[side][j].w};
 #pragma unroll
@@ -475,8 +510,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         h[2 * u] = *reinterpret_cast<const uint32_t *>(&l);
                         h[2 * u + 1] = *reinterpret_cast<const uint32_t *>(&g);
                     }
-                    uint8_t *line = tile + chunk / 4 * (kN * 128) + row * 128;
-                    const int c = chunk % 4 * 2;
+                    uint8_t *line = tile + group_of(j) * 2048 + (chunk / 4 * (kN * 128) + row * 128);
+                    const uint32_t c = chunk % 4 * 2;
                     *reinterpret_cast<uint4 *>(line + ((c ^ row % 8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4 *>(line + ((c + 1 ^ row % 8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
@@ -499,7 +534,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int m = warp / 4, r = tid;
         if (m < groups) {
         const uint32_t quad = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t s_at = C::kS(m) + quad, o_at = C::kO(m) + quad;
+        const uint32_t s_at = quad, p_at = C::kP(m) + quad, o_at = C::kO(m) + quad;
         const int pos = PREFIX ? len - 1 : pos0 + (r0 + r) / share;
         const int see = r < rows ? pos + 1 : 0;
         const int low = !PREFIX && a.window && pos >= a.window ? pos - a.window + 1 : 0;
@@ -517,12 +552,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const float4 *of_s = at_s + slot * C::kGroups;
             if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
             tc_fence_after();
+            const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
             uint32_t v[kN / 32][32];  // the row's scores
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) tmem_ld32(s_at + 32 * c, v[c]);
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
-            const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty);
             if (edge) {  // what the row does not see
 #pragma unroll
                 for (int c = 0; c < kN / 32; ++c) {
@@ -534,15 +572,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             }
             // the largest exponent, relative to the reference
-            float top = -INFINITY;
+            float y[C::kGroups], top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) y[g] = __uint_as_float(v[g / 2][g % 2 * 16]);
+#pragma unroll
+            for (int u = 1; u < 16; ++u)  // the groups side by side, not one after another
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) y[g] = fmaxf(y[g], __uint_as_float(v[g / 2][g % 2 * 16 + u]));
+            // (a score of -inf times 0 would be no number)
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) {
                 const float2 of = *reinterpret_cast<const float2 *>(of_s + g);
-                const uint32_t *x = v[g / 2] + g % 2 * 16;
-                float y = __uint_as_float(x[0]);
-#pragma unroll
-                for (int u = 1; u < 16; ++u) y = fmaxf(y, __uint_as_float(x[u]));
-                if (y > -INFINITY) top = fmaxf(top, fmaf(y, of.x * mul, of.y - ref));
+                top = fmaxf(top, fmaf(y[g], fmaxf(of.x * mul, 1e-37f), of.y - ref));
             }
             const bool move = none ? top > -INFINITY : top > kTileMost;
             if (__any_sync(0xffffffffu, move)) {
@@ -554,6 +595,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     none = false;
                 }
                 if (i > 0) {
+                    // O is at rest once the last P of the tile before is used up
+#pragma unroll
+                    for (int u = 0; u < kSlots; ++u)
+                        if (ok) ok = all_wait(&p_empty[2 * m + u], (kSlots == 2 ? i - 1 : 2 * i - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t o[16];
@@ -566,52 +613,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             }
 #pragma unroll
-            for (int c = 0; c < kN / 32; ++c) {
-                uint32_t hi[16], lo[16];
+            for (int half = 0; half < 2; ++half) {
+                uint32_t hi[kHalf / 2], lo[kHalf / 2];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 of = of_s[2 * c + g];
-                    // (a score of -inf times 0 would be no number)
+                for (int g = 0; g < kHalf / 16; ++g) {
+                    const float4 of = of_s[half * (kHalf / 16) + g];
                     const float f = fmaxf(of.x * mul, 1e-37f), off = of.y - ref;
                     const uint64_t ff = pair_of(f, f), oo = pair_of(off, off);
-                    const uint32_t *x = v[c] + 16 * g;
+                    const uint32_t *x = v[(half * kHalf + 16 * g) / 32] + (half * kHalf + 16 * g) % 32;
                     float p[16];
 #pragma unroll
                     for (int u = 0; u < 16; u += 2) {
                         unpair(fma2(pair_of(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), ff, oo), p[u], p[u + 1]);
                         p[u] = tile_exp2(p[u]), p[u + 1] = tile_exp2(p[u + 1]);
                     }
-                    uint64_t part = pair_of(p[0], p[1]);
+                    uint64_t part[2] = {pair_of(p[0], p[1]), pair_of(p[2], p[3])};
 #pragma unroll
-                    for (int u = 2; u < 16; u += 2) part = add2(part, pair_of(p[u], p[u + 1]));
+                    for (int u = 4; u < 16; u += 2) part[u / 2 % 2] = add2(part[u / 2 % 2], pair_of(p[u], p[u + 1]));
                     float even, odd;
-                    unpair(part, even, odd);
+                    unpair(add2(part[0], part[1]), even, odd);
                     sum = fmaf(even + odd, of.z, sum);
 #pragma unroll
                     for (int u = 0; u < 16; u += 2) {
-                        if (kPParts == 1) {
-                            const __half2 h = __floats2half2_rn(p[u], p[u + 1]);
-                            hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
-                        } else {  // the first 11 bits, and 11 of the rest
-                            const float a0 = __uint_as_float(__float_as_uint(p[u]) & 0xffffe000u);
-                            const float a1 = __uint_as_float(__float_as_uint(p[u + 1]) & 0xffffe000u);
-                            const __half2 h = __floats2half2_rn(a0, a1);
-                            const __half2 rest = __floats2half2_rn(p[u] - a0, p[u + 1] - a1);
-                            hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                        const __half2 h = __floats2half2_rn(p[u], p[u + 1]);
+                        hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                        if (kPParts == 2) {
+                            const float2 back = __half22float2(h);
+                            const __half2 rest = __floats2half2_rn(p[u] - back.x, p[u + 1] - back.y);
                             lo[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&rest);
                         }
                     }
                 }
-                tmem_st16(s_at + 32 * c, hi);
-                if (kPParts == 2) tmem_st16(s_at + 32 * c + 16, lo);
+                // its place is free when what was there has been multiplied
+                const int place = half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
+                if (use > 0 && !(ok = all_wait(&p_empty[2 * m + place], (use - 1) & 1))) break;
+                tc_fence_after();
+                tmem_store(p_at + place * (kHalf / 2), hi);
+                if (kPParts == 2) tmem_store(p_at + kHalf / 2, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * m + place]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&p_full[m]);
-                mbar_arrive(&at_empty[slot]);
-            }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&at_empty[slot]);
         }
         if (ok && tiles > 0) {
             ok = all_wait(&o_full[m], 0);
