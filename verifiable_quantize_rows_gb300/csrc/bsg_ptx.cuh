@@ -49,19 +49,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// As mbar_try_wait, but asleep for up to some microseconds where the phase is not complete.
-__device__ __forceinline__ bool mbar_sleep_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
-        : "memory");
-    return ok != 0;
-}
-
 // Wait until the phase with the given parity of `bar` has completed.
 // Returns false if `*abort` became non-zero or the wait ran past its limit;
 // the caller then takes its error path.

@@ -52,6 +52,7 @@ struct TileArgs {
 
 constexpr float kTileTop = 9.0f, kTileMost = 15.0f;  // exponents of a new reference's largest p', and of any
 constexpr int kAtSlots = 4;
+constexpr int kWaitTries = 1 << 23;  // of some tens of clocks at least: far above any wait here
 
 __device__ __forceinline__ float tile_exp2(float x) {
     float y;
@@ -119,9 +120,8 @@ struct TileCfg {
     static constexpr int kGroups = kN / 16;
     static constexpr int kOffStage = kM * kQParts * kQBytes;
     static constexpr int kOffAt = kOffStage + kStages * kStageBytes;
-    static constexpr int kOffMul = kOffAt + kAtSlots * kGroups * 16;
-    static constexpr int kOffBar = kOffMul + kM * 128 * 4;
-    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 1 + 6 * kM;
+    static constexpr int kOffBar = kOffAt + kAtSlots * kGroups * 16;
+    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 1 + 7 * kM;
     static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     static constexpr int kBytes = (kUsed > 118000 ? kUsed : 118000) + 1024;  // one CTA on an SM (all its tensor memory)
     static_assert(kStages >= 2 && kBytes <= 232448, "shared memory");
@@ -168,11 +168,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // of a tile's groups of 16 positions: key scale, log2 of the value scale, its reciprocal,
     // and the place in the pool (in groups; unseen: exponents of -inf, any place)
     float4 *at_s = reinterpret_cast<float4 *>(smem + C::kOffAt);
-    float *mul_s = reinterpret_cast<float *>(smem + C::kOffMul);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *kv_full = bars, *kv_empty = bars + kStages, *at_full = bars + 2 * kStages;
     uint64_t *at_empty = at_full + kAtSlots, *s_empty = at_empty + kAtSlots, *s_full = s_empty + 1;
     uint64_t *o_full = s_full + kM, *p_full = o_full + kM, *p_empty = p_full + 2 * kM;  // [m][slot]
+    uint64_t *q_full = p_empty + 2 * kM;
     // P goes to the tensor cores by halves of a tile: one part has room for both, two parts for one
     constexpr int kSlots = kPParts == 1 ? 2 : 1, kHalf = kN / 2;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(bars + C::kBars);
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int m = 0; m < kM; ++m) {
             mbar_init(&s_full[m], 1);
             mbar_init(&o_full[m], 1);
+            mbar_init(&q_full[m], 4);
             for (int u = 0; u < 2; ++u) {
                 mbar_init(&p_full[2 * m + u], 4);
                 mbar_init(&p_empty[2 * m + u], 1);
@@ -249,63 +250,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     griddep_launch_dependents();
 
-    // Queries: each row relative to a power of two near its largest |q| (with the sign of
-    // the scale), in f16 parts, rows of 64 dims in the 128-byte swizzle.
-    auto load_queries = [&](auto type) {
-        using T = decltype(type);
-        constexpr int kAhead = 4, kMine = kM * 128 / (kTileThreads / 32);  // rows of a warp
-        // where row `lane` of the warp's is
-        const int n = (r0 + warp * kMine + lane) / share, h = (r0 + warp * kMine + lane) % share;
-        const int64_t where = (PREFIX ? n / a.tokens * a.q.stride_batch + n % a.tokens * a.q.stride_token
-                                      : b * a.q.stride_batch + n * a.q.stride_token) + (hk * share + h) * a.q.stride_head;
-#pragma unroll 1
-        for (int r1 = 0; r1 < kMine; r1 += kAhead) {
-            const int rr = warp * kMine + r1;
-            if (rr >= groups * 128) break;
-            float q[kAhead][D / 32];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const T *row = static_cast<const T *>(a.q.data) + __shfl_sync(0xffffffffu, where, r1 + i) + lane;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) q[i][j] = rr + i < rows ? to_f32(row[32 * j]) : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                float m = 0.0f;
-                bool bad = false;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    bad |= !isfinite(q[i][j]);
-                    m = fmaxf(m, fabsf(q[i][j]));
-                }
-                if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
-                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-                // 2^e with m 2^e in [2^13, 2^14); e <= 126 leaves subnormal rows their small error
-                const int e = max(-126, min(126, 13 + 127 - (int)(__float_as_uint(m) >> 23)));
-                const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
-                const int r = rr + i;
-                if (lane == 0) mul_s[r] = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - e) << 23);
-                uint8_t *tile = smem + r / 128 * kQParts * C::kQBytes;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const int d = lane + 32 * j;
-                    const int at = d / 64 * 16384 + r % 128 * 128 + ((d % 64 / 8 ^ r % 8) << 4) + d % 8 * 2;
-                    const float y = q[i][j] * up;
-                    const __half hi = __float2half_rn(y);
-                    *reinterpret_cast<__half *>(tile + at) = hi;
-                    if (kQParts == 2)
-                        *reinterpret_cast<__half *>(tile + C::kQBytes + at) = __float2half_rn(y - __half2float(hi));
-                }
-            }
-        }
-    };
-    if constexpr (kQParts == 2) {
-        load_queries(float{});
-    } else if constexpr (kPParts == 2) {
-        load_queries(__half{});
-    } else {
-        load_queries(__nv_bfloat16{});
-    }
     fence_async_shared();
     tc_fence_before();
     __syncthreads();
@@ -317,14 +261,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     // a whole warp's wait
     auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-        bool ok = mbar_sleep_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        const long long t0 = clock64();
+        bool ok = mbar_try_wait(bar, parity);
+        // (some twenty copies of this: as little code as may be, for the instruction caches)
 #pragma unroll 1
-        while (!ok) {
-            if (*abort_flag || clock64() - t0 > kWaitLimitCycles) break;
-            ok = mbar_sleep_wait(bar, parity);
-        }
+        for (int n = 0; !ok && n < kWaitTries && !*abort_flag; ++n) ok = mbar_try_wait(bar, parity);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) give_up();
         return ok;
@@ -344,73 +284,68 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const bool two = __reduce_max_sync(0xffffffffu, groups) > 1;
             const bool one = elect_one();
             bool ok = true;
-            // P V of tile i, by halves
-            auto outputs = [&](int m, int i, int vs) {
-                const uint64_t v = v_desc + vs * (C::kStageBytes / 16);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int slot = 2 * m + half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
-                    if (!(ok = all_wait(&p_full[slot], use & 1))) return;
+            // S(0), S(1), ... of tiles and rows in turn take one place, each when the one before
+            // it has been read; P V of a tile follows the S that is `groups` places ahead of it.
+            // (Loops rolled up: the code of all roles has to share the instruction caches.)
+            const int all = two ? 2 * n : n, ahead = two ? 2 : 1;
+            int k_stage = 0, v_stage = 1;  // fills K 0, V 0, K 1, V 1, ...
+            uint32_t k_phase = 0, v_phase = 0;
+            int s_next = 0, s_m = 0, m = 0, i = 0;
+            auto step = [&](int &stage, uint32_t &phase) {
+                stage += 2;
+                if (stage >= kStages) stage -= kStages, phase ^= 1;
+            };
+#pragma unroll 1
+            for (int q = 0; q < all && ok; ++q) {
+#pragma unroll 1
+                while (s_next < all && s_next <= q + ahead) {
+                    if (s_next < ahead && !(ok = all_wait(&q_full[s_m], 0))) break;
+                    if (s_m == 0 && !(ok = all_wait(&kv_full[k_stage], k_phase))) break;
+                    if (s_next > 0 && !(ok = all_wait(s_empty, (s_next - 1) & 1))) break;
                     tc_fence_after();
+                    const uint64_t kd = k_desc + k_stage * (C::kStageBytes / 16);
+                    const uint64_t qd = q_desc + s_m * (kQParts * C::kQBytes / 16);
+                    if (one) {
+#pragma unroll
+                        for (int part = 0; part < kQParts; ++part)
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j)
+                                mma_f16_ss(0, qd + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                                           kd + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
+                        mma_commit(&s_full[s_m]);
+                        if (s_m == ahead - 1) mma_commit(&kv_empty[k_stage]);
+                    }
+                    if (++s_m == ahead) {
+                        s_m = 0;
+                        step(k_stage, k_phase);
+                    }
+                    ++s_next;
+                }
+                if (!ok || (m == 0 && !(ok = all_wait(&kv_full[v_stage], v_phase)))) break;
+                const uint64_t v = v_desc + v_stage * (C::kStageBytes / 16);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {  // P V of tile i
+                    const int slot = 2 * m + half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
+                    if (!(ok = all_wait(&p_full[slot], use & 1))) break;
+                    tc_fence_after();
+                    const uint32_t o_at = C::kO(0) + m * D, p_at = C::kP(0) + m * C::kPCols + half % kSlots * (kHalf / 2);
+                    const uint64_t vd = v + half * (kHalf / 16 * 128);
                     if (one) {
 #pragma unroll
                         for (int j = 0; j < kHalf / 16; ++j)
 #pragma unroll
                             for (int part = 0; part < kPParts; ++part)
-                                mma_f16_ts(C::kO(m),
-                                           C::kP(m) + half % kSlots * (kHalf / 2) + part * (kHalf / 2) + 8 * j,
-                                           v + (half * (kHalf / 16) + j) * 128, kIdescO, half + j + part > 0 ? 1 : i > 0);
+                                mma_f16_ts(o_at, p_at + part * (kHalf / 2) + 8 * j, vd + j * 128, kIdescO,
+                                           j + part > 0 ? 1 : half + i > 0);
                         mma_commit(&p_empty[slot]);
-                        if (half == 1 && i + 1 == n) mma_commit(&o_full[m]);
                     }
                 }
-            };
-            auto scores = [&](int m, int ks) {  // S of a tile
-                const uint64_t k = k_desc + ks * (C::kStageBytes / 16);
-                const uint64_t q = q_desc + m * (kQParts * C::kQBytes / 16);
-                if (one) {
-#pragma unroll
-                    for (int part = 0; part < kQParts; ++part)
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j)
-                            mma_f16_ss(0, q + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
-                                       k + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
-                    mma_commit(&s_full[m]);
+                if (one && i + 1 == n) mma_commit(&o_full[m]);
+                if (++m == ahead) {
+                    if (one) mma_commit(&kv_empty[v_stage]);
+                    step(v_stage, v_phase);
+                    m = 0, ++i;
                 }
-            };
-            // S(0), S(1), ... of rows and tiles in turn take one place, each when the one before
-            // it has been read; P V of a tile follows the S that is `groups` places ahead of it.
-            int s_uses = 0, k_stage = 0, v_stage = 1;  // fills K 0, V 0, K 1, V 1, ...
-            uint32_t k_phase = 0, v_phase = 0;
-            auto step = [&](int &stage, uint32_t &phase) {
-                stage += 2;
-                if (stage >= kStages) stage -= kStages, phase ^= 1;
-            };
-            auto next_scores = [&](int m, bool first, bool last) {
-                if (first && !(ok = all_wait(&kv_full[k_stage], k_phase))) return;
-                if (s_uses > 0 && !(ok = all_wait(s_empty, (s_uses - 1) & 1))) return;
-                ++s_uses;
-                tc_fence_after();
-                scores(m, k_stage);
-                if (last) {
-                    if (one) mma_commit(&kv_empty[k_stage]);
-                    step(k_stage, k_phase);
-                }
-            };
-            next_scores(0, true, !two);
-            if (ok && kM == 2 && two) next_scores(kM - 1, false, true);
-            if (ok && n > 1) next_scores(0, true, !two);
-#pragma unroll 1
-            for (int i = 0; i < n && ok; ++i) {
-                if (!(ok = all_wait(&kv_full[v_stage], v_phase))) break;
-                outputs(0, i, v_stage);
-                if (kM == 2 && two) {
-                    if (ok && i + 1 < n) next_scores(kM - 1, false, true);
-                    if (ok) outputs(kM - 1, i, v_stage);
-                }
-                if (one) mma_commit(&kv_empty[v_stage]);
-                step(v_stage, v_phase);
-                if (ok && i + 2 < n) next_scores(0, true, !two);
             }
             if (!ok && one) {  // wait until every MMA issued so far has finished
                 mma_commit(&o_full[0]);
@@ -492,6 +427,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t phase = 0;
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
+            const bool more = i + 1 < tiles;
+            const int slot = (i + 1) % kAtSlots;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 if (!ok || !(ok = all_wait(&kv_empty[stage], phase ^ 1))) break;
@@ -519,8 +456,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kv_full[stage]);
                 if (++stage == kStages) stage = 0, phase ^= 1;
-                if (i + 1 < tiles) {  // the next tile's, into the registers that are free
-                    const int slot = (i + 1) % kAtSlots;
+                if (more) {  // the next tile's, into the registers that are free
                     if (side == 0 && !(ok = all_wait(&at_full[slot], (i + 1) / kAtSlots & 1))) break;
                     load(buf[side], side ? a.c.v : a.c.k, i + 1);
                     __syncwarp();
@@ -543,7 +479,65 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int all_see = PREFIX ? len : pos0 + (r0 + m * 128) / share + 1;
         const int last_pos = PREFIX ? 0 : pos0 + (r0 + last) / share;
         const int all_low = !PREFIX && a.window && last_pos >= a.window ? last_pos - a.window + 1 : 0;
-        const float mul = mul_s[r];
+        // Queries, the warp's own rows: each relative to a power of two near its largest |q| (with
+        // the sign of the scale), in f16 parts, rows of 64 dims in the 128-byte swizzle.
+        float mul = 0.0f;
+        auto load_queries = [&](auto type) {
+            using T = decltype(type);
+            constexpr int kAhead = D == 256 ? 8 : 16;
+            const int n = (r0 + r) / share, h = (r0 + r) % share;  // where row `lane` is
+            const int64_t where = (PREFIX ? n / a.tokens * a.q.stride_batch + n % a.tokens * a.q.stride_token
+                                          : b * a.q.stride_batch + n * a.q.stride_token) + (hk * share + h) * a.q.stride_head;
+            uint8_t *const tile = smem + m * kQParts * C::kQBytes;
+#pragma unroll 1
+            for (int r1 = 0; r1 < 32; r1 += kAhead) {
+                float q[kAhead][D / 32];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const T *row = static_cast<const T *>(a.q.data) + __shfl_sync(0xffffffffu, where, r1 + i) + lane;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) q[i][j] = warp * 32 + r1 + i < rows ? to_f32(row[32 * j]) : 0.0f;
+                }
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    float x = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        bad |= !isfinite(q[i][j]);
+                        x = fmaxf(x, fabsf(q[i][j]));
+                    }
+                    x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+                    // 2^e with x 2^e in [2^13, 2^14); e <= 126 leaves subnormal rows their small error
+                    const int e = max(-126, min(126, 13 + 127 - (int)(__float_as_uint(x) >> 23)));
+                    const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
+                    const int at_r = warp % 4 * 32 + r1 + i;
+                    if (lane == r1 + i)
+                        mul = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        const int d = lane + 32 * j;
+                        const int at = d / 64 * 16384 + at_r * 128 + ((d % 64 / 8 ^ at_r % 8) << 4) + d % 8 * 2;
+                        const float y = q[i][j] * up;
+                        const __half hi = __float2half_rn(y);
+                        *reinterpret_cast<__half *>(tile + at) = hi;
+                        if (kQParts == 2)
+                            *reinterpret_cast<__half *>(tile + C::kQBytes + at) = __float2half_rn(y - __half2float(hi));
+                    }
+                }
+                if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+            }
+        };
+        if constexpr (kQParts == 2) {
+            load_queries(float{});
+        } else if constexpr (kPParts == 2) {
+            load_queries(__half{});
+        } else {
+            load_queries(__nv_bfloat16{});
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[m]);
         float ref = 0.0f, sum = 0.0f;
         bool none = true, ok = true;
 #pragma unroll 1
@@ -553,6 +547,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
             tc_fence_after();
             const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
+            if (edge) {  // what the row does not see, where S lies (seldom; rolled up)
+#pragma unroll 1
+                for (int c = 0; c < kN / 16; ++c) {
+                    const int j = tile + 16 * c;
+                    const uint32_t mask = below(see - j) & (~below(low - j) | below(a.sinks - j));
+                    uint32_t x[16];
+                    tmem_ld16(s_at + 16 * c, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        if (!(mask & 1u << u)) x[u] = 0xff800000u;
+                    tmem_st16(s_at + 16 * c, x);
+                }
+                tmem_st_wait();
+            }
             uint32_t v[kN / 32][32];  // the row's scores
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) tmem_ld32(s_at + 32 * c, v[c]);
@@ -561,16 +570,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty);
-            if (edge) {  // what the row does not see
-#pragma unroll
-                for (int c = 0; c < kN / 32; ++c) {
-                    const int j = tile + 32 * c;
-                    const uint32_t mask = below(see - j) & (~below(low - j) | below(a.sinks - j));
-#pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        if (!(mask & 1u << u)) v[c][u] = 0xff800000u;
-                }
-            }
             // the largest exponent, relative to the reference
             float y[C::kGroups], top = -INFINITY;
 #pragma unroll
