@@ -8,7 +8,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <string.h>
+
 #include "bsg_internal.h"
+#include "bsg_ptx.cuh"
 #include "serve.cuh"
 
 namespace bsg {
@@ -20,9 +23,14 @@ constexpr int kTokenThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads)
     wcols_tokens_kernel(const T *__restrict__ X, int64_t ldx, int K, int ldk, __half *__restrict__ op,
-                        float *__restrict__ scale, unsigned int *ticket, int32_t *dstatus) {
+                        float *__restrict__ scale, uint4 *__restrict__ zero, int64_t zeros,
+                        int32_t *dstatus) {
     __shared__ uint32_t red[kTokenThreads / 32];
     const int64_t row = blockIdx.x;
+    griddep_launch_dependents();
+    // what the next launch adds into
+    for (int64_t i = row * kTokenThreads + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * kTokenThreads)
+        zero[i] = make_uint4(0, 0, 0, 0);
     const T *x = X + row * ldx;
     uint32_t m = 0;  // the largest |x|, as bits: Inf and NaN are the largest of all
     for (int k = threadIdx.x; k < K; k += kTokenThreads)
@@ -39,24 +47,399 @@ __global__ void __launch_bounds__(kTokenThreads)
     if (threadIdx.x == 0) {
         scale[row] = s;
         if (m >= 0x7f800000u) set_status(dstatus, BSG_DSTATUS_NONFINITE);
-        if (row == 0) ticket[0] = ticket[1] = 0;
     }
 }
 
+// ---- a few tokens: the weight's codes turned into operands on their way ---------
+//
+// kFewTokens tokens at a time (more: each block of them on its own, the codes then from L2).  D[column][token] += W^T X^T with the weight as the A operand, 128
+// columns as its rows: W lies k by k, columns side by side, which is A's "MN-major" form, so
+// codes become f16 where they are, without a transposition.  All k-blocks (64 x 128 codes) of
+// all column tiles form one list that the CTAs share in equal runs; a run ends a tile's sums
+// where it ends, and what is not a whole tile is added up in L2, in integers, so that the order
+// does not matter; the last to add writes Y.  Sums are exact: f32 sums of at most 1024
+// products, then int32.
+//
+// Roles: warps 0-3 take sums out of tensor memory; warps 4-11 fetch codes (cp.async into a
+// ring of each warp's own, kAhead blocks ahead) and turn them into operands; warp 12 issues
+// the MMAs; warp 13 sends for the tokens (TMA).
+constexpr int kFewTokens = 64;
+constexpr int kFewThreads = 14 * 32;
+constexpr int kFewStages = 4, kAhead = 8;
+constexpr int kWBytes = 128 * 64 * 2, kXBytes = kFewTokens * 64 * 2;  // of a stage
+constexpr int kPitch = 144;                                            // of a row of codes in the ring: 128 and its overhang
+constexpr int kRingBytes = 8 * kAhead * 8 * kPitch;                    // 8 warps, 8 rows of a block each
+constexpr int kFewSmem = kFewStages * (kWBytes + kXBytes) + kRingBytes + 256 + 1024;
+
+struct FewArgs {
+    const int8_t *Q;
+    int64_t ldq;
+    const float *token_scale, *scale;
+    int M, Mp, N, K, blocks;  // Mp: tokens rounded up to 16; blocks of 64 of K
+    int64_t all;              // blocks of all column tiles
+    int relu, dtype;
+    void *Y;
+    int64_t ldy;
+    unsigned long long *sums;  // [block of tokens][tile][Mp / 2][128]: two tokens' sums in one word
+    unsigned int *counts;      // [block of tokens][tile]: blocks added
+    int32_t *dstatus;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void few_store(const FewArgs &a, int m, int n, int32_t s, float sw) {
+    float y = __fmul_rn(__fmul_rn(__int2float_rn(s), __ldg(a.token_scale + m)), sw);
+    if (a.relu) y = y > 0.0f ? y : 0.0f;
+    const int64_t at = (int64_t)m * a.ldy + n;
+    if (a.dtype == BSG_F32)
+        static_cast<float *>(a.Y)[at] = y;
+    else if (a.dtype == BSG_F16)
+        static_cast<__half *>(a.Y)[at] = __float2half_rn(y);
+    else
+        static_cast<__nv_bfloat16 *>(a.Y)[at] = __float2bfloat16_rn(y);
+}
+
+// A place in the list of blocks.
+struct FewAt {
+    int tile, block;
+    __device__ __forceinline__ FewAt(const FewArgs &a, int64_t b) : tile((int)(b / a.blocks)), block((int)(b - (int64_t)tile * a.blocks)) {}
+    __device__ __forceinline__ void next(const FewArgs &a) {
+        if (++block == a.blocks) block = 0, ++tile;
+    }
+};
+
+// ALIGNED: every row of codes begins on 16 bytes.  kCols: columns of sums in a thread's
+// registers (tokens, rounded up).
+template <int kCols, bool ALIGNED>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    wcols_few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ CUtensorMap tokens) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    uint8_t *ring_s = smem + kFewStages * (kWBytes + kXBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring_s + kRingBytes);
+    uint64_t *full = bars, *empty = bars + kFewStages, *sum_full = bars + 2 * kFewStages, *sum_empty = sum_full + 2;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(sum_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
+    volatile int *last_s = reinterpret_cast<volatile int *>(tmem_ptr + 2);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    // this CTA's run of the list
+    const int64_t b0 = a.all * blockIdx.x / gridDim.x, b1 = a.all * (blockIdx.x + 1) / gridDim.x;
+    const int n_blocks = (int)(b1 - b0);
+    const int m0 = blockIdx.y * kFewTokens, rows = min(a.M - m0, kFewTokens);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kFewStages; ++s) {
+            mbar_init(&full[s], 8 + 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sum_full[s], 1);
+            mbar_init(&sum_empty[s], 4);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        fence_async_shared();
+    }
+    if (warp == 12) {
+        tmem_alloc(tmem_ptr, 2 * kFewTokens);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_ptr;
+    auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            set_status(a.dstatus, BSG_DSTATUS_TIMEOUT);
+        }
+        return ok;
+    };
+    // Blocks that one accumulator takes from block b on: to the end of the tile, of the run, or
+    // of 1024 products.
+    auto chunk_of = [&](int block, int left) { return min(min(a.blocks - block, kChunkK / 64), left); };
+
+    if (warp == 13) {
+        // ---- tokens
+        if (lane == 0) {
+            prefetch_tmap(&tokens);
+            griddep_wait();
+            FewAt at(a, b0);
+            for (int i = 0; i < n_blocks; ++i, at.next(a)) {
+                const int stage = i % kFewStages;
+                if (!mbar_wait(&empty[stage], (i / kFewStages & 1) ^ 1, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                mbar_arrive_expect_tx(&full[stage], a.Mp * 128);
+                tma_load_2d(&tokens, &full[stage], smem + stage * (kWBytes + kXBytes) + kWBytes,
+                            at.block * 64, m0);
+            }
+            if (*abort_flag) {  // let the copies land
+                const long long t0 = clock64();
+                while (clock64() - t0 < 2000000) {
+                }
+            }
+        }
+    } else if (warp == 12) {
+        // ---- MMAs
+        const uint32_t idesc = idesc_f16_f32(128, a.Mp) | kIdescAMn;
+        const bool one = elect_one();
+        bool ok = true;
+        int block = FewAt(a, b0).block;
+#pragma unroll 1
+        for (int i = 0, c = 0; i < n_blocks && ok; ++c) {
+            const int n = chunk_of(block, n_blocks - i), buffer = c & 1;
+            block = block + n == a.blocks ? 0 : block + n;
+            if (!(ok = all_wait(&sum_empty[buffer], (c >> 1 & 1) ^ 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < n && ok; ++j, ++i) {
+                const int stage = i % kFewStages;
+                if (!(ok = all_wait(&full[stage], i / kFewStages & 1))) break;
+                tc_fence_after();
+                const uint32_t w = smem_u32(smem + stage * (kWBytes + kXBytes));
+                const uint64_t wd = sdesc_mn128(w, 64 * 128), xd = sdesc_k128(w + kWBytes);
+                if (one) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_ss(tmem + buffer * kFewTokens, wd + k * 128, xd + 2 * k, idesc, j + k > 0);
+                    mma_commit(&empty[stage]);
+                    if (j == n - 1) mma_commit(&sum_full[buffer]);
+                }
+            }
+        }
+        if (!ok && one) {  // wait until every MMA issued so far has finished
+            mma_commit(&sum_full[0]);
+            const long long t0 = clock64();
+            while (clock64() - t0 < 2000000) {
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- codes: rows 8 w .. 8 w + 7 of each block, 8 pieces of 16 columns each
+        const int w = warp - 4;
+        const uint32_t ring = smem_u32(ring_s) + w * kAhead * 8 * kPitch;
+        FewAt ahead(a, b0);
+        auto fetch = [&](int i) {
+            if (i < n_blocks) {
+                const int k0 = ahead.block * 64 + 8 * w;
+                const uint32_t dst = ring + i % kAhead * 8 * kPitch;
+                const int64_t n0 = (int64_t)ahead.tile * 128;
+                const int cols = (int)min((int64_t)128, a.N - n0);
+                ahead.next(a);
+#pragma unroll
+                for (int u = 0; u < (ALIGNED ? 2 : 3); ++u) {
+                    // rows past K repeat the last: the tokens are 0 there
+                    const int e = lane + 32 * u, row = ALIGNED ? e / 8 : e / 9, c = ALIGNED ? e % 8 : e % 9;
+                    if (row >= 8) break;
+                    const int8_t *p = a.Q + (int64_t)min(k0 + row, a.K - 1) * a.ldq + n0;
+                    const uintptr_t from = (reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15) + 16 * c;
+                    // only pieces that hold some of the row's columns
+                    if (from < reinterpret_cast<uintptr_t>(p) + cols)
+                        copy16(dst + row * kPitch + 16 * c, reinterpret_cast<const void *>(from));
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+        bool ok = true;
+        FewAt at(a, b0);
+#pragma unroll 1
+        for (int i = 0; i < n_blocks; ++i, at.next(a)) {
+            const int stage = i % kFewStages;
+            __syncwarp();  // every lane has read what the next copies replace
+            fetch(i + kAhead - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            if (!(ok = all_wait(&empty[stage], (i / kFewStages & 1) ^ 1))) break;
+            const uint8_t *src = ring_s + (w * kAhead + i % kAhead) * 8 * kPitch;
+            uint8_t *tile = smem + stage * (kWBytes + kXBytes);
+            const int k0 = at.block * 64 + 8 * w;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // eight lanes store to two rows of either parity: all banks
+                const int row = u * 4 + lane / 16 * 2 + lane % 8 / 4, c = lane % 4 + lane / 8 % 2 * 4;
+                uint4 x = *reinterpret_cast<const uint4 *>(src + row * kPitch + 16 * c);
+                uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                if (!ALIGNED) {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(src + row * kPitch + 16 * c + 16);
+                    const uint32_t s = (uint32_t)(reinterpret_cast<uintptr_t>(a.Q) +
+                                                  (uint64_t)min(k0 + row, a.K - 1) * a.ldq + (uint64_t)at.tile * 128) & 15;
+                    uint32_t t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int q = 0; q < 6; ++q) t[q] = s & 8 ? t[q + 2] : t[q];
+#pragma unroll
+                    for (int q = 0; q < 5; ++q) t[q] = s & 4 ? t[q + 1] : t[q];
+                    const uint32_t sel = 0x3210 + (s & 3) * 0x1111;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = __byte_perm(t[q], t[q + 1], sel);
+                }
+                uint32_t h[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // code + 128, as f16 1024 + that, less 1152
+                    const uint32_t z = v[q] ^ 0x80808080u, bias = 0x64806480u;
+                    const uint32_t lo = __byte_perm(z, 0x64646464u, 0x4140), hi = __byte_perm(z, 0x64646464u, 0x4342);
+                    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&lo), *reinterpret_cast<const __half2 *>(&bias));
+                    const __half2 g = __hsub2(*reinterpret_cast<const __half2 *>(&hi), *reinterpret_cast<const __half2 *>(&bias));
+                    h[2 * q] = *reinterpret_cast<const uint32_t *>(&l);
+                    h[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&g);
+                }
+                uint8_t *line = tile + c / 4 * (64 * 128) + (8 * w + row) * 128;
+                *reinterpret_cast<uint4 *>(line + ((c % 4 * 2 ^ row) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(line + ((c % 4 * 2 + 1 ^ row) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+        // ---- sums: a column a thread
+        const uint32_t quad = (uint32_t)(warp * 32) << 16;
+        const int n_of = warp * 32 + lane;
+        int32_t s[kCols];
+        bool ok = true;
+        int c = 0;
+        FewAt at(a, b0);
+        int left = n_blocks;
+#pragma unroll 1
+        while (left > 0 && ok) {
+            // the run's part of a tile
+            const int tile = at.tile, part = min(a.blocks - at.block, left);
+#pragma unroll
+            for (int m = 0; m < kCols; ++m) s[m] = 0;
+#pragma unroll 1
+            for (int done = 0; done < part; ++c) {
+                done += chunk_of(at.block + done, left - done);
+                if (!(ok = all_wait(&sum_full[c & 1], c >> 1 & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int m = 0; m < kCols; m += 16) {
+                    if (m >= a.Mp) break;
+                    uint32_t x[16];
+                    tmem_ld16(tmem + quad + (c & 1) * kFewTokens + m, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) s[m + u] += __float2int_rn(__uint_as_float(x[u]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sum_empty[c & 1]);
+            }
+            at.block = 0, ++at.tile;
+            left -= part;
+            if (!ok) break;
+            const int64_t n = (int64_t)tile * 128 + n_of, tiles = (a.N + 127) / 128, of = blockIdx.y * tiles + tile;
+            const float sw = n < a.N ? __ldg(a.scale + n) : 0.0f;
+            griddep_wait();  // the tokens' scales, and zeros to add to
+            if (part == a.blocks) {
+                if (n < a.N)
+#pragma unroll
+                    for (int m = 0; m < kCols; ++m)
+                        if (m < rows) few_store(a, m0 + m, (int)n, s[m], sw);
+                continue;
+            }
+            unsigned long long *sums = a.sums + of * (a.Mp / 2) * 128 + n_of;
+#pragma unroll
+            for (int m = 0; m < kCols; m += 2)
+                // the lower sum's borrow comes out of the upper one, and goes back when they are read
+                if (m < rows)
+                    atomicAdd(sums + m / 2 * 128, (unsigned long long)((long long)s[m] + ((long long)s[m + 1] << 32)));
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (threadIdx.x == 0)
+                *last_s = atomicAdd(a.counts + of, (unsigned)part) + (unsigned)part == (unsigned)a.blocks;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (!*last_s) continue;
+            __threadfence();
+#pragma unroll
+            for (int m = 0; m < kCols; m += 2)
+                if (m < rows) {
+                    const long long v = (long long)__ldcg(sums + m / 2 * 128);
+                    s[m] = (int32_t)v, s[m + 1] = (int32_t)((v - s[m]) >> 32);
+                }
+            if (n < a.N)
+#pragma unroll
+                for (int m = 0; m < kCols; ++m)
+                    if (m < rows) few_store(a, m0 + m, (int)n, s[m], sw);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kFewTokens);
+    }
+}
+
+template <int kCols, bool ALIGNED>
+cudaError_t launch_few_as(const FewArgs &a, const CUtensorMap &map, cudaStream_t st) {
+    static bool set[64] = {false};  // this kernel's shared memory, on each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(wcols_few_kernel<kCols, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
+    }
+    const int64_t sms = device_sm_count();
+    cudaLaunchConfig_t cfg = {};
+    const int64_t blocks = (a.M + kFewTokens - 1) / kFewTokens;
+    const int64_t runs = (sms + blocks - 1) / blocks;
+    cfg.gridDim = dim3((unsigned)(a.all < runs ? a.all : runs), (unsigned)blocks);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, wcols_few_kernel<kCols, ALIGNED>, a, map);
+}
+
+cudaError_t launch_few(const FewArgs &a, const CUtensorMap &map, cudaStream_t st) {
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.Q) | (uintptr_t)a.ldq) % 16 == 0;
+    if (a.Mp <= 16) return aligned ? launch_few_as<16, true>(a, map, st) : launch_few_as<16, false>(a, map, st);
+    return aligned ? launch_few_as<64, true>(a, map, st) : launch_few_as<64, false>(a, map, st);
+}
+
+// Where the weight is turned into an operand of its own (5 bytes moved for each code) rather than
+// on its way, for each 64 tokens again.
+constexpr int kFewMost = 256;
+
+int few_rows(int64_t M) { return M > kFewTokens ? kFewTokens : (int)round_up(M, 16); }
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace: the tokens' operand and scales; then sums and counts, or the weight's operand,
+// its scales and the GEMM's tile counter.
 struct Layout {
-    int64_t ldk;
-    size_t tokens, weights, token_scale, col_scale, ticket, bytes;
+    int64_t ldk, zeros;  // zeros: 16-byte pieces from `zero` on that the tokens' launch clears
+    size_t token_scale, zero, counts, weights, col_scale, bytes;
 };
 Layout layout(int64_t M, int64_t N, int64_t K) {
-    Layout l;
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Layout l = {};
     l.ldk = operand_ld(K);
-    l.tokens = 0;
-    l.weights = up((size_t)M * l.ldk * 2);
-    l.token_scale = l.weights + up((size_t)N * l.ldk * 2);
-    l.col_scale = l.token_scale + up((size_t)round_up(M, kBM) * 4);
-    l.ticket = l.col_scale + up((size_t)(round_up(N, kBN) + kBN) * 4);
-    l.bytes = l.ticket + 256;
+    l.token_scale = up256((size_t)M * l.ldk * 2);
+    l.zero = l.token_scale + up256((size_t)round_up(M, kBM) * 4);
+    if (M <= kFewMost) {
+        const size_t tiles = (size_t)(N + 127) / 128, blocks = (size_t)(M + kFewTokens - 1) / kFewTokens;
+        l.counts = l.zero + blocks * tiles * few_rows(M) * 128 * 4;
+        l.bytes = l.counts + up256(blocks * tiles * 4);
+        l.zeros = (int64_t)(l.bytes - l.zero) / 16;
+    } else {
+        l.zeros = 1;  // the tile counter
+        l.weights = l.zero + 256;
+        l.col_scale = l.weights + up256((size_t)N * l.ldk * 2);
+        l.bytes = l.col_scale + up256((size_t)(round_up(N, kBN) + kBN) * 4);
+    }
     return l;
 }
 
@@ -69,24 +452,37 @@ cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int
                                 void *Y, int64_t ldy, void *ws, int32_t *dstatus, cudaStream_t st) {
     const Layout l = layout(M, N, K);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    __half *aop = reinterpret_cast<__half *>(w + l.tokens), *bop = reinterpret_cast<__half *>(w + l.weights);
-    float *sa = reinterpret_cast<float *>(w + l.token_scale), *sb = reinterpret_cast<float *>(w + l.col_scale);
-    unsigned int *ticket = reinterpret_cast<unsigned int *>(w + l.ticket);
+    __half *aop = reinterpret_cast<__half *>(w);
+    float *sa = reinterpret_cast<float *>(w + l.token_scale);
     cudaError_t e = with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         wcols_tokens_kernel<T><<<(unsigned)M, kTokenThreads, 0, st>>>(static_cast<const T *>(X), ldx, (int)K,
-                                                                      (int)l.ldk, aop, sa, ticket, dstatus);
+                                                                      (int)l.ldk, aop, sa,
+                                                                      reinterpret_cast<uint4 *>(w + l.zero), l.zeros, dstatus);
         count_launches(1);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
+    if (M <= kFewMost) {
+        FewArgs a{Q, ldq, sa, scale, (int)M, few_rows(M), (int)N, (int)K, (int)((K + 63) / 64), 0, relu, dtype,
+                  Y, ldy, reinterpret_cast<unsigned long long *>(w + l.zero), reinterpret_cast<unsigned int *>(w + l.counts), dstatus};
+        a.all = (N + 127) / 128 * a.blocks;
+        CUtensorMap map;
+        memset(&map, 0, sizeof(map));
+        if (!make_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, aop, (uint64_t)l.ldk, (uint64_t)M, (uint64_t)l.ldk,
+                          64, (uint32_t)a.Mp))
+            return cudaErrorInvalidValue;
+        return launch_few(a, map, st);
+    }
+    __half *bop = reinterpret_cast<__half *>(w + l.weights);
+    float *sb = reinterpret_cast<float *>(w + l.col_scale);
     // the GEMM reads whole tiles of scales
     e = cudaMemcpyAsync(sb, scale, (size_t)N * 4, cudaMemcpyDeviceToDevice, st);
     if (e != cudaSuccess) return e;
     e = launch_i8_cols_to_half(Q, K, N, ldq, bop, l.ldk, st);
     if (e != cudaSuccess) return e;
     return launch_gemm_tc(aop, bop, M, N, K, sa, sb, relu, dtype == BSG_F32 ? 0 : dtype == BSG_F16 ? 2 : 3, Y,
-                          ldy, dstatus, ticket, st);
+                          ldy, dstatus, reinterpret_cast<unsigned int *>(w + l.zero), st);
 }
 
 }  // namespace bsg
