@@ -22,7 +22,7 @@ constexpr int kTokenThreads = 256;
 // Step 1 of one token, a CTA each.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads)
-    wcols_tokens_kernel(const T *__restrict__ X, int64_t ldx, int K, int ldk, __half *__restrict__ op,
+    wcols_tokens_kernel(const T *__restrict__ X, int64_t ldx, int64_t M, int K, int ldk, __half *__restrict__ op,
                         float *__restrict__ scale, uint4 *__restrict__ zero, int64_t zeros,
                         int32_t *dstatus) {
     __shared__ uint32_t red[kTokenThreads / 32];
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kTokenThreads)
     // what the next launch adds into
     for (int64_t i = row * kTokenThreads + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * kTokenThreads)
         zero[i] = make_uint4(0, 0, 0, 0);
+    if (row >= M) return;
     const T *x = X + row * ldx;
     uint32_t m = 0;  // the largest |x|, as bits: Inf and NaN are the largest of all
     for (int k = threadIdx.x; k < K; k += kTokenThreads)
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kTokenThreads)
 //
 // kFewTokens tokens at a time (more: each block of them on its own, the codes then from L2).  D[column][token] += W^T X^T with the weight as the A operand, 128
 // columns as its rows: W lies k by k, columns side by side, which is A's "MN-major" form, so
-// codes become f16 where they are, without a transposition.  All k-blocks (64 x 128 codes) of
+// codes become f16 where they are, without a transposition.  All k-blocks (128 x 128 codes) of
 // all column tiles form one list that the CTAs share in equal runs; a run ends a tile's sums
 // where it ends, and what is not a whole tile is added up in L2, in integers, so that the order
 // does not matter; the last to add writes Y.  Sums are exact: f32 sums of at most 1024
@@ -65,17 +66,19 @@ __global__ void __launch_bounds__(kTokenThreads)
 // the MMAs; warp 13 sends for the tokens (TMA).
 constexpr int kFewTokens = 64;
 constexpr int kFewThreads = 14 * 32;
-constexpr int kFewStages = 4, kAhead = 8;
-constexpr int kWBytes = 128 * 64 * 2, kXBytes = kFewTokens * 64 * 2;  // of a stage
-constexpr int kPitch = 144;                                            // of a row of codes in the ring: 128 and its overhang
-constexpr int kRingBytes = 8 * kAhead * 8 * kPitch;                    // 8 warps, 8 rows of a block each
+constexpr int kFewStages = 3, kAhead = 4;
+constexpr int kDeep = 128;                                                   // k of a block
+constexpr int kWBytes = 128 * kDeep * 2, kXBytes = kFewTokens * kDeep * 2;  // of a stage
+constexpr int kPitch = 144;                             // of a row of codes in the ring: 128 and its overhang
+constexpr int kRows = kDeep / 8;                        // of a block, to a warp
+constexpr int kRingBytes = 8 * kAhead * kRows * kPitch;
 constexpr int kFewSmem = kFewStages * (kWBytes + kXBytes) + kRingBytes + 256 + 1024;
 
 struct FewArgs {
     const int8_t *Q;
     int64_t ldq;
     const float *token_scale, *scale;
-    int M, Mp, N, K, blocks;  // Mp: tokens rounded up to 16; blocks of 64 of K
+    int M, Mp, N, K, blocks;  // Mp: tokens rounded up to 16; blocks of kDeep of K
     int64_t all;              // blocks of all column tiles
     int relu, dtype;
     void *Y;
@@ -150,7 +153,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
-    auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+    auto all_wait = [&](uint64_t *bar, uint32_t parity, bool long_one = false) {
+        if (long_one)  // (polls would take issue slots from the warps that work)
+#pragma unroll 1
+            for (int n = 0; n < 100000 && !mbar_try_wait(bar, parity); ++n) __nanosleep(100);
         const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         if (!ok && lane == 0) {
             *abort_flag = 1;
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     };
     // Blocks that one accumulator takes from block b on: to the end of the tile, of the run, or
     // of 1024 products.
-    auto chunk_of = [&](int block, int left) { return min(min(a.blocks - block, kChunkK / 64), left); };
+    auto chunk_of = [&](int block, int left) { return min(min(a.blocks - block, kChunkK / kDeep), left); };
 
     if (warp == 13) {
         // ---- tokens
@@ -174,9 +180,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     *abort_flag = 1;
                     break;
                 }
-                mbar_arrive_expect_tx(&full[stage], a.Mp * 128);
-                tma_load_2d(&tokens, &full[stage], smem + stage * (kWBytes + kXBytes) + kWBytes,
-                            at.block * 64, m0);
+                mbar_arrive_expect_tx(&full[stage], a.Mp * kDeep * 2);
+                uint8_t *x = smem + stage * (kWBytes + kXBytes) + kWBytes;
+#pragma unroll
+                for (int u = 0; u < kDeep / 64; ++u)  // (past the operand's end: zeros)
+                    tma_load_2d(&tokens, &full[stage], x + u * (kFewTokens * 128), at.block * kDeep + 64 * u, m0);
             }
             if (*abort_flag) {  // let the copies land
                 const long long t0 = clock64();
@@ -202,11 +210,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (!(ok = all_wait(&full[stage], i / kFewStages & 1))) break;
                 tc_fence_after();
                 const uint32_t w = smem_u32(smem + stage * (kWBytes + kXBytes));
-                const uint64_t wd = sdesc_mn128(w, 64 * 128), xd = sdesc_k128(w + kWBytes);
+                const uint64_t wd = sdesc_mn128(w, kDeep * 128), xd = sdesc_k128(w + kWBytes);
                 if (one) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ss(tmem + buffer * kFewTokens, wd + k * 128, xd + 2 * k, idesc, j + k > 0);
+                    for (int k = 0; k < kDeep / 16; ++k)
+                        mma_f16_ss(tmem + buffer * kFewTokens, wd + k * 128, xd + k / 4 * (kFewTokens * 8) + k % 4 * 2, idesc, j + k > 0);
                     mma_commit(&empty[stage]);
                     if (j == n - 1) mma_commit(&sum_full[buffer]);
                 }
@@ -220,61 +228,66 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // ---- codes: rows 8 w .. 8 w + 7 of each block, 8 pieces of 16 columns each
+        // ---- codes: rows kRows w .. of each block, 8 pieces of 16 columns each, and one more
+        // where the row begins inside its first.  Rows kDeep apart begin alike.
         const int w = warp - 4;
-        const uint32_t ring = smem_u32(ring_s) + w * kAhead * 8 * kPitch;
+        const uint32_t ring = smem_u32(ring_s) + w * kAhead * kRows * kPitch;
         FewAt ahead(a, b0);
+        int in_ahead = 0;
         auto fetch = [&](int i) {
             if (i < n_blocks) {
-                const int k0 = ahead.block * 64 + 8 * w;
-                const uint32_t dst = ring + i % kAhead * 8 * kPitch;
+                const int k0 = ahead.block * kDeep + kRows * w;
+                const uint32_t dst = ring + in_ahead * (kRows * kPitch);
                 const int64_t n0 = (int64_t)ahead.tile * 128;
                 const int cols = (int)min((int64_t)128, a.N - n0);
+                const int8_t *first = a.Q + n0 + k0 * a.ldq, *last = a.Q + n0 + (int64_t)(a.K - 1) * a.ldq;
                 ahead.next(a);
-#pragma unroll
-                for (int u = 0; u < (ALIGNED ? 2 : 3); ++u) {
+                auto piece = [&](int row, int c) {
                     // rows past K repeat the last: the tokens are 0 there
-                    const int e = lane + 32 * u, row = ALIGNED ? e / 8 : e / 9, c = ALIGNED ? e % 8 : e % 9;
-                    if (row >= 8) break;
-                    const int8_t *p = a.Q + (int64_t)min(k0 + row, a.K - 1) * a.ldq + n0;
+                    const int8_t *p = k0 + row < a.K ? first + row * a.ldq : last;
                     const uintptr_t from = (reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15) + 16 * c;
                     // only pieces that hold some of the row's columns
                     if (from < reinterpret_cast<uintptr_t>(p) + cols)
                         copy16(dst + row * kPitch + 16 * c, reinterpret_cast<const void *>(from));
-                }
+                };
+#pragma unroll
+                for (int u = 0; u < kRows / 4; ++u) piece(4 * u + lane / 8, lane % 8);
+                if (!ALIGNED && lane < kRows) piece(lane, 8);
             }
+            in_ahead = in_ahead + 1 == kAhead ? 0 : in_ahead + 1;
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // The lane's pieces: eight lanes store to two rows of either parity, which spreads them
+        // over all banks.
+        const int row0 = lane / 16 * 2 + lane % 8 / 4, c = lane % 4 + lane / 8 % 2 * 4;
+        uint32_t shift[kRows / 4];  // where the row begins in its first 16 bytes
+#pragma unroll
+        for (int u = 0; u < kRows / 4; ++u)
+            shift[u] = ALIGNED ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(a.Q) + (uint64_t)(kRows * w + row0 + 4 * u) * a.ldq) & 15;
 #pragma unroll 1
         for (int i = 0; i < kAhead - 1; ++i) fetch(i);
-        bool ok = true;
-        FewAt at(a, b0);
+        int stage = 0, in_ring = 0;
+        uint32_t phase = 1;
 #pragma unroll 1
-        for (int i = 0; i < n_blocks; ++i, at.next(a)) {
-            const int stage = i % kFewStages;
+        for (int i = 0; i < n_blocks; ++i) {
             __syncwarp();  // every lane has read what the next copies replace
             fetch(i + kAhead - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-            if (!(ok = all_wait(&empty[stage], (i / kFewStages & 1) ^ 1))) break;
-            const uint8_t *src = ring_s + (w * kAhead + i % kAhead) * 8 * kPitch;
-            uint8_t *tile = smem + stage * (kWBytes + kXBytes);
-            const int k0 = at.block * 64 + 8 * w;
+            if (!all_wait(&empty[stage], phase)) break;
+            const uint8_t *src = ring_s + (w * kAhead + in_ring) * (kRows * kPitch) + row0 * kPitch + 16 * c;
+            uint8_t *line = smem + stage * (kWBytes + kXBytes) + c / 4 * (kDeep * 128) + (kRows * w + row0) * 128;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                // eight lanes store to two rows of either parity: all banks
-                const int row = u * 4 + lane / 16 * 2 + lane % 8 / 4, c = lane % 4 + lane / 8 % 2 * 4;
-                uint4 x = *reinterpret_cast<const uint4 *>(src + row * kPitch + 16 * c);
+            for (int u = 0; u < kRows / 4; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch);
                 uint32_t v[4] = {x.x, x.y, x.z, x.w};
                 if (!ALIGNED) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(src + row * kPitch + 16 * c + 16);
-                    const uint32_t s = (uint32_t)(reinterpret_cast<uintptr_t>(a.Q) +
-                                                  (uint64_t)min(k0 + row, a.K - 1) * a.ldq + (uint64_t)at.tile * 128) & 15;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch + 16);
                     uint32_t t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int q = 0; q < 6; ++q) t[q] = s & 8 ? t[q + 2] : t[q];
+                    for (int q = 0; q < 6; ++q) t[q] = shift[u] & 8 ? t[q + 2] : t[q];
 #pragma unroll
-                    for (int q = 0; q < 5; ++q) t[q] = s & 4 ? t[q + 1] : t[q];
-                    const uint32_t sel = 0x3210 + (s & 3) * 0x1111;
+                    for (int q = 0; q < 5; ++q) t[q] = shift[u] & 4 ? t[q + 1] : t[q];
+                    const uint32_t sel = 0x3210 + (shift[u] & 3) * 0x1111;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = __byte_perm(t[q], t[q + 1], sel);
                 }
@@ -288,13 +301,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     h[2 * q] = *reinterpret_cast<const uint32_t *>(&l);
                     h[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&g);
                 }
-                uint8_t *line = tile + c / 4 * (64 * 128) + (8 * w + row) * 128;
-                *reinterpret_cast<uint4 *>(line + ((c % 4 * 2 ^ row) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(line + ((c % 4 * 2 + 1 ^ row) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                const int at = c % 4 * 2, row = row0 + 4 * u;
+                *reinterpret_cast<uint4 *>(line + 4 * u * 128 + ((at ^ row % 8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(line + 4 * u * 128 + ((at + 1 ^ row % 8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage]);
+            if (++stage == kFewStages) stage = 0, phase ^= 1;
+            in_ring = in_ring + 1 == kAhead ? 0 : in_ring + 1;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
             for (int done = 0; done < part; ++c) {
                 done += chunk_of(at.block + done, left - done);
-                if (!(ok = all_wait(&sum_full[c & 1], c >> 1 & 1))) break;
+                if (!(ok = all_wait(&sum_full[c & 1], c >> 1 & 1, true))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int m = 0; m < kCols; m += 16) {
@@ -456,7 +471,9 @@ cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int
     float *sa = reinterpret_cast<float *>(w + l.token_scale);
     cudaError_t e = with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        wcols_tokens_kernel<T><<<(unsigned)M, kTokenThreads, 0, st>>>(static_cast<const T *>(X), ldx, (int)K,
+        // a CTA to a token, and some more where there is much to clear
+        const int64_t clear = l.zeros / (4 * kTokenThreads), ctas = M > clear ? M : clear < 1024 ? clear : 1024;
+        wcols_tokens_kernel<T><<<(unsigned)ctas, kTokenThreads, 0, st>>>(static_cast<const T *>(X), ldx, M, (int)K,
                                                                       (int)l.ldk, aop, sa,
                                                                       reinterpret_cast<uint4 *>(w + l.zero), l.zeros, dstatus);
         count_launches(1);
@@ -464,7 +481,7 @@ cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int
     });
     if (e != cudaSuccess) return e;
     if (M <= kFewMost) {
-        FewArgs a{Q, ldq, sa, scale, (int)M, few_rows(M), (int)N, (int)K, (int)((K + 63) / 64), 0, relu, dtype,
+        FewArgs a{Q, ldq, sa, scale, (int)M, few_rows(M), (int)N, (int)K, (int)((K + kDeep - 1) / kDeep), 0, relu, dtype,
                   Y, ldy, reinterpret_cast<unsigned long long *>(w + l.zero), reinterpret_cast<unsigned int *>(w + l.counts), dstatus};
         a.all = (N + 127) / 128 * a.blocks;
         CUtensorMap map;
