@@ -17,38 +17,113 @@
 namespace bsg {
 namespace {
 
-constexpr int kTokenThreads = 256;
-
-// Step 1 of one token, a CTA each.
-template <typename T>
-__global__ void __launch_bounds__(kTokenThreads)
+// Step 1 of a token, a CTA each: its values in registers between the maximum and the codes
+// (up to 32 a thread; longer rows are read again).  VEC: values of 16 bytes, where every row
+// begins on 16; 1 otherwise.
+constexpr int kTokenKept = 32;
+template <typename T, int VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     wcols_tokens_kernel(const T *__restrict__ X, int64_t ldx, int64_t M, int K, int ldk, __half *__restrict__ op,
                         float *__restrict__ scale, uint4 *__restrict__ zero, int64_t zeros,
                         int32_t *dstatus) {
-    __shared__ uint32_t red[kTokenThreads / 32];
+    __shared__ uint32_t red[THREADS / 32];
     const int64_t row = blockIdx.x;
     griddep_launch_dependents();
     // what the next launch adds into
-    for (int64_t i = row * kTokenThreads + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * kTokenThreads)
+    for (int64_t i = row * THREADS + threadIdx.x; i < zeros; i += (int64_t)gridDim.x * THREADS)
         zero[i] = make_uint4(0, 0, 0, 0);
     if (row >= M) return;
     const T *x = X + row * ldx;
+    constexpr int kPer = kTokenKept / VEC, kStep = THREADS * VEC;
+    struct alignas(VEC * sizeof(T)) Piece {
+        T v[VEC];
+    };
+    Piece piece[kPer];
     uint32_t m = 0;  // the largest |x|, as bits: Inf and NaN are the largest of all
-    for (int k = threadIdx.x; k < K; k += kTokenThreads)
-        m = max(m, __float_as_uint(to_f32(x[k])) & 0x7fffffffu);
+    auto read = [&](int k, Piece &p) {
+        if (VEC > 1 && k + VEC <= K) {
+            p = *reinterpret_cast<const Piece *>(x + k);
+        } else {
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) p.v[u] = k + u < K ? x[k + u] : from_f32<T>(0.0f);
+        }
+    };
+    auto largest = [&](const Piece &p) {
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) m = max(m, __float_as_uint(to_f32(p.v[u])) & 0x7fffffffu);
+    };
+    const int k0 = threadIdx.x * VEC;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i * kStep < K) read(k0 + i * kStep, piece[i]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i * kStep < K) largest(piece[i]);
+    for (int k = k0 + kPer * kStep; k < K; k += kStep) {
+        Piece p;
+        read(k, p);
+        largest(p);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kTokenThreads / 32; ++i) m = max(m, red[i]);
+    for (int i = 0; i < THREADS / 32; ++i) m = max(m, red[i]);
     // the unit's quotients, whose f32 divisions equal the f64 ones rounded
     const float s = fmaxf(__fdiv_rn(__uint_as_float(m), 127.0f), 1e-8f), inv = __fdiv_rn(1.0f, s);
-    for (int k = threadIdx.x; k < ldk; k += kTokenThreads)
-        op[row * ldk + k] = __int2half_rn(k < K ? (int)(int8_t)unit_code(to_f32(x[k]), inv) : 0);
+    auto write = [&](int k, const Piece &p) {
+        __half h[VEC];
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) {  // the unit's code: floors below 2^23 are exact in f32
+            const float c = floorf(__fadd_rn(__fmul_rn(to_f32(p.v[u]), inv), 0.5f));
+            h[u] = __float2half_rn(c);
+        }
+        if (k < ldk) {  // (a whole number of pieces)
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint4 *>(op + row * ldk + k) = *reinterpret_cast<const uint4 *>(h);
+            else if constexpr (VEC == 4)
+                *reinterpret_cast<uint2 *>(op + row * ldk + k) = *reinterpret_cast<const uint2 *>(h);
+            else
+                op[row * ldk + k] = h[0];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i * kStep < ldk) {
+            if (i * kStep >= K) read(K, piece[i]);  // zeros past the end
+            write(k0 + i * kStep, piece[i]);
+        }
+    for (int k = k0 + kPer * kStep; k < ldk; k += kStep) {
+        Piece p;
+        read(k, p);
+        write(k, p);
+    }
     if (threadIdx.x == 0) {
         scale[row] = s;
         if (m >= 0x7f800000u) set_status(dstatus, BSG_DSTATUS_NONFINITE);
     }
+}
+
+template <typename T, int VEC, int THREADS>
+cudaError_t launch_tokens_as(const T *X, int64_t ldx, int64_t M, int K, int ldk, __half *op, float *scale, uint4 *zero,
+                             int64_t zeros, int32_t *dstatus, cudaStream_t st) {
+    // a CTA to a token, and some more where there is much to clear
+    const int64_t clear = zeros / (4 * THREADS), ctas = M > clear ? M : clear < 1024 ? clear : M > 1024 ? M : 1024;
+    wcols_tokens_kernel<T, VEC, THREADS><<<(unsigned)ctas, THREADS, 0, st>>>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __half *op, float *scale, uint4 *zero,
+                          int64_t zeros, int32_t *dstatus, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    const bool aligned = (reinterpret_cast<uintptr_t>(X) | (uintptr_t)(ldx * (int64_t)sizeof(T))) % 16 == 0;
+    if (K <= 1024)
+        return aligned ? launch_tokens_as<T, VEC, 128>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus, st)
+                       : launch_tokens_as<T, 1, 128>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus, st);
+    return aligned ? launch_tokens_as<T, VEC, 512>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus, st)
+                   : launch_tokens_as<T, 1, 512>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus, st);
 }
 
 // ---- a few tokens: the weight's codes turned into operands on their way ---------
@@ -61,17 +136,18 @@ __global__ void __launch_bounds__(kTokenThreads)
 // does not matter; the last to add writes Y.  Sums are exact: f32 sums of at most 1024
 // products, then int32.
 //
-// Roles: warps 0-3 take sums out of tensor memory; warps 4-11 fetch codes (cp.async into a
-// ring of each warp's own, kAhead blocks ahead) and turn them into operands; warp 12 issues
-// the MMAs; warp 13 sends for the tokens (TMA).
+// Roles: warps 0-7 take sums out of tensor memory, half of the tokens each four; warps 8-23
+// fetch codes (cp.async into a ring of each warp's own, kAhead blocks ahead) and turn them
+// into operands; warp 24 issues the MMAs; warp 25 sends for the tokens (TMA).
 constexpr int kFewTokens = 64;
-constexpr int kFewThreads = 14 * 32;
+constexpr int kSumWarps = 8, kCodeWarps = 16;
+constexpr int kFewThreads = (kSumWarps + kCodeWarps + 2) * 32;
 constexpr int kFewStages = 3, kAhead = 4;
 constexpr int kDeep = 128;                                                   // k of a block
 constexpr int kWBytes = 128 * kDeep * 2, kXBytes = kFewTokens * kDeep * 2;  // of a stage
 constexpr int kPitch = 144;                             // of a row of codes in the ring: 128 and its overhang
-constexpr int kRows = kDeep / 8;                        // of a block, to a warp
-constexpr int kRingBytes = 8 * kAhead * kRows * kPitch;
+constexpr int kRows = kDeep / kCodeWarps;                        // of a block, to a warp
+constexpr int kRingBytes = kCodeWarps * kAhead * kRows * kPitch;
 constexpr int kFewSmem = kFewStages * (kWBytes + kXBytes) + kRingBytes + 256 + 1024;
 
 struct FewArgs {
@@ -134,18 +210,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kFewStages; ++s) {
-            mbar_init(&full[s], 8 + 1);
+            mbar_init(&full[s], kCodeWarps + 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sum_full[s], 1);
-            mbar_init(&sum_empty[s], 4);
+            mbar_init(&sum_empty[s], kSumWarps);
         }
         *abort_flag = 0;
         fence_mbar_init();
         fence_async_shared();
     }
-    if (warp == 12) {
+    constexpr int kMmaWarp = kSumWarps + kCodeWarps;
+    if (warp == kMmaWarp) {
         tmem_alloc(tmem_ptr, 2 * kFewTokens);
         tmem_relinquish();
     }
@@ -168,7 +245,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // of 1024 products.
     auto chunk_of = [&](int block, int left) { return min(min(a.blocks - block, kChunkK / kDeep), left); };
 
-    if (warp == 13) {
+    if (warp > kMmaWarp) {
         // ---- tokens
         if (lane == 0) {
             prefetch_tmap(&tokens);
@@ -192,7 +269,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == kMmaWarp) {
         // ---- MMAs
         const uint32_t idesc = idesc_f16_f32(128, a.Mp) | kIdescAMn;
         const bool one = elect_one();
@@ -227,10 +304,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp >= kSumWarps) {
         // ---- codes: rows kRows w .. of each block, 8 pieces of 16 columns each, and one more
         // where the row begins inside its first.  Rows kDeep apart begin alike.
-        const int w = warp - 4;
+        const int w = warp - kSumWarps;
         const uint32_t ring = smem_u32(ring_s) + w * kAhead * kRows * kPitch;
         FewAt ahead(a, b0);
         int in_ahead = 0;
@@ -313,10 +390,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
-        // ---- sums: a column a thread
-        const uint32_t quad = (uint32_t)(warp * 32) << 16;
-        const int n_of = warp * 32 + lane;
-        int32_t s[kCols];
+        // ---- sums: a column and half of the tokens (from t0 on) to a thread
+        constexpr int kMine = kCols / 2;
+        const int t0 = warp / 4 * kMine, quad = warp % 4, n_of = quad * 32 + lane;
+        const uint32_t sums_at = tmem + ((uint32_t)(quad * 32) << 16) + t0;
+        int32_t s[kMine];
         bool ok = true;
         int c = 0;
         FewAt at(a, b0);
@@ -326,20 +404,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             // the run's part of a tile
             const int tile = at.tile, part = min(a.blocks - at.block, left);
 #pragma unroll
-            for (int m = 0; m < kCols; ++m) s[m] = 0;
+            for (int m = 0; m < kMine; ++m) s[m] = 0;
 #pragma unroll 1
             for (int done = 0; done < part; ++c) {
                 done += chunk_of(at.block + done, left - done);
                 if (!(ok = all_wait(&sum_full[c & 1], c >> 1 & 1, true))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int m = 0; m < kCols; m += 16) {
-                    if (m >= a.Mp) break;
-                    uint32_t x[16];
-                    tmem_ld16(tmem + quad + (c & 1) * kFewTokens + m, x);
+                for (int m = 0; m < kMine; m += 8) {
+                    if (t0 + m >= a.Mp) break;
+                    uint32_t x[8];
+                    tmem_ld8(sums_at + (c & 1) * kFewTokens + m, x);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) s[m + u] += __float2int_rn(__uint_as_float(x[u]));
+                    for (int u = 0; u < 8; ++u) s[m + u] += __float2int_rn(__uint_as_float(x[u]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -354,38 +432,38 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (part == a.blocks) {
                 if (n < a.N)
 #pragma unroll
-                    for (int m = 0; m < kCols; ++m)
-                        if (m < rows) few_store(a, m0 + m, (int)n, s[m], sw);
+                    for (int m = 0; m < kMine; ++m)
+                        if (t0 + m < rows) few_store(a, m0 + t0 + m, (int)n, s[m], sw);
                 continue;
             }
-            unsigned long long *sums = a.sums + of * (a.Mp / 2) * 128 + n_of;
+            unsigned long long *sums = a.sums + (of * (a.Mp / 2) + t0 / 2) * 128 + n_of;
 #pragma unroll
-            for (int m = 0; m < kCols; m += 2)
+            for (int m = 0; m < kMine; m += 2)
                 // the lower sum's borrow comes out of the upper one, and goes back when they are read
-                if (m < rows)
+                if (t0 + m < rows)
                     atomicAdd(sums + m / 2 * 128, (unsigned long long)((long long)s[m] + ((long long)s[m + 1] << 32)));
             __threadfence();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
             if (threadIdx.x == 0)
                 *last_s = atomicAdd(a.counts + of, (unsigned)part) + (unsigned)part == (unsigned)a.blocks;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
             if (!*last_s) continue;
             __threadfence();
 #pragma unroll
-            for (int m = 0; m < kCols; m += 2)
-                if (m < rows) {
+            for (int m = 0; m < kMine; m += 2)
+                if (t0 + m < rows) {
                     const long long v = (long long)__ldcg(sums + m / 2 * 128);
                     s[m] = (int32_t)v, s[m + 1] = (int32_t)((v - s[m]) >> 32);
                 }
             if (n < a.N)
 #pragma unroll
-                for (int m = 0; m < kCols; ++m)
-                    if (m < rows) few_store(a, m0 + m, (int)n, s[m], sw);
+                for (int m = 0; m < kMine; ++m)
+                    if (t0 + m < rows) few_store(a, m0 + t0 + m, (int)n, s[m], sw);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 2 * kFewTokens);
     }
@@ -471,13 +549,8 @@ cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int
     float *sa = reinterpret_cast<float *>(w + l.token_scale);
     cudaError_t e = with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        // a CTA to a token, and some more where there is much to clear
-        const int64_t clear = l.zeros / (4 * kTokenThreads), ctas = M > clear ? M : clear < 1024 ? clear : 1024;
-        wcols_tokens_kernel<T><<<(unsigned)ctas, kTokenThreads, 0, st>>>(static_cast<const T *>(X), ldx, M, (int)K,
-                                                                      (int)l.ldk, aop, sa,
-                                                                      reinterpret_cast<uint4 *>(w + l.zero), l.zeros, dstatus);
-        count_launches(1);
-        return cudaGetLastError();
+        return launch_tokens(static_cast<const T *>(X), ldx, M, (int)K, (int)l.ldk, aop, sa,
+                             reinterpret_cast<uint4 *>(w + l.zero), l.zeros, dstatus, st);
     });
     if (e != cudaSuccess) return e;
     if (M <= kFewMost) {
