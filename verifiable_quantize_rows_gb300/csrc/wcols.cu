@@ -136,19 +136,27 @@ cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __
 // does not matter; the last to add writes Y.  Sums are exact: f32 sums of at most 1024
 // products, then int32.
 //
-// Roles: warps 0-7 take sums out of tensor memory, half of the tokens each four; warps 8-23
-// fetch codes (cp.async into a ring of each warp's own, kAhead blocks ahead) and turn them
-// into operands; warp 24 issues the MMAs; warp 25 sends for the tokens (TMA).
+// Roles: warps 0-7 take sums out of tensor memory, half of the tokens each four; warps 8-23,
+// in two teams that take blocks in turn (a block's chain of waits, reads and writes is some
+// 1300 clocks, twice what its MMAs take), fetch codes (cp.async into a ring of each warp's own,
+// two of its blocks ahead) and turn them into operands; warp 24 issues the MMAs; warp 25
+// sends for the tokens (TMA).  Blocks are this deep because every wait of the MMAs' warp costs
+// some 100 clocks, its barrier complete or not.
 constexpr int kFewTokens = 64;
 constexpr int kSumWarps = 8, kCodeWarps = 16;
 constexpr int kFewThreads = (kSumWarps + kCodeWarps + 2) * 32;
-constexpr int kFewStages = 3, kAhead = 4;
-constexpr int kDeep = 128;                                                   // k of a block
-constexpr int kWBytes = 128 * kDeep * 2, kXBytes = kFewTokens * kDeep * 2;  // of a stage
-constexpr int kPitch = 144;                             // of a row of codes in the ring: 128 and its overhang
-constexpr int kRows = kDeep / kCodeWarps;                        // of a block, to a warp
+constexpr int kDeep = 128;     // k of a block
+constexpr int kTeam = 8, kTeams = kCodeWarps / kTeam, kRows = kDeep / kTeam;  // rows of a block, to a warp
+constexpr int kAhead = 2;      // blocks of a warp's ring
+constexpr int kPitch = 144;    // of a row of codes in the ring: 128 and its overhang
 constexpr int kRingBytes = kCodeWarps * kAhead * kRows * kPitch;
-constexpr int kFewSmem = kFewStages * (kWBytes + kXBytes) + kRingBytes + 256 + 1024;
+template <int kCols>
+struct FewCfg {
+    static constexpr int kWBytes = 128 * kDeep * 2, kXBytes = kCols * kDeep * 2, kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = kCols == 16 ? 4 : 3;
+    static constexpr int kBytes = kStages * kStageBytes + kRingBytes + 256 + 1024;
+    static_assert(kXBytes % 1024 == 0 && kBytes <= 232448, "shared memory");
+};
 
 struct FewArgs {
     const int8_t *Q;
@@ -194,11 +202,13 @@ struct FewAt {
 template <int kCols, bool ALIGNED>
 __global__ void __launch_bounds__(kFewThreads, 1)
     wcols_few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ CUtensorMap tokens) {
+    using C = FewCfg<kCols>;
+    constexpr int kStages = C::kStages, kWBytes = C::kWBytes, kStageBytes = C::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    uint8_t *ring_s = smem + kFewStages * (kWBytes + kXBytes);
+    uint8_t *ring_s = smem + kStages * kStageBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring_s + kRingBytes);
-    uint64_t *full = bars, *empty = bars + kFewStages, *sum_full = bars + 2 * kFewStages, *sum_empty = sum_full + 2;
+    uint64_t *full = bars, *empty = bars + kStages, *sum_full = bars + 2 * kStages, *sum_empty = sum_full + 2;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(sum_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
     volatile int *last_s = reinterpret_cast<volatile int *>(tmem_ptr + 2);
@@ -209,8 +219,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int m0 = blockIdx.y * kFewTokens, rows = min(a.M - m0, kFewTokens);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kFewStages; ++s) {
-            mbar_init(&full[s], kCodeWarps + 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], kTeam + 1);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -230,10 +240,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_ptr;
-    auto all_wait = [&](uint64_t *bar, uint32_t parity, bool long_one = false) {
-        if (long_one)  // (polls would take issue slots from the warps that work)
-#pragma unroll 1
-            for (int n = 0; n < 100000 && !mbar_try_wait(bar, parity); ++n) __nanosleep(100);
+    auto all_wait = [&](uint64_t *bar, uint32_t parity) {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         if (!ok && lane == 0) {
             *abort_flag = 1;
@@ -252,16 +259,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             griddep_wait();
             FewAt at(a, b0);
             for (int i = 0; i < n_blocks; ++i, at.next(a)) {
-                const int stage = i % kFewStages;
-                if (!mbar_wait(&empty[stage], (i / kFewStages & 1) ^ 1, abort_flag)) {
+                const int stage = i % kStages;
+                if (!mbar_wait(&empty[stage], (i / kStages & 1) ^ 1, abort_flag)) {
                     *abort_flag = 1;
                     break;
                 }
                 mbar_arrive_expect_tx(&full[stage], a.Mp * kDeep * 2);
-                uint8_t *x = smem + stage * (kWBytes + kXBytes) + kWBytes;
+                uint8_t *x = smem + stage * kStageBytes + kWBytes;
 #pragma unroll
                 for (int u = 0; u < kDeep / 64; ++u)  // (past the operand's end: zeros)
-                    tma_load_2d(&tokens, &full[stage], x + u * (kFewTokens * 128), at.block * kDeep + 64 * u, m0);
+                    tma_load_2d(&tokens, &full[stage], x + u * (kCols * 128), at.block * kDeep + 64 * u, m0);
             }
             if (*abort_flag) {  // let the copies land
                 const long long t0 = clock64();
@@ -272,9 +279,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     } else if (warp == kMmaWarp) {
         // ---- MMAs
         const uint32_t idesc = idesc_f16_f32(128, a.Mp) | kIdescAMn;
+        const uint64_t w_desc = sdesc_mn128(smem_u32(smem), kDeep * 128), x_desc = sdesc_k128(smem_u32(smem) + kWBytes);
         const bool one = elect_one();
         bool ok = true;
-        int block = FewAt(a, b0).block;
+        int block = FewAt(a, b0).block, stage = 0;
+        uint32_t phase = 0;
 #pragma unroll 1
         for (int i = 0, c = 0; i < n_blocks && ok; ++c) {
             const int n = chunk_of(block, n_blocks - i), buffer = c & 1;
@@ -283,18 +292,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < n && ok; ++j, ++i) {
-                const int stage = i % kFewStages;
-                if (!(ok = all_wait(&full[stage], i / kFewStages & 1))) break;
+                if (!(ok = all_wait(&full[stage], phase))) break;
                 tc_fence_after();
-                const uint32_t w = smem_u32(smem + stage * (kWBytes + kXBytes));
-                const uint64_t wd = sdesc_mn128(w, kDeep * 128), xd = sdesc_k128(w + kWBytes);
+                const uint64_t wd = w_desc + stage * (kStageBytes / 16), xd = x_desc + stage * (kStageBytes / 16);
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < kDeep / 16; ++k)
-                        mma_f16_ss(tmem + buffer * kFewTokens, wd + k * 128, xd + k / 4 * (kFewTokens * 8) + k % 4 * 2, idesc, j + k > 0);
+                        mma_f16_ss(tmem + buffer * kFewTokens, wd + k * 128, xd + k / 4 * (kCols * 8) + k % 4 * 2, idesc, j + k > 0);
                     mma_commit(&empty[stage]);
                     if (j == n - 1) mma_commit(&sum_full[buffer]);
                 }
+                if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
         if (!ok && one) {  // wait until every MMA issued so far has finished
@@ -305,11 +313,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kSumWarps) {
-        // ---- codes: rows kRows w .. of each block, 8 pieces of 16 columns each, and one more
-        // where the row begins inside its first.  Rows kDeep apart begin alike.
-        const int w = warp - kSumWarps;
-        const uint32_t ring = smem_u32(ring_s) + w * kAhead * kRows * kPitch;
+        // ---- codes: rows kRows w .. of every other block, 8 pieces of 16 columns each, and one
+        // more where the row begins inside its first.  Rows kDeep apart begin alike.
+        const int w = (warp - kSumWarps) % kTeam, team = (warp - kSumWarps) / kTeam;
+        uint8_t *const own = ring_s + (warp - kSumWarps) * kAhead * kRows * kPitch;
+        const uint32_t ring = smem_u32(own);
         FewAt ahead(a, b0);
+        for (int i = 0; i < team; ++i) ahead.next(a);
         int in_ahead = 0;
         auto fetch = [&](int i) {
             if (i < n_blocks) {
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const int64_t n0 = (int64_t)ahead.tile * 128;
                 const int cols = (int)min((int64_t)128, a.N - n0);
                 const int8_t *first = a.Q + n0 + k0 * a.ldq, *last = a.Q + n0 + (int64_t)(a.K - 1) * a.ldq;
-                ahead.next(a);
+                for (int u = 0; u < kTeams; ++u) ahead.next(a);
                 auto piece = [&](int row, int c) {
                     // rows past K repeat the last: the tokens are 0 there
                     const int8_t *p = k0 + row < a.K ? first + row * a.ldq : last;
@@ -342,24 +352,29 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int u = 0; u < kRows / 4; ++u)
             shift[u] = ALIGNED ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(a.Q) + (uint64_t)(kRows * w + row0 + 4 * u) * a.ldq) & 15;
 #pragma unroll 1
-        for (int i = 0; i < kAhead - 1; ++i) fetch(i);
-        int stage = 0, in_ring = 0;
-        uint32_t phase = 1;
+        for (int i = 0; i < kAhead; ++i) fetch(team + i * kTeams);
+        int stage = team % kStages, in_ring = 0;
+        uint32_t phase = (team / kStages & 1) ^ 1;
 #pragma unroll 1
-        for (int i = 0; i < n_blocks; ++i) {
-            __syncwarp();  // every lane has read what the next copies replace
-            fetch(i + kAhead - 1);
+        for (int i = team; i < n_blocks; i += kTeams) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-            if (!all_wait(&empty[stage], phase)) break;
-            const uint8_t *src = ring_s + (w * kAhead + in_ring) * (kRows * kPitch) + row0 * kPitch + 16 * c;
-            uint8_t *line = smem + stage * (kWBytes + kXBytes) + c / 4 * (kDeep * 128) + (kRows * w + row0) * 128;
+            __syncwarp();
+            const uint8_t *src = own + in_ring * (kRows * kPitch) + row0 * kPitch + 16 * c;
+            uint4 x[kRows / 4], y[kRows / 4];
 #pragma unroll
             for (int u = 0; u < kRows / 4; ++u) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch);
-                uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                x[u] = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch);
+                if (!ALIGNED) y[u] = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch + 16);
+            }
+            __syncwarp();  // every lane has what the next copies replace
+            fetch(i + kAhead * kTeams);
+            if (!all_wait(&empty[stage], phase)) break;
+            uint8_t *line = smem + stage * kStageBytes + c / 4 * (kDeep * 128) + (kRows * w + row0) * 128;
+#pragma unroll
+            for (int u = 0; u < kRows / 4; ++u) {
+                uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
                 if (!ALIGNED) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(src + 4 * u * kPitch + 16);
-                    uint32_t t[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    uint32_t t[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
                     for (int q = 0; q < 6; ++q) t[q] = shift[u] & 8 ? t[q + 2] : t[q];
 #pragma unroll
@@ -385,7 +400,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage]);
-            if (++stage == kFewStages) stage = 0, phase ^= 1;
+            stage += kTeams;
+            if (stage >= kStages) stage -= kStages, phase ^= 1;
             in_ring = in_ring + 1 == kAhead ? 0 : in_ring + 1;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -408,7 +424,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
             for (int done = 0; done < part; ++c) {
                 done += chunk_of(at.block + done, left - done);
-                if (!(ok = all_wait(&sum_full[c & 1], c >> 1 & 1, true))) break;
+                // one warp polls, the others are out of the way of those that work
+                if (warp == 0) all_wait(&sum_full[c & 1], c >> 1 & 1);
+                asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
+                if (!(ok = !*abort_flag)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int m = 0; m < kMine; m += 8) {
@@ -476,7 +495,7 @@ cudaError_t launch_few_as(const FewArgs &a, const CUtensorMap &map, cudaStream_t
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(wcols_few_kernel<kCols, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+        e = cudaFuncSetAttribute(wcols_few_kernel<kCols, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<kCols>::kBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
@@ -486,7 +505,7 @@ cudaError_t launch_few_as(const FewArgs &a, const CUtensorMap &map, cudaStream_t
     const int64_t runs = (sms + blocks - 1) / blocks;
     cfg.gridDim = dim3((unsigned)(a.all < runs ? a.all : runs), (unsigned)blocks);
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.dynamicSmemBytes = FewCfg<kCols>::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
