@@ -161,8 +161,13 @@ cudaError_t launch_selftest_scales(uint32_t first, uint32_t last, unsigned long 
 // int8 -> f16 operand conversions for the integer-only entry point.
 cudaError_t launch_i8_rows_to_half(const int8_t *Q, int64_t rows, int64_t cols, int64_t ldq,
                                    __half *out, int64_t ldo, cudaStream_t st);
+// (cols: transposed; out's rows 16-byte aligned, ldo at least rows rounded up to 64.  scale, scale_out:
+// cols floats to copy along, or NULL.  beside: the launch may run beside the one before it in
+// the stream, which it touches nothing of.)
 cudaError_t launch_i8_cols_to_half(const int8_t *Q, int64_t rows, int64_t cols, int64_t ldq,
-                                   __half *out, int64_t ldo, cudaStream_t st);
+                                   __half *out, int64_t ldo, cudaStream_t st,
+                                   const float *scale = nullptr, float *scale_out = nullptr,
+                                   bool beside = false);
 
 // The tile width (64, 128, 192 or 256) the GEMM uses for an M x N problem (or
 // a launch of n of them), and whether it runs 256-row tiles on CTA pairs
