@@ -25,7 +25,8 @@ LIB = os.path.join(BUILD, "libbsgemm.so")
 
 SOURCES = ["bsgemm_api.cu", "quantize.cu", "gemm_tc.cu", "epilogue.cu", "probe.cu", "noalloc.cu",
            "audit.cu", "wquant.cu", "mma_ceiling.cu", "serving_api.cu", "wgroups.cu", "kv8.cu",
-           "logprobs.cu", "wcols.cu", "kv8_more.cu"]
+           "logprobs.cu", "wcols.cu", "kv8_more.cu",
+           "kv8_few_window.cu", "kv8_few_prefix.cu", "kv8_tiles_window.cu", "kv8_tiles_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fno-strict-aliasing", "-I", INCLUDE, "-I", CSRC]

@@ -6,7 +6,9 @@
 
 #include <type_traits>
 
-#include "kv8_tiles.cuh"
+#include "bsg_ptx.cuh"
+#include "kv8_more.h"
+#include "serve.cuh"
 
 namespace bsg {
 namespace {
@@ -28,6 +30,12 @@ struct JoinArgs {
 };
 
 constexpr int kJoinThreads = 128;
+
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __grid_constant__ JoinArgs a) {
@@ -67,7 +75,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __gr
             const int list = i >= a.splits[0];
             const float2 x = a.ml[list][at(i)];
             if (x.y == 0.0f) continue;
-            const float f = tile_exp2(x.x - m);
+            const float f = exp2_of(x.x - m);
             const float4 v = *reinterpret_cast<const float4 *>(a.o[list] + at(i) * D + 4 * col);
             o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
             l = fmaf(x.y, f, l);
@@ -124,74 +132,33 @@ cudaError_t launch_join(const JoinArgs &a, int dim, int dtype, cudaStream_t st) 
     });
 }
 
-// ---- the tiles ----------------------------------------------------------------
-
-struct TilePlan {
-    int row_blocks, splits;
-    int64_t groups;
-    size_t floats, parts;  // of partial outputs, and their count
-};
-
-int64_t most_tiles(const bsg_kv8_cache &c, int64_t table_ld, int64_t tokens, int window, int sinks) {
-    const int64_t all = table_ld * c.page_tokens, n = c.dim == 256 ? 64 : 128;
-    int64_t see = all;
-    if (window && window + tokens + sinks < all) see = window + tokens + sinks;
-    return (see + n - 1) / n + (window ? 2 : 0);
-}
-
-// As many chunks as fill the card once, of two tiles at least.
-TilePlan tile_plan(const bsg_kv8_cache &c, int64_t rows, int64_t groups, int64_t tiles, bool later) {
-    TilePlan p;
-    const int64_t block = c.dim == 256 ? 128 : 256;
-    p.row_blocks = (int)((rows + block - 1) / block);
-    p.groups = groups;
-    int64_t splits = device_sm_count() / (p.row_blocks * groups);
-    if (splits > tiles / 2) splits = tiles / 2;
-    p.splits = (int)(splits < 1 ? 1 : splits);
-    p.parts = p.splits > 1 || later ? (size_t)groups * rows * p.splits : 0;
-    p.floats = p.parts * (c.dim + 2);
-    return p;
-}
-
-template <int D, int kQ, int kP, bool PREFIX>
-cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
-    using C = TileCfg<D, kQ>;
-    static bool set[64] = {false};  // this kernel's shared memory, on each device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(kv8_tiles_kernel<D, kQ, kP, PREFIX>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) set[dev] = true;
-    }
-    const int64_t blocks = a.row_blocks * a.groups;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), kTileThreads, C::kBytes, st>>>(a);
-    count_launches(1);
-    return cudaGetLastError();
-}
-
-template <bool PREFIX>
-cudaError_t launch_tiles(TileArgs a, const TilePlan &p, int dtype, cudaStream_t st) {
-    a.row_blocks = p.row_blocks, a.groups = p.groups, a.splits = p.splits;
-    return with_dim(a.c.dim, [&](auto d) {
-        constexpr int D = decltype(d)::value;
-        if (dtype == BSG_F32) return launch_tiles_as<D, 2, 2, PREFIX>(a, st);
-        if (dtype == BSG_F16) return launch_tiles_as<D, 1, 2, PREFIX>(a, st);
-        return launch_tiles_as<D, 1, 1, PREFIX>(a, st);
-    });
-}
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Which kernel a call takes: up to kFewSlots query rows (f32's twice) of a key/value head the one
+// of few rows, whose 8 slots a tile read the cache at its rate; beyond, 128 rows a tile.
+constexpr int kFewSlots = 32;
+bool few(int64_t rows, int dtype) { return rows * (dtype == BSG_F32 ? 2 : 1) <= kFewSlots; }
+
+// The workspace of one part of a call, largest over the types.
+size_t part_floats(const bsg_kv8_cache &c, int64_t rows, int64_t B, int64_t positions, bool later) {
+    size_t most = 0;
+    for (int dtype = BSG_F32; dtype <= BSG_F16; ++dtype) {
+        const KvPlan p = kv_plan(c, few(rows, dtype), dtype, rows, B, positions, later);
+        if (p.parts * (c.dim + 2) > most) most = p.parts * (c.dim + 2);
+    }
+    return most;
+}
+
+int64_t seen_positions(const bsg_kv8_cache &c, int64_t table_ld, int64_t tokens, int window, int sinks) {
+    const int64_t all = table_ld * c.page_tokens, some = (int64_t)window + tokens + sinks + 3 * 128;
+    return window && some < all ? some : all;
+}
 
 }  // namespace
 
 size_t kv8_window_workspace_bytes(const bsg_kv8_cache &c, int64_t table_ld, int64_t B, int64_t T,
                                   int heads, int window, int sinks) {
-    const TilePlan p = tile_plan(c, T * (heads / c.heads), B * c.heads, most_tiles(c, table_ld, T, window, sinks), false);
-    return up256(p.floats * 4 + 1);
+    return up256(part_floats(c, T * (heads / c.heads), B, seen_positions(c, table_ld, T, window, sinks), false) * 4 + 1);
 }
 
 cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *table, int64_t table_ld,
@@ -200,24 +167,23 @@ cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *tabl
                                      int heads, int window, int sinks, float scale, float *lse,
                                      void *ws, int32_t *dstatus, cudaStream_t st) {
     const int64_t rows = T * (heads / c.heads);
-    const TilePlan p = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, window, sinks), false);
-    float *part_o = static_cast<float *>(ws);
-    float2 *part_ml = reinterpret_cast<float2 *>(part_o + p.parts * c.dim);
-    const TileArgs a{c, table, table_ld, lens, counts, q, out, (int)T, heads, window, sinks, (int)rows, 0, 0, 0, 0,
-                     scale, lse, part_o, part_ml, dstatus};
-    cudaError_t e = launch_tiles<false>(a, p, dtype, st);
+    const bool is_few = few(rows, dtype);
+    const KvPlan p = kv_plan(c, is_few, dtype, rows, B, seen_positions(c, table_ld, T, window, sinks), false);
+    KvCall a{c, table, table_ld, lens, counts, q, out, dtype, (int)T, heads, window, sinks, B, rows, scale, lse, 0,
+             static_cast<float *>(ws), nullptr, dstatus};
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.parts * c.dim);
+    cudaError_t e = is_few ? launch_few_window(a, p, st) : launch_tiles_window(a, p, st);
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_join({out, c.heads, heads, (int)T, (int)B, nullptr, counts, 0, {part_o, nullptr},
-                        {part_ml, nullptr}, {p.splits, 0}, lse},
+    return launch_join({out, c.heads, heads, (int)T, (int)B, nullptr, counts, 0, {a.part_o, nullptr},
+                        {a.part_ml, nullptr}, {p.splits, 0}, lse},
                        c.dim, dtype, st);
 }
 
 size_t kv8_shared_workspace_bytes(const bsg_kv8_cache &c, int64_t prefix_pages, int64_t table_ld,
                                   int64_t B, int64_t T, int heads) {
     const int64_t rows = T * (heads / c.heads);
-    const TilePlan own = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, 0, 0), true);
-    const TilePlan pre = tile_plan(c, B * rows, c.heads, most_tiles(c, prefix_pages, 0, 0, 0), true);
-    return up256((own.floats + pre.floats) * 4);
+    return up256((part_floats(c, rows, B, table_ld * c.page_tokens, true) +
+                  part_floats(c, B * rows, 1, prefix_pages * c.page_tokens, true)) * 4);
 }
 
 cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *prefix,
@@ -228,17 +194,18 @@ cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *pref
                                      void *ws, int32_t *dstatus, cudaStream_t st) {
     const int64_t rows = T * (heads / c.heads);
     if (B * rows > INT32_MAX) return cudaErrorInvalidValue;
-    const TilePlan own = tile_plan(c, rows, B * c.heads, most_tiles(c, table_ld, T, 0, 0), true);
-    const TilePlan pre = tile_plan(c, B * rows, c.heads, most_tiles(c, prefix_pages, 0, 0, 0), true);
+    const bool few_own = few(rows, dtype), few_pre = few(B * rows, dtype);
+    const KvPlan own = kv_plan(c, few_own, dtype, rows, B, table_ld * c.page_tokens, true);
+    const KvPlan pre = kv_plan(c, few_pre, dtype, B * rows, 1, prefix_pages * c.page_tokens, true);
     float *own_o = static_cast<float *>(ws), *pre_o = own_o + own.parts * c.dim;
     float2 *own_ml = reinterpret_cast<float2 *>(pre_o + pre.parts * c.dim), *pre_ml = own_ml + own.parts;
-    TileArgs a{c, table, table_ld, lens, nullptr, q, out, (int)T, heads, 0, 0, (int)rows, 0, 0, 0, 1,
-               scale, lse, own_o, own_ml, dstatus};
-    cudaError_t e = launch_tiles<false>(a, own, dtype, st);
+    KvCall a{c, table, table_ld, lens, nullptr, q, out, dtype, (int)T, heads, 0, 0, B, rows, scale, lse, 1,
+             own_o, own_ml, dstatus};
+    cudaError_t e = few_own ? launch_few_window(a, own, st) : launch_tiles_window(a, own, st);
     if (e != cudaSuccess) return e;
-    a.table = prefix, a.table_ld = prefix_pages, a.lens = prefix_len, a.rows = (int)(B * rows);
+    a.table = prefix, a.table_ld = prefix_pages, a.lens = prefix_len, a.B = 1, a.rows = B * rows;
     a.part_o = pre_o, a.part_ml = pre_ml;
-    e = launch_tiles<true>(a, pre, dtype, st);
+    e = few_pre ? launch_few_prefix(a, pre, st) : launch_tiles_prefix(a, pre, st);
     if (e != cudaSuccess) return e;
     return launch_join({out, c.heads, heads, (int)T, (int)B, lens, nullptr, table_ld * c.page_tokens, {own_o, pre_o},
                         {own_ml, pre_ml}, {own.splits, pre.splits}, lse},

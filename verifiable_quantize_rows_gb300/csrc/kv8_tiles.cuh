@@ -28,6 +28,8 @@
 
 #include "bsg_internal.h"
 #include "bsg_ptx.cuh"
+#include "kv8_more.h"
+#include "kv8_seen.cuh"
 #include "serve.cuh"
 
 namespace bsg {
@@ -85,28 +87,6 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16])
 
 // The lowest n bits.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
-// What a CTA of some rows sees: the tiles from `first`, then (whose few positions would
-// begin with a low reference) `sink_tiles` from the sequence's start.
-struct Seen {
-    int tiles, sink_tiles, first;
-    int low, see;  // the lowest position of the window part, and the end
-};
-template <int kN>
-__device__ __forceinline__ Seen seen_by(int first_pos, int last_pos, int window, int sinks) {
-    Seen s;
-    s.see = last_pos + 1;
-    s.low = window && first_pos >= window ? first_pos - window + 1 : 0;
-    if (s.see <= 0) {
-        s.tiles = s.sink_tiles = s.first = 0;
-        return s;
-    }
-    const int k = min(sinks, s.low);
-    s.sink_tiles = (k + kN - 1) / kN;
-    s.first = max(s.sink_tiles, s.low / kN);
-    s.tiles = s.sink_tiles + max(0, (s.see + kN - 1) / kN - s.first);
-    return s;
-}
 
 template <int D, int kQParts>
 struct TileCfg {
@@ -215,11 +195,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int begin = (int)((int64_t)seen.tiles * split / a.splits);
     const int tiles = (int)((int64_t)seen.tiles * (split + 1) / a.splits) - begin;
     const int groups = rows > 128 ? kM : 1;  // of 128 rows
-    auto position = [&](int i) {  // of the CTA's tile i
-        const int v = begin + i;
-        const int near = seen.tiles - seen.sink_tiles;
-        return (v < near ? seen.first + v : v - near) * kN;
-    };
+    auto position = [&](int i) { return seen.tile(begin + i) * kN; };  // of the CTA's tile i
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -722,6 +698,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(0, 512);
+    }
+}
+
+template <int D, int kQ, int kP, bool PREFIX>
+cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
+    using C = TileCfg<D, kQ>;
+    static bool set[64] = {false};  // this kernel's shared memory, on each device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(kv8_tiles_kernel<D, kQ, kP, PREFIX>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
+    }
+    const int64_t blocks = a.row_blocks * a.groups;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), kTileThreads, C::kBytes, st>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int D, bool PREFIX>
+cudaError_t launch_tiles_dim(const TileArgs &a, int dtype, cudaStream_t st) {
+    if (dtype == BSG_F32) return launch_tiles_as<D, 2, 2, PREFIX>(a, st);
+    if (dtype == BSG_F16) return launch_tiles_as<D, 1, 2, PREFIX>(a, st);
+    return launch_tiles_as<D, 1, 1, PREFIX>(a, st);
+}
+
+template <bool PREFIX>
+cudaError_t launch_tiles(const KvCall &k, const KvPlan &p, cudaStream_t st) {
+    const TileArgs a{k.c, k.table, k.table_ld, k.lens, k.counts, k.q, k.out, k.tokens, k.heads, k.window, k.sinks,
+                     (int)k.rows, p.row_blocks, k.B * k.c.heads, p.splits, k.later, k.scale, k.lse, k.part_o, k.part_ml,
+                     k.dstatus};
+    switch (k.c.dim) {
+        case 32: return launch_tiles_dim<32, PREFIX>(a, k.dtype, st);
+        case 64: return launch_tiles_dim<64, PREFIX>(a, k.dtype, st);
+        case 96: return launch_tiles_dim<96, PREFIX>(a, k.dtype, st);
+        case 128: return launch_tiles_dim<128, PREFIX>(a, k.dtype, st);
+        default: return launch_tiles_dim<256, PREFIX>(a, k.dtype, st);
     }
 }
 
