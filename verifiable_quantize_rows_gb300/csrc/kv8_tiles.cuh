@@ -18,8 +18,8 @@
 //              tile in registers;
 //   8-11       codes into f16 operands, in a ring of shared memory that K and V tiles take
 //              in turn; each tile's loads are sent two fills ahead;
-//   12         issues the MMAs: S of a tile as soon as the one before it has been read into
-//              registers, P V of each half tile as it comes;
+//   12, 14     issue the MMAs of a group of rows each: S of a tile as soon as the one before
+//              it has been read into registers, P V of each half tile as it comes;
 //   13         finds where the tiles' pages lie, and their scales, some tiles at a time.
 #pragma once
 
@@ -101,7 +101,7 @@ struct TileCfg {
     static constexpr int kOffStage = kM * kQParts * kQBytes;
     static constexpr int kOffAt = kOffStage + kStages * kStageBytes;
     static constexpr int kOffBar = kOffAt + kAtSlots * kGroups * 16;
-    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 1 + 7 * kM;
+    static constexpr int kBars = 2 * kStages + 2 * kAtSlots + 8 * kM;
     static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     static constexpr int kBytes = (kUsed > 118000 ? kUsed : 118000) + 1024;  // one CTA on an SM (all its tensor memory)
     static_assert(kStages >= 2 && kBytes <= 232448, "shared memory");
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     float4 *at_s = reinterpret_cast<float4 *>(smem + C::kOffAt);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     uint64_t *kv_full = bars, *kv_empty = bars + kStages, *at_full = bars + 2 * kStages;
-    uint64_t *at_empty = at_full + kAtSlots, *s_empty = at_empty + kAtSlots, *s_full = s_empty + 1;
+    uint64_t *at_empty = at_full + kAtSlots, *s_empty = at_empty + kAtSlots, *s_full = s_empty + kM;
     uint64_t *o_full = s_full + kM, *p_full = o_full + kM, *p_empty = p_full + 2 * kM;  // [m][slot]
     uint64_t *q_full = p_empty + 2 * kM;
     // P goes to the tensor cores by halves of a tile: one part has room for both, two parts for one
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&kv_full[s], 4);
-            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_empty[s], groups);  // the MMAs' warps
         }
         for (int s = 0; s < kAtSlots; ++s) {
             mbar_init(&at_full[s], 1);
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int m = 0; m < kM; ++m) {
             mbar_init(&s_full[m], 1);
+            mbar_init(&s_empty[m], 4);
             mbar_init(&o_full[m], 1);
             mbar_init(&q_full[m], 4);
             for (int u = 0; u < 2; ++u) {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 mbar_init(&p_empty[2 * m + u], 1);
             }
         }
-        mbar_init(s_empty, 4);
+
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -248,63 +249,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     if (warp >= 12) {
         fewer_registers<kOtherRegs>();
-        if (warp == kMmaWarp && tiles > 0) {
-            // ------------------------------------------------ MMA issuer
+        const int m = (warp - kMmaWarp) / 2;  // of the MMAs' warps
+        if (warp % 2 == 0 && m < groups && tiles > 0) {
+            // ------------------------------------------------ MMA issuers
             // The whole warp goes along, so that descriptors stay in uniform registers (one
-            // lane alone took 90 clocks to issue an MMA of 64); one lane issues.
+            // lane alone took 90 clocks to issue an MMA of 64); one lane issues.  A warp to
+            // each group of rows: every wait costs some 100 clocks, its barrier complete or
+            // not, and one warp's for both took longer than the MMAs.
             constexpr uint32_t kIdescS = idesc_f16_f32(128, kN), kIdescO = idesc_f16_f32(128, D) | kIdescBMn;
             const uint32_t stage0 = smem_u32(smem + C::kOffStage);
-            const uint64_t q_desc = sdesc_k128(smem_u32(smem)), k_desc = sdesc_k128(stage0);
+            const uint64_t q_desc = sdesc_k128(smem_u32(smem) + m * (kQParts * C::kQBytes)), k_desc = sdesc_k128(stage0);
             const uint64_t v_desc = sdesc_mn128(stage0, kN * 128);
             const int n = __reduce_max_sync(0xffffffffu, tiles);
             const bool two = __reduce_max_sync(0xffffffffu, groups) > 1;
             const bool one = elect_one();
+            const uint32_t o_at = C::kO(0) + m * D;
             bool ok = true;
-            // S(0), S(1), ... of tiles and rows in turn take one place, each when the one before
-            // it has been read; P V of a tile follows the S that is `groups` places ahead of it.
-            // (Loops rolled up: the code of all roles has to share the instruction caches.)
-            const int all = two ? 2 * n : n, ahead = two ? 2 : 1;
+            // S of tiles and rows in turn take one place, each when the one before it has been
+            // read; P V of a tile follows the S of the next.
             int k_stage = 0, v_stage = 1;  // fills K 0, V 0, K 1, V 1, ...
             uint32_t k_phase = 0, v_phase = 0;
-            int s_next = 0, s_m = 0, m = 0, i = 0;
             auto step = [&](int &stage, uint32_t &phase) {
                 stage += 2;
                 if (stage >= kStages) stage -= kStages, phase ^= 1;
             };
+            ok = all_wait(&q_full[m], 0);
+            int s_next = 0;
 #pragma unroll 1
-            for (int q = 0; q < all && ok; ++q) {
+            for (int i = 0; i < n && ok; ++i) {
 #pragma unroll 1
-                while (s_next < all && s_next <= q + ahead) {
-                    if (s_next < ahead && !(ok = all_wait(&q_full[s_m], 0))) break;
-                    if (s_m == 0 && !(ok = all_wait(&kv_full[k_stage], k_phase))) break;
-                    if (s_next > 0 && !(ok = all_wait(s_empty, (s_next - 1) & 1))) break;
+                while (s_next < n && s_next <= i + 1) {
+                    if (!(ok = all_wait(&kv_full[k_stage], k_phase))) break;
+                    if (two && m == 1) {  // after the first rows' S of this tile
+                        ok = all_wait(&s_empty[0], s_next & 1);
+                    } else if (s_next > 0) {  // after the S before: the other rows', or this group's own
+                        ok = all_wait(&s_empty[two ? kM - 1 : 0], (s_next - 1) & 1);
+                    }
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t kd = k_desc + k_stage * (C::kStageBytes / 16);
-                    const uint64_t qd = q_desc + s_m * (kQParts * C::kQBytes / 16);
                     if (one) {
 #pragma unroll
                         for (int part = 0; part < kQParts; ++part)
 #pragma unroll
                             for (int j = 0; j < D / 16; ++j)
-                                mma_f16_ss(0, qd + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                                mma_f16_ss(0, q_desc + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
                                            kd + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
-                        mma_commit(&s_full[s_m]);
-                        if (s_m == ahead - 1) mma_commit(&kv_empty[k_stage]);
+                        mma_commit(&s_full[m]);
+                        mma_commit(&kv_empty[k_stage]);
                     }
-                    if (++s_m == ahead) {
-                        s_m = 0;
-                        step(k_stage, k_phase);
-                    }
+                    step(k_stage, k_phase);
                     ++s_next;
                 }
-                if (!ok || (m == 0 && !(ok = all_wait(&kv_full[v_stage], v_phase)))) break;
+                if (!ok || !(ok = all_wait(&kv_full[v_stage], v_phase))) break;
                 const uint64_t v = v_desc + v_stage * (C::kStageBytes / 16);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {  // P V of tile i
                     const int slot = 2 * m + half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
                     if (!(ok = all_wait(&p_full[slot], use & 1))) break;
                     tc_fence_after();
-                    const uint32_t o_at = C::kO(0) + m * D, p_at = C::kP(0) + m * C::kPCols + half % kSlots * (kHalf / 2);
+                    const uint32_t p_at = C::kP(0) + m * C::kPCols + half % kSlots * (kHalf / 2);
                     const uint64_t vd = v + half * (kHalf / 16 * 128);
                     if (one) {
 #pragma unroll
@@ -316,17 +320,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         mma_commit(&p_empty[slot]);
                     }
                 }
-                if (one && i + 1 == n) mma_commit(&o_full[m]);
-                if (++m == ahead) {
-                    if (one) mma_commit(&kv_empty[v_stage]);
-                    step(v_stage, v_phase);
-                    m = 0, ++i;
+                if (one) {
+                    mma_commit(&kv_empty[v_stage]);
+                    if (i + 1 == n) mma_commit(&o_full[m]);
                 }
+                step(v_stage, v_phase);
             }
             if (!ok && one) {  // wait until every MMA issued so far has finished
-                mma_commit(&o_full[0]);
+                mma_commit(&o_full[m]);
                 const long long t0 = clock64();
-                while (!mbar_try_wait(&o_full[0], 0) && clock64() - t0 < kWaitLimitCycles) {
+                while (!mbar_try_wait(&o_full[m], 0) && clock64() - t0 < kWaitLimitCycles) {
                 }
             }
         } else if (warp == 13) {
@@ -504,12 +507,88 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
             }
         };
+        // The same by 16 bytes, where rows begin on them and a row's pieces are 1 to 32 lanes, a power
+        // of two.
+        auto load_pieces = [&](auto type) {
+            using T = decltype(type);
+            constexpr int kE = 16 / sizeof(T), kL = D / kE, kR = 32 / kL, kAhead = kQParts == 2 ? 8 : 32 / kR < 8 ? 32 / kR : 8;
+            const int n = (r0 + r) / share, h = (r0 + r) % share;
+            const int64_t where = (PREFIX ? n / a.tokens * a.q.stride_batch + n % a.tokens * a.q.stride_token
+                                          : b * a.q.stride_batch + n * a.q.stride_token) + (hk * share + h) * a.q.stride_head;
+            uint8_t *const tile = smem + m * kQParts * C::kQBytes;
+            struct alignas(16) Piece {
+                T v[kE];
+            };
+#pragma unroll 1
+            for (int r1 = 0; r1 < 32; r1 += kR * kAhead) {
+                Piece q[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int row = r1 + i * kR + lane / kL;
+                    const int64_t at = __shfl_sync(0xffffffffu, where, row);
+                    if (warp * 32 + row < rows) {
+                        q[i] = *reinterpret_cast<const Piece *>(static_cast<const T *>(a.q.data) + at + lane % kL * kE);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kE; ++j) q[i].v[j] = from_f32<T>(0.0f);
+                    }
+                }
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    float x = 0.0f, y[kE];
+#pragma unroll
+                    for (int j = 0; j < kE; ++j) {
+                        y[j] = to_f32(q[i].v[j]);
+                        bad |= !isfinite(y[j]);
+                        x = fmaxf(x, fabsf(y[j]));
+                    }
+#pragma unroll
+                    for (int o = kL / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    const int e = max(-126, min(126, 13 + 127 - (int)(__float_as_uint(x) >> 23)));
+                    const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
+                    const float its = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - e) << 23);
+                    const float from = __shfl_sync(0xffffffffu, its, (lane - r1 - i * kR) * kL & 31);
+                    if (lane >= r1 + i * kR && lane < r1 + (i + 1) * kR) mul = from;
+                    const int at_r = warp % 4 * 32 + r1 + i * kR + lane / kL, d = lane % kL * kE;
+                    uint8_t *const to = tile + d / 64 * 16384 + at_r * 128 + ((d % 64 / 8 ^ at_r % 8) << 4) + d % 8 * 2;
+                    __half2 hi[kE / 2], lo[kE / 2];
+#pragma unroll
+                    for (int j = 0; j < kE / 2; ++j) {
+                        const float y0 = y[2 * j] * up, y1 = y[2 * j + 1] * up;
+                        hi[j] = __floats2half2_rn(y0, y1);
+                        const float2 back = __half22float2(hi[j]);
+                        lo[j] = __floats2half2_rn(y0 - back.x, y1 - back.y);
+                    }
+                    if constexpr (kQParts == 2) {
+                        *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(hi);
+                        *reinterpret_cast<uint2 *>(to + C::kQBytes) = *reinterpret_cast<const uint2 *>(lo);
+                    } else {
+                        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(hi);
+                    }
+                }
+                if (bad) set_status(a.dstatus, BSG_DSTATUS_NONFINITE);
+            }
+        };
+        auto load_any = [&](auto type) {
+            using T = decltype(type);
+            constexpr bool kPieces = D != 96 && (D * (int)sizeof(T)) / 16 <= 32;
+            const uintptr_t all = reinterpret_cast<uintptr_t>(a.q.data) | (uintptr_t)(a.q.stride_batch * (int64_t)sizeof(T)) |
+                                  (uintptr_t)(a.q.stride_token * (int64_t)sizeof(T)) | (uintptr_t)(a.q.stride_head * (int64_t)sizeof(T));
+            if constexpr (kPieces) {
+                if (all % 16 == 0) {
+                    load_pieces(type);
+                    return;
+                }
+            }
+            load_queries(type);
+        };
         if constexpr (kQParts == 2) {
-            load_queries(float{});
+            load_any(float{});
         } else if constexpr (kPParts == 2) {
-            load_queries(__half{});
+            load_any(__half{});
         } else {
-            load_queries(__nv_bfloat16{});
+            load_any(__nv_bfloat16{});
         }
         fence_async_shared();
         __syncwarp();
@@ -545,7 +624,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty);
+            if (lane == 0) mbar_arrive(&s_empty[m]);
             // the largest exponent, relative to the reference
             float y[C::kGroups], top = -INFINITY;
 #pragma unroll
@@ -695,6 +774,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     }
     __syncthreads();
+    if (PREFIX) griddep_wait();  // this grid never ends before the one that it was launched beside
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(0, 512);
@@ -716,9 +796,18 @@ cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
     }
     const int64_t blocks = a.row_blocks * a.groups;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    kv8_tiles_kernel<D, kQ, kP, PREFIX><<<dim3((unsigned)blocks, (unsigned)a.splits), kTileThreads, C::kBytes, st>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.splits);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PREFIX ? 1 : 0;  // beside the sequences' own positions' launch
     count_launches(1);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kv8_tiles_kernel<D, kQ, kP, PREFIX>, a);
 }
 
 template <int D, bool PREFIX>
