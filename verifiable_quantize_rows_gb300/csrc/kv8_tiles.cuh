@@ -88,7 +88,7 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16])
 // The lowest n bits.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-template <int D, int kQParts>
+template <int D, int kQParts, int kPParts>
 struct TileCfg {
     static constexpr int kM = D == 256 ? 1 : 2;
     static constexpr int kN = D == 256 ? 64 : 128;
@@ -105,11 +105,15 @@ struct TileCfg {
     static constexpr int kUsed = kOffBar + kBars * 8 + 16;
     static constexpr int kBytes = (kUsed > 118000 ? kUsed : 118000) + 1024;  // one CTA on an SM (all its tensor memory)
     static_assert(kStages >= 2 && kBytes <= 232448, "shared memory");
-    // columns of tensor memory: S (the groups of rows in turn), P's and O's
-    static constexpr int kPCols = kN / 2;  // one part of a tile, or two of half a tile
-    static __device__ constexpr int kP(int m) { return kN + m * kPCols; }
-    static __device__ constexpr int kO(int m) { return kN + kM * kPCols + m * D; }
-    static_assert(kN + kM * (kPCols + D) <= 512, "tensor memory");
+    // Columns of tensor memory.  S in one place that the groups of rows use in turn, P's two
+    // halves and O of each group; where that is more than there is (two parts of P, 96 or 128
+    // dims), each group has a place for S, which its P takes afterwards.
+    static constexpr int kPCols = kPParts * kN / 2;
+    static constexpr bool kInPlace = kN + kM * (kPCols + D) > 512;
+    static constexpr int kSStep = kInPlace ? kN : 0;                     // from one group's S to the next's
+    static constexpr int kP0 = kInPlace ? 0 : kN, kPStep = kInPlace ? kN : kPCols;
+    static constexpr int kO0 = kInPlace ? kM * kN : kN + kM * kPCols;
+    static_assert(kO0 + kM * D <= 512 && kPCols <= kN, "tensor memory");
 };
 
 constexpr int kTileThreads = 512;
@@ -141,7 +145,7 @@ __device__ __forceinline__ uint4 load_codes(const int8_t *p) {
 template <int D, int kQParts, int kPParts, bool PREFIX>
 __global__ void __launch_bounds__(kTileThreads, 1)
     kv8_tiles_kernel(const __grid_constant__ TileArgs a) {
-    using C = TileCfg<D, kQParts>;
+    using C = TileCfg<D, kQParts, kPParts>;
     constexpr int kM = C::kM, kN = C::kN, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
@@ -153,8 +157,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t *at_empty = at_full + kAtSlots, *s_empty = at_empty + kAtSlots, *s_full = s_empty + kM;
     uint64_t *o_full = s_full + kM, *p_full = o_full + kM, *p_empty = p_full + 2 * kM;  // [m][slot]
     uint64_t *q_full = p_empty + 2 * kM;
-    // P goes to the tensor cores by halves of a tile: one part has room for both, two parts for one
-    constexpr int kSlots = kPParts == 1 ? 2 : 1, kHalf = kN / 2;
+    constexpr int kHalf = kN / 2;  // P goes to the tensor cores by halves of a tile
+    constexpr bool kInPlace = C::kInPlace;
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(bars + C::kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
 
@@ -263,10 +267,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int n = __reduce_max_sync(0xffffffffu, tiles);
             const bool two = __reduce_max_sync(0xffffffffu, groups) > 1;
             const bool one = elect_one();
-            const uint32_t o_at = C::kO(0) + m * D;
+            const uint32_t s_at = m * C::kSStep, o_at = C::kO0 + m * D;
             bool ok = true;
             // S of tiles and rows in turn take one place, each when the one before it has been
-            // read; P V of a tile follows the S of the next.
+            // read, and P V of a tile follows the S of the next; in place S follows the P V.
             int k_stage = 0, v_stage = 1;  // fills K 0, V 0, K 1, V 1, ...
             uint32_t k_phase = 0, v_phase = 0;
             auto step = [&](int &stage, uint32_t &phase) {
@@ -278,9 +282,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
 #pragma unroll 1
-                while (s_next < n && s_next <= i + 1) {
+                while (s_next < n && s_next <= i + (kInPlace ? 0 : 1)) {
                     if (!(ok = all_wait(&kv_full[k_stage], k_phase))) break;
-                    if (two && m == 1) {  // after the first rows' S of this tile
+                    if (kInPlace) {
+                    } else if (two && m == 1) {  // after the first rows' S of this tile
                         ok = all_wait(&s_empty[0], s_next & 1);
                     } else if (s_next > 0) {  // after the S before: the other rows', or this group's own
                         ok = all_wait(&s_empty[two ? kM - 1 : 0], (s_next - 1) & 1);
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         for (int part = 0; part < kQParts; ++part)
 #pragma unroll
                             for (int j = 0; j < D / 16; ++j)
-                                mma_f16_ss(0, q_desc + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
+                                mma_f16_ss(s_at, q_desc + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
                                            kd + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
                         mma_commit(&s_full[m]);
                         mma_commit(&kv_empty[k_stage]);
@@ -305,10 +310,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const uint64_t v = v_desc + v_stage * (C::kStageBytes / 16);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {  // P V of tile i
-                    const int slot = 2 * m + half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
-                    if (!(ok = all_wait(&p_full[slot], use & 1))) break;
+                    if (!(ok = all_wait(&p_full[2 * m + half], i & 1))) break;
                     tc_fence_after();
-                    const uint32_t p_at = C::kP(0) + m * C::kPCols + half % kSlots * (kHalf / 2);
+                    const uint32_t p_at = C::kP0 + m * C::kPStep + half * (C::kPCols / 2);
                     const uint64_t vd = v + half * (kHalf / 16 * 128);
                     if (one) {
 #pragma unroll
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             for (int part = 0; part < kPParts; ++part)
                                 mma_f16_ts(o_at, p_at + part * (kHalf / 2) + 8 * j, vd + j * 128, kIdescO,
                                            j + part > 0 ? 1 : half + i > 0);
-                        mma_commit(&p_empty[slot]);
+                        if (!kInPlace) mma_commit(&p_empty[2 * m + half]);
                     }
                 }
                 if (one) {
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int m = warp / 4, r = tid;
         if (m < groups) {
         const uint32_t quad = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t s_at = quad, p_at = C::kP(m) + quad, o_at = C::kO(m) + quad;
+        const uint32_t s_at = m * C::kSStep + quad, p_at = C::kP0 + m * C::kPStep + quad, o_at = C::kO0 + m * D + quad;
         const int pos = PREFIX ? len - 1 : pos0 + (r0 + r) / share;
         const int see = r < rows ? pos + 1 : 0;
         const int low = !PREFIX && a.window && pos >= a.window ? pos - a.window + 1 : 0;
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[m]);
+            if (!kInPlace && lane == 0) mbar_arrive(&s_empty[m]);
             // the largest exponent, relative to the reference
             float y[C::kGroups], top = -INFINITY;
 #pragma unroll
@@ -649,10 +653,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     none = false;
                 }
                 if (i > 0) {
-                    // O is at rest once the last P of the tile before is used up
+                    // O is at rest once the last P of the tile before is used up (in place: as S is there)
 #pragma unroll
-                    for (int u = 0; u < kSlots; ++u)
-                        if (ok) ok = all_wait(&p_empty[2 * m + u], (kSlots == 2 ? i - 1 : 2 * i - 1) & 1);
+                    for (int u = 0; u < 2; ++u)
+                        if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -699,15 +703,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                 }
                 // its place is free when what was there has been multiplied
-                const int place = half % kSlots, use = kSlots == 2 ? i : 2 * i + half;
-                if (use > 0 && !(ok = all_wait(&p_empty[2 * m + place], (use - 1) & 1))) break;
+                if (!kInPlace && i > 0 && !(ok = all_wait(&p_empty[2 * m + half], (i - 1) & 1))) break;
                 tc_fence_after();
-                tmem_store(p_at + place * (kHalf / 2), hi);
-                if (kPParts == 2) tmem_store(p_at + kHalf / 2, lo);
+                tmem_store(p_at + half * (C::kPCols / 2), hi);
+                if (kPParts == 2) tmem_store(p_at + half * (C::kPCols / 2) + kHalf / 2, lo);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * m + place]);
+                if (lane == 0) mbar_arrive(&p_full[2 * m + half]);
             }
             if (!ok) break;
             if (lane == 0) mbar_arrive(&at_empty[slot]);
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 template <int D, int kQ, int kP, bool PREFIX>
 cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
-    using C = TileCfg<D, kQ>;
+    using C = TileCfg<D, kQ, kP>;
     static bool set[64] = {false};  // this kernel's shared memory, on each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
