@@ -374,8 +374,8 @@ bsg_status bsg_wgroups_matvec(const void *X, bsg_dtype dtype, int64_t ldx, const
  * type, not X's memory.  The same bits on every run and for any M: a token's row of Y
  * does not depend on the others'.  Inf or NaN in X sets BSG_DSTATUS_NONFINITE (that row of Y
  * is then unspecified).  M, N < 2^31, M N <= 2^40; K <= BSG_MAX_K.  `workspace`:
- * bsg_wcols_matmul_workspace_size(M, N, K) bytes, 256-byte aligned (0 for sizes that the
- * call refuses).  Fastest with Q 16-byte aligned and ldq a multiple of 16. */
+ * bsg_wcols_matmul_workspace_size(M, N, K) bytes, 256-byte aligned (small products need none:
+ * 0, and any pointer; 0 too for sizes that the call refuses).  Fastest with Q 16-byte aligned and ldq a multiple of 16. */
 size_t bsg_wcols_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 bsg_status bsg_wcols_matmul(const void *X, bsg_dtype dtype, int64_t ldx, const int8_t *Q,
                             int64_t ldq, const float *scale, int64_t M, int64_t N, int64_t K,

@@ -251,8 +251,9 @@ def wcols_matmul(X, Q, scale, relu: bool = False, out=None, dstatus=None, stream
     Y = _output(out, X, (M, N), stream)
     if Y.data_ptr() == X.data_ptr():
         raise ValueError("out must not share X's memory")
+    need = _matmul_bytes(M, N, K)
     on = _stream(stream, dev)
-    wp, wn = _workspace(workspace, _matmul_bytes(M, N, K), dev, stream, on)
+    wp, wn = _workspace(workspace, need, dev, stream, on) if need else (None, 0)
     _bsg._check(_lib().bsg_wcols_matmul(
         X.data_ptr(), code, _rows(X, "X"), Q.data_ptr(), _rows(Q, "Q"), sp, M, N, K, bool(relu), Y.data_ptr(),
         _rows(Y, "out"), wp, wn, _status(dstatus, dev), on), "bsg_wcols_matmul")
