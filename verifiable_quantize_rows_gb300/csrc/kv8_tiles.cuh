@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
-    const int64_t group = blockIdx.x % a.groups;
-    const int hk = (int)(group % a.c.heads), b = (int)(group / a.c.heads), split = blockIdx.y;
+    const unsigned block = blockIdx.x / (unsigned)a.groups, group = blockIdx.x - block * (unsigned)a.groups;
+    const int b = (int)(group / (unsigned)a.c.heads), hk = (int)(group - (unsigned)b * a.c.heads), split = blockIdx.y;
     const int share = a.heads / a.c.heads, P = a.c.page_tokens;
     // later rows see more: they go first
-    const int r0 = (a.row_blocks - 1 - (int)(blockIdx.x / a.groups)) * (kM * 128);
+    const int r0 = (a.row_blocks - 1 - (int)block) * (kM * 128);
     const int64_t most = a.table_ld * P;
 
     // The rows that are there, and what they see.
@@ -201,29 +201,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int groups = rows > 128 ? kM : 1;  // of 128 rows
     auto position = [&](int i) { return seen.tile(begin + i) * kN; };  // of the CTA's tile i
 
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&kv_full[s], 4);
-            mbar_init(&kv_empty[s], groups);  // the MMAs' warps
-        }
-        for (int s = 0; s < kAtSlots; ++s) {
-            mbar_init(&at_full[s], 1);
-            mbar_init(&at_empty[s], 4 + 4 * groups);  // the warps that read a slot
-        }
-        for (int m = 0; m < kM; ++m) {
-            mbar_init(&s_full[m], 1);
-            mbar_init(&s_empty[m], 4);
-            mbar_init(&o_full[m], 1);
-            mbar_init(&q_full[m], 4);
-            for (int u = 0; u < 2; ++u) {
-                mbar_init(&p_full[2 * m + u], 4);
-                mbar_init(&p_empty[2 * m + u], 1);
-            }
-        }
-
-        *abort_flag = 0;
+    if (tid < C::kBars) {
+        int count = 4;                                             // kv_full, s_empty, p_full, q_full: the warps of a role
+        if (bars + tid >= kv_empty) count = groups;                // the MMAs' warps
+        if (bars + tid >= at_full) count = 1;
+        if (bars + tid >= at_empty) count = 4 + 4 * groups;        // the warps that read a slot
+        if (bars + tid >= s_empty) count = 4;
+        if (bars + tid >= s_full) count = 1;                       // and o_full: commits
+        if (bars + tid >= p_full) count = 4;
+        if (bars + tid >= p_empty) count = 1;
+        if (bars + tid >= q_full) count = 4;
+        mbar_init(bars + tid, count);
         fence_mbar_init();
     }
+    if (tid == 0) *abort_flag = 0;
     constexpr int kMmaWarp = 12;
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_ptr, 512);
@@ -540,15 +531,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 bool bad = false;
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    float x = 0.0f, y[kE];
+                    // the row's largest |q|: bits order as magnitudes do, Inf and NaN above all
+                    float x, y[kE];
+                    const uint32_t *bits = reinterpret_cast<const uint32_t *>(&q[i]);
+                    if constexpr (sizeof(T) == 2) {
+                        uint32_t most = __vmaxu2(__vmaxu2(bits[0] & 0x7fff7fffu, bits[1] & 0x7fff7fffu),
+                                                 __vmaxu2(bits[2] & 0x7fff7fffu, bits[3] & 0x7fff7fffu));
+                        most = max(most >> 16, most & 0xffffu);
 #pragma unroll
-                    for (int j = 0; j < kE; ++j) {
-                        y[j] = to_f32(q[i].v[j]);
-                        bad |= !isfinite(y[j]);
-                        x = fmaxf(x, fabsf(y[j]));
+                        for (int o = kL / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        const uint16_t h = (uint16_t)most;
+                        x = to_f32(*reinterpret_cast<const T *>(&h));
+                    } else {
+                        uint32_t most = max(max(bits[0] & 0x7fffffffu, bits[1] & 0x7fffffffu),
+                                            max(bits[2] & 0x7fffffffu, bits[3] & 0x7fffffffu));
+#pragma unroll
+                        for (int o = kL / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                        x = __uint_as_float(most);
                     }
+                    bad |= !isfinite(x);
 #pragma unroll
-                    for (int o = kL / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    for (int j = 0; j < kE; ++j) y[j] = to_f32(q[i].v[j]);
                     const int e = max(-126, min(126, 13 + 127 - (int)(__float_as_uint(x) >> 23)));
                     const float up = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), a.scale);
                     const float its = fabsf(a.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - e) << 23);
