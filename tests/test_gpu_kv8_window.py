@@ -97,6 +97,17 @@ def test_rows_that_see_nothing(T, dtype):
     check(q, cache, table, lens, None, 0, 0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,B", [(2, 1), (3, 70), (8, 40), (16, 150), (150, 3)])
+def test_windows_that_begin_behind_a_tile_another_row_sees(T, B, dtype):
+    """The rows of a CTA begin to see at different tiles, in whatever order they come: few chunks
+    and many (by the batch's size), windows that begin at the ends of tiles, sinks and none."""
+    for window, sinks in ((150, 0), (145, 3), (209, 17), (16 * T // 2 + 1, 0)):
+        lens = [T + 16 * i % 256 + 160 for i in range(B)]
+        q, cache, table = case(B, T, 2, 1, 32, 16, lens, dtype, window)
+        check(q, cache, table, lens, None, window, sinks)
+
+
 @pytest.mark.parametrize("T", [1, 5, 64, 300])
 def test_a_window_of_one_gives_the_newest_value(T):
     """Exactly: code x scale, rounded; whatever the scores are."""

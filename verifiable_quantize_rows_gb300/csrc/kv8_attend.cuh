@@ -475,8 +475,13 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
     const int all_low = a.window && last_pos >= a.window ? last_pos - a.window + 1 : 0;
 
     // Rows that have seen nothing yet (bit 2n + u; their ref is 0): only before
-    // the warp's first tile, or where that is one some row may not see.
-    uint32_t none = 0xffffffffu;
+    // the warp's first tile, or where that is one some row may not see (kWindow: or some tiles on).
+    uint32_t none = 0xffffffffu, live = 0;  // live: rows that see something at all
+    if (kMode == kWindow)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; u += kParts) live |= see[n][u] > 0 ? 1u << (2 * n + u) : 0u;
     bool fresh = true;
     for (int tile = tile0 + warp; tile < tiles; tile += kWarps) {
         copies_wait<kStages - 1>();
@@ -532,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
         };
         exponents();
         if (__any_sync(0xffffffffu, most > kMost || fresh || edge)) {
-            fresh = false;
+            if (kMode != kWindow) fresh = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float keep[2];
@@ -558,6 +563,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
 #pragma unroll
                     for (int u = 0; u < 4; ++u) acc[n][i][u] *= keep[u % 2];
             }
+            // a row whose window begins after this tile sees its first one later
+            if (kMode == kWindow) fresh = __any_sync(0xffffffffu, (none & live) != 0);
             exponents();
         }
         // Probabilities, as the B operand of the second product.

@@ -25,6 +25,12 @@ KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_
     if (few) {
         const AttendPlan a = attend_plan_of(c, (positions + 15) / 16, B, rows, dtype == BSG_F32 ? 2 : 1);
         p.splits = a.splits, p.nt = a.nt, p.row_tiles = a.row_tiles, p.width = a.width;
+        // Where chunks fill the card, 256 positions at least to each, four tiles to each of its warps:
+        // smaller ones leave little but their start and their part of the join (64 sequences of up to
+        // 511 own tokens behind a prefix: 66 -> 60 us for all).
+        const int64_t fill = (5 * (int64_t)device_sm_count() + groups - 1) / groups, most = (positions + 255) / 256;
+        const int64_t cap = fill > most ? fill : most;
+        if (p.splits > cap) p.splits = (int)cap;
     } else {
         // as many chunks as fill the card once, of two tiles at least
         const int64_t block = c.dim == 256 ? 128 : 256, tile = c.dim == 256 ? 64 : 128;

@@ -30,6 +30,7 @@ struct JoinArgs {
 };
 
 constexpr int kJoinThreads = 128;
+constexpr int kMaxChunks = 2048;  // of both lists: no plan has more than 1024 to a list
 
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
@@ -60,35 +61,46 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __gr
     auto at = [&](int i) {  // chunk i: its list's place
         return i < a.splits[0] ? row[0] * a.splits[0] + i : row[1] * a.splits[1] + i - a.splits[0];
     };
-    float m = -3.0e38f;
-    for (int i = tid % 32; i < n; i += 32) {
-        const float2 x = a.ml[i >= a.splits[0]][at(i)];
-        if (x.y != 0.0f) m = fmaxf(m, x.x);
-    }
+    // the chunks' weights first, a thread each, so that the outputs' loads wait for nothing
+    __shared__ float f_s[kMaxChunks], red[kJoinThreads / 32];
+    float m = -3.0e38f, l = 0.0f;
+    if (!idle)
+        for (int i = tid; i < n; i += kJoinThreads) {
+            const float2 x = a.ml[i >= a.splits[0]][at(i)];
+            if (x.y != 0.0f) m = fmaxf(m, x.x);
+        }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int col = tid % kCols, side = tid / kCols;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    if (side < kSides && !idle)
-        for (int i = side; i < n; i += kSides) {
-            const int list = i >= a.splits[0];
-            const float2 x = a.ml[list][at(i)];
-            if (x.y == 0.0f) continue;
-            const float f = exp2_of(x.x - m);
-            const float4 v = *reinterpret_cast<const float4 *>(a.o[list] + at(i) * D + 4 * col);
-            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-            l = fmaf(x.y, f, l);
-        }
-    __shared__ float l_s[kSides];
-    if (side < kSides) {
-        o_s[side][col] = o;
-        if (col == 0) l_s[side] = l;
+    if (tid % 32 == 0) red[tid / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[i]);
+    __syncthreads();
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const float2 x = a.ml[i >= a.splits[0]][at(i)];
+        const float f = x.y == 0.0f || idle ? 0.0f : exp2_of(x.x - m);
+        f_s[i] = f;
+        if (f != 0.0f) l = fmaf(x.y, f, l);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (tid % 32 == 0) red[tid / 32] = l;
     __syncthreads();
     l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSides; ++i) l += l_s[i];
+    for (int i = 0; i < kJoinThreads / 32; ++i) l += red[i];
+    const int col = tid % kCols, side = tid / kCols;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (side < kSides)
+#pragma unroll 4
+        for (int i = side; i < n; i += kSides) {
+            const float f = f_s[i];
+            if (f == 0.0f) continue;  // what a chunk that saw nothing left is no output
+            const float4 v = *reinterpret_cast<const float4 *>(a.o[i >= a.splits[0]] + at(i) * D + 4 * col);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        }
+    if (side < kSides) o_s[side][col] = o;
+    __syncthreads();
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     T *out = static_cast<T *>(a.out.data) + b * a.out.stride_batch + t * a.out.stride_token + h * a.out.stride_head;
