@@ -39,8 +39,8 @@ def softmax_attend(q, k, v, see, scale, parts):
     tol, what float32 scores and sums may be off: scores by 2^-20 of sum |q k| for the
     products and their float32 sums and 2^-21 of max|q| sum |k| for q's parts, exp's
     argument by 2^-21 |s - max|, sums by 2^-20; and, where probabilities are one f16
-    part (parts = 1), each by 2^-11 of itself or 2^-25 of what is at least 2^-12 of the
-    largest kept (2^-36 of the largest is left out in any case).  lse_tol: the mean of the
+    part (parts = 1), each by 2^-11 of itself.  f16 ends in steps of 2^-24, and a row's
+    largest probability is kept as 2^9 or more: half a step, 2^-25, is 2^-34 of it.  lse_tol: the mean of the
     scores' errors, 2^-20 of the sum and of lse itself."""
     R, D = q.shape
     out, tol, lse, lse_tol = np.zeros((R, D)), np.zeros((R, D)), np.full(R, -np.inf), np.zeros(R)
@@ -57,7 +57,7 @@ def softmax_attend(q, k, v, see, scale, parts):
     ds = abs(scale) * (2.0 ** -20 * (np.abs(q) @ np.abs(k).T)
                        + 2.0 ** -21 * np.abs(q).max(1, keepdims=True) * np.abs(k).sum(1)[None])
     ds = np.where(see, ds + 2.0 ** -21 * np.minimum(np.abs(np.where(see, s, 0) - m), 100), 0)
-    w = p * (ds + (p * ds).sum(1, keepdims=True) + 2.0 ** -20 + (2.0 ** -11 if parts == 1 else 0)) + np.where(see, 2.0 ** -36, 0) / l
+    w = p * (ds + (p * ds).sum(1, keepdims=True) + 2.0 ** -20 + (2.0 ** -11 if parts == 1 else 0)) + np.where(see, 2.0 ** -34, 0) / l
     out[some], lse[some] = p @ v, (m + np.log(l))[:, 0]
     tol[some] = w @ np.abs(v)
     lse_tol[some] = (p * ds).sum(1) + 2.0 ** -20 * (2 + np.abs(lse[some]))

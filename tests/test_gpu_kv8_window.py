@@ -269,6 +269,29 @@ def test_long_lengths():
     assert float((y[0].double() - want).abs().max()) < 1e-4 * want
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", [0, 1])
+def test_f32_sums_do_not_drift(D, gap):
+    """Equal scores and values of one sign, where what a sum of f32 loses adds up.  Tensor cores
+    lose less than 2^-23 of a sum with each product of 16 positions, two products to each (the
+    probability's parts), and a sum of theirs takes 640 positions at most: 80 times 2^-23.  The
+    rest: 16384 / 512 sums of those by 2^-24 each, and 2^-20 for what a score and a probability of
+    22 bits are off.  (The scales are powers of two: the sum of the probabilities is exact.)"""
+    B, T, Hk, n, page = 40, 64, 4, 16384, 64
+    rng = np.random.default_rng(D)
+    codes = [np.ones((n // page, Hk, page, D), np.int8), rng.integers(90, 128, (n // page, Hk, page, D)).astype(np.int8)]
+    cache = codes + [np.full((n // page, Hk), 2.0 ** -7, np.float32)] * 2
+    given = bsg.Kv8Cache(*map(dev, cache))
+    table = dev(np.tile(np.arange(n // page, dtype=np.int32), (B, 1)))   # all sequences' positions are the same ones
+    q = torch.zeros(B, T, Hk, D, device="cuda")
+    out = torch.full((B, T, Hk, D + gap), KEPT, device="cuda")[..., :D]
+    bsg.kv8_attend_window(q, given, table, dev(np.full(B, n, np.int32)), out=out)
+    v = codes[1].astype(np.float64).transpose(1, 0, 2, 3).reshape(Hk, n, D) * 2.0 ** -7
+    sums = np.cumsum(v, 1)[:, n - T:] / np.arange(n - T + 1, n + 1)[:, None]
+    want = np.broadcast_to(sums.transpose(1, 0, 2)[None], q.shape)
+    within(f64(out), want, np.abs(want) * (80 * 2.0 ** -23 + 32 * 2.0 ** -24 + 2.0 ** -20), "out")
+
+
 def test_graph_and_streams():
     """Captured, replayed at other lengths; calls on several streams at once."""
     for T in (1, 6, 130):

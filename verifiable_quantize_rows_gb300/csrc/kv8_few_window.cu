@@ -37,6 +37,13 @@ KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_
         p.row_blocks = (int)((rows + block - 1) / block);
         int64_t splits = device_sm_count() / (p.row_blocks * groups);
         if (splits > (positions + tile - 1) / tile / 2) splits = (positions + tile - 1) / tile / 2;
+        // The tensor cores cut off what they add to O, always towards 0: 2^-25.7 of it measured for
+        // each MMA of 16 positions, two of them where P has two parts.  f32's O is begun anew in time;
+        // chunks of f16 and bf16 stay so short that they lose less than the type's own rounding
+        // (2^-12.7 and 2^-10.7), and their join adds in f32.
+        const int64_t most = dtype == BSG_F16 ? 65536 : 524288;
+        const int64_t least = dtype == BSG_F32 ? 1 : (positions + most - 1) / most;
+        if (splits < least) splits = least < 1024 ? least : 1024;
         p.splits = (int)(splits < 1 ? 1 : splits);
     }
     p.parts = p.splits > 1 || later ? (size_t)groups * rows * p.splits : 0;

@@ -5,7 +5,7 @@
 // times tokens) and walks the tiles of kN positions that some of them see:
 //   S = Q K^T          128 x kN, in tensor memory, one place that the groups of 128 rows use in turn
 //   p' = 2^(S ks mul + log2 vs - ref)   a thread to a row, in f16, half a tile at a time
-//   O += P V           P read from tensor memory, O stays there
+//   O += P V           P (f32, f16: two f16 parts, 22 bits; bf16: one) read from tensor memory, O stays there
 // with ks, vs the page's scales (one for each 16 positions of a tile), mul the row's
 // multiplier, ref the row's running reference, which follows the maximum only when that is
 // above 2^15 (what f16 holds) and makes it 2^9 then: O is rescaled where it lies, a few times
@@ -114,6 +114,16 @@ struct TileCfg {
     static constexpr int kP0 = kInPlace ? 0 : kN, kPStep = kInPlace ? kN : kPCols;
     static constexpr int kO0 = kInPlace ? kM * kN : kN + kM * kPCols;
     static_assert(kO0 + kM * D <= 512 && kPCols <= kN, "tensor memory");
+    // What the tensor cores add to an f32 sum is cut off below its last bit, not rounded: some 2^-25
+    // of O is lost with each 16 positions, always towards 0.  f32's O is therefore added (rounded)
+    // to a sum in memory every 512 positions and begun anew, but for the last 640; 16-bit outputs do
+    // not show it.  (64 rows behind 131072 positions in 19 chunks: 1.6e-5 off 64 bits without, 2.4e-6
+    // by 1024 positions, 1.4e-6 by 512.  Prompts of some 400 seen positions, which stay without: 47 us,
+    // 59 with one such sum.)
+    static constexpr int kFlush = kQParts == 2 ? 512 / kN : 0;  // tiles
+    static __device__ bool flush_at(int i, int tiles) {
+        return kFlush > 0 && i > 0 && i % (kFlush ? kFlush : 1) == 0 && tiles - i > kFlush / 4;
+    }
 };
 
 constexpr int kTileThreads = 512;
@@ -286,11 +296,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     const uint64_t kd = k_desc + k_stage * (C::kStageBytes / 16);
                     if (one) {
 #pragma unroll
-                        for (int part = 0; part < kQParts; ++part)
+                        for (int part = kQParts - 1; part >= 0; --part)  // the small part first: sums are cut to 24 bits
 #pragma unroll
                             for (int j = 0; j < D / 16; ++j)
                                 mma_f16_ss(s_at, q_desc + part * (C::kQBytes / 16) + j / 4 * 1024 + 2 * (j % 4),
-                                           kd + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part + j > 0);
+                                           kd + j / 4 * (kN * 8) + 2 * (j % 4), kIdescS, part < kQParts - 1 || j > 0);
                         mma_commit(&s_full[m]);
                         mma_commit(&kv_empty[k_stage]);
                     }
@@ -311,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                             for (int part = 0; part < kPParts; ++part)
                                 mma_f16_ts(o_at, p_at + part * (kHalf / 2) + 8 * j, vd + j * 128, kIdescO,
-                                           j + part > 0 ? 1 : half + i > 0);
+                                           j + part > 0 ? 1 : half > 0 || (i > 0 && !C::flush_at(i, n)));
                         if (!kInPlace) mma_commit(&p_empty[2 * m + half]);
                     }
                 }
@@ -602,6 +612,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[m]);
         float ref = 0.0f, sum = 0.0f;
         bool none = true, ok = true;
+        // f32: the sum of what O was before it was begun anew, in the output's place, relative to acc_ref
+        auto acc_place = [&]() {
+            return PREFIX || a.splits > 1 || a.later
+                       ? a.part_o + ((((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + split) * D
+                       : static_cast<float *>(a.out.data) + b * a.out.stride_batch + (r0 + r) / share * a.out.stride_token +
+                             (hk * share + (r0 + r) % share) * a.out.stride_head;
+        };
+        float acc_ref = 0.0f;
+        bool acc_some = false;
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
             const int tile = position(i), slot = i % kAtSlots;
@@ -609,6 +628,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
             tc_fence_after();
             const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
+            if (C::flush_at(i, tiles)) {
+                // O is at rest once the last P of the tile before is used up (in place: as S is there)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float f = acc_some ? tile_exp2(acc_ref - ref) : 0.0f;
+                float *const acc = acc_place();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tmem_ld16(o_at + 16 * c, o);
+                    tmem_ld_wait();
+                    if (r >= rows) continue;
+                    if (reinterpret_cast<uintptr_t>(acc) % 16 == 0) {
+                        float4 *const at = reinterpret_cast<float4 *>(acc + 16 * c), none4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        float4 before[4] = {none4, none4, none4, none4};
+                        if (f > 0.0f)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) before[u] = at[u];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            at[u] = make_float4(fmaf(before[u].x, f, __uint_as_float(o[4 * u])),
+                                                fmaf(before[u].y, f, __uint_as_float(o[4 * u + 1])),
+                                                fmaf(before[u].z, f, __uint_as_float(o[4 * u + 2])),
+                                                fmaf(before[u].w, f, __uint_as_float(o[4 * u + 3])));
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < 16; ++u) {
+                            uint32_t now = o[0];
+#pragma unroll
+                            for (int w = 1; w < 16; ++w)
+                                if (w == u) now = o[w];
+                            acc[16 * c + u] = fmaf(f > 0.0f ? acc[16 * c + u] : 0.0f, f, __uint_as_float(now));
+                        }
+                    }
+                }
+                acc_ref = ref, acc_some = !none;
+            }
             if (edge) {  // what the row does not see, where S lies (seldom; rolled up)
 #pragma unroll 1
                 for (int c = 0; c < kN / 16; ++c) {
@@ -725,11 +785,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // ---- the row's outputs
         const int64_t n = (r0 + r) / share;
         const int head = hk * share + (r0 + r) % share;
-        const bool there = r < rows && ok;
         const bool direct = !PREFIX && a.splits == 1 && !a.later;
         const int64_t part = (((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + split;
+        const bool there = r < rows && ok;
         const bool some = sum > 0.0f || sum != sum;
         const float inv = some ? __frcp_rn(sum) : 0.0f;
+        const float of_acc = acc_some ? tile_exp2(acc_ref - ref) : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -742,6 +803,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float o[32];
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] = tiles == 0 || (!some && direct) ? 0.0f : __uint_as_float(v[u]);
+            if (kQParts == 2 && of_acc > 0.0f) {
+                const float *const acc = acc_place() + 32 * c;
+                if (reinterpret_cast<uintptr_t>(acc) % 16 == 0) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const float4 x = reinterpret_cast<const float4 *>(acc)[u];
+                        o[4 * u] = fmaf(x.x, of_acc, o[4 * u]);
+                        o[4 * u + 1] = fmaf(x.y, of_acc, o[4 * u + 1]);
+                        o[4 * u + 2] = fmaf(x.z, of_acc, o[4 * u + 2]);
+                        o[4 * u + 3] = fmaf(x.w, of_acc, o[4 * u + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) o[u] = fmaf(acc[u], of_acc, o[u]);
+                }
+            }
             if (direct) {
                 auto store = [&](auto type) {
                     using T = decltype(type);
