@@ -457,7 +457,7 @@ bsg_status bsg_kv8_attend(const bsg_kv8_cache *cache, const int32_t *table, int6
  * The rest is as for bsg_kv8_attend: a query that sees no position gives 0 and lse -inf;
  * scores and sums are f32, f32 queries keep 22 bits of their row's largest, and
  * probabilities keep 22 bits of themselves or 2^-34 of the largest; those of bf16 keep 11
- * bits where a key/value head has more than 32 query rows (tokens times its heads).  Tokens t >= counts[b] are not read, and
+ * bits where a key/value head has more than 16 query rows (tokens times its heads).  Tokens t >= counts[b] are not read, and
  * nothing is written for them.  A count that is not in 0..T leaves its sequence out and sets
  * BSG_DSTATUS_RANGE; lengths and pages out of range as for bsg_kv8_attend (of pages that some
  * query sees).  T * (heads / cache->heads) < 2^31.  window, sinks >= 0.
@@ -479,7 +479,7 @@ bsg_status bsg_kv8_attend_window(const bsg_kv8_cache *cache, const int32_t *tabl
  * none: it sees nothing, not the prefix either (a slot of length 0 is idle).  A prefix
  * length out of range is cut to the pages' and sets BSG_DSTATUS_RANGE.  The rest is as
  * for bsg_kv8_attend, but that bf16's probabilities of the prefix keep 11 bits where a
- * key/value head has more than 32 query rows in all sequences together, and those of the
+ * key/value head has more than 16 query rows in all sequences together, and those of the
  * own tokens where a sequence has.  `workspace`: bsg_kv8_attend_shared_workspace_size bytes. */
 size_t bsg_kv8_attend_shared_workspace_size(const bsg_kv8_cache *cache, int64_t prefix_pages,
                                             int64_t table_ld, int64_t B, int64_t T, int heads);

@@ -146,10 +146,14 @@ cudaError_t launch_join(const JoinArgs &a, int dim, int dtype, cudaStream_t st) 
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Which kernel a call takes: up to kFewSlots query rows (f32's twice) of a key/value head the one
-// of few rows, whose 8 slots a tile read the cache at its rate; beyond, 128 rows a tile.
-constexpr int kFewSlots = 32;
-bool few(int64_t rows, int dtype) { return rows * (dtype == BSG_F32 ? 2 : 1) <= kFewSlots; }
+// Which kernel a call takes: up to this many query rows of a key/value head the one of few rows,
+// which reads the cache at its rate by 16 rows of 16 bits (or 8 of f32) and again for as many more;
+// beyond, 128 rows a tile.  Both in us, few rows then tiles, by 8 heads of 128 dims:
+//                                       16 rows           20 rows    |  f32 32 rows      48 rows
+//   16 sequences of 16384, bf16 (f16)   132, 208 (266)    233, 208   |  274, 480         390, 477
+//   16 of 2048                          36, 32 (40)       61, 32     |  64, 64           86, 65
+//   one of 16384                        29, 23 (27)       46, 23     |  46, 37           55, 37
+bool few(int64_t rows, int dtype) { return rows <= (dtype == BSG_F32 ? 32 : 16); }
 
 // The workspace of one part of a call, largest over the types.
 size_t part_floats(const bsg_kv8_cache &c, int64_t rows, int64_t B, int64_t positions, bool later) {

@@ -637,34 +637,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_after();
                 const float f = acc_some ? tile_exp2(acc_ref - ref) : 0.0f;
                 float *const acc = acc_place();
+                const bool wide = reinterpret_cast<uintptr_t>(acc) % 16 == 0;
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t o[16];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    alignas(16) float before[32];
                     __syncwarp();
-                    tmem_ld16(o_at + 16 * c, o);
-                    tmem_ld_wait();
-                    if (r >= rows) continue;
-                    if (reinterpret_cast<uintptr_t>(acc) % 16 == 0) {
-                        float4 *const at = reinterpret_cast<float4 *>(acc + 16 * c), none4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        float4 before[4] = {none4, none4, none4, none4};
-                        if (f > 0.0f)
+                    tmem_ld32(o_at + 32 * c, o);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) before[u] = at[u];
+                    for (int u = 0; u < 32; ++u) before[u] = 0.0f;
+                    if (r < rows && f > 0.0f) {
+                        if (wide) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            at[u] = make_float4(fmaf(before[u].x, f, __uint_as_float(o[4 * u])),
-                                                fmaf(before[u].y, f, __uint_as_float(o[4 * u + 1])),
-                                                fmaf(before[u].z, f, __uint_as_float(o[4 * u + 2])),
-                                                fmaf(before[u].w, f, __uint_as_float(o[4 * u + 3])));
-                    } else {
-#pragma unroll 1
-                        for (int u = 0; u < 16; ++u) {
-                            uint32_t now = o[0];
+                            for (int u = 0; u < 8; ++u)
+                                *reinterpret_cast<float4 *>(before + 4 * u) = reinterpret_cast<const float4 *>(acc + 32 * c)[u];
+                        } else {
 #pragma unroll
-                            for (int w = 1; w < 16; ++w)
-                                if (w == u) now = o[w];
-                            acc[16 * c + u] = fmaf(f > 0.0f ? acc[16 * c + u] : 0.0f, f, __uint_as_float(now));
+                            for (int u = 0; u < 32; ++u) before[u] = acc[32 * c + u];
                         }
+                    }
+                    __syncwarp();
+                    tmem_ld_wait32(o);
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) before[u] = fmaf(before[u], f, __uint_as_float(o[u]));
+                    if (r >= rows) continue;
+                    if (wide) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            reinterpret_cast<float4 *>(acc + 32 * c)[u] = *reinterpret_cast<const float4 *>(before + 4 * u);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) acc[32 * c + u] = before[u];
                     }
                 }
                 acc_ref = ref, acc_some = !none;
