@@ -64,6 +64,30 @@ def test_strides(M, dtype):
         assert bool((rest == 7).all())
 
 
+LONG = [(17, 1030, 300), (40, 700, 12289), (64, 769, 11000), (64, 1025, 129), (65, 2049, 129), (100, 2300, 1000), (128, 2304, 384),
+        (129, 4097, 200), (193, 2050, 1), (200, 2100, 700), (256, 8191, 272), (256, 2304, 768)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("M,K,N", LONG)
+def test_sizes_of_long_columns_and_wide_weights(M, K, N, dtype):
+    same(*inputs(M, K, N, dtype, M + K + N), relu=bool(N % 2))
+
+
+@pytest.mark.parametrize("M", [40, 150])
+def test_strides_of_long_columns(M):
+    K, N = 2100, 336
+    x, w, s = inputs(M, K, N, torch.bfloat16)
+    for shift in (0, 1, 8):
+        wide = torch.zeros((M, K + 16), dtype=torch.bfloat16, device="cuda")
+        wide[:, shift:shift + K] = x
+        rows = torch.full((K, N + 32), -128, dtype=torch.int8, device="cuda")
+        rows[:, shift:shift + N] = w
+        out = torch.full((M, N + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        same(wide[:, shift:shift + K], rows[:, shift:shift + N], s, out=out[:, shift:shift + N])
+        assert bool((torch.cat((out[:, :shift], out[:, shift + N:]), 1) == 7).all())
+
+
 @pytest.mark.parametrize("M", [1, 30, 200, 300])
 def test_long_sums_and_largest_codes(M):
     """The largest K, every product 127 x 127: the sums fill 31 bits."""

@@ -1104,7 +1104,7 @@ __global__ void i8_rows_to_half_kernel(const int8_t *__restrict__ Q, int64_t row
 // x 128 columns a CTA, transposed through shared memory.  A thread turns 8 rows x 4 columns of
 // codes into four pieces of 8 halves (two rows' bytes side by side, as f16 1024 + code + 128 less
 // 1152), whose places are permuted by their column so that neither side has bank conflicts.
-// Bound by the 3 bytes that a code moves (8192 x 8192: 34 us, 0.87 of the measured copy rate;
+// Bound by the 3 bytes that a code moves (8192 x 8192: 47 us, 0.63 of the measured copy rate;
 // element by element through a padded tile 80).
 __global__ void __launch_bounds__(256)
     i8_cols_to_half_kernel(const int8_t *__restrict__ Q, int64_t rows, int64_t cols, int64_t ldq,

@@ -126,7 +126,7 @@ cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __
                           int64_t zeros, int32_t *dstatus, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const bool aligned = (reinterpret_cast<uintptr_t>(X) | (uintptr_t)(ldx * (int64_t)sizeof(T))) % 16 == 0;
-    // many rows: as few threads as keep one (8192 rows of 768 bf16: 11 us by 128 threads, 7 by 32);
+    // many rows: as few threads as keep one (8192 rows of 768 bf16: 11 us by 128 threads, 8 by 32);
     // few: as many as make it quick
     if (M >= 512 && K <= 32 * kTokenKept)
         return aligned ? launch_tokens_as<T, VEC, 32>(X, ldx, M, K, ldk, op, scale, zero, zeros, dstatus, st)
@@ -143,9 +143,10 @@ cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __
 
 // ---- a few tokens: the weight's codes turned into operands on their way ---------
 //
-// kFewTokens tokens at a time (more: each block of them on its own, the codes then from L2).  D[column][token] += W^T X^T with the weight as the A operand, 128
-// columns as its rows: W lies k by k, columns side by side, which is A's "MN-major" form, so
-// codes become f16 where they are, without a transposition.  All k-blocks (128 x 128 codes) of
+// kFewTokens tokens at a time (more: each block of them on its own, the codes then from L2).
+// D[column][token] += W^T X^T with the weight as the A operand, 128 columns as its rows: W lies k
+// by k, columns side by side, which is A's "MN-major" form, so codes become f16 where they are,
+// without a transposition.  All k-blocks (128 x 128 codes) of
 // all column tiles form one list that the CTAs share in equal runs; a run ends a tile's sums
 // where it ends, and what is not a whole tile is added up in L2, in integers, so that the order
 // does not matter; the last to add writes Y.  Sums are exact: f32 sums of at most 1024
@@ -157,6 +158,12 @@ cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __
 // two of its blocks ahead) and turn them into operands; warp 24 issues the MMAs; warp 25
 // sends for the tokens (TMA).  Blocks are this deep because every wait of the MMAs' warp costs
 // some 100 clocks, its barrier complete or not.
+//
+// What bounds it: the tokens, which every CTA reads again from L2 for each of its blocks (as many
+// bytes as the codes), and the chain of waits of the MMAs' warp; HBM is at 0.35 and the tensor
+// cores at 0.13 of their rates.  61 tokens, 8191 x 12289 bf16 (odd rows: codes by 4 bytes) 53 us,
+// the floor's bytes 15; 8192 x 8192 (floor 10): 16 tokens 22, 64 tokens 29.  Measured and not kept: rings
+// of three and four blocks, two stages of operands, four teams of 64-deep blocks.
 constexpr int kFewTokens = 64;
 constexpr int kSumWarps = 8, kCodeWarps = 16;
 constexpr int kFewThreads = (kSumWarps + kCodeWarps + 2) * 32;
@@ -537,9 +544,19 @@ cudaError_t launch_few(const FewArgs &a, const CUtensorMap &map, cudaStream_t st
     return aligned ? launch_few_as<64, true>(a, map, st) : launch_few_as<64, false>(a, map, st);
 }
 
-// Where the weight is turned into an operand of its own (5 bytes moved for each code) rather than
-// on its way, for each 64 tokens again.
-constexpr int kFewMost = 256;
+// Where the weight's codes are turned into operands on their way, for each 64 tokens again, rather
+// than once into an operand in memory (5 bytes moved for each code) for the unit's GEMM: the
+// latter's chain of k-blocks is what short columns have little of.  Both in us, bf16:
+//   K x N         tokens: on the way, operand
+//   768 x 2304    16: 7.9, 10.2    32: 12.1, 10.2   128: 18.4, 12.6
+//   768 x 50304   16: 17, 51       64: 29, 49       256: 78, 52
+//   2048 x 8192   16: 14, 27       64: 20, 21       128: 23, 22      256: 32, 24
+//   4096 x 4096                    64: 21, 29       128: 23, 29      256: 30, 32
+//   8192 x 8192                    64: 29, 90                        256: 71, 96     320: 156, 100
+//   16384 x 4096                                    128: 43, 117     256: 71, 121
+bool few_form(int64_t M, int64_t N, int64_t K) {
+    return M <= 16 || (M <= 64 && (K > 1024 || N * K > 1 << 23)) || (M <= 256 && K > 2048);
+}
 
 // ---- a token or a few and a small weight: one launch ------------------------------
 //
@@ -672,7 +689,7 @@ Layout layout(int64_t M, int64_t N, int64_t K) {
     l.ldk = operand_ld(K);
     l.token_scale = up256((size_t)M * l.ldk * 2);
     l.zero = l.token_scale + up256((size_t)round_up(M, kBM) * 4);
-    if (M <= kFewMost) {
+    if (few_form(M, N, K)) {
         const size_t tiles = (size_t)(N + 127) / 128, blocks = (size_t)(M + kFewTokens - 1) / kFewTokens;
         l.counts = l.zero + blocks * tiles * few_rows(M) * 128 * 4;
         l.bytes = l.counts + up256(blocks * tiles * 4);
@@ -711,7 +728,7 @@ cudaError_t launch_wcols_matmul(const void *X, int dtype, int64_t ldx, const int
                              reinterpret_cast<uint4 *>(w + l.zero), l.zeros, dstatus, st);
     });
     if (e != cudaSuccess) return e;
-    if (M <= kFewMost) {
+    if (few_form(M, N, K)) {
         FewArgs a{Q, ldq, sa, scale, (int)M, few_rows(M), (int)N, (int)K, (int)((K + kDeep - 1) / kDeep), 0, relu, dtype,
                   Y, ldy, reinterpret_cast<unsigned long long *>(w + l.zero), reinterpret_cast<unsigned int *>(w + l.counts), dstatus};
         a.all = (N + 127) / 128 * a.blocks;
