@@ -292,6 +292,22 @@ def test_f32_sums_do_not_drift(D, gap):
     within(f64(out), want, np.abs(want) * (80 * 2.0 ** -23 + 32 * 2.0 ** -24 + 2.0 ** -20), "out")
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+def test_tables_far_wider_than_what_they_hold(dtype):
+    """Room for 8 chunks of 65536 positions (bf16: one of 524288) in each of 80 sequences: some hold two of
+    them, most less than a tile, one nothing."""
+    B, T, page, width = 80, 17, 1024, 512
+    lens = [0, 17, 70000, 65536, 131073] + [100 + 3 * b for b in range(B - 5)]
+    rng = np.random.default_rng(5)
+    cache = pool(160, 1, page, 32, 5)
+    table = np.full((B, width), -1, np.int32)
+    for b, n in enumerate(lens):
+        table[b, : -(-n // page)] = rng.permutation(160)[: -(-n // page)]
+    q = dev(rng.standard_normal((B, T, 1, 32)).astype(np.float32)).to(dtype)
+    check(q, cache, table, lens)
+    check(q, cache, table, lens, counts=[T if b % 3 else b % T for b in range(B)])
+
+
 def test_graph_and_streams():
     """Captured, replayed at other lengths; calls on several streams at once."""
     for T in (1, 6, 130):

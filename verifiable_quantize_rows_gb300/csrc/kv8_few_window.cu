@@ -41,10 +41,11 @@ KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_
         // each MMA of 16 positions, two of them where P has two parts.  f32's O is begun anew in time;
         // chunks of f16 and bf16 stay so short that they lose less than the type's own rounding
         // (2^-12.7 and 2^-10.7), and their join adds in f32.
-        const int64_t most = dtype == BSG_F16 ? 65536 : 524288;
-        const int64_t least = dtype == BSG_F32 ? 1 : (positions + most - 1) / most;
-        if (splits < least) splits = least < 1024 ? least : 1024;
-        p.splits = (int)(splits < 1 ? 1 : splits);
+        const int64_t most = dtype == BSG_F32 ? INT32_MAX / 2 : dtype == BSG_F16 ? 65536 : 524288;
+        const int64_t least = (positions + most - 1) / most;
+        p.fill = (int)(splits < 1 ? 1 : splits);
+        p.chunk_most = (int)(most / tile);
+        p.splits = (int)(splits >= least ? p.fill : least < 1024 ? least : 1024);
     }
     p.parts = p.splits > 1 || later ? (size_t)groups * rows * p.splits : 0;
     return p;

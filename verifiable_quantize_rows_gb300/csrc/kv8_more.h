@@ -30,7 +30,7 @@ struct KvCall {
 struct KvPlan {
     int splits;
     size_t parts;
-    int row_blocks;      // of the tiles' kernel
+    int row_blocks, fill, chunk_most;  // of the tiles' kernel (TileArgs)
     int nt, row_tiles, width;  // of the kernel of few rows
 };
 KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_t B, int64_t positions, bool later);

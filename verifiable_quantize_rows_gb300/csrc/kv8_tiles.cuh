@@ -44,7 +44,8 @@ struct TileArgs {
     int tokens, heads, window, sinks;
     int rows, row_blocks;      // of a key/value head (and sequence); CTAs that they take
     int64_t groups;            // key/value heads (of all sequences)
-    int splits, later;         // chunks of a CTA's tiles; 1: what is found is joined later
+    int splits, later;         // chunks of a CTA's tiles, at most; 1: what is found is joined later
+    int fill, chunk_most;      // chunks of few tiles; beyond them, as many as leave no more tiles to each
     float scale;
     float *lse;
     float *part_o;             // [sequence][head][row][split][D]: outputs before the division by the sum,
@@ -206,8 +207,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int pos0 = PREFIX ? 0 : len - count;  // token 0's position
     const Seen seen = PREFIX ? seen_by<kN>(0, len - 1, 0, 0)
                              : seen_by<kN>(pos0 + r0 / share, pos0 + (r0 + rows - 1) / share, a.window, a.sinks);
-    const int begin = (int)((int64_t)seen.tiles * split / a.splits);
-    const int tiles = (int)((int64_t)seen.tiles * (split + 1) / a.splits) - begin;
+    const int chunks = min(a.splits, max(a.fill, (seen.tiles + a.chunk_most - 1) / a.chunk_most));
+    const int begin = (int)((int64_t)seen.tiles * min(split, chunks) / chunks);
+    const int tiles = (int)((int64_t)seen.tiles * min(split + 1, chunks) / chunks) - begin;
+    if (tiles == 0 && split > 0) {  // the join reads no output of such a chunk
+        if (tid < rows)
+            a.part_ml[(((int64_t)b * a.c.heads + hk) * a.rows + r0 + tid) * a.splits + split] = make_float2(0.0f, 0.0f);
+        if (PREFIX) griddep_wait();
+        return;
+    }
     const int groups = rows > 128 ? kM : 1;  // of 128 rows
     auto position = [&](int i) { return seen.tile(begin + i) * kN; };  // of the CTA's tile i
 
@@ -906,7 +914,7 @@ cudaError_t launch_tiles_dim(const TileArgs &a, int dtype, cudaStream_t st) {
 template <bool PREFIX>
 cudaError_t launch_tiles(const KvCall &k, const KvPlan &p, cudaStream_t st) {
     const TileArgs a{k.c, k.table, k.table_ld, k.lens, k.counts, k.q, k.out, k.tokens, k.heads, k.window, k.sinks,
-                     (int)k.rows, p.row_blocks, k.B * k.c.heads, p.splits, k.later, k.scale, k.lse, k.part_o, k.part_ml,
+                     (int)k.rows, p.row_blocks, k.B * k.c.heads, p.splits, k.later, p.fill, p.chunk_most, k.scale, k.lse, k.part_o, k.part_ml,
                      k.dstatus};
     switch (k.c.dim) {
         case 32: return launch_tiles_dim<32, PREFIX>(a, k.dtype, st);
