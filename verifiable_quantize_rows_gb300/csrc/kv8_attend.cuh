@@ -69,6 +69,7 @@ namespace {
 // 12 heads of 64 6.4 us.  What bounds it: HBM with few rows; with 16 and more the tensor
 // cores beside the unpacking (probabilities in one part, whose outputs were not good to
 // their last bit: 146 us, and 92 with one query token); the short ones their two launches.
+// Through windows of 4096, 64 sequences of one token (407 MB) 96 us, 0.80.
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;

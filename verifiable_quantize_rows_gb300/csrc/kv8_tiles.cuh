@@ -21,6 +21,20 @@
 //   12, 14     issue the MMAs of a group of rows each: S of a tile as soon as the one before
 //              it has been read into registers, P V of each half tile as it comes;
 //   13         finds where the tiles' pages lie, and their scales, some tiles at a time.
+//
+// What bounds it: the chain of a tile (S, its way into registers, maximum, exponentials, P, O) that
+// the two groups of rows take in turn; no one pipe (a prompt of 4096 through a window of 2048:
+// tensor 0.39 of the active cycles, ALU 0.40, XU 0.20).  Two prompts of up to 16384, window 4096,
+// 32/8 heads of 128, bf16: 1.54 ms, 0.56 of the products' floor; 64 rows behind 131071 shared
+// positions, 8 heads of 128, f16 (two parts of P): 167 us of the call's 185, tensor 0.55; ragged
+// prompts of up to 1021, 5 heads of 64, f32: 47 us, three rounds of CTAs of five tiles, whose start
+// and end take some 10 of each 16 us.
+// Why so: S in registers and a split of these by role 3.6 -> 2.06 ms (S read from tensor memory
+// in pieces spilled or came twice); MMAs issued by a converged warp, descriptors in uniform
+// registers 1.91; P apart from S, so that the next S does not wait for P V, by halves, so that P V
+// begins early, 1.76; a warp to issue for each group of rows, barriers and maxima side by side
+// 1.54.  P in S's place without a pass for the maximum (sums above 2^15 tell) took 1.87, P by
+// quarters 188 us where halves take 175 (f16).
 #pragma once
 
 #include <cuda_runtime.h>
