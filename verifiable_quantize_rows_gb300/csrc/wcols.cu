@@ -75,11 +75,14 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS)
     }
     // the unit's quotients, whose f32 divisions equal the f64 ones rounded
     const float s = fmaxf(__fdiv_rn(__uint_as_float(m), 127.0f), 1e-8f), inv = __fdiv_rn(1.0f, s);
+    // A row with Inf or NaN has codes of 0 and no number for its scale: codes that are none (a NaN's
+    // scale is the least one) would overflow its sums, which share words with another token's.
+    const bool finite = m < 0x7f800000u;
     auto write = [&](int k, const Piece &p) {
         __half h[VEC];
 #pragma unroll
         for (int u = 0; u < VEC; ++u) {  // the unit's code: floors below 2^23 are exact in f32
-            const float c = floorf(__fadd_rn(__fmul_rn(to_f32(p.v[u]), inv), 0.5f));
+            const float c = finite ? floorf(__fadd_rn(__fmul_rn(to_f32(p.v[u]), inv), 0.5f)) : 0.0f;
             h[u] = __float2half_rn(c);
         }
         if (k < ldk) {  // (a whole number of pieces)
@@ -103,8 +106,8 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS)
         write(k, p);
     }
     if (tid == 0) {
-        scale[row] = s;
-        if (m >= 0x7f800000u) set_status(dstatus, BSG_DSTATUS_NONFINITE);
+        scale[row] = finite ? s : __uint_as_float(0x7fffffffu);
+        if (!finite) set_status(dstatus, BSG_DSTATUS_NONFINITE);
     }
 }
 
