@@ -38,3 +38,18 @@ def test_the_sums_warps_leave_together():
     assert sums.count("abort_flag") == one.count("abort_flag")
     loop = sums[sums.index(one) + len(one):]
     assert loop.index("bar.sync 1") < loop.index("break;")        # decided behind the barrier, by its word
+
+
+def test_no_block_of_a_grid_launched_beside_another_ends_before_it():
+    """A grid launched while the one before it still runs has to wait for it in every block: were
+    all to leave early (a join where no token is there), the next call could begin to write the
+    workspace while the first grid is still at it."""
+    for name, head in (("kv8_more.cu", "kv8_join_lists_kernel(const"), ("kv8.cu", "kv8_join_kernel(const")):
+        kernel = body(source(name), head)
+        assert "return;" not in kernel[:kernel.index("griddep_wait();")], name
+    kernel = body(source("quantize.cu"), "i8_cols_to_half_kernel(const")
+    assert "return" not in re.sub(r"return \*reinterpret_cast[^;]*;", "", kernel) and kernel.rstrip().endswith("griddep_wait();")
+    # the tiles' kernel: a block without rows leaves at once, which those of a prefix are not; one without tiles waits
+    kernel = body(source("kv8_tiles.cuh"), "kv8_tiles_kernel(const")
+    early = body(kernel, "if (tiles == 0 && split > 0)")
+    assert early.index("if (PREFIX) griddep_wait();") < early.index("return;")

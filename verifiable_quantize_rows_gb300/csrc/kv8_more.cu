@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __gr
     const int h = blockIdx.x % a.heads, t = blockIdx.x / a.heads % a.tokens, b = blockIdx.x / a.heads / a.tokens;
     const int hk = h / share;
     bool idle = false;
+    griddep_wait();  // every block, those of tokens that are not there too: this grid never ends before the ones it joins
     if (a.counts) {
         const int count = __ldg(a.counts + b);
         if (t >= count || count > a.tokens) return;
@@ -58,7 +59,6 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_lists_kernel(const __gr
     }
     const int64_t row[2] = {((int64_t)b * a.kv_heads + hk) * a.tokens * share + t * share + h % share,
                             (((int64_t)hk * a.B + b) * a.tokens + t) * share + h % share};
-    griddep_wait();
     const int n = a.splits[0] + a.splits[1];
     auto at = [&](int i) {  // chunk i: its list's place
         return i < a.splits[0] ? row[0] * a.splits[0] + i : row[1] * a.splits[1] + i - a.splits[0];
