@@ -54,6 +54,18 @@ namespace {
 // is more than 2^4 above: a p' stays below 2^15, which f16 holds, the largest is at
 // least 2^11, and the outputs are rescaled a few times per row instead of at every tile.
 
+// The tensor cores cut off what they add to an f32 sum, always towards 0 (some 2^-24 of it with each
+// product), and a plain sum of many equal terms rounds the same way each time.  So a warp's outputs
+// and sums are added, rounded, to a second set every kAnew tiles of its chunk and begun anew.  That
+// set lies in local memory, beside a pass over the outputs that a moved reference takes as well.
+// Off 64 bits with equal scores and values of one sign, 512 sequences of 131072 positions, one chunk
+// each: f32 2.0e-4 (mean) without, 7e-7 with, 2.6e-6 every 64 tiles, 3.5e-7 every 16; f16, 2^20
+// positions, 9.0e-4 and 2e-5 (128 tiles).  It takes a kernel of its own, for chunks that may have more
+// tiles to a warp: 512 sequences of 8192, 8 heads of 128, f32 1272 us without, 1400 with (1335 every
+// 64 tiles); 256 of 32768 and 64 dims, bf16 1286 and 1410.
+// (More chunks instead of it cost less where tables are full, but where they have room for 131072 and
+// hold 4096 a call of 256 sequences took 675 us in place of 346.)
+
 // The positions are cut into chunks, a CTA each, several for each place on the
 // card, so that the hardware's own scheduling evens out what SMs and lengths
 // differ by.  (Equal shares of all tiles for just the resident CTAs were slower,
@@ -75,6 +87,9 @@ constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kMaxSplits = 1024;
 constexpr float kRefNone = -3.0e38f;  // the reference of a row that has seen nothing
+// Tiles of a warp to one sum.  f32: 32 products, 2^-20 or so; 16 bits: 256, 2^-16, where f16's own rounding is 2^-12.
+template <int kParts>
+constexpr int kAnew = kParts == 2 ? 32 : 128;
 constexpr float kTop = 11.0f, kMost = 15.0f;  // exponents of a new reference's largest p', and of any
 
 // 16 bytes from global to shared memory, asynchronously, past L1.
@@ -279,7 +294,7 @@ __device__ __forceinline__ int chunk_begin(const AttendArgs &a, int i) {
 }
 
 // grid (heads x row tiles, B, splits): the first chunks of all first
-template <int D, int NT, int kParts, int kMode>
+template <int D, int NT, int kParts, int kMode, bool kLong>
 __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
     kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int kRows = 8 * NT / kParts;  // rows of a group
@@ -484,6 +499,52 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
 #pragma unroll
             for (int u = 0; u < 2; u += kParts) live |= see[n][u] > 0 ? 1u << (2 * n + u) : 0u;
     bool fresh = true;
+    int due = kAnew<kParts>;  // the warp's tile before which its sums are begun anew (or the next that is there)
+    // kLong: what was added up before the sums were begun anew, relative to the references then (a
+    // row that had seen nothing: -inf, no part of it).
+    alignas(16) float kept[NT][kStep][4];
+    volatile float kept_sum[NT][2], kept_ref[NT][2];
+    auto with_kept = [&](bool some, bool keep) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
+            for (int u = 0; u < 2; u += kParts) {
+                f[u] = some ? exp2_fast(kept_ref[n][u] - ref[n][u]) : 0.0f;
+                if (some) sum[n][u] = fmaf(kept_sum[n][u], f[u], sum[n][u]);
+                if (keep) {
+                    kept_sum[n][u] = sum[n][u];
+                    sum[n][u] = 0.0f;
+                    kept_ref[n][u] = none & (1u << (2 * n + u)) ? -INFINITY : ref[n][u];
+                }
+            }
+            if (kParts == 2) f[1] = f[0];
+            constexpr int kBatch = kStep % 4 ? 2 : 4;  // loads sent together
+#pragma unroll
+            for (int i0 = 0; i0 < kStep; i0 += kBatch) {
+                float before[kBatch][4];
+                if (some)
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        asm volatile("ld.local.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(before[i][0]), "=f"(before[i][1]), "=f"(before[i][2]), "=f"(before[i][3])
+                                     : "l"(__cvta_generic_to_local(kept[n][i0 + i])) : "memory");
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    float(&o)[4] = acc[n][i0 + i];
+                    if (some)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) o[u] = fmaf(before[i][u], f[u % 2], o[u]);
+                    if (keep) {
+                        asm volatile("st.local.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(__cvta_generic_to_local(kept[n][i0 + i])),
+                                     "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]) : "memory");
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) o[u] = 0.0f;
+                    }
+                }
+            }
+        }
+    };
     for (int tile = tile0 + warp; tile < tiles; tile += kWarps) {
         copies_wait<kStages - 1>();
         __syncwarp();
@@ -537,7 +598,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
                 }
         };
         exponents();
-        if (__any_sync(0xffffffffu, most > kMost || fresh || edge)) {
+        const bool anew = kLong && (tile - tile0) / kWarps >= due;
+        if (__any_sync(0xffffffffu, most > kMost || fresh || edge || anew)) {
             if (kMode != kWindow) fresh = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -564,6 +626,11 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
 #pragma unroll
                     for (int u = 0; u < 4; ++u) acc[n][i][u] *= keep[u % 2];
             }
+            if constexpr (kLong)
+                if (anew) {
+                    with_kept(due > kAnew<kParts>, true);
+                    due = (tile - tile0) / kWarps + kAnew<kParts>;
+                }
             // a row whose window begins after this tile sees its first one later
             if (kMode == kWindow) fresh = __any_sync(0xffffffffu, (none & live) != 0);
             exponents();
@@ -623,6 +690,8 @@ __global__ void __launch_bounds__(kWarps * 32, attend_per_sm<D, NT>())
         stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
+    if constexpr (kLong)
+        if (due > kAnew<kParts>) with_kept(true, false);
     copies_wait<0>();
     __syncthreads();  // the rings are free
 
@@ -725,23 +794,32 @@ inline AttendPlan attend_plan(const bsg_kv8_cache &c, int64_t table_ld, int64_t 
     return attend_plan_of(c, table_ld * (c.page_tokens / 16), B, T * (heads / c.heads), parts);
 }
 
-template <int D, int NT, int kParts, int kMode>
-cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
+template <int D, int NT, int kParts, int kMode, bool kLong>
+cudaError_t launch_attend_as(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
     constexpr int smem = attend_smem<D, NT, kParts>();
     static bool set[64] = {false};  // this kernel's shared memory, on each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (smem > 48 * 1024 && (dev >= 64 || !set[dev])) {
-        e = cudaFuncSetAttribute(kv8_attend_kernel<D, NT, kParts, kMode>,
+        e = cudaFuncSetAttribute(kv8_attend_kernel<D, NT, kParts, kMode, kLong>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
     }
     const dim3 grid((unsigned)(a.c.heads * p.row_tiles), (unsigned)B, (unsigned)p.splits);
-    kv8_attend_kernel<D, NT, kParts, kMode><<<grid, kWarps * 32, smem, st>>>(a);
+    kv8_attend_kernel<D, NT, kParts, kMode, kLong><<<grid, kWarps * 32, smem, st>>>(a);
     count_launches(1);
     return cudaGetLastError();
+}
+
+// The kernel that begins sums anew where a warp may have more tiles than one sum takes: the first
+// chunk is the longest.
+template <int D, int NT, int kParts, int kMode>
+cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, int64_t B, cudaStream_t st) {
+    const int64_t n = p.splits, most = n == 1 ? p.width / kWarps : (16 * n - 6) * (p.width / kWarps) / (10 * n * n) + 1;
+    return most > kAnew<kParts> ? launch_attend_as<D, NT, kParts, kMode, true>(a, p, B, st)
+                                : launch_attend_as<D, NT, kParts, kMode, false>(a, p, B, st);
 }
 
 template <int D, int kMode>
