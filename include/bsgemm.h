@@ -457,8 +457,11 @@ bsg_status bsg_kv8_attend(const bsg_kv8_cache *cache, const int32_t *table, int6
  * The rest is as for bsg_kv8_attend: a query that sees no position gives 0 and lse -inf;
  * scores and sums are f32, f32 queries keep 22 bits of their row's largest, and
  * probabilities keep 22 bits of themselves or 2^-34 of the largest; those of bf16 keep 11
- * bits where a key/value head has more than 16 query rows (tokens times its heads).  Tokens t >= counts[b] are not read, and
- * nothing is written for them.  A count that is not in 0..T leaves its sequence out and sets
+ * bits where a key/value head has more than 16 query rows (tokens times its heads).  Sums over any
+ * number of positions lose some 2^-19 of sum p |v| in f32, 2^-14 with f16 and 2^-12 with bf16
+ * queries (the tensor cores cut off, so they are begun anew in time and joined by rounded
+ * additions), beside the output's own rounding.  Tokens t >= counts[b] are not read, and nothing
+ * is written for them.  A count that is not in 0..T leaves its sequence out and sets
  * BSG_DSTATUS_RANGE; lengths and pages out of range as for bsg_kv8_attend (of pages that some
  * query sees).  T * (heads / cache->heads) < 2^31.  window, sinks >= 0.
  * `workspace`: bsg_kv8_attend_window_workspace_size bytes. */

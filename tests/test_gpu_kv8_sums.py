@@ -67,13 +67,37 @@ def test_few_rows(call, dtype, B, T, D, n):
     equal_scores(call, dtype, B, T, 8, D, n, run, -(-n // (64 * (32 if dtype == F32 else 128))))
 
 
+# A sum of the tensor cores' takes 640 positions at most (f16: 10240, bf16: 40960), two products to each 16 (bf16: one).
+@pytest.mark.parametrize("dtype,B,T,D,n", [(F32, 40, 64, 64, 1 << 18), (F32, 40, 64, 256, 1 << 17), (F32, 40, 33, 32, 40000), (F16, 40, 64, 64, 1 << 16),
+                                           (F16, 40, 17, 96, 1 << 18), (F16, 40, 200, 256, 1 << 17), (BF16, 40, 64, 64, 1 << 19)])
+def test_many_rows(dtype, B, T, D, n):
+    run, positions = {F32: (80, 512), F16: (1280, 8192), BF16: (2560, 32768)}[dtype]
+    equal_scores(bsg.kv8_attend_window, dtype, B, T, 4, D, n, run, -(-n // positions))
+
+
+@pytest.mark.parametrize("dtype,n", [(F32, 1 << 17), (F16, 1 << 18), (BF16, 1 << 19)])
+def test_a_long_prefix(dtype, n):
+    """The prefix's positions in one chunk, by equal scores; the own token is one position more."""
+    B, Hk, D, pool = 1024, 8, 64, 256
+    cache = cache_of(pool, Hk, D, 9)
+    order = np.random.default_rng(1).integers(0, pool, n // PAGE).astype(np.int32)
+    q = torch.zeros(B, 4, Hk, D, dtype=dtype, device="cuda")
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    y = bsg.kv8_attend_shared(q, bsg.Kv8Cache(*map(dev, cache)), dev(order), dev(np.int32([n])), table, torch.full((B,), 4, dtype=torch.int32, device="cuda"))
+    own = cache[1][0, :, 0].astype(np.float64) * cache[3][0].astype(np.float64)[:, None]       # the first own position
+    want = np.broadcast_to((means(cache, order, n) * n + own) / (n + 1), (B, Hk, D))
+    run, positions = {F32: (80, 512), F16: (1280, 8192), BF16: (2560, 32768)}[dtype]
+    off = 2.0 ** -19 + run * 2.0 ** -22 + 2 * (run + n // positions + 16) * 2.0 ** -24
+    within(f64(y[:, 0]), want, want * off * 1.01 + rounding(want, dtype))
+
+
 def test_own_tokens_behind_a_prefix():
     prefix, n0 = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     equal_scores(lambda q, c, table, lens: bsg.kv8_attend_shared(q, c, prefix, n0, table, lens), F32, 400, 1, 8, 128, 65536, 32, 32)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
-@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("T", [1, 3, 40])
 @pytest.mark.parametrize("scores", ["rise", "fall", "any"])
 def test_references_that_move_between_sums(scores, T, dtype):
     """Long chunks whose scores rise all along, fall, or do neither, against the definition."""

@@ -19,7 +19,8 @@ cudaError_t launch_few_window(const KvCall &a, const KvPlan &p, cudaStream_t st)
     }
 }
 
-KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_t B, int64_t positions, bool later) {
+KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_t B, int64_t positions, int64_t of_block,
+               bool later) {
     KvPlan p = {};
     const int64_t groups = B * c.heads;
     if (few) {
@@ -37,15 +38,8 @@ KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_
         p.row_blocks = (int)((rows + block - 1) / block);
         int64_t splits = device_sm_count() / (p.row_blocks * groups);
         if (splits > (positions + tile - 1) / tile / 2) splits = (positions + tile - 1) / tile / 2;
-        // The tensor cores cut off what they add to O, always towards 0: 2^-25.7 of it measured for
-        // each MMA of 16 positions, two of them where P has two parts.  f32's O is begun anew in time;
-        // chunks of f16 and bf16 stay so short that they lose less than the type's own rounding
-        // (2^-12.7 and 2^-10.7), and their join adds in f32.
-        const int64_t most = dtype == BSG_F32 ? INT32_MAX / 2 : dtype == BSG_F16 ? 65536 : 524288;
-        const int64_t least = (positions + most - 1) / most;
-        p.fill = (int)(splits < 1 ? 1 : splits);
-        p.chunk_most = (int)(most / tile);
-        p.splits = (int)(splits >= least ? p.fill : least < 1024 ? least : 1024);
+        p.splits = (int)(splits < 1 ? 1 : splits);
+        p.tiles = (int)((of_block + tile * p.splits - 1) / (tile * p.splits));
     }
     p.parts = p.splits > 1 || later ? (size_t)groups * rows * p.splits : 0;
     return p;

@@ -161,7 +161,7 @@ bool few(int64_t rows, int dtype) { return rows <= (dtype == BSG_F32 ? 32 : 16);
 size_t part_floats(const bsg_kv8_cache &c, int64_t rows, int64_t B, int64_t positions, bool later) {
     size_t most = 0;
     for (int dtype = BSG_F32; dtype <= BSG_F16; ++dtype) {
-        const KvPlan p = kv_plan(c, few(rows, dtype), dtype, rows, B, positions, later);
+        const KvPlan p = kv_plan(c, few(rows, dtype), dtype, rows, B, positions, positions, later);
         if (p.parts * (c.dim + 2) > most) most = p.parts * (c.dim + 2);
     }
     return most;
@@ -186,7 +186,10 @@ cudaError_t launch_kv8_attend_window(const bsg_kv8_cache &c, const int32_t *tabl
                                      void *ws, int32_t *dstatus, cudaStream_t st) {
     const int64_t rows = T * (heads / c.heads);
     const bool is_few = few(rows, dtype);
-    const KvPlan p = kv_plan(c, is_few, dtype, rows, B, seen_positions(c, table_ld, T, window, sinks), false);
+    // a CTA of tiles has 256 rows
+    const int64_t share = heads / c.heads, some = 255 / share + 2;
+    const KvPlan p = kv_plan(c, is_few, dtype, rows, B, seen_positions(c, table_ld, T, window, sinks),
+                             seen_positions(c, table_ld, T < some ? T : some, window, sinks), false);
     KvCall a{c, table, table_ld, lens, counts, q, out, dtype, (int)T, heads, window, sinks, B, rows, scale, lse, 0,
              static_cast<float *>(ws), nullptr, dstatus};
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + p.parts * c.dim);
@@ -213,8 +216,9 @@ cudaError_t launch_kv8_attend_shared(const bsg_kv8_cache &c, const int32_t *pref
     const int64_t rows = T * (heads / c.heads);
     if (B * rows > INT32_MAX) return cudaErrorInvalidValue;
     const bool few_own = few(rows, dtype), few_pre = few(B * rows, dtype);
-    const KvPlan own = kv_plan(c, few_own, dtype, rows, B, table_ld * c.page_tokens, true);
-    const KvPlan pre = kv_plan(c, few_pre, dtype, B * rows, 1, prefix_pages * c.page_tokens, true);
+    const int64_t own_most = table_ld * c.page_tokens, pre_most = prefix_pages * c.page_tokens;
+    const KvPlan own = kv_plan(c, few_own, dtype, rows, B, own_most, own_most, true);
+    const KvPlan pre = kv_plan(c, few_pre, dtype, B * rows, 1, pre_most, pre_most, true);
     float *own_o = static_cast<float *>(ws), *pre_o = own_o + own.parts * c.dim;
     float2 *own_ml = reinterpret_cast<float2 *>(pre_o + pre.parts * c.dim), *pre_ml = own_ml + own.parts;
     KvCall a{c, table, table_ld, lens, nullptr, q, out, dtype, (int)T, heads, 0, 0, B, rows, scale, lse, 1,

@@ -30,10 +30,12 @@ struct KvCall {
 struct KvPlan {
     int splits;
     size_t parts;
-    int row_blocks, fill, chunk_most;  // of the tiles' kernel (TileArgs)
+    int row_blocks, tiles;     // of the tiles' kernel (TileArgs), and the tiles of a chunk at most
     int nt, row_tiles, width;  // of the kernel of few rows
 };
-KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_t B, int64_t positions, bool later);
+// positions: that the rows of a head and sequence see at most; of_block: those that some rows of one CTA see.
+KvPlan kv_plan(const bsg_kv8_cache &c, bool few, int dtype, int64_t rows, int64_t B, int64_t positions, int64_t of_block,
+               bool later);
 
 cudaError_t launch_few_window(const KvCall &a, const KvPlan &p, cudaStream_t st);
 cudaError_t launch_few_prefix(const KvCall &a, const KvPlan &p, cudaStream_t st);

@@ -58,8 +58,7 @@ struct TileArgs {
     int tokens, heads, window, sinks;
     int rows, row_blocks;      // of a key/value head (and sequence); CTAs that they take
     int64_t groups;            // key/value heads (of all sequences)
-    int splits, later;         // chunks of a CTA's tiles, at most; 1: what is found is joined later
-    int fill, chunk_most;      // chunks of few tiles; beyond them, as many as leave no more tiles to each
+    int splits, later;         // chunks of a CTA's tiles; 1: what is found is joined later
     float scale;
     float *lse;
     float *part_o;             // [sequence][head][row][split][D]: outputs before the division by the sum,
@@ -103,7 +102,7 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16])
 // The lowest n bits.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-template <int D, int kQParts, int kPParts>
+template <int D, int kQParts, int kPParts, bool kLong>
 struct TileCfg {
     static constexpr int kM = D == 256 ? 1 : 2;
     static constexpr int kN = D == 256 ? 64 : 128;
@@ -129,15 +128,20 @@ struct TileCfg {
     static constexpr int kP0 = kInPlace ? 0 : kN, kPStep = kInPlace ? kN : kPCols;
     static constexpr int kO0 = kInPlace ? kM * kN : kN + kM * kPCols;
     static_assert(kO0 + kM * D <= 512 && kPCols <= kN, "tensor memory");
-    // What the tensor cores add to an f32 sum is cut off below its last bit, not rounded: some 2^-25
-    // of O is lost with each 16 positions, always towards 0.  f32's O is therefore added (rounded)
-    // to a sum in memory every 512 positions and begun anew, but for the last 640; 16-bit outputs do
-    // not show it.  (64 rows behind 131072 positions in 19 chunks: 1.6e-5 off 64 bits without, 2.4e-6
-    // by 1024 positions, 1.4e-6 by 512.  Prompts of some 400 seen positions, which stay without: 47 us,
-    // 59 with one such sum.)
-    static constexpr int kFlush = kQParts == 2 ? 512 / kN : 0;  // tiles
+    // What the tensor cores add to an f32 sum is cut off below its last bit, not rounded: some 2^-24
+    // of O is lost with each product of 16 positions, always towards 0; and the sum of p, of as many
+    // terms, rounds the same way each time where they are alike.  Both are therefore added (rounded)
+    // to a second set, which lies in local memory, every kFlush tiles and begun anew, but for the last
+    // quarter as many more.  Off 64 bits on the mean, with equal scores and values of one sign: f32, 65536
+    // positions, 1.2e-6 (the sum of p in one piece 1.7e-5); f16, 131072, 5e-5 (in one piece of 65536
+    // 4.2e-4; its rounding 4.9e-4 at most); bf16, 524288, 2.5e-4 (3.7e-3; 3.9e-3).  Times as before but
+    // for f16's of more positions, whose registers spill more: prompts of 16384 without a window 5.1 ->
+    // 5.5 ms, every 4096 positions 5.6; bf16 3.38 -> 3.36, every 4096 3.55.  In local memory a warp's
+    // second set lies side by side; f32's in the outputs' rows took 11.2 ms there in place of 8.0.
+    static constexpr int kFlush = (kQParts == 2 ? 512 : kPParts == 2 ? 8192 : 32768) / kN;  // tiles
+    static constexpr int kFlushMost = kFlush + kFlush / 4;
     static __device__ bool flush_at(int i, int tiles) {
-        return kFlush > 0 && i > 0 && i % (kFlush ? kFlush : 1) == 0 && tiles - i > kFlush / 4;
+        return kLong && i > 0 && i % kFlush == 0 && tiles - i > kFlush / 4;
     }
 };
 
@@ -167,10 +171,10 @@ __device__ __forceinline__ uint4 load_codes(const int8_t *p) {
 // PREFIX: rows are those of all sequences (rows = B x tokens x heads of a group), every one
 // sees the positions below *lens; what a CTA finds is joined later.  The report of bad lengths
 // is the first CTA's.
-template <int D, int kQParts, int kPParts, bool PREFIX>
+template <int D, int kQParts, int kPParts, bool PREFIX, bool kLong>
 __global__ void __launch_bounds__(kTileThreads, 1)
     kv8_tiles_kernel(const __grid_constant__ TileArgs a) {
-    using C = TileCfg<D, kQParts, kPParts>;
+    using C = TileCfg<D, kQParts, kPParts, kLong>;
     constexpr int kM = C::kM, kN = C::kN, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
@@ -221,9 +225,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int pos0 = PREFIX ? 0 : len - count;  // token 0's position
     const Seen seen = PREFIX ? seen_by<kN>(0, len - 1, 0, 0)
                              : seen_by<kN>(pos0 + r0 / share, pos0 + (r0 + rows - 1) / share, a.window, a.sinks);
-    const int chunks = min(a.splits, max(a.fill, (seen.tiles + a.chunk_most - 1) / a.chunk_most));
-    const int begin = (int)((int64_t)seen.tiles * min(split, chunks) / chunks);
-    const int tiles = (int)((int64_t)seen.tiles * min(split + 1, chunks) / chunks) - begin;
+    const int begin = (int)((int64_t)seen.tiles * split / a.splits);
+    const int tiles = (int)((int64_t)seen.tiles * (split + 1) / a.splits) - begin;
     if (tiles == 0 && split > 0) {  // the join reads no output of such a chunk
         if (tid < rows)
             a.part_ml[(((int64_t)b * a.c.heads + hk) * a.rows + r0 + tid) * a.splits + split] = make_float2(0.0f, 0.0f);
@@ -634,15 +637,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[m]);
         float ref = 0.0f, sum = 0.0f;
         bool none = true, ok = true;
-        // f32: the sum of what O was before it was begun anew, in the output's place, relative to acc_ref
-        auto acc_place = [&]() {
-            return PREFIX || a.splits > 1 || a.later
-                       ? a.part_o + ((((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + split) * D
-                       : static_cast<float *>(a.out.data) + b * a.out.stride_batch + (r0 + r) / share * a.out.stride_token +
-                             (hk * share + (r0 + r) % share) * a.out.stride_head;
-        };
-        float acc_ref = 0.0f;
-        bool acc_some = false;
+        // What O was before it was begun anew, the sum, and the reference then (a row that had seen
+        // nothing: -inf, no part of it): in local memory, and in no register from one time to the next.
+        volatile float kept[D + 2];
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
             const int tile = position(i), slot = i % kAtSlots;
@@ -657,42 +654,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const float f = acc_some ? tile_exp2(acc_ref - ref) : 0.0f;
-                float *const acc = acc_place();
-                const bool wide = reinterpret_cast<uintptr_t>(acc) % 16 == 0;
+                const bool some_kept = i > C::kFlush;
+                const float f = some_kept ? tile_exp2(kept[D + 1] - ref) : 0.0f;
+                kept[D] = some_kept ? fmaf(kept[D], f, sum) : sum;
+                kept[D + 1] = none ? -INFINITY : ref;
+                sum = 0.0f;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
-                    alignas(16) float before[32];
+                    float before[32];
                     __syncwarp();
                     tmem_ld32(o_at + 32 * c, o);
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) before[u] = 0.0f;
-                    if (r < rows && f > 0.0f) {
-                        if (wide) {
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                *reinterpret_cast<float4 *>(before + 4 * u) = reinterpret_cast<const float4 *>(acc + 32 * c)[u];
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) before[u] = acc[32 * c + u];
-                        }
-                    }
-                    __syncwarp();
+                    for (int u = 0; u < 32; ++u) before[u] = some_kept ? kept[32 * c + u] : 0.0f;
                     tmem_ld_wait32(o);
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) before[u] = fmaf(before[u], f, __uint_as_float(o[u]));
-                    if (r >= rows) continue;
-                    if (wide) {
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            reinterpret_cast<float4 *>(acc + 32 * c)[u] = *reinterpret_cast<const float4 *>(before + 4 * u);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) acc[32 * c + u] = before[u];
-                    }
+                    for (int u = 0; u < 32; ++u) kept[32 * c + u] = fmaf(before[u], f, __uint_as_float(o[u]));
                 }
-                acc_ref = ref, acc_some = !none;
             }
             if (edge) {  // what the row does not see, where S lies (seldom; rolled up)
 #pragma unroll 1
@@ -813,9 +791,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool direct = !PREFIX && a.splits == 1 && !a.later;
         const int64_t part = (((int64_t)b * a.c.heads + hk) * a.rows + r0 + r) * a.splits + split;
         const bool there = r < rows && ok;
+        const bool some_kept = C::flush_at(C::kFlush, tiles);
+        const float of_kept = some_kept ? tile_exp2(kept[D + 1] - ref) : 0.0f;
+        if (some_kept) sum = fmaf(kept[D], of_kept, sum);
         const bool some = sum > 0.0f || sum != sum;
         const float inv = some ? __frcp_rn(sum) : 0.0f;
-        const float of_acc = acc_some ? tile_exp2(acc_ref - ref) : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -828,22 +808,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float o[32];
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] = tiles == 0 || (!some && direct) ? 0.0f : __uint_as_float(v[u]);
-            if (kQParts == 2 && of_acc > 0.0f) {
-                const float *const acc = acc_place() + 32 * c;
-                if (reinterpret_cast<uintptr_t>(acc) % 16 == 0) {
+            if (some_kept)
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float4 x = reinterpret_cast<const float4 *>(acc)[u];
-                        o[4 * u] = fmaf(x.x, of_acc, o[4 * u]);
-                        o[4 * u + 1] = fmaf(x.y, of_acc, o[4 * u + 1]);
-                        o[4 * u + 2] = fmaf(x.z, of_acc, o[4 * u + 2]);
-                        o[4 * u + 3] = fmaf(x.w, of_acc, o[4 * u + 3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] = fmaf(acc[u], of_acc, o[u]);
-                }
-            }
+                for (int u = 0; u < 32; ++u) o[u] = fmaf(kept[32 * c + u], of_kept, o[u]);
             if (direct) {
                 auto store = [&](auto type) {
                     using T = decltype(type);
@@ -889,15 +856,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
 }
 
-template <int D, int kQ, int kP, bool PREFIX>
+template <int D, int kQ, int kP, bool PREFIX, bool kLong>
 cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
-    using C = TileCfg<D, kQ, kP>;
+    using C = TileCfg<D, kQ, kP, kLong>;
     static bool set[64] = {false};  // this kernel's shared memory, on each device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(kv8_tiles_kernel<D, kQ, kP, PREFIX>,
+        e = cudaFuncSetAttribute(kv8_tiles_kernel<D, kQ, kP, PREFIX, kLong>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) set[dev] = true;
@@ -915,27 +882,36 @@ cudaError_t launch_tiles_as(const TileArgs &a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = PREFIX ? 1 : 0;  // beside the sequences' own positions' launch
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kv8_tiles_kernel<D, kQ, kP, PREFIX>, a);
+    return cudaLaunchKernelEx(&cfg, kv8_tiles_kernel<D, kQ, kP, PREFIX, kLong>, a);
+}
+
+// most: tiles of a chunk.  Chunks that one sum takes need none of the code that begins it anew, which
+// 16-bit types' registers have little room for (f16, prompts of 16384 through a window of 4096: 2541
+// us without, 2727 with).
+template <int D, int kQ, int kP, bool PREFIX>
+cudaError_t launch_tiles_long(const TileArgs &a, int most, cudaStream_t st) {
+    if constexpr (kQ == 1)
+        if (most <= TileCfg<D, kQ, kP, true>::kFlushMost) return launch_tiles_as<D, kQ, kP, PREFIX, false>(a, st);
+    return launch_tiles_as<D, kQ, kP, PREFIX, true>(a, st);
 }
 
 template <int D, bool PREFIX>
-cudaError_t launch_tiles_dim(const TileArgs &a, int dtype, cudaStream_t st) {
-    if (dtype == BSG_F32) return launch_tiles_as<D, 2, 2, PREFIX>(a, st);
-    if (dtype == BSG_F16) return launch_tiles_as<D, 1, 2, PREFIX>(a, st);
-    return launch_tiles_as<D, 1, 1, PREFIX>(a, st);
+cudaError_t launch_tiles_dim(const TileArgs &a, int dtype, int most, cudaStream_t st) {
+    if (dtype == BSG_F32) return launch_tiles_long<D, 2, 2, PREFIX>(a, most, st);
+    if (dtype == BSG_F16) return launch_tiles_long<D, 1, 2, PREFIX>(a, most, st);
+    return launch_tiles_long<D, 1, 1, PREFIX>(a, most, st);
 }
 
 template <bool PREFIX>
 cudaError_t launch_tiles(const KvCall &k, const KvPlan &p, cudaStream_t st) {
     const TileArgs a{k.c, k.table, k.table_ld, k.lens, k.counts, k.q, k.out, k.tokens, k.heads, k.window, k.sinks,
-                     (int)k.rows, p.row_blocks, k.B * k.c.heads, p.splits, k.later, p.fill, p.chunk_most, k.scale, k.lse, k.part_o, k.part_ml,
-                     k.dstatus};
+                     (int)k.rows, p.row_blocks, k.B * k.c.heads, p.splits, k.later, k.scale, k.lse, k.part_o, k.part_ml, k.dstatus};
     switch (k.c.dim) {
-        case 32: return launch_tiles_dim<32, PREFIX>(a, k.dtype, st);
-        case 64: return launch_tiles_dim<64, PREFIX>(a, k.dtype, st);
-        case 96: return launch_tiles_dim<96, PREFIX>(a, k.dtype, st);
-        case 128: return launch_tiles_dim<128, PREFIX>(a, k.dtype, st);
-        default: return launch_tiles_dim<256, PREFIX>(a, k.dtype, st);
+        case 32: return launch_tiles_dim<32, PREFIX>(a, k.dtype, p.tiles, st);
+        case 64: return launch_tiles_dim<64, PREFIX>(a, k.dtype, p.tiles, st);
+        case 96: return launch_tiles_dim<96, PREFIX>(a, k.dtype, p.tiles, st);
+        case 128: return launch_tiles_dim<128, PREFIX>(a, k.dtype, p.tiles, st);
+        default: return launch_tiles_dim<256, PREFIX>(a, k.dtype, p.tiles, st);
     }
 }
 
