@@ -23,3 +23,14 @@ def test_chunks_are_bounded_by_the_card(lib, B, T):  # noqa: F811
     """Fewer rows than fill the card: at most one chunk of 256 rows for each of some 200 places."""
     for positions in (32768, 1 << 20):
         assert sizes(lib, positions, B=B, T=T) <= (200 * 256 * 4 + 256) * (128 + 2) * 4
+
+
+def test_every_type_is_sized():
+    """A workspace serves any type of the call: the size is the largest over all that there are."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    types = set(re.findall(r"\b(BSG_(?:F32|F16|BF16|F64|F8\w*))\s*=", open(os.path.join(root, "include", "bsgemm.h")).read()))
+    text = open(os.path.join(root, "verifiable_quantize_rows_gb300", "csrc", "kv8_more.cu")).read()
+    assert len(types) >= 3 and set(re.findall(r"BSG_\w+", re.search(r"kDtypes\[\] = \{([^}]*)\}", text).group(1))) == types
+    assert "for (const int dtype : kDtypes)" in text

@@ -157,10 +157,11 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 //   one of 16384                        29, 23 (27)       46, 23     |  46, 37           55, 37
 bool few(int64_t rows, int dtype) { return rows <= (dtype == BSG_F32 ? 32 : 16); }
 
-// The workspace of one part of a call, largest over the types.
+// The workspace of one part of a call, largest over the types: a call takes the plan of its own.
+constexpr int kDtypes[] = {BSG_F32, BSG_F16, BSG_BF16};
 size_t part_floats(const bsg_kv8_cache &c, int64_t rows, int64_t B, int64_t positions, bool later) {
     size_t most = 0;
-    for (int dtype = BSG_F32; dtype <= BSG_F16; ++dtype) {
+    for (const int dtype : kDtypes) {
         const KvPlan p = kv_plan(c, few(rows, dtype), dtype, rows, B, positions, positions, later);
         if (p.parts * (c.dim + 2) > most) most = p.parts * (c.dim + 2);
     }
