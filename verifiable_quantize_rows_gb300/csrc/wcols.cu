@@ -13,6 +13,7 @@
 #include "bsg_internal.h"
 #include "bsg_ptx.cuh"
 #include "serve.cuh"
+#include "wcols_runs.h"
 
 namespace bsg {
 namespace {
@@ -536,8 +537,7 @@ cudaError_t launch_few_as(const FewArgs &a, const CUtensorMap &map, cudaStream_t
     const int64_t sms = device_sm_count();
     cudaLaunchConfig_t cfg = {};
     const int64_t blocks = (a.M + kFewTokens - 1) / kFewTokens;
-    const int64_t runs = (sms + blocks - 1) / blocks;
-    cfg.gridDim = dim3((unsigned)(a.all < runs ? a.all : runs), (unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)wcols_runs(a.all, blocks, sms), (unsigned)blocks);
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = FewCfg<kCols>::kBytes;
     cfg.stream = st;
@@ -563,11 +563,15 @@ cudaError_t launch_few(const FewArgs &a, const CUtensorMap &map, cudaStream_t st
 //   768 x 2304    16: 7.9, 10.2    32: 12.1, 10.2   128: 18.4, 12.6
 //   768 x 50304   16: 17, 51       64: 29, 49       256: 78, 52
 //   2048 x 8192   16: 14, 27       64: 20, 21       128: 23, 22      256: 32, 24
-//   4096 x 4096                    64: 21, 29       128: 23, 29      256: 30, 32
-//   8192 x 8192                    64: 29, 90                        256: 71, 96     320: 156, 100
-//   16384 x 4096                                    128: 43, 117     256: 71, 121
+//   2304 x 2304                    64: 18, 19       128: 19, 19      192: 26, 21
+//   2600 x 4096                                     128: 22, 22      160: 24, 23      256: 27, 24
+//   3500 x 8192                                                      160: 38, 42      256: 45, 43
+//   4096 x 4096                    64: 21, 29       128: 23, 29      192: 32, 31      256: 31, 31
+//   4096 x 12288                                                     160: 49, 71      256: 61, 72
+//   8192 x 8192                    64: 29, 90       128: 45, 91      192: 60, 94      256: 71, 96     320: 156, 100
+//   16384 x 4096                                    128: 43, 117     192: 60, 120     256: 71, 121
 bool few_form(int64_t M, int64_t N, int64_t K) {
-    return M <= 16 || (M <= 64 && (K > 1024 || N * K > 1 << 23)) || (M <= 256 && K > 2048);
+    return M <= 16 || (M <= 64 && (K > 1024 || N * K > 1 << 23)) || (M <= 128 && K > 2560) || (M <= 256 && K > 3200);
 }
 
 // ---- a token or a few and a small weight: one launch ------------------------------
