@@ -28,16 +28,15 @@ def body(text, head):
 def test_the_sums_warps_leave_together():
     """The warps that take sums meet at a barrier of their own in every round.  Another role may
     set the abort flag at any time, so a thread that read it for itself could leave while its
-    neighbours go on to that barrier for good: only one thread may read it, and all go by what
-    that one wrote before the barrier."""
+    neighbours go on to that barrier for good: one warp waits, and all go by what the barrier
+    itself answers."""
     kernel = body(source("wcols.cu"), "wcols_few_kernel(const")
     sums = kernel[kernel.index("} else {", kernel.index("const int row0 = lane / 16")):]   # the last role
     assert "bar.sync 1" in sums and "atomicAdd" in sums
-    one = body(sums, "if (warp == 0)")
-    assert "abort_flag" in one and "lane == 0" in one
-    assert sums.count("abort_flag") == one.count("abort_flag")
-    loop = sums[sums.index(one) + len(one):]
-    assert loop.index("bar.sync 1") < loop.index("break;")        # decided behind the barrier, by its word
+    assert "abort_flag" not in sums
+    assert "if (warp == 0) came = all_wait(&sum_full[c & 1], c >> 1 & 1);" in sums
+    assert "if (!(ok = sums_barrier_all(came))) break;" in sums     # the barrier's own answer, one for all
+    assert sums.count("all_wait") == 1 and "barrier.cta.red.and.pred" in body(source("wcols.cu"), "bool sums_barrier_all(bool x)")
 
 
 def test_no_block_of_a_grid_launched_beside_another_ends_before_it():

@@ -216,6 +216,20 @@ __device__ __forceinline__ void few_store(const FewArgs &a, int m, int n, int32_
         static_cast<__nv_bfloat16 *>(a.Y)[at] = __float2bfloat16_rn(y);
 }
 
+// The barrier of the warps that take sums: whether `x` holds for every thread of theirs.
+__device__ __forceinline__ bool sums_barrier_all(bool x) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)x), "n"(kSumWarps * 32)
+        : "memory");
+    return all != 0;
+}
+
 // A place in the list of blocks.
 struct FewAt {
     int tile, block;
@@ -240,7 +254,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(sum_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_ptr + 1);
     volatile int *last_s = reinterpret_cast<volatile int *>(tmem_ptr + 2);
-    volatile int *sum_there = reinterpret_cast<volatile int *>(tmem_ptr + 3);  // [buffer]: its sum came
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     // this CTA's run of the list
     const int64_t b0 = a.all * blockIdx.x / gridDim.x, b1 = a.all * (blockIdx.x + 1) / gridDim.x;
@@ -334,7 +347,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
-        __syncwarp();  // the flag stands before the commit below completes a sum that is none
         if (!ok && one) {  // wait until every MMA issued so far has finished
             mma_commit(&sum_full[0]);
             const long long t0 = clock64();
@@ -454,15 +466,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll 1
             for (int done = 0; done < part; ++c) {
                 done += chunk_of(at.block + done, left - done);
-                // One warp polls, the others are out of the way of those that work, and one thread's
-                // word is what all go by: any other role may give up between two threads' reads of the
-                // flag, and those that went on would wait at the next barrier for those that left.
-                if (warp == 0) {
-                    const bool came = all_wait(&sum_full[c & 1], c >> 1 & 1);
-                    if (lane == 0) sum_there[c & 1] = came && !*abort_flag;
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
-                if (!(ok = sum_there[c & 1] != 0)) break;
+                // One warp polls, the others are out of the way of those that work, and its answer is
+                // what the barrier gives to all: any other role may give up between two threads' reads
+                // of the flag, and those that went on would wait at the next barrier for those that left.
+                bool came = true;
+                if (warp == 0) came = all_wait(&sum_full[c & 1], c >> 1 & 1);
+                if (!(ok = sums_barrier_all(came))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int m = 0; m < kMine; m += 8) {
