@@ -141,12 +141,8 @@ __device__ __forceinline__ uint32_t codes_half2(uint32_t x) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Which dim the lane's word `w` of a key row starts at (t = lane % 4), and of a
-// value row (g = lane / 4): 16-byte pieces of 64 (128) bytes, then smaller ones.
-template <int D>
-__host__ __device__ constexpr int key_dim(int w, int t) {
-    return w < D / 64 * 4 ? w / 4 * 64 + 16 * t + w % 4 * 4 : D / 64 * 64 + 8 * t + (w - D / 64 * 4) * 4;
-}
+// Which dim the lane's word `w` of a value row starts at (g = lane / 4): 16-byte pieces of 128
+// bytes, then smaller ones.  (A key row's, t = lane % 4: of 64 bytes, load_key_row's.)
 template <int D>
 __host__ __device__ constexpr int value_dim(int w, int g) {
     return D >= 128  ? w / 4 * 128 + 16 * g + w % 4 * 4
