@@ -385,7 +385,7 @@ bsg_status bsg_wcols_matmul(const void *X, bsg_dtype dtype, int64_t ldx, const i
 /* A key/value cache in int8 codes: a pool of pages of `page_tokens` tokens,
  * with one scale for each page and head.  Layout: k, v int8
  * [pages][heads][page_tokens][dim], 16-byte aligned; k_scale, v_scale f32
- * [pages][heads].  page_tokens: a multiple of 16, at most 1024; dim: 32, 64,
+ * [pages][heads], above 0 as bsg_kv8_append makes them.  page_tokens: a multiple of 16, at most 1024; dim: 32, 64,
  * 96, 128 or 256.  A sequence b owns the pages table[b][0..table_ld-1] (int32,
  * DEVICE; table_ld pages hold table_ld * page_tokens tokens at most), its
  * token at position p being token p % page_tokens of page

@@ -50,11 +50,15 @@ def equal_scores(call, dtype, B, T, Hk, D, n, run, runs, pool=256):
     order = rng.integers(0, pool, -(-n // PAGE)).astype(np.int32)      # a page may stand in a table often
     table = dev(np.broadcast_to(order, (B, len(order))).copy())
     q = torch.zeros(B, T, Hk, D, dtype=dtype, device="cuda")
-    out = call(q, bsg.Kv8Cache(*map(dev, cache)), table, torch.full((B,), n, dtype=torch.int32, device="cuda"))
+    lse = torch.empty(B, T, Hk, device="cuda")
+    out = call(q, bsg.Kv8Cache(*map(dev, cache)), table, torch.full((B,), n, dtype=torch.int32, device="cuda"), lse=lse)
     off = 2.0 ** -19 + run * 2.0 ** -22 + 2 * (run + runs + 16) * 2.0 ** -24
     for t in {0, T - 1}:
         want = np.broadcast_to(means(cache, order, n - T + 1 + t), (B, Hk, D))
         within(f64(out[:, t]), want, np.abs(want) * off * 1.01 + rounding(want, dtype), f"token {t}")
+        # log n; the sum's error, and f32's in the reference and the logarithm (prompts_ref's 2^-20)
+        want = np.full((B, Hk), np.log(n - T + 1 + t))
+        within(f64(lse[:, t]), want, off + 2.0 ** -20 * (2 + want), f"lse of token {t}")
 
 
 # Sequences enough that a chunk is a whole sequence or a good part of one; a warp takes every
@@ -93,7 +97,7 @@ def test_a_long_prefix(dtype, n):
 
 def test_own_tokens_behind_a_prefix():
     prefix, n0 = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
-    equal_scores(lambda q, c, table, lens: bsg.kv8_attend_shared(q, c, prefix, n0, table, lens), F32, 400, 1, 8, 128, 65536, 32, 32)
+    equal_scores(lambda q, c, table, lens, lse: bsg.kv8_attend_shared(q, c, prefix, n0, table, lens, lse=lse), F32, 400, 1, 8, 128, 65536, 32, 32)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
