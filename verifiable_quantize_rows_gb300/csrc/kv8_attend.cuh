@@ -87,7 +87,7 @@ constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kMaxSplits = 1024;
 constexpr float kRefNone = -3.0e38f;  // the reference of a row that has seen nothing
-// Tiles of a warp to one sum.  f32: 32 products, 2^-20 or so; 16 bits: 256, 2^-16, where f16's own rounding is 2^-12.
+// Tiles of a warp to one sum.  f32: 32 products, 2^-20 or so; 16 bits: 256, 2^-16, where f16's own rounding is 2^-11.
 template <int kParts>
 constexpr int kAnew = kParts == 2 ? 32 : 128;
 constexpr float kTop = 11.0f, kMost = 15.0f;  // exponents of a new reference's largest p', and of any

@@ -151,10 +151,10 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Which kernel a call takes: up to this many query rows of a key/value head the one of few rows,
 // which reads the cache at its rate by 16 rows of 16 bits (or 8 of f32) and again for as many more;
 // beyond, 128 rows a tile.  Both in us, few rows then tiles, by 8 heads of 128 dims:
-//                                       16 rows           20 rows    |  f32 32 rows      48 rows
-//   16 sequences of 16384, bf16 (f16)   132, 208 (266)    233, 208   |  274, 480         390, 477
-//   16 of 2048                          36, 32 (40)       61, 32     |  64, 64           86, 65
-//   one of 16384                        29, 23 (27)       46, 23     |  46, 37           55, 37
+//                                 16 rows, bf16 (f16)     20 rows         |  f32 20 rows    32         48
+//   16 sequences of 16384         132, 203 (131, 272)     233, 203 (272)  |  295, 445   299, 446   428, 446
+//   16 of 2048                    36, 32 (36, 41)         61, 32 (41)     |  62, 59     65, 59     86, 60
+//   one of 16384                  30, 24 (30, 28)         46, 24 (28)     |  46, 36     47, 37     55, 37
 bool few(int64_t rows, int dtype) { return rows <= (dtype == BSG_F32 ? 32 : 16); }
 
 // The workspace of one part of a call, largest over the types: a call takes the plan of its own.

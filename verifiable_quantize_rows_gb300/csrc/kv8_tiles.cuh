@@ -5,11 +5,15 @@
 // times tokens) and walks the tiles of kN positions that some of them see:
 //   S = Q K^T          128 x kN, in tensor memory, one place that the groups of 128 rows use in turn
 //   p' = 2^(S ks mul + log2 vs - ref)   a thread to a row, in f16, half a tile at a time
-//   O += P V           P (f32, f16: two f16 parts, 22 bits; bf16: one) read from tensor memory, O stays there
+//   O += P V           P (f32, f16: two f16 parts, 22 bits; bf16: one, 11) read from tensor memory, O stays there
 // with ks, vs the page's scales (one for each 16 positions of a tile), mul the row's
 // multiplier, ref the row's running reference, which follows the maximum only when that is
 // above 2^15 (what f16 holds) and makes it 2^9 then: O is rescaled where it lies, a few times
 // in a row's life.  Sums of p = p' / vs in f32.
+// bf16's one part: each p is off by 2^-11 of itself at most, an output by 2^-11 of sum p |v|, where its own
+// rounding is 2^-8 of itself; beside 64 bits the listed prompts and shared beginnings are 1.669e-3 off,
+// 1.659e-3 with two parts (and with f32 throughout), which take 2.19 ms in place of 1.54 and 72 us in place
+// of 60.  Where values cancel, an output smaller than sum p |v| / 8 shows it: such sums want f16 or f32.
 // Codes are exact in f16, so K and V are too; queries are relative to a power of two near
 // their row's largest, f32's as two f16 parts (22 bits).
 //
@@ -27,8 +31,9 @@
 // tensor 0.39 of the active cycles, ALU 0.40, XU 0.20).  Two prompts of up to 16384, window 4096,
 // 32/8 heads of 128, bf16: 1.54 ms, 0.56 of the products' floor; 64 rows behind 131071 shared
 // positions, 8 heads of 128, f16 (two parts of P): 167 us of the call's 185, tensor 0.55; ragged
-// prompts of up to 1021, 5 heads of 64, f32: 47 us, three rounds of CTAs of five tiles, whose start
-// and end take some 10 of each 16 us.
+// prompts of up to 1021, 5 heads of 64, f32: 46 us, three rounds of CTAs of five tiles, whose start
+// and end take some 10 of each 16 us.  Prompts of 16384 without a window: bf16 3.4 ms, f16 4.9, f32 7.9;
+// f16's and f32's softmax threads spill 40 to 200 bytes each (-Xptxas -v), bf16's 20 to 40.
 // Why so: S in registers and a split of these by role 3.6 -> 2.06 ms (S read from tensor memory
 // in pieces spilled or came twice); MMAs issued by a converged warp, descriptors in uniform
 // registers 1.91; P apart from S, so that the next S does not wait for P V, by halves, so that P V
@@ -134,10 +139,10 @@ struct TileCfg {
     // to a second set, which lies in local memory, every kFlush tiles and begun anew, but for the last
     // quarter as many more.  Off 64 bits on the mean, with equal scores and values of one sign: f32, 65536
     // positions, 1.2e-6 (the sum of p in one piece 1.7e-5); f16, 131072, 5e-5 (in one piece of 65536
-    // 4.2e-4; its rounding 4.9e-4 at most); bf16, 524288, 2.5e-4 (3.7e-3; 3.9e-3).  Times as before but
-    // for f16's of more positions, whose registers spill more: prompts of 16384 without a window 5.1 ->
-    // 5.5 ms, every 4096 positions 5.6; bf16 3.38 -> 3.36, every 4096 3.55.  In local memory a warp's
-    // second set lies side by side; f32's in the outputs' rows took 11.2 ms there in place of 8.0.
+    // 4.2e-4; its rounding 4.9e-4 at most); bf16, 524288, 2.5e-4 (3.7e-3; 3.9e-3).  Between runs of
+    // tiles and not within the loop over them: prompts of 16384 without a window, f16 5.5 -> 4.9 ms, f32
+    // 8.0 -> 7.9 (16 sequences of 16384 by 48 rows 421 -> 445 us).  In local memory a warp's second set
+    // lies side by side; f32's in the outputs' rows took 11.2 ms there.
     static constexpr int kFlush = (kQParts == 2 ? 512 : kPParts == 2 ? 8192 : 32768) / kN;  // tiles
     static constexpr int kFlushMost = kFlush + kFlush / 4;
     static __device__ bool flush_at(int i, int tiles) {
@@ -640,15 +645,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // What O was before it was begun anew, the sum, and the reference then (a row that had seen
         // nothing: -inf, no part of it): in local memory, and in no register from one time to the next.
         volatile float kept[D + 2];
+        // runs of tiles between which the sums are begun anew
 #pragma unroll 1
-        for (int i = 0; i < tiles; ++i) {
-            const int tile = position(i), slot = i % kAtSlots;
-            const float4 *of_s = at_s + slot * C::kGroups;
-            if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
-            tc_fence_after();
-            const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
+        for (int i = 0; i < tiles;) {
             if (C::flush_at(i, tiles)) {
-                // O is at rest once the last P of the tile before is used up (in place: as S is there)
+                // O is at rest once the last P of the tile before is used up (in place: as the next S is there)
+                if (kInPlace) ok = all_wait(&s_full[m], i & 1);
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
@@ -672,114 +674,124 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int u = 0; u < 32; ++u) kept[32 * c + u] = fmaf(before[u], f, __uint_as_float(o[u]));
                 }
             }
-            if (edge) {  // what the row does not see, where S lies (seldom; rolled up)
+            const int stop = C::flush_at(i + C::kFlush, tiles) ? i + C::kFlush : tiles;
 #pragma unroll 1
-                for (int c = 0; c < kN / 16; ++c) {
-                    const int j = tile + 16 * c;
-                    const uint32_t mask = below(see - j) & (~below(low - j) | below(a.sinks - j));
-                    uint32_t x[16];
-                    tmem_ld16(s_at + 16 * c, x);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        if (!(mask & 1u << u)) x[u] = 0xff800000u;
-                    tmem_st16(s_at + 16 * c, x);
-                }
-                tmem_st_wait();
-            }
-            uint32_t v[kN / 32][32];  // the row's scores
-#pragma unroll
-            for (int c = 0; c < kN / 32; ++c) tmem_ld32(s_at + 32 * c, v[c]);
-#pragma unroll
-            for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
-            tc_fence_before();
-            __syncwarp();
-            if (!kInPlace && lane == 0) mbar_arrive(&s_empty[m]);
-            // the largest exponent, relative to the reference
-            float y[C::kGroups], top = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < C::kGroups; ++g) y[g] = __uint_as_float(v[g / 2][g % 2 * 16]);
-#pragma unroll
-            for (int u = 1; u < 16; ++u)  // the groups side by side, not one after another
-#pragma unroll
-                for (int g = 0; g < C::kGroups; ++g) y[g] = fmaxf(y[g], __uint_as_float(v[g / 2][g % 2 * 16 + u]));
-            // (a score of -inf times 0 would be no number)
-#pragma unroll
-            for (int g = 0; g < C::kGroups; ++g) {
-                const float2 of = *reinterpret_cast<const float2 *>(of_s + g);
-                top = fmaxf(top, fmaf(y[g], fmaxf(of.x * mul, 1e-37f), of.y - ref));
-            }
-            const bool move = none ? top > -INFINITY : top > kTileMost;
-            if (__any_sync(0xffffffffu, move)) {
-                float keep = 1.0f;
-                if (move) {  // each row by itself: no other row's values move its reference
-                    if (!none) keep = tile_exp2(kTileTop - top);
-                    ref += top - kTileTop;
-                    sum *= keep;
-                    none = false;
-                }
-                if (i > 0) {
-                    // O is at rest once the last P of the tile before is used up (in place: as S is there)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
+            for (; i < stop; ++i) {
+                const int tile = position(i), slot = i % kAtSlots;
+                const float4 *of_s = at_s + slot * C::kGroups;
+                if (!(ok = all_wait(&at_full[slot], i / kAtSlots & 1) && all_wait(&s_full[m], i & 1))) break;
+                tc_fence_after();
+                const bool edge = tile + kN > all_see || (tile < all_low && tile + kN > a.sinks);
+                if (edge) {  // what the row does not see, where S lies (seldom; rolled up)
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16(o_at + 16 * c, o);
+                    for (int c = 0; c < kN / 16; ++c) {
+                        const int j = tile + 16 * c;
+                        const uint32_t mask = below(see - j) & (~below(low - j) | below(a.sinks - j));
+                        uint32_t x[16];
+                        tmem_ld16(s_at + 16 * c, x);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-                        tmem_st16(o_at + 16 * c, o);
+                        for (int u = 0; u < 16; ++u)
+                            if (!(mask & 1u << u)) x[u] = 0xff800000u;
+                        tmem_st16(s_at + 16 * c, x);
                     }
+                    tmem_st_wait();
                 }
-            }
+                uint32_t v[kN / 32][32];  // the row's scores
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t hi[kHalf / 2], lo[kHalf / 2];
+                for (int c = 0; c < kN / 32; ++c) tmem_ld32(s_at + 32 * c, v[c]);
 #pragma unroll
-                for (int g = 0; g < kHalf / 16; ++g) {
-                    const float4 of = of_s[half * (kHalf / 16) + g];
-                    const float f = fmaxf(of.x * mul, 1e-37f), off = of.y - ref;
-                    const uint64_t ff = pair_of(f, f), oo = pair_of(off, off);
-                    const uint32_t *x = v[(half * kHalf + 16 * g) / 32] + (half * kHalf + 16 * g) % 32;
-                    float p[16];
+                for (int c = 0; c < kN / 32; ++c) tmem_ld_wait32(v[c]);
+                tc_fence_before();
+                __syncwarp();
+                if (!kInPlace && lane == 0) mbar_arrive(&s_empty[m]);
+                // the largest exponent, relative to the reference
+                float y[C::kGroups], top = -INFINITY;
 #pragma unroll
-                    for (int u = 0; u < 16; u += 2) {
-                        unpair(fma2(pair_of(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), ff, oo), p[u], p[u + 1]);
-                        p[u] = tile_exp2(p[u]), p[u + 1] = tile_exp2(p[u + 1]);
+                for (int g = 0; g < C::kGroups; ++g) y[g] = __uint_as_float(v[g / 2][g % 2 * 16]);
+#pragma unroll
+                for (int u = 1; u < 16; ++u)  // the groups side by side, not one after another
+#pragma unroll
+                    for (int g = 0; g < C::kGroups; ++g) y[g] = fmaxf(y[g], __uint_as_float(v[g / 2][g % 2 * 16 + u]));
+                // (a score of -inf times 0 would be no number)
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
+                    const float2 of = *reinterpret_cast<const float2 *>(of_s + g);
+                    top = fmaxf(top, fmaf(y[g], fmaxf(of.x * mul, 1e-37f), of.y - ref));
+                }
+                const bool move = none ? top > -INFINITY : top > kTileMost;
+                if (__any_sync(0xffffffffu, move)) {
+                    float keep = 1.0f;
+                    if (move) {  // each row by itself: no other row's values move its reference
+                        if (!none) keep = tile_exp2(kTileTop - top);
+                        ref += top - kTileTop;
+                        sum *= keep;
+                        none = false;
                     }
-                    uint64_t part[2] = {pair_of(p[0], p[1]), pair_of(p[2], p[3])};
+                    if (i > 0) {
+                        // O is at rest once the last P of the tile before is used up (in place: as S is there)
 #pragma unroll
-                    for (int u = 4; u < 16; u += 2) part[u / 2 % 2] = add2(part[u / 2 % 2], pair_of(p[u], p[u + 1]));
-                    float even, odd;
-                    unpair(add2(part[0], part[1]), even, odd);
-                    sum = fmaf(even + odd, of.z, sum);
+                        for (int u = 0; u < 2; ++u)
+                            if (!kInPlace && ok) ok = all_wait(&p_empty[2 * m + u], (i - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + 16 * c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 16; u += 2) {
-                        const __half2 h = __floats2half2_rn(p[u], p[u + 1]);
-                        hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
-                        if (kPParts == 2) {
-                            const float2 back = __half22float2(h);
-                            const __half2 rest = __floats2half2_rn(p[u] - back.x, p[u + 1] - back.y);
-                            lo[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&rest);
+                            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+                            tmem_st16(o_at + 16 * c, o);
                         }
                     }
                 }
-                // its place is free when what was there has been multiplied
-                if (!kInPlace && i > 0 && !(ok = all_wait(&p_empty[2 * m + half], (i - 1) & 1))) break;
-                tc_fence_after();
-                tmem_store(p_at + half * (C::kPCols / 2), hi);
-                if (kPParts == 2) tmem_store(p_at + half * (C::kPCols / 2) + kHalf / 2, lo);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * m + half]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[kHalf / 2], lo[kHalf / 2];
+#pragma unroll
+                    for (int g = 0; g < kHalf / 16; ++g) {
+                        const float4 of = of_s[half * (kHalf / 16) + g];
+                        const float f = fmaxf(of.x * mul, 1e-37f), off = of.y - ref;
+                        const uint64_t ff = pair_of(f, f), oo = pair_of(off, off);
+                        const uint32_t *x = v[(half * kHalf + 16 * g) / 32] + (half * kHalf + 16 * g) % 32;
+                        float p[16];
+#pragma unroll
+                        for (int u = 0; u < 16; u += 2) {
+                            unpair(fma2(pair_of(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), ff, oo), p[u], p[u + 1]);
+                            p[u] = tile_exp2(p[u]), p[u + 1] = tile_exp2(p[u + 1]);
+                        }
+                        uint64_t part[2] = {pair_of(p[0], p[1]), pair_of(p[2], p[3])};
+#pragma unroll
+                        for (int u = 4; u < 16; u += 2) part[u / 2 % 2] = add2(part[u / 2 % 2], pair_of(p[u], p[u + 1]));
+                        float even, odd;
+                        unpair(add2(part[0], part[1]), even, odd);
+                        sum = fmaf(even + odd, of.z, sum);
+#pragma unroll
+                        for (int u = 0; u < 16; u += 2) {
+                            const __half2 h = __floats2half2_rn(p[u], p[u + 1]);
+                            hi[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                            if (kPParts == 2) {
+                                const float2 back = __half22float2(h);
+                                const __half2 rest = __floats2half2_rn(p[u] - back.x, p[u + 1] - back.y);
+                                lo[8 * g + u / 2] = *reinterpret_cast<const uint32_t *>(&rest);
+                            }
+                        }
+                    }
+                    // its place is free when what was there has been multiplied
+                    if (!kInPlace && i > 0 && !(ok = all_wait(&p_empty[2 * m + half], (i - 1) & 1))) break;
+                    tc_fence_after();
+                    tmem_store(p_at + half * (C::kPCols / 2), hi);
+                    if (kPParts == 2) tmem_store(p_at + half * (C::kPCols / 2) + kHalf / 2, lo);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * m + half]);
+                }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&at_empty[slot]);
             }
             if (!ok) break;
-            if (lane == 0) mbar_arrive(&at_empty[slot]);
         }
         if (ok && tiles > 0) {
             ok = all_wait(&o_full[m], 0);

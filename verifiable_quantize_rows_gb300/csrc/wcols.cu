@@ -167,7 +167,8 @@ cudaError_t launch_tokens(const T *X, int64_t ldx, int64_t M, int K, int ldk, __
 // bytes as the codes), and the chain of waits of the MMAs' warp; HBM is at 0.35 and the tensor
 // cores at 0.13 of their rates.  61 tokens, 8192 x 12288 bf16 38 us (the floor's bytes 15), 8191 x
 // 12289 51: rows that begin anywhere take nine pieces of 16 bytes where others take eight, from
-// DRAM half as many bytes again (145 MB), and shifts.  8192 x 8192 (floor 10): 16 tokens 22, 64
+// DRAM half as many bytes again (145 MB), and shifts.  (64 tokens' sums spill some 50 bytes a thread:
+// 72 registers are what 832 threads leave.)  8192 x 8192 (floor 10): 16 tokens 22, 64
 // tokens 29.  Measured and not kept: rings
 // of three and four blocks, two stages of operands, four teams of 64-deep blocks.
 constexpr int kFewTokens = 64;
