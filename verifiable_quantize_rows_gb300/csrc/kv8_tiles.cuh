@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             set_status(a.dstatus, BSG_DSTATUS_RANGE);
                         } else {
                             const int64_t ph = (int64_t)page * a.c.heads + hk;
-                            const float v = fmaxf(__ldg(a.c.v_scale + ph), 1e-30f);
+                            // finite: a masked score of -inf and the logarithm of Inf would be no number
+                            // for rows that do not see the page (NaN: the least scale)
+                            const float v = fminf(fmaxf(__ldg(a.c.v_scale + ph), 1e-30f), 3e38f);
                             at = make_float4(__ldg(a.c.k_scale + ph), log2f(v), __frcp_rn(v),
                                              __int_as_float((int)(ph * (P / 16) + pos % P / 16)));
                         }
